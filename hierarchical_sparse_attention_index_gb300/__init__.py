@@ -24,6 +24,8 @@ HSA_FLAG_INDEX_RANGE, HSA_FLAG_WRITE_RANGE, HSA_FLAG_TIMEOUT = 1, 2, 4
 HSA_CACHE_ROPE, HSA_CACHE_POOL_TAIL = 1, 2
 HSA_POOL_TAIL_SLOTS = 160
 HSA_ROPE_DIMS, HSA_ROPE_THETA = 64, 160000.0
+HSA_BF16, HSA_F16, HSA_E4M3 = 0, 1, 2
+HSA_MAX_GROUP = 128
 
 STATUS = {0: "HSA_OK", 1: "HSA_ERR_INVALID_ARG", 2: "HSA_ERR_SHAPE", 3: "HSA_ERR_ALIGN",
           4: "HSA_ERR_WORKSPACE", 5: "HSA_ERR_CUDA", 6: "HSA_ERR_TIMEOUT", 7: "HSA_ERR_UNSUPPORTED"}
@@ -32,7 +34,8 @@ STATUS_CODES = {v: k for k, v in STATUS.items()}
 EXPORTS = ("hsa_abi_version", "hsa_status_string", "hsa_workspace_bytes", "hsa_workspace_init",
            "hsa_cache_write_compress", "hsa_index_full", "hsa_index_reindex", "hsa_sparse_attn_decode",
            "hsa_schedule_step", "hsa_get_device_status", "hsa_index_full_noalloc", "hsa_set_wait_limit",
-           "hsa_debug_stall_next_scan")
+           "hsa_debug_stall_next_scan", "hsa_paged_cache_write", "hsa_paged_attn_workspace_bytes",
+           "hsa_paged_attn_decode", "hsa_prompt_attn")
 
 
 class HsaError(RuntimeError):
@@ -57,6 +60,24 @@ class hsa_step_args(ctypes.Structure):
                 ("vis", ctypes.c_void_p), ("max_vis", ctypes.c_int64), ("sm_scale", ctypes.c_float)]
 
 
+class hsa_paged_cache(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
+
+
+class hsa_prompt_args(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("heads_kv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("n_q", ctypes.c_int64), ("n_k", ctypes.c_int64), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("cu_q", ctypes.c_void_p),
+                ("cu_k", ctypes.c_void_p), ("sm_scale", ctypes.c_float), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -70,7 +91,7 @@ def load_library(path: str = LIB_PATH):
                            "`python -m hierarchical_sparse_attention_index_gb300.build`")
     lib = ctypes.CDLL(path)
     P, I32, I64, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
-    C = ctypes.POINTER(hsa_cache)
+    C, G = ctypes.POINTER(hsa_cache), ctypes.POINTER(hsa_paged_cache)
     sig = {
         "hsa_abi_version": (I32, []),
         "hsa_status_string": (ctypes.c_char_p, [I32]),
@@ -85,6 +106,10 @@ def load_library(path: str = LIB_PATH):
         "hsa_index_full_noalloc": (I32, [C, P, P, P, I32, I64, P, P, P]),
         "hsa_set_wait_limit": (I32, [ctypes.c_uint64]),
         "hsa_debug_stall_next_scan": (I32, []),
+        "hsa_paged_cache_write": (I32, [G, P, P, I32, I64, I64, I64, P, P, P]),
+        "hsa_paged_attn_workspace_bytes": (SZ, [G, I32, I32, I64]),
+        "hsa_paged_attn_decode": (I32, [G, P, I32, I32, P, I32, I64, I32, F, P, P, P, SZ, P]),
+        "hsa_prompt_attn": (I32, [ctypes.POINTER(hsa_prompt_args), P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -227,6 +252,129 @@ def hsa_schedule_step(caches, step: StepArgs, ws, stream=None):
     descs = (hsa_cache * n)(*[c.desc for c in caches])
     _check("hsa_schedule_step", load_library().hsa_schedule_step(
         descs, ctypes.byref(step.args), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- dense attention
+def _dtype(t):
+    """The hsa_dtype of a tensor."""
+    import torch
+    try:
+        return {torch.bfloat16: HSA_BF16, torch.float16: HSA_F16, torch.float8_e4m3fn: HSA_E4M3}[t.dtype]
+    except KeyError:
+        raise ValueError(f"unsupported type {t.dtype}") from None
+
+
+def _rows(name, t, heads, dim):
+    """Row stride of [rows][heads][dim] values: rows may stand apart, a row is contiguous."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows][{heads}][{dim}]")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: a row of [{heads}][{dim}] must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _given(name, t, dtype, shape, device):
+    """Check a contiguous tensor argument (the library takes its address alone); None passes."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: expected contiguous {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} "
+                         f"on {t.device}")
+    return t.data_ptr()
+
+
+def _on_device(name, t):
+    """The library launches on the current device, so its tensors have to be there."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}: expected the current CUDA device")
+    return t.device
+
+
+class PagedCache:
+    """Caller-owned paged key-value cache of a dense attention layer: pools k and v
+    [n_pages][heads][page_size][head_dim] (bfloat16, float16 or float8_e4m3fn) and an int32 table
+    [batch][max_pages] of page ids, all contiguous. A value is its stored number times its scale."""
+
+    def __init__(self, k, v, table, k_scale=1.0, v_scale=1.0):
+        import torch
+        if k.dim() != 4 or table.dim() != 2:
+            raise ValueError("k and v are [n_pages][heads][page_size][head_dim], table is [batch][max_pages]")
+        self.k, self.v, self.table = k, v, table
+        _given("v", v, k.dtype, k.shape, k.device)
+        _given("k", k, k.dtype, k.shape, k.device)
+        _given("table", table, torch.int32, table.shape, k.device)
+        n_pages, self.heads, self.page_size, self.head_dim = k.shape
+        self.batch, max_pages = table.shape
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self.desc = hsa_paged_cache(self.batch, self.heads, self.head_dim, self.page_size, _dtype(k), 0, n_pages, max_pages,
+                                    _ptr(k), _ptr(v), _ptr(table), self.k_scale, self.v_scale)
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+
+def hsa_paged_cache_write(cache: PagedCache, k, v, cu=None, start=None, stream=None):
+    """k, v: [n_tokens][heads][head_dim], rows at any stride; cu: int32 [batch + 1] or None (equal
+    shares); start: int64 [batch] or None (0)."""
+    import torch
+    dev = _on_device("cache", cache.k)
+    k_stride, v_stride = (_rows(n, t, cache.heads, cache.head_dim) for n, t in (("k", k), ("v", v)))
+    if k.shape != v.shape or k.dtype != v.dtype or k.device != dev or v.device != dev:
+        raise ValueError("k and v differ in shape or type, or are not on the cache's device")
+    _check("hsa_paged_cache_write", load_library().hsa_paged_cache_write(
+        cache.ref, k.data_ptr(), v.data_ptr(), _dtype(k), k_stride, v_stride, k.shape[0],
+        _given("cu", cu, torch.int32, (cache.batch + 1,), dev), _given("start", start, torch.int64, (cache.batch,), dev),
+        _stream(stream)))
+
+
+def hsa_paged_attn_workspace_bytes(cache: PagedCache, heads_q, nq, max_vis):
+    return load_library().hsa_paged_attn_workspace_bytes(cache.ref, heads_q, nq, max_vis)
+
+
+def new_paged_workspace(cache: PagedCache, heads_q, nq, max_vis):
+    """Allocate (torch) a workspace of hsa_paged_attn_decode for the given sizes."""
+    import torch
+    n = hsa_paged_attn_workspace_bytes(cache, heads_q, nq, max_vis)
+    if n == 0:
+        raise ValueError("invalid workspace sizes")
+    return torch.empty(n, dtype=torch.uint8, device=cache.k.device)
+
+
+def hsa_paged_attn_decode(cache: PagedCache, q, vis, max_vis, sm_scale, out, ws, window=0, lse=None, stream=None):
+    """q, out: [batch][nq][heads_q][head_dim]; vis: int32 [batch][nq]; lse: float32 [batch][nq][heads_q] or None."""
+    import torch
+    dev = _on_device("cache", cache.k)
+    if q.dim() != 4 or q.shape[0] != cache.batch or q.shape[3] != cache.head_dim:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [{cache.batch}][nq][heads_q][{cache.head_dim}]")
+    _, nq, heads_q, _ = q.shape
+    _check("hsa_paged_attn_decode", load_library().hsa_paged_attn_decode(
+        cache.ref, _given("q", q, q.dtype, q.shape, dev), _dtype(q), heads_q,
+        _given("vis", vis, torch.int32, (cache.batch, nq), dev), nq, max_vis, window, float(sm_scale),
+        _given("out", out, q.dtype, q.shape, dev), _given("lse", lse, torch.float32, q.shape[:3], dev), _ptr(ws),
+        ws.numel() * ws.element_size() if ws is not None and ws.device == dev else 0, _stream(stream)))
+
+
+def hsa_prompt_attn(q, k, v, cu_q, sm_scale, out, cu_k=None, window=0, lse=None, stream=None):
+    """q, out: [n_q][heads_q][head_dim], k, v: [n_k][heads_kv][head_dim], rows at any stride; cu_q,
+    cu_k: int32 [batch + 1] (cu_k None: cu_q); lse: float32 [n_q][heads_q] or None."""
+    import torch
+    dev = _on_device("q", q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k, v and out are [rows][heads][head_dim]")
+    (n_q, heads_q, dim), (n_k, heads_kv, _) = q.shape, k.shape
+    q_stride, out_stride = (_rows(n, t, heads_q, dim) for n, t in (("q", q), ("out", out)))
+    k_stride, v_stride = (_rows(n, t, heads_kv, dim) for n, t in (("k", k), ("v", v)))
+    if out.shape != q.shape or k.shape != v.shape or any(t.dtype != q.dtype or t.device != dev for t in (k, v, out)):
+        raise ValueError("q, k, v and out differ in type or device, q and out or k and v in shape")
+    batch = cu_q.numel() - 1
+    a = hsa_prompt_args(batch, heads_q, heads_kv, dim, _dtype(q), window, n_q, n_k, q.data_ptr(), k.data_ptr(),
+                        v.data_ptr(), q_stride, k_stride, v_stride, out_stride,
+                        _given("cu_q", cu_q, torch.int32, (batch + 1,), dev),
+                        _given("cu_k", cu_k, torch.int32, (batch + 1,), dev), float(sm_scale), out.data_ptr(),
+                        _given("lse", lse, torch.float32, (n_q, heads_q), dev))
+    _check("hsa_prompt_attn", load_library().hsa_prompt_attn(ctypes.byref(a), _stream(stream)))
 
 
 def hsa_set_wait_limit(ns):

@@ -450,6 +450,173 @@ hsa_status hsa_schedule_step(const hsa_cache* caches, const hsa_step_args* a, vo
   return HSA_OK;
 }
 
+// ------------------------------------------------------------------ dense attention
+// The fields of a paged cache that sizes follow from; its pointers are checked by check_paged.
+static hsa_status check_paged_sizes(const hsa_paged_cache* c) {
+  if (!c) return HSA_ERR_INVALID_ARG;
+  if (c->dtype != HSA_BF16 && c->dtype != HSA_F16 && c->dtype != HSA_E4M3) return HSA_ERR_INVALID_ARG;
+  if (c->flags) return HSA_ERR_INVALID_ARG;
+  if (c->batch < 1 || c->heads < 1 || c->heads > 1024 || (c->head_dim != 64 && c->head_dim != 128)) return HSA_ERR_SHAPE;
+  if (c->page_size < 16 || c->page_size > 4096 || c->page_size % 16) return HSA_ERR_SHAPE;
+  if (c->n_pages < 1 || c->n_pages > (int64_t)INT32_MAX || c->max_pages < 1 || c->max_pages > (int64_t)INT32_MAX / c->page_size)
+    return HSA_ERR_SHAPE;
+  return HSA_OK;
+}
+static hsa_status check_paged(const hsa_paged_cache* c) {
+  const hsa_status st = check_paged_sizes(c);
+  if (st != HSA_OK) return st;
+  if (!c->k || !c->v || !c->table) return HSA_ERR_INVALID_ARG;
+  if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || !isfinite(c->k_scale) || !isfinite(c->v_scale)) return HSA_ERR_INVALID_ARG;
+  if (c->dtype != HSA_E4M3 && (c->k_scale != 1.f || c->v_scale != 1.f)) return HSA_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v)) return HSA_ERR_ALIGN;
+  return HSA_OK;
+}
+// q (or new keys and values) against the cache's type: 16-bit, and the cache's own unless that is E4M3
+static bool type_fits(int32_t dtype, int32_t cache) {
+  return (dtype == HSA_BF16 || dtype == HSA_F16) && (cache == HSA_E4M3 || cache == dtype);
+}
+static hsa_status check_paged_query(const hsa_paged_cache* c, int32_t heads_q, int32_t nq, int64_t max_vis) {
+  if (heads_q < 1 || heads_q % c->heads || heads_q / c->heads > HSA_MAX_GROUP) return HSA_ERR_SHAPE;
+  if (nq < 1 || nq > HSA_MAX_NQ) return HSA_ERR_SHAPE;
+  if (max_vis < 0 || max_vis > HSA_MAX_VIS || max_vis > c->max_pages * c->page_size) return HSA_ERR_SHAPE;
+  return HSA_OK;
+}
+struct PagedWs {
+  size_t off_o, off_ml, total;
+};
+static PagedWs paged_ws(const hsa_paged_cache* c, int32_t rows, int32_t n_splits) {
+  PagedWs w;
+  const size_t parts = n_splits > 1 ? (size_t)c->batch * c->heads * n_splits * rows : 0;
+  w.off_o = 0;
+  w.off_ml = parts * c->head_dim * 4;
+  w.total = (w.off_ml + parts * 8 + 255) / 256 * 256 + 256;
+  return w;
+}
+
+hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const void* k, const void* v, int32_t dtype,
+                                 int64_t k_stride, int64_t v_stride, int64_t n_tokens, const int32_t* cu,
+                                 const int64_t* start, hsa_stream_t stream) {
+  NvtxRange range("hsa_paged_cache_write");
+  const hsa_status st = check_paged(cache);
+  if (st != HSA_OK) return st;
+  if (!type_fits(dtype, cache->dtype)) return HSA_ERR_INVALID_ARG;
+  if (n_tokens < 0 || n_tokens > (int64_t)INT32_MAX) return HSA_ERR_SHAPE;
+  if (n_tokens == 0) return HSA_OK;
+  if (!k || !v) return HSA_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)cache->heads * cache->head_dim;
+  if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8 || k_stride > (int64_t)INT32_MAX ||
+      v_stride > (int64_t)INT32_MAX)
+    return HSA_ERR_SHAPE;
+  if (!cu && n_tokens % cache->batch) return HSA_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v)) return HSA_ERR_ALIGN;
+  uint32_t* status;
+  int sms;
+  if (!device_info(&status, &sms)) return HSA_ERR_UNSUPPORTED;
+  PagedWriteParams p;
+  memset(&p, 0, sizeof(p));
+  p.batch = cache->batch;
+  p.heads = cache->heads;
+  p.head_dim = cache->head_dim;
+  p.page_size = cache->page_size;
+  p.n_pages = cache->n_pages;
+  p.max_pages = cache->max_pages;
+  p.k_pool = static_cast<uint8_t*>(cache->k);
+  p.v_pool = static_cast<uint8_t*>(cache->v);
+  p.table = cache->table;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.n_tokens = n_tokens;
+  p.bf16 = dtype == HSA_BF16;
+  p.cu = cu;
+  p.per_request = n_tokens / cache->batch;
+  p.start = start;
+  p.status = status;
+  return cuda_fail(launch_paged_write(p, cache->dtype == HSA_E4M3, (cudaStream_t)stream), "paged write launch");
+}
+
+size_t hsa_paged_attn_workspace_bytes(const hsa_paged_cache* cache, int32_t heads_q, int32_t nq, int64_t max_vis) {
+  if (check_paged_sizes(cache) != HSA_OK || check_paged_query(cache, heads_q, nq, max_vis) != HSA_OK) return 0;
+  const int32_t rows = nq * (heads_q / cache->heads);
+  return paged_ws(cache, rows, paged_split(cache->batch, cache->heads, rows, max_vis, 0, nq).n_splits).total;
+}
+
+hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, int32_t q_dtype, int32_t heads_q,
+                                 const int32_t* vis, int32_t nq, int64_t max_vis, int32_t window, float sm_scale,
+                                 void* out, float* lse, void* ws, size_t ws_bytes, hsa_stream_t stream) {
+  NvtxRange range("hsa_paged_attn_decode");
+  hsa_status st = check_paged(cache);
+  if (st != HSA_OK) return st;
+  st = check_paged_query(cache, heads_q, nq, max_vis);
+  if (st != HSA_OK) return st;
+  if (!q || !vis || !out || !type_fits(q_dtype, cache->dtype)) return HSA_ERR_INVALID_ARG;
+  if (window < 0 || !(sm_scale > 0.f) || !isfinite(sm_scale)) return HSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return HSA_ERR_ALIGN;
+  const int32_t group = heads_q / cache->heads, rows = nq * group;
+  const PagedSplit sp = paged_split(cache->batch, cache->heads, rows, max_vis, window, nq);
+  if ((int64_t)sp.n_splits * sp.chunks * cache->heads * cache->batch > (int64_t)INT32_MAX) return HSA_ERR_SHAPE;
+  const PagedWs L = paged_ws(cache, rows, sp.n_splits);
+  if (!ws || ws_bytes < L.total) return HSA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return HSA_ERR_ALIGN;
+  uint32_t* status;
+  int sms;
+  if (!device_info(&status, &sms)) return HSA_ERR_UNSUPPORTED;
+  PagedAttnParams p;
+  memset(&p, 0, sizeof(p));
+  p.batch = cache->batch;
+  p.heads = cache->heads;
+  p.page_size = cache->page_size;
+  p.n_pages = cache->n_pages;
+  p.max_pages = cache->max_pages;
+  p.k_pool = static_cast<const uint8_t*>(cache->k);
+  p.v_pool = static_cast<const uint8_t*>(cache->v);
+  p.table = cache->table;
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_bf16 = q_dtype == HSA_BF16;
+  p.heads_q = heads_q;
+  p.group = group;
+  p.nq = nq;
+  p.window = window;
+  p.vis = vis;
+  p.max_vis = max_vis;
+  p.scale_log2 = sm_scale * cache->k_scale * 1.4426950408889634f;
+  p.v_scale = cache->v_scale;
+  p.chunk_rows = sp.chunk_rows;
+  p.chunks = sp.chunks;
+  p.n_splits = sp.n_splits;
+  p.split_len = sp.split_len;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.off_o);
+  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.off_ml);
+  p.status = status;
+  return cuda_fail(launch_paged_attn(p, cache->head_dim, cache->dtype, (cudaStream_t)stream), "paged attention launch");
+}
+
+hsa_status hsa_prompt_attn(const hsa_prompt_args* a, hsa_stream_t stream) {
+  NvtxRange range("hsa_prompt_attn");
+  if (!a) return HSA_ERR_INVALID_ARG;
+  if (a->dtype != HSA_BF16 && a->dtype != HSA_F16) return HSA_ERR_INVALID_ARG;
+  if (a->window < 0 || !(a->sm_scale > 0.f) || !isfinite(a->sm_scale)) return HSA_ERR_INVALID_ARG;
+  if (a->batch < 1 || a->heads_kv < 1 || a->heads_kv > 1024 || (a->head_dim != 64 && a->head_dim != 128)) return HSA_ERR_SHAPE;
+  if (a->heads_q < 1 || a->heads_q % a->heads_kv || a->heads_q / a->heads_kv > HSA_MAX_GROUP) return HSA_ERR_SHAPE;
+  if (a->n_q < 0 || a->n_k < 0 || a->n_q > (int64_t)INT32_MAX || a->n_k > (int64_t)INT32_MAX) return HSA_ERR_SHAPE;
+  if (a->n_q == 0) return HSA_OK;
+  if (!a->q || !a->out || !a->cu_q || (a->n_k > 0 && (!a->k || !a->v))) return HSA_ERR_INVALID_ARG;
+  const int64_t row_q = (int64_t)a->heads_q * a->head_dim, row_k = (int64_t)a->heads_kv * a->head_dim;
+  const int64_t strides[4] = {a->q_stride, a->out_stride, a->k_stride, a->v_stride};
+  for (int i = 0; i < 4; ++i)
+    if (strides[i] < (i < 2 ? row_q : row_k) || strides[i] % 8 || strides[i] > (int64_t)INT32_MAX) return HSA_ERR_SHAPE;
+  if (!aligned16(a->q) || !aligned16(a->out) || !aligned16(a->k) || !aligned16(a->v)) return HSA_ERR_ALIGN;
+  uint32_t* status;
+  int sms;
+  if (!device_info(&status, &sms)) return HSA_ERR_UNSUPPORTED;
+  return cuda_fail(launch_prompt_attn(*a, status, wait_limit_ns(), (cudaStream_t)stream), "prompt attention launch");
+}
+
 hsa_status hsa_set_wait_limit(uint64_t ns) {
   g_wait_ns.store(ns ? ns : kWaitLimitNs, std::memory_order_relaxed);
   return HSA_OK;

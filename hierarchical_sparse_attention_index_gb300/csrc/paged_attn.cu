@@ -1,0 +1,602 @@
+// Attention of a few new tokens per request over a paged key-value cache (hsa_paged_attn_decode):
+//   o = sum_j softmax_j(scale q.k_j) v_j over the positions j a query sees, split over the
+// cache's length and joined.
+//
+// Bound: every key and value is read once and used by nq x group query rows only, so the reads
+// from HBM decide (at 16 rows of 128 dims the products take a fifth of the time of the reads at
+// the warp MMA's rate). Hence
+//  - one CTA per (request, key-value head, 16 or 32 query rows, split of the length); the rows are
+//    the queries and the heads of the group together, so that grouped heads share every load;
+//  - inside a CTA each of 4 warps streams its own 16-key groups (a group never leaves a page)
+//    through a private ring of cp.async stages: 16 rows of one head lie in one contiguous piece, no
+//    block barrier is ever needed, and two CTAs per SM keep up to 192 KB in flight;
+//  - products by the warp MMA m16n8k16 (a tile of 16 rows would fill an eighth of a tcgen05
+//    instruction). The k index is permuted so that a thread's B fragments of K are the 16-byte
+//    pieces of its row: one shared load feeds two (16-bit) or four (E4M3) k-steps. V goes through
+//    transposed matrix loads, or, in E4M3, byte permutes and converts in registers;
+//  - softmax in one pass with the running maximum and sum in fp32. The maximum is only raised, and
+//    the outputs rescaled, when some logit passes it by 2^8: the weights then stay below 256, which
+//    16-bit weights and fp32 sums hold, and most groups need one vote instead of shuffles;
+//  - the weights P are rounded to the 16-bit operand type of the product with V (relative 2^-9 in
+//    bf16, 2^-12 in f16, independent from key to key); the sum l takes them unrounded.
+// The four warps' (m, l, O) are merged in shared memory; with one split the CTA writes the result,
+// else the partial goes to the workspace and paged_join_kernel joins the splits in their order.
+#include "hsa_common.cuh"
+#include "hsa_internal.h"
+
+namespace hsa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kGroup = 16;               // keys per stage of a warp
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRaise = 8.f;            // log2 of how far a logit may pass the running maximum
+
+enum KvType { kBf16 = HSA_BF16, kF16 = HSA_F16, kE4M3 = HSA_E4M3 };
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    mma_f16_16816(c, a[0], a[1], a[2], a[3], b0, b1);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The positions some query of request b sees, [lo, hi), and each split's share of them
+struct Span {
+  int lo, hi, base, len, used;           // split s: [base + s len, base + (s + 1) len) cut to hi; `used` of them hold any
+};
+__device__ __forceinline__ int clamp_vis(const PagedAttnParams& p, int v) {
+  return min(max(v, 0), (int)p.max_vis);
+}
+__device__ __forceinline__ Span request_span(const PagedAttnParams& p, int b) {
+  Span s;
+  s.lo = 0x7fffffff;
+  s.hi = 0;
+  for (int i = 0; i < p.nq; ++i) {
+    const int v = clamp_vis(p, p.vis[(int64_t)b * p.nq + i]);
+    s.hi = max(s.hi, v);
+    if (v > 0) s.lo = min(s.lo, p.window > 0 ? max(v - p.window, 0) : 0);
+  }
+  if (s.hi == 0) s.lo = 0;
+  s.base = s.lo & ~(kGroup - 1);
+  const int need = (s.hi - s.base + p.n_splits - 1) / p.n_splits;
+  s.len = max(p.split_len, (need + 63) & ~63);
+  s.used = max(1, (s.hi - s.base + s.len - 1) / s.len);
+  return s;
+}
+
+template <int D, int KV>
+struct Tile {
+  static constexpr int kElem = KV == kE4M3 ? 1 : 2;
+  static constexpr int kRow = D * kElem;                 // bytes of a key's row
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kHalf = kGroup * kRow;            // K, then V
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = kStage >= 8192 ? 3 : 6;
+  static constexpr int kRing = kStage * kStages;
+  // 16-byte piece c of row r. K: pieces 4i..4i+3 of two neighbouring rows are read together; V: one
+  // piece of 8 rows (matrix loads), or two pieces of rows 0, 2, 4, 6 (E4M3)
+  static __device__ __forceinline__ uint32_t k_at(int r, int c) {
+    return (uint32_t)(r * kRow + (kChunks >= 8 ? (c ^ ((r & 1) << 2)) : c) * 16);
+  }
+  static __device__ __forceinline__ uint32_t v_at(int r, int c) {
+    return (uint32_t)(r * kRow + (kChunks >= 8 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3))) * 16);
+  }
+};
+
+template <int D, int KV, int RT>
+__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+  using T = Tile<D, KV>;
+  constexpr bool kB = KV == kBf16;                       // products in bf16, else in f16
+  constexpr int kSteps = D / 16, kNt = D / 8;
+  constexpr int kOutRows = 16 * RT;
+  static_assert(kOutRows * D * 4 <= T::kRing, "a warp's outputs fit its ring");
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ float s_m[kWarps][kOutRows], s_l[kWarps][kOutRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+
+  griddep_wait();
+  griddep_launch_dependents();
+
+  int idx = blockIdx.x;
+  const int chunk = idx % p.chunks;
+  idx /= p.chunks;
+  const int h = idx % p.heads;
+  idx /= p.heads;
+  const int b = idx % p.batch, split = idx / p.batch;
+  const Span sp = request_span(p, b);
+  if (split >= sp.used) return;
+  const int begin = sp.base + split * sp.len, end = min(begin + sp.len, sp.hi);   // keys of this CTA
+  const int rows = p.nq * p.group, row0 = chunk * kOutRows;
+
+  // this lane's rows (C layout: g and g + 8 of each 16-row tile): query, limits
+  int lo[2 * RT], hi[2 * RT];
+  int all_lo = 0, all_hi = 0x7fffffff;                   // inside [all_lo, all_hi) no row masks anything
+#pragma unroll
+  for (int j = 0; j < 2 * RT; ++j) {
+    const int r = row0 + 8 * j + g;
+    lo[j] = hi[j] = 0;
+    if (r < rows) {
+      const int raw = p.vis[(int64_t)b * p.nq + r / p.group];
+      hi[j] = clamp_vis(p, raw);
+      if (raw != hi[j] && split == 0 && h == 0) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
+      lo[j] = p.window > 0 ? max(hi[j] - p.window, 0) : 0;
+      all_lo = max(all_lo, lo[j]);
+      all_hi = min(all_hi, hi[j]);
+    }
+  }
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
+    all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
+  }
+
+  // ---------------------------------------------------------------- the ring: 16-key groups of this warp
+  const uint32_t ring = smem_u32(sm) + (uint32_t)warp * T::kRing;
+  const int n_groups = max(0, (end - begin + kGroup * (kWarps - warp) - 1) / (kGroup * kWarps));
+  const int64_t head_bytes = (int64_t)p.page_size * T::kRow;
+  uint32_t bad = 0;                                      // bit s: the group in stage s lies on no page
+  // table entries of 32 groups at a time, one per lane, loaded a turn ahead of their use
+  auto load_pages = [&](int turn) {
+    const int i = 32 * turn + lane;
+    return i < n_groups ? p.table[(int64_t)b * p.max_pages + (begin + kGroup * (warp + kWarps * i)) / p.page_size] : -1;
+  };
+  int pages = load_pages(0), pages_next = load_pages(1);
+  auto issue = [&](int i, int stage) {                   // called with i = 0, 1, 2, ...
+    const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+    if ((i & 31) == 31) {
+      pages = pages_next;
+      pages_next = load_pages((i >> 5) + 2);
+    }
+    if (i < n_groups) {
+      const int pos = begin + kGroup * (warp + kWarps * i);
+      const bool ok = page >= 0 && page < p.n_pages;
+      if (!ok && lane == 0) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
+      bad = (bad & ~(1u << stage)) | ((ok ? 0u : 1u) << stage);
+      const int64_t at = ok ? ((int64_t)page * p.heads + h) * head_bytes + (int64_t)(pos % p.page_size) * T::kRow : 0;
+      const uint8_t* k = p.k_pool + at;
+      const uint8_t* v = p.v_pool + at;
+      const uint32_t dk = ring + (uint32_t)stage * T::kStage, dv = dk + T::kHalf;
+#pragma unroll
+      for (int u = 0; u < kGroup * T::kChunks / 32; ++u) {
+        const int e = u * 32 + lane, r = e / T::kChunks, c = e % T::kChunks;
+        // rows no query sees are not read: they become zeros, whatever the pool holds there
+        const uint32_t n = (ok && pos + r >= sp.lo && pos + r < sp.hi) ? 16u : 0u;
+        cp_async16(dk + T::k_at(r, c), k + (n ? e * 16 : 0), n);
+        cp_async16(dv + T::v_at(r, c), v + (n ? e * 16 : 0), n);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < T::kStages - 1; ++s) issue(s, s);
+
+  // ---------------------------------------------------------------- queries into A fragments
+  // k-step ks covers, of thread t, the 4 consecutive elements q_elem(ks): the same elements that
+  // its piece of a key's row brings to that step
+  uint32_t qa[RT][kSteps][4];
+  float scale[2 * RT];
+  {
+    constexpr int kPer = 16 / T::kElem;                  // elements of a 16-byte piece
+#pragma unroll
+    for (int j = 0; j < 2 * RT; ++j) {
+      const int r = row0 + 8 * j + g;
+      const bool real = r < rows;
+      const int qi = real ? r / p.group : 0, hq = h * p.group + (real ? r % p.group : 0);
+      const uint16_t* q = p.q + (((int64_t)b * p.nq + qi) * p.heads_q + hq) * D;
+      uint2 x[kSteps];
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) {
+        const int piece = 4 * (ks / (kPer / 4)) + t;
+        x[ks] = real ? *reinterpret_cast<const uint2*>(q + piece * kPer + 4 * (ks % (kPer / 4))) : make_uint2(0u, 0u);
+      }
+      scale[j] = p.scale_log2;
+      if (KV == kE4M3 && p.q_bf16) {
+        // bf16 queries against f16 keys: to f16 after a power-of-two shift of the row, taken back in its scale
+        float amax = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) {
+          const uint32_t w[2] = {x[ks].x, x[ks].y};
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[u] << 16)), fabsf(__uint_as_float(w[u] & 0xFFFF0000u))));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        int sh = 0;
+        if (amax > 0.f && amax < INFINITY) {
+          int e;
+          frexpf(amax, &e);
+          sh = max(-120, min(120, 12 - e));              // amax 2^sh in [2^11, 2^12): products and their sums stay in fp32
+        }
+        const float mul = __uint_as_float((uint32_t)(127 + sh) << 23);
+        scale[j] *= __uint_as_float((uint32_t)(127 - sh) << 23);
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) {
+          x[ks].x = pack2<false>(__uint_as_float(x[ks].x << 16) * mul, __uint_as_float(x[ks].x & 0xFFFF0000u) * mul);
+          x[ks].y = pack2<false>(__uint_as_float(x[ks].y << 16) * mul, __uint_as_float(x[ks].y & 0xFFFF0000u) * mul);
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) {              // a0, a2: row g; a1, a3: row g + 8
+        qa[j >> 1][ks][j & 1] = x[ks].x;
+        qa[j >> 1][ks][2 + (j & 1)] = x[ks].y;
+      }
+    }
+  }
+
+  float o[RT][kNt][4];
+  float m[2 * RT], l[2 * RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int n = 0; n < kNt; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[rt][n][e] = 0.f;
+#pragma unroll
+  for (int j = 0; j < 2 * RT; ++j) {
+    m[j] = -INFINITY;
+    l[j] = 0.f;
+  }
+
+  int stage = 0;
+  for (int i = 0; i < n_groups; ++i) {
+    cp_async_wait<T::kStages - 2>();
+    __syncwarp();
+    const bool skip = (bad >> stage) & 1u;
+    const uint32_t sk = ring + (uint32_t)stage * T::kStage, sv = sk + T::kHalf;
+    const int pos = begin + kGroup * (warp + kWarps * i);
+    // the stage freed by the last iteration takes the group kStages - 1 ahead
+    issue(i + T::kStages - 1, stage == 0 ? T::kStages - 1 : stage - 1);
+    if (!skip) {
+      // ------------------------------------------------------------ S = Q K^T
+      float s[RT][2][4];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[rt][n][e] = 0.f;
+#pragma unroll
+      for (int c4 = 0; c4 < T::kChunks / 4; ++c4) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint4 kw = lds128(sk + T::k_at(8 * n + g, 4 * c4 + t));
+          const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+          if constexpr (KV == kE4M3) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint32_t b0 = e4m3x2_to_f16x2((uint16_t)(w[u] & 0xFFFFu)), b1 = e4m3x2_to_f16x2((uint16_t)(w[u] >> 16));
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) mma16816<kB>(s[rt][n], qa[rt][4 * c4 + u], b0, b1);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) mma16816<kB>(s[rt][n], qa[rt][2 * c4 + u], w[2 * u], w[2 * u + 1]);
+          }
+        }
+      }
+      // ------------------------------------------------------------ softmax, one pass
+      const bool whole = pos >= all_lo && pos + kGroup <= all_hi;
+      bool raise = false;
+#pragma unroll
+      for (int j = 0; j < 2 * RT; ++j) {
+        float* x0 = &s[j >> 1][0][2 * (j & 1)];
+        float* x1 = &s[j >> 1][1][2 * (j & 1)];
+        x0[0] *= scale[j];
+        x0[1] *= scale[j];
+        x1[0] *= scale[j];
+        x1[1] *= scale[j];
+        if (!whole) {
+          const int k0 = pos + 2 * t;
+          if (k0 < lo[j] || k0 >= hi[j]) x0[0] = -INFINITY;
+          if (k0 + 1 < lo[j] || k0 + 1 >= hi[j]) x0[1] = -INFINITY;
+          if (k0 + 8 < lo[j] || k0 + 8 >= hi[j]) x1[0] = -INFINITY;
+          if (k0 + 9 < lo[j] || k0 + 9 >= hi[j]) x1[1] = -INFINITY;
+        }
+        raise |= fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x1[0], x1[1])) > m[j] + kRaise;
+      }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int j = 0; j < 2 * RT; ++j) {
+          const float* x0 = &s[j >> 1][0][2 * (j & 1)];
+          const float* x1 = &s[j >> 1][1][2 * (j & 1)];
+          float mx = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x1[0], x1[1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          mx = fmaxf(mx, m[j]);
+          const float f = (mx == -INFINITY) ? 1.f : ex2_ftz(m[j] - mx);   // m = -inf before: 0, on sums that are 0
+          m[j] = mx;
+          l[j] *= f;
+#pragma unroll
+          for (int n = 0; n < kNt; ++n) {
+            o[j >> 1][n][2 * (j & 1)] *= f;
+            o[j >> 1][n][2 * (j & 1) + 1] *= f;
+          }
+        }
+      }
+      uint32_t pa[RT][4];
+#pragma unroll
+      for (int j = 0; j < 2 * RT; ++j) {
+        const float mu = m[j] == -INFINITY ? 0.f : m[j];
+        const float* x0 = &s[j >> 1][0][2 * (j & 1)];
+        const float* x1 = &s[j >> 1][1][2 * (j & 1)];
+        const float p0 = ex2_ftz(x0[0] - mu), p1 = ex2_ftz(x0[1] - mu), p2 = ex2_ftz(x1[0] - mu), p3 = ex2_ftz(x1[1] - mu);
+        l[j] += (p0 + p1) + (p2 + p3);
+        pa[j >> 1][j & 1] = pack2<kB>(p0, p1);
+        pa[j >> 1][2 + (j & 1)] = pack2<kB>(p2, p3);
+      }
+      // ------------------------------------------------------------ O += P V
+      if constexpr (KV == kE4M3) {
+        // thread column g is dims kNt g .. kNt g + kNt - 1, one per n-tile: rows 2t, 2t+1, 2t+8, 2t+9
+        uint32_t w[4][kNt / 4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = 2 * t + (u & 1) + 8 * (u >> 1);
+          if constexpr (D == 128) {
+            const uint4 x = lds128(sv + T::v_at(r, g));
+            w[u][0] = x.x;
+            w[u][1] = x.y;
+            w[u][2] = x.z;
+            w[u][3] = x.w;
+          } else {
+            const uint2 x = lds64(sv + T::v_at(r, g >> 1) + 8 * (g & 1));
+            w[u][0] = x.x;
+            w[u][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int n4 = 0; n4 < kNt / 4; ++n4) {
+          const uint32_t a01 = __byte_perm(w[0][n4], w[1][n4], 0x5140), a23 = __byte_perm(w[0][n4], w[1][n4], 0x7362);
+          const uint32_t c01 = __byte_perm(w[2][n4], w[3][n4], 0x5140), c23 = __byte_perm(w[2][n4], w[3][n4], 0x7362);
+          const uint32_t b0[4] = {e4m3x2_to_f16x2((uint16_t)(a01 & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(a01 >> 16)),
+                                  e4m3x2_to_f16x2((uint16_t)(a23 & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(a23 >> 16))};
+          const uint32_t b1[4] = {e4m3x2_to_f16x2((uint16_t)(c01 & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(c01 >> 16)),
+                                  e4m3x2_to_f16x2((uint16_t)(c23 & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(c23 >> 16))};
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) mma16816<kB>(o[rt][4 * n4 + u], pa[rt], b0[u], b1[u]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < T::kChunks; c += 2) {
+          uint32_t r4[4];
+          ldmatrix_x4_trans(sv + T::v_at(lane & 15, c + (lane >> 4)), r4);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            mma16816<kB>(o[rt][c], pa[rt], r4[0], r4[1]);
+            mma16816<kB>(o[rt][c + 1], pa[rt], r4[2], r4[3]);
+          }
+        }
+      }
+    }
+    __syncwarp();                        // every lane has read the stage before it is filled again
+    stage = stage + 1 == T::kStages ? 0 : stage + 1;
+  }
+
+  // ---------------------------------------------------------------- merge the warps
+  cp_async_wait<0>();
+  __syncwarp();
+  float* so = reinterpret_cast<float*>(sm + (size_t)warp * T::kRing);   // [row][D]
+#pragma unroll
+  for (int j = 0; j < 2 * RT; ++j) {
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
+    const int r = 8 * j + g;
+    if (t == 0) {
+      s_m[warp][r] = m[j];
+      s_l[warp][r] = l[j];
+    }
+    // columns 2t, 2t + 1 of n-tile n: dims 8n + 2t, + 1, or with E4M3's split columns kNt (2t) + n and kNt (2t + 1) + n
+    if constexpr (KV == kE4M3) {
+#pragma unroll
+      for (int n = 0; n < kNt; n += 4) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int q2 = 2 * (j & 1) + e;
+          *reinterpret_cast<float4*>(so + r * D + kNt * (2 * t + e) + n) =
+              make_float4(o[j >> 1][n][q2], o[j >> 1][n + 1][q2], o[j >> 1][n + 2][q2], o[j >> 1][n + 3][q2]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+        *reinterpret_cast<float2*>(so + r * D + 8 * n + 2 * t) =
+            make_float2(o[j >> 1][n][2 * (j & 1)], o[j >> 1][n][2 * (j & 1) + 1]);
+    }
+  }
+  __syncthreads();
+  constexpr int kQuads = D / 4;
+  const bool last = sp.used == 1;
+  for (int e = tid; e < kOutRows * kQuads; e += kThreads) {
+    const int r = e / kQuads, d4 = e % kQuads, row = row0 + r;
+    if (row >= rows) break;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = s_m[w][r] == -INFINITY ? 0.f : ex2_ftz(s_m[w][r] - M);
+      const float4 x = *reinterpret_cast<const float4*>(sm + (size_t)w * T::kRing + ((size_t)r * D + 4 * d4) * 4);
+      if (s_m[w][r] != -INFINITY || s_l[w][r] != 0.f) {  // a warp that saw no key adds nothing
+        a.x += f * x.x;
+        a.y += f * x.y;
+        a.z += f * x.z;
+        a.w += f * x.w;
+        L += f * s_l[w][r];
+      }
+    }
+    if (last) {
+      const int64_t at = ((int64_t)b * p.nq + row / p.group) * p.heads_q + h * p.group + row % p.group;
+      const float inv = L != 0.f ? p.v_scale / L : 0.f;
+      uint2 y;
+      if (p.q_bf16)
+        y = make_uint2(pack2<true>(a.x * inv, a.y * inv), pack2<true>(a.z * inv, a.w * inv));
+      else
+        y = make_uint2(pack2<false>(a.x * inv, a.y * inv), pack2<false>(a.z * inv, a.w * inv));
+      *reinterpret_cast<uint2*>(p.out + at * D + 4 * d4) = y;
+      if (p.lse && d4 == 0) p.lse[at] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    } else {
+      const int64_t at = (((int64_t)b * p.heads + h) * p.n_splits + split) * rows + row;
+      *reinterpret_cast<float4*>(p.part_o + at * D + 4 * d4) = a;
+      if (d4 == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(M, L);
+    }
+  }
+}
+
+// The splits of one row, joined in their order: o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
+// A warp per row, a lane per D / 32 dims; a few KB per row, so what counts is that the loads of
+// several splits are in flight at once (unrolled by 4).
+template <int D>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, rows = p.nq * p.group;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);       // (b, h, row)
+  if (id >= (int64_t)p.batch * p.heads * rows) return;
+  const int row = (int)(id % rows);
+  const int64_t bh = id / rows;
+  const int b = (int)(bh / p.heads), h = (int)(bh % p.heads);
+  const Span sp = request_span(p, b);
+  if (sp.used == 1) return;              // written by its only split
+  constexpr int V = D / 32;
+  const int64_t first = bh * p.n_splits * rows + row;
+  float M = -INFINITY;
+  for (int c = lane; c < sp.used; c += 32) M = fmaxf(M, __ldcg(p.part_ml + 2 * (first + (int64_t)c * rows)));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float a[V], L = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) a[e] = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < sp.used; ++c) {
+    const int64_t at = first + (int64_t)c * rows;
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at));
+    float x[V];
+    if constexpr (V == 4) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + lane);
+      x[0] = y.x;
+      x[1] = y.y;
+      x[V - 2] = y.z;
+      x[V - 1] = y.w;
+    } else {
+      const float2 y = __ldcg(reinterpret_cast<const float2*>(p.part_o + at * D) + lane);
+      x[0] = y.x;
+      x[1] = y.y;
+    }
+    if (ml.x != -INFINITY || ml.y != 0.f) {
+      const float f = ml.x == -INFINITY ? 0.f : ex2_ftz(ml.x - M);
+      L += f * ml.y;
+#pragma unroll
+      for (int e = 0; e < V; ++e) a[e] += f * x[e];
+    }
+  }
+  const int64_t at = ((int64_t)b * p.nq + row / p.group) * p.heads_q + h * p.group + row % p.group;
+  const float inv = L != 0.f ? p.v_scale / L : 0.f;
+  uint32_t y[V / 2];
+#pragma unroll
+  for (int e = 0; e < V; e += 2)
+    y[e / 2] = p.q_bf16 ? pack2<true>(a[e] * inv, a[e + 1] * inv) : pack2<false>(a[e] * inv, a[e + 1] * inv);
+  uint16_t* out = p.out + at * D + V * lane;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[V / 2 - 1]);
+  else
+    *reinterpret_cast<uint32_t*>(out) = y[0];
+  if (p.lse && lane == 0) p.lse[at] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+}
+
+template <int D, int KV, int RT>
+cudaError_t launch(const PagedAttnParams& p, cudaStream_t s) {
+  auto kernel = paged_attn_kernel<D, KV, RT>;
+  constexpr size_t smem = (size_t)kWarps * Tile<D, KV>::kRing;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
+  const unsigned blocks = (unsigned)p.n_splits * p.batch * p.heads * p.chunks;
+  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, s, p);
+}
+template <int D, int KV>
+cudaError_t launch_rt(const PagedAttnParams& p, cudaStream_t s) {
+  return p.chunk_rows == 16 ? launch<D, KV, 1>(p, s) : launch<D, KV, 2>(p, s);
+}
+template <int D>
+cudaError_t launch_kv(const PagedAttnParams& p, int kv, cudaStream_t s) {
+  switch (kv) {
+    case kBf16: return launch_rt<D, kBf16>(p, s);
+    case kF16: return launch_rt<D, kF16>(p, s);
+    default: return launch_rt<D, kE4M3>(p, s);
+  }
+}
+
+}  // namespace
+
+// Query rows per CTA and splits of the length. Up to 16 rows one MMA tile, above that two (a CTA of
+// 32 rows reads its keys once for both); more rows take more CTAs, whose keys then come from L2.
+// The splits fill the GPU about four times over (2 CTAs per SM on 152 SMs), so that ragged lengths
+// even out, but no split is shorter than 256 keys: 4 groups for each warp, about what the ring holds.
+PagedSplit paged_split(int32_t batch, int32_t heads, int32_t rows, int64_t max_vis, int32_t window, int32_t nq) {
+  PagedSplit s;
+  s.chunk_rows = rows <= 16 ? 16 : 32;
+  s.chunks = (rows + s.chunk_rows - 1) / s.chunk_rows;
+  int64_t span = max_vis;
+  if (window > 0 && (int64_t)window + nq + 15 < span) span = (int64_t)window + nq + 15;   // vis one apart, as in a draft
+  const int64_t ctas = (int64_t)batch * heads * s.chunks;
+  int64_t n = (4 * 304 + ctas - 1) / ctas;
+  n = imax64(1, imin64(n, (span + 255) / 256));
+  s.n_splits = (int32_t)n;
+  s.split_len = (int32_t)imax64(64, ((span + n - 1) / n + 63) / 64 * 64);
+  return s;
+}
+
+cudaError_t launch_paged_attn(const PagedAttnParams& p, int32_t head_dim, int32_t kv_dtype, cudaStream_t s) {
+  cudaError_t e = head_dim == 128 ? launch_kv<128>(p, kv_dtype, s) : launch_kv<64>(p, kv_dtype, s);
+  if (e != cudaSuccess || p.n_splits == 1) return e;
+  const int64_t ids = (int64_t)p.batch * p.heads * p.nq * p.group;
+  const dim3 grid((unsigned)((ids + 3) / 4));
+  return head_dim == 128 ? launch_pdl(paged_join_kernel<128>, grid, dim3(128), 0, s, p)
+                         : launch_pdl(paged_join_kernel<64>, grid, dim3(128), 0, s, p);
+}
+
+}  // namespace hsa

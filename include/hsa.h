@@ -114,6 +114,50 @@ typedef struct {
   uint8_t* ik_s;
 } hsa_cache;
 
+/* Value types of the dense attention calls and of their paged caches */
+typedef enum { HSA_BF16 = 0, HSA_F16 = 1, HSA_E4M3 = 2 } hsa_dtype;
+
+#define HSA_MAX_GROUP 128     /* dense attention: query heads per key-value head at most      */
+
+/* Caller-owned paged key-value cache of one dense (uncompressed, grouped-head) attention layer.
+ * Position t of request b lies in row t % page_size of page table[b][t / page_size]; requests
+ * may share pages they only read. The pools and the table are device memory; pools 16-byte
+ * aligned. A value is its stored number times k_scale or v_scale. */
+typedef struct {
+  int32_t batch;          /* requests                                               */
+  int32_t heads;          /* key-value heads, 1..1024                               */
+  int32_t head_dim;       /* 64 or 128                                              */
+  int32_t page_size;      /* positions per page: a multiple of 16, at most 4096     */
+  int32_t dtype;          /* hsa_dtype of k and v                                   */
+  int32_t flags;          /* 0                                                      */
+  int64_t n_pages;        /* pages in each pool                                     */
+  int64_t max_pages;      /* table row length; max_pages * page_size <= 2^31 - 1    */
+  void* k;                /* [n_pages][heads][page_size][head_dim]                  */
+  void* v;                /* [n_pages][heads][page_size][head_dim]                  */
+  const int32_t* table;   /* i32 [batch][max_pages]; entries no position needs are not read */
+  float k_scale, v_scale; /* finite and > 0; 1 unless dtype is HSA_E4M3             */
+} hsa_paged_cache;
+
+/* Arguments of hsa_prompt_attn. All pointers are device memory; q, k, v and out 16-byte aligned. */
+typedef struct {
+  int32_t batch;       /* sequences, >= 1                                                   */
+  int32_t heads_q;     /* a multiple of heads_kv, at most HSA_MAX_GROUP of it               */
+  int32_t heads_kv;    /* 1..1024                                                           */
+  int32_t head_dim;    /* 64 or 128                                                         */
+  int32_t dtype;       /* HSA_BF16 or HSA_F16, of q, k, v and out                           */
+  int32_t window;      /* keys a query sees, itself among them; 0: everything before it     */
+  int64_t n_q, n_k;    /* rows of q (and out) and of k and v                                */
+  const void* q;       /* [n_q][heads_q][head_dim], q_stride elements from row to row       */
+  const void* k;       /* [n_k][heads_kv][head_dim], k_stride elements from row to row      */
+  const void* v;       /* [n_k][heads_kv][head_dim], v_stride elements from row to row      */
+  int64_t q_stride, k_stride, v_stride, out_stride; /* multiples of 8, at least a row; < 2^31 */
+  const int32_t* cu_q; /* i32 [batch + 1]: rows [cu_q[b], cu_q[b+1]) of q are sequence b    */
+  const int32_t* cu_k; /* i32 [batch + 1], the same for k and v; NULL: cu_q                 */
+  float sm_scale;      /* softmax scale applied to q.k; finite and > 0                      */
+  void* out;           /* [n_q][heads_q][head_dim], out_stride elements from row to row     */
+  float* lse;          /* f32 [n_q][heads_q] or NULL                                        */
+} hsa_prompt_args;
+
 /* Per-step arguments of hsa_schedule_step. Arrays indexed by layer slot l in [0, n_layers)
  * are HOST arrays of DEVICE pointers. */
 typedef struct {
@@ -259,6 +303,64 @@ HSA_API hsa_status hsa_sparse_attn_decode(const hsa_cache* cache, const void* q,
  * pool rows, while the previous kernel of the step drains. */
 HSA_API hsa_status hsa_schedule_step(const hsa_cache* caches, const hsa_step_args* args, void* ws,
                              size_t ws_bytes, hsa_stream_t stream);
+
+/* ---------------------------------------------------------------- dense attention
+ * Layers without a compressed cache (dense layers, and layers with a sliding window only) keep
+ * keys and values per position and key-value head. Three calls serve them: the prompt's
+ * attention, the write of its keys and values into pages, and the attention of each new token
+ * over the pages. Query head h belongs to key-value head h / (heads_q / heads_kv). */
+
+/* Write keys and values into a paged cache. Row t of k and v belongs to the request b with
+ * cu[b] <= t < cu[b+1] and becomes position start[b] + t - cu[b] of it:
+ *   page value = round(x / scale): the fp32 quotient to nearest even, to HSA_E4M3 saturating at
+ *   +-448 (NaN stays NaN); a 16-bit cache takes the values as they are.
+ *   k, v      bf16 or f16 (`dtype`) [n_tokens][heads][head_dim], k_stride / v_stride elements from
+ *             row to row (a multiple of 8, at least a row); 16-byte aligned. dtype must be the
+ *             cache's unless the cache is HSA_E4M3
+ *   n_tokens  rows of k and v, >= 0 (0: nothing is launched) and < 2^31
+ *   cu        i32 [batch + 1] ascending; rows outside [cu[0], cu[batch]) are padding and not written.
+ *             NULL: every request brings n_tokens / batch rows (which must divide)
+ *   start     i64 [batch]; NULL means 0 for every request
+ * Positions outside the table or on a page id outside [0, n_pages) are skipped and flagged
+ * HSA_FLAG_WRITE_RANGE. Two rows that land on one slot (requests sharing a page they both
+ * write) leave one of them there, whole 16-byte pieces of either. Everything else in the pools stays. */
+HSA_API hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const void* k, const void* v, int32_t dtype,
+                                 int64_t k_stride, int64_t v_stride, int64_t n_tokens, const int32_t* cu,
+                                 const int64_t* start, hsa_stream_t stream);
+
+/* Workspace bytes of hsa_paged_attn_decode for this cache's batch, heads and head_dim (its
+ * pointers are not looked at). Host only; returns 0 for invalid sizes. */
+HSA_API size_t hsa_paged_attn_workspace_bytes(const hsa_paged_cache* cache, int32_t heads_q, int32_t nq, int64_t max_vis);
+
+/* Attention of nq new tokens per request over its pages, split over the cache's length and
+ * joined. For request b, query i and head h, with j over [max(0, vis[b][i] - window), vis[b][i])
+ * (window 0: from position 0):
+ *   o = sum_j softmax_j(sm_scale * q_h . k_j) v_j,   lse = log sum_j exp(sm_scale * q_h . k_j).
+ * With no positions o is 0 and lse is -inf. Sums are fp32; the weights are rounded to the
+ * 16-bit type that the products use (bf16 for a bf16 cache, else f16).
+ *   q, out    bf16 or f16 (`q_dtype`) [B][nq][heads_q][head_dim], 16-byte aligned. q_dtype must
+ *             be the cache's unless the cache is HSA_E4M3
+ *   vis       i32 [B][nq], 0 <= vis <= max_vis; another value counts as the nearer border and is
+ *             flagged HSA_FLAG_INDEX_RANGE. max_vis <= max_pages * page_size and <= HSA_MAX_VIS
+ *   lse       f32 [B][nq][heads_q] or NULL
+ *   ws        hsa_paged_attn_workspace_bytes bytes, 16-byte aligned; needs no initialisation
+ * Positions on a page id outside [0, n_pages) are skipped and flagged HSA_FLAG_INDEX_RANGE. What
+ * the pools hold at positions that no query of the request sees is never used, whatever it is. */
+HSA_API hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, int32_t q_dtype, int32_t heads_q,
+                                 const int32_t* vis, int32_t nq, int64_t max_vis, int32_t window,
+                                 float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                                 hsa_stream_t stream);
+
+/* Causal attention over packed prompts. Query i of a sequence with lq queries and lk keys stands
+ * at position p = i + lk - lq (its keys end where its queries end: a chunk behind lk - lq
+ * earlier keys) and sees the keys j of [max(0, p - window + 1), p] (window 0: from 0):
+ *   o = sum_j softmax_j(sm_scale * q_h . k_j) v_j,   lse = log sum_j exp(sm_scale * q_h . k_j).
+ * With no keys (p < 0) o is 0 and lse is -inf. Sums are fp32; the weights are rounded to dtype.
+ * Rows of q, out and lse outside [cu_q[0], cu_q[batch]) are neither read for a result nor written.
+ * A sequence never uses another's rows, nor rows outside [cu_k[0], cu_k[batch]), whatever they
+ * hold. A sequence whose bounds are not ascending inside [0, n_q] and [0, n_k] is skipped and
+ * flagged HSA_FLAG_INDEX_RANGE. n_q and n_k < 2^31; n_q = 0 launches nothing. */
+HSA_API hsa_status hsa_prompt_attn(const hsa_prompt_args* args, hsa_stream_t stream);
 
 /* Limit of the kernels' bounded waits (for a copy or a tensor-core result that does not arrive),
  * in nanoseconds, for launches made after the call from any thread, on every device. A wait that
