@@ -2,25 +2,32 @@
 //   o_i = sum_j softmax_j(scale q_i.k_j) v_j over the keys j a query sees.
 //
 // Bound: the two products, 4 d flops per visible (query, key) pair and head, on the tensor cores;
-// the exponentials and the rest of the softmax run beside them. One CTA takes two tiles of 128
-// rows. A row is one query head of one token: the `group` heads that share a key-value head stand
-// together (tt = 128 / group tokens per tile), so that grouped heads share every key tile and a
-// tile spans few tokens, which keeps the masked part at the diagonal small.
-//  - one warp loads Q once and 128-key tiles of K and V into a ring by TMA (128-byte swizzle);
-//  - one thread issues the tcgen05 products: S_t = Q_t K^T (128 x 128, fp32 in tensor memory), then
-//    O_t += P_t V with P_t read from tensor memory and V as an MN-major operand. In order:
-//    PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1), so each tile's softmax runs while the tensor core works
-//    on the other tile;
-//  - two warp groups do the softmax of one tile each, one row per thread (no shuffles): the
-//    running maximum and sum in fp32, P rounded to the operand type over S's columns. The maximum
-//    is only raised, and O rescaled in tensor memory, when a logit passes it by 2^8; after the
-//    first tiles that hardly happens, so the rescaling needs no warps of its own;
+// the exponentials and the rest of the softmax run beside them. One CTA per SM takes two tiles of
+// 128 rows at a time. A row is one query head of one token: the `group` heads that share a key-value
+// head stand together (tt = 128 / group tokens per tile), so that grouped heads share every key tile
+// and a tile spans few tokens, which keeps the masked part at the diagonal small.
+//  - CTAs stay and take the next block's work themselves (cluster launch control), while the loads
+//    of the next work already run; the first work has the most keys;
+//  - one warp loads Q, and 64-key tiles of K and V into a ring, by TMA (128-byte swizzle);
+//  - a warp per query tile issues its tcgen05 products: S = Q K^T (128 x 64, fp32 in tensor memory,
+//    two buffers, one key tile ahead), then O += P V with P read from tensor memory and V as an
+//    MN-major operand. So S of the next key tile is there when the softmax comes to it. (A product
+//    for 64 keys reads 6 KB of shared memory in the 32 clocks that it computes, 128 bytes a clock
+//    can be read; one for 128 keys reads 8 KB in 64, but leaves room for one buffer only: 16,384
+//    tokens took the same time, packed prompts 15 % more);
+//  - a warp group does the softmax of each tile, one row per thread (no shuffles): the running
+//    maximum and sum in fp32, P rounded to the operand type (a relative 2^-9 in bf16, 2^-12 in f16,
+//    independent from key to key) over S's columns. The maximum is only raised, and O rescaled in
+//    tensor memory, when a logit passes it by 2^8: weights stay below 256, and after the first
+//    tiles that hardly happens, so the rescaling needs no warps of its own;
 //  - keys come from the diagonal downwards, so the first tile already holds each row's own key;
-//  - one warp clears the rows of V past the end of the sequence in its last tile: their weights
+//  - the rows of V's tiles that are no keys of the sequence are cleared before use: their weights
 //    are zero, but zero times another sequence's infinity would not be.
-// TMEM: S_0, S_1 (128 columns each, P over the first 64), O_0, O_1 (head_dim columns each).
-// Every wait is bounded; a role that gives up leaves its loop, and the others follow at their
-// next wait.
+// TMEM: S 2 x 64 columns per query tile (P over the first half of its buffer), O head_dim columns each.
+// Every wait is bounded; a role that gives up leaves its loop, and the others follow at their next
+// wait.
+// Measured (16,384 tokens, 32 heads over 4, 128 dims): 1,444 us, 1,523 TFLOP/s, 0.79 of the measured
+// bf16 peak; without the softmax's part 1,340 us, where shared memory bounds the products.
 #include "hsa_common.cuh"
 #include "hsa_internal.h"
 #include "hsa_tc.cuh"
@@ -28,15 +35,35 @@
 namespace hsa {
 namespace {
 
-constexpr int kTile = 128;               // rows of a query tile, keys of a key tile
+// mbar_wait with a suspend hint: a waiting warp sleeps in the barrier unit instead of coming back to
+// ask, which would take shared-memory cycles from the products (4 % of a long prompt's time)
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_sleep(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_sleep(bar, parity))
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  return true;
+}
+
+constexpr int kTile = 128;               // rows of a query tile
+constexpr int kKeys = 64;                // keys of a key tile
 constexpr int kSoftWarps = 8;            // 4 per query tile: two warp groups; the third holds the other roles
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kClearWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;              // a warp per query tile's products; warp 11 finds the work
 constexpr int kThreads = 12 * 32;
 // registers per thread: 168 at launch (65,536 over 384 threads, in steps of 8), then 208 for the
 // softmax groups, whose threads hold a row of 128 logits, and 88 for the third: 2 x 208 + 88 = 3 x 168
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168, "setmaxnreg draws on the launch's registers");
-constexpr uint32_t kBlock = kTile * 128; // 64 dims of 128 rows, 128 bytes a row
+constexpr uint32_t kBlockQ = kTile * 128, kBlockK = kKeys * 128;   // 64 dims of a tile, 128 bytes a row
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;            // log2 of how far a logit may pass the running maximum
 
@@ -55,27 +82,55 @@ struct PromptParams {
 
 template <int D>
 struct Shape {
-  static constexpr uint32_t kTileBytes = (D / 64) * kBlock;      // of Q, K or V
-  static constexpr int kStages = D == 128 ? 4 : 6;               // K and V tiles in turn
-  static constexpr uint32_t kOffQ = 0, kOffKv = 2 * kTileBytes, kOffMisc = kOffKv + kStages * kTileBytes;
-  static constexpr uint32_t kSmem = kOffMisc + 256 + 1024;       // + alignment slack
+  static constexpr uint32_t kQBytes = (D / 64) * kBlockQ, kKvBytes = (D / 64) * kBlockK;
+  static constexpr int kStages = 8;                              // tiles of K and V in the ring
+  static constexpr uint32_t kOffQ = 0, kOffKv = 2 * kQBytes, kOffStage = kOffKv + kStages * kKvBytes;
+  static constexpr uint32_t kSmem = kOffStage + kSoftWarps * 2048 + 1024;   // + alignment slack
 };
 
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-      "  tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u));
+// Products and commits issued by one lane (`one` is nonzero in it) of a warp that stays together: in
+// code that the whole warp runs, descriptors live in uniform registers, where these instructions
+// take them from; under a branch of the one lane every product would first have to move its four
+// there (88 clocks a product instead of 64 and less)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t one;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.b32 %0, 1, 0, p; }" : "=r"(one));
+  return one;
 }
-#define TMEM_ST32(taddr, r)                                                                                     \
-  asm volatile(                                                                                                 \
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"  \
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),                          \
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),        \
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),           \
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),           \
-      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)                        \
-      : "memory")
+__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.ne.b32 e, %5, 0;\n"
+      "  @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one));
+}
+__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.ne.b32 e, %5, 0;\n"
+      "  @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(one));
+}
+__device__ __forceinline__ void umma_commit_one(uint32_t one, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred e; setp.ne.b32 e, %1, 0;\n"
+      "  @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+      "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+#define TMEM_ST8(taddr, r)                                                                                      \
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),  \
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)                     \
+               : "memory")
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -102,19 +157,29 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// What a CTA works on: sequence b, tokens [i0, i0 + n) of its lq, and the key tiles of each query tile
+// One piece of work: tokens [i0, i0 + n) of a sequence for key-value head h, as two query tiles, and
+// the key tiles of each. Key tile j holds the keys kbase + 64 j ..; kbase is 0, or, with a window,
+// such that the top tile ends at the last key (so that a window of w meets as few tiles as it can).
 struct Job {
-  int b, i0, n, off;                     // off = lk - lq: token i stands at position i + off
-  int q0, k0, lk;
+  int h, i0, n, off;                     // off = lk - lq: token i stands at position i + off
+  int q0, k0, lk, kbase;
   int jlo[2], jhi[2];                    // key tiles [jlo, jhi) of query tile t; empty: jlo = jhi = 0
+  int clear_j, clear_lo, clear_hi;       // rows [clear_lo, clear_hi) of V's tile clear_j are no keys of the sequence
+  int more;                              // 0: no work is left, the other fields are not set
+  __device__ bool has(int t) const { return jhi[t] > jlo[t]; }
+  __device__ bool active(int t, int j) const { return j >= jlo[t] && j < jhi[t]; }
+  __device__ int top() const { return max(jhi[0], jhi[1]); }
+  __device__ int bottom() const { return min(has(0) ? jlo[0] : 0x7fffffff, has(1) ? jlo[1] : 0x7fffffff); }
 };
 
-// Tiles of the sequences in order, the last tiles (the most keys) of each first. One warp; `found`
-// false: no such tile. With `check_all`, sequences past the tile are looked at too, for their bounds.
-__device__ __forceinline__ bool find_job(const PromptParams& p, int64_t tile, bool check_all, Job& job) {
+// Tiles of the sequences in order, the last tiles (the most keys) of each first. One warp; false:
+// no such tile. With `check_all`, sequences past the tile are looked at too, for their bounds.
+__device__ __forceinline__ bool find_job(const PromptParams& p, int64_t id, bool check_all, Job& job) {
   const int lane = threadIdx.x & 31, tpc = 2 * p.tt;
+  const int64_t tile = id / p.heads_kv;
   int64_t before = 0;
   bool found = false;
+  job.h = (int)(id % p.heads_kv);
   for (int base = 0; base < p.batch && (!found || check_all); base += 32) {
     const int b = base + lane;
     int q0 = 0, lq = 0, k0 = 0, lk = 0;
@@ -141,7 +206,6 @@ __device__ __forceinline__ bool find_job(const PromptParams& p, int64_t tile, bo
     if (past && !found) {
       const int src = __ffs(past) - 1;
       const int64_t end = __shfl_sync(0xffffffffu, upto, src);
-      job.b = base + src;
       job.q0 = __shfl_sync(0xffffffffu, q0, src);
       job.k0 = __shfl_sync(0xffffffffu, k0, src);
       job.lk = __shfl_sync(0xffffffffu, lk, src);
@@ -154,283 +218,433 @@ __device__ __forceinline__ bool find_job(const PromptParams& p, int64_t tile, bo
     before = __shfl_sync(0xffffffffu, upto, 31);
   }
   if (!found) return false;
+  const int top = job.i0 + job.n + job.off;              // past the last position, at most lk
+  const int bottom = p.window > 0 ? max(job.i0 + job.off - p.window + 1, 0) : 0;
+  job.kbase = 0;
+  if (p.window > 0 && top > 0) job.kbase = top - ((top - bottom + kKeys - 1) / kKeys) * kKeys;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int n = min(p.tt, job.n - t * p.tt), first = job.i0 + t * p.tt + job.off;   // first position
     const int hi = first + n;                                                         // past the last position
     job.jlo[t] = job.jhi[t] = 0;
     if (n > 0 && hi > 0) {
-      job.jhi[t] = (hi + kTile - 1) / kTile;
-      job.jlo[t] = p.window > 0 ? max(first - p.window + 1, 0) / kTile : 0;
+      job.jhi[t] = (hi - job.kbase + kKeys - 1) / kKeys;
+      job.jlo[t] = p.window > 0 ? (max(first - p.window + 1, 0) - job.kbase) / kKeys : 0;
     }
   }
+  // the one tile that reaches past the sequence: the lowest with a negative kbase, else the top one
+  job.clear_j = -1;
+  job.clear_lo = job.clear_hi = 0;
+  if (job.top() > 0) {
+    const int end = job.kbase + job.top() * kKeys;
+    if (job.kbase < 0) {
+      job.clear_j = 0;
+      job.clear_hi = -job.kbase;
+    } else if (end > job.lk) {
+      job.clear_j = job.top() - 1;
+      job.clear_lo = kKeys - (end - job.lk);
+      job.clear_hi = kKeys;
+    }
+  }
+  job.more = 1;
   return true;
 }
+
+// Cluster launch control: ask the launcher for a block of this grid that has not started. The
+// 16-byte answer lands in shared memory; it holds the block's index, or nothing if none is left.
+__device__ __forceinline__ void next_block_ask(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool next_block_take(uint32_t answer, uint32_t& block) {
+  uint32_t got;
+  asm volatile(
+      "{ .reg .pred p; .reg .b128 a; ld.shared.b128 a, [%2];\n"
+      "  clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n"
+      "  selp.u32 %0, 1, 0, p; mov.u32 %1, 0;\n"
+      "  @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a; }"
+      : "=r"(got), "=r"(block)
+      : "r"(answer)
+      : "memory");
+  return got != 0;
+}
+
+constexpr int kJobSlots = 2;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptParams p) {
   using L = Shape<D>;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ Job s_job[kJobSlots];
+  __shared__ __align__(16) uint4 s_answer;
+  __shared__ uint32_t s_tmem;
+  __shared__ __align__(8) uint64_t s_bars[21 + 2 * kJobSlots + 2 * L::kStages];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-  uint8_t* sm = smem_raw + (base - raw);
   const uint32_t sQ = base + L::kOffQ, sKv = base + L::kOffKv;
-  uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kOffMisc);
-  uint32_t* s_tmem = misc;
-  // mbarriers: q_full[2], s_full[2], p_full[2], o_full[2], cleared, drain, then kv_full[stage], kv_empty[stage]
-  const uint32_t bars = smem_u32(misc + 2);
-  const uint32_t q_full = bars, s_full = bars + 16, p_full = bars + 32, o_full = bars + 48, cleared = bars + 64,
-                 drain = bars + 72, kv_full = bars + 80, kv_empty = kv_full + 8 * L::kStages;
-  static_assert(8 + 80 + 16 * L::kStages <= 256, "barriers");
+  // mbarriers, one for each query tile: Q of a job loaded / read by its last product, O read, every
+  // product done; two for each query tile, for key tiles in turn: S computed, P written, P V added to
+  // O (one barrier for all key tiles would not do: the softmax may be two of them ahead of P V, and a
+  // parity cannot tell that). Then the launcher's answer, the jobs and the ring of K and V
+  const uint32_t bars = smem_u32(s_bars);
+  const uint32_t q_full = bars, q_empty = bars + 16, o_empty = bars + 32, drain = bars + 48, s_full = bars + 64,
+                 p_full = bars + 96, o_full = bars + 128, answered = bars + 160, job_full = bars + 168,
+                 job_empty = job_full + 8 * kJobSlots, kv_full = job_empty + 8 * kJobSlots,
+                 kv_empty = kv_full + 8 * L::kStages;
+  static_assert(168 + 16 * kJobSlots + 16 * L::kStages <= sizeof(s_bars), "barriers");
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (warp == kMmaWarp) tmem_alloc(smem_u32(s_tmem), 512);
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), 512);
   if (tid == 0) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full + 8 * t, 1);
-      mbar_init(s_full + 8 * t, 1);
-      mbar_init(p_full + 8 * t, 4);
-      mbar_init(o_full + 8 * t, 1);
+      mbar_init(q_empty + 8 * t, 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(s_full + 16 * t + 8 * b, 1);
+        mbar_init(p_full + 16 * t + 8 * b, 4);
+        mbar_init(o_full + 16 * t + 8 * b, 1);
+      }
+      mbar_init(o_empty + 8 * t, 4);
+      mbar_init(drain + 8 * t, 1);
     }
-    mbar_init(cleared, 1);
-    mbar_init(drain, 1);
+    mbar_init(answered, 1);
+    for (int s = 0; s < kJobSlots; ++s) {
+      mbar_init(job_full + 8 * s, 1);
+      mbar_init(job_empty + 8 * s, kSoftWarps + 3);
+    }
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(kv_full + 8 * s, 1);
-      mbar_init(kv_empty + 8 * s, 1);
+      mbar_init(kv_empty + 8 * s, 2);      // both tiles' products
     }
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(s_tmem);
+  const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(&s_tmem));
   griddep_wait();
   griddep_launch_dependents();
-
-  const int h = blockIdx.x % p.heads_kv;
-  Job job = {};
-  // every warp looks its job up itself (the same loads): no broadcast, no block barrier
-  const bool any = find_job(p, blockIdx.x / p.heads_kv, blockIdx.x == gridDim.x - 1, job);
-  const int j_top = max(job.jhi[0], job.jhi[1]);
-  const int j_bot = min(job.jhi[0] > job.jlo[0] ? job.jlo[0] : 0x7fffffff, job.jhi[1] > job.jlo[1] ? job.jlo[1] : 0x7fffffff);
-  const bool clear = any && (int64_t)j_top * kTile > job.lk;      // the top tile reaches past the sequence
-  auto active = [&](int t, int j) { return j >= job.jlo[t] && j < job.jhi[t]; };
   bool ok = true;
 
-  if (!any) {
-    // a CTA past the last tile
-  } else if (warp >= kSoftWarps) {
+  // Job `it` of this CTA, by one warp: waits for it; free_job frees its slot, once it has been read.
+  auto wait_job = [&](int it) {
+    const int s = it % kJobSlots;
+    ok = wait_bar(job_full + 8 * s, (it / kJobSlots) & 1, p.wait_ns) && ok;
+    ok = __all_sync(0xffffffffu, ok);
+    return ok && s_job[s].more != 0;
+  };
+  auto free_job = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(job_empty + 8 * (it % kJobSlots));
+  };
+  auto take_job = [&](int it, Job& job) {
+    if (!wait_job(it)) return false;
+    job = s_job[it % kJobSlots];
+    free_job(it);
+    return true;
+  };
+
+  if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
-      // ---------------------------------------------------------------- loads
-      if (lane == 0 && j_top > 0) {
+      // -------------------------------------------------------------- loads
+      // The ring holds K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1), tiles counted from the top: the
+      // products of S run a key tile ahead of those with V.
+      int n_q[2] = {0, 0}, c = 0;        // queries loaded; tiles of the ring loaded
+      auto load_kv = [&](const Job& job, int j, const CUtensorMap* map) {
+        const int s = c % L::kStages;
+        ok = ok && wait_bar(kv_empty + 8 * s, ((c / L::kStages) & 1) ^ 1, p.wait_ns);
+        if (!ok) return;
+        mbar_arrive_expect_tx(kv_full + 8 * s, L::kKvBytes);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (job.jhi[t] > job.jlo[t]) {
-            mbar_arrive_expect_tx(q_full + 8 * t, (D / 64) * (uint32_t)(p.tt * p.group) * 128u);
+        for (int d = 0; d < D / 64; ++d)
+          tma_3d(sKv + s * L::kKvBytes + d * kBlockK, map, 64 * d, job.h, job.k0 + job.kbase + kKeys * j, kv_full + 8 * s);
+        ++c;
+      };
+      auto load_q = [&](const Job& job, int t) {
+        ok = ok && wait_bar(q_empty + 8 * t, (n_q[t] & 1) ^ 1, p.wait_ns);
+        if (!ok) return;
+        mbar_arrive_expect_tx(q_full + 8 * t, (D / 64) * (uint32_t)(p.tt * p.group) * 128u);
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              tma_4d(sQ + t * L::kTileBytes + c * kBlock, &p.qm, 64 * c, 0, h, job.q0 + job.i0 + t * p.tt, q_full + 8 * t);
-          }
-        int c = 0;                         // tiles loaded so far: K, V, K, V, ...
-        for (int j = j_top - 1; j >= j_bot && ok; --j) {
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++c) {
-            const int s = c % L::kStages;
-            ok = ok && mbar_wait(kv_empty + 8 * s, ((c / L::kStages) & 1) ^ 1, p.wait_ns);
-            if (!ok) break;
-            mbar_arrive_expect_tx(kv_full + 8 * s, L::kTileBytes);
-#pragma unroll
-            for (int d = 0; d < D / 64; ++d)
-              tma_3d(sKv + s * L::kTileBytes + d * kBlock, kv ? &p.vm : &p.km, 64 * d, h, job.k0 + kTile * j, kv_full + 8 * s);
+        for (int d = 0; d < D / 64; ++d)
+          tma_4d(sQ + t * L::kQBytes + d * kBlockQ, &p.qm, 64 * d, 0, job.h, job.q0 + job.i0 + t * p.tt, q_full + 8 * t);
+        ++n_q[t];
+      };
+      Job job;
+      for (int it = 0; take_job(it, job); ++it) {
+        if (lane == 0) {
+          const int top = job.top(), bottom = job.bottom();
+          if (top > 0) load_kv(job, top - 1, &p.km);
+          if (job.has(0)) load_q(job, 0);
+          if (job.has(1)) load_q(job, 1);
+          for (int j = top - 1; j >= bottom && ok; --j) {
+            if (j > bottom) load_kv(job, j - 1, &p.km);
+            load_kv(job, j, &p.vm);
           }
         }
-        // nothing of this CTA's may be in flight when it ends, whatever the other roles did
+        __syncwarp();
+      }
+      // nothing of this CTA's may be in flight when it ends, whatever the other roles did
+      if (lane == 0) {
         for (int e = max(0, c - L::kStages); e < c; ++e)
-          ok = mbar_wait(kv_full + 8 * (e % L::kStages), (e / L::kStages) & 1, p.wait_ns) && ok;
+          ok = wait_bar(kv_full + 8 * (e % L::kStages), (e / L::kStages) & 1, p.wait_ns) && ok;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (job.jhi[t] > job.jlo[t]) ok = mbar_wait(q_full + 8 * t, 0, p.wait_ns) && ok;
+          if (n_q[t]) ok = wait_bar(q_full + 8 * t, (n_q[t] - 1) & 1, p.wait_ns) && ok;
       }
-    } else if (warp == kMmaWarp) {
-      // ---------------------------------------------------------------- products
-      if (lane == 0 && j_top > 0) {
-        const uint32_t id_qk = idesc_f16(128, 128, false, false, BF16), id_pv = idesc_f16(128, D, false, true, BF16);
-        auto qk = [&](int t, int c) {
-          const uint64_t a = sdesc(sQ + t * L::kTileBytes, 16u, 1024u), b = sdesc(sKv + (c % L::kStages) * L::kTileBytes, 16u, 1024u);
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      // -------------------------------------------------------------- products of one query tile
+      const int t = warp - kMmaWarp;
+      const uint32_t tS = tmem + 128 * t, tO = tmem + 256 + 128 * t;
+      const uint32_t id_qk = idesc_f16(kTile, kKeys, false, false, BF16), id_pv = idesc_f16(kTile, D, false, true, BF16);
+      const uint64_t dq = sdesc(sQ + t * L::kQBytes, 16u, 1024u);
+      auto wait = [&](uint32_t bar, int n) {
+        ok = wait_bar(bar, n & 1, p.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        return ok;
+      };
+      int n_q = 0, n_s = 0, n_p = 0, c = 0;      // jobs with keys for this tile, key tiles of S and P, tiles of the ring
+      auto wait_kv = [&]() { return wait(kv_full + 8 * (c % L::kStages), c / L::kStages); };
+      const uint32_t one = elect_one();
+      auto free_kv = [&]() {
+        umma_commit_one(one, kv_empty + 8 * (c % L::kStages));
+        ++c;
+      };
+      // S of the next key tile, into the buffer whose P the product with V before last has read
+      auto qk = [&](bool last) {
+        const uint64_t dk = sdesc(sKv + (c % L::kStages) * L::kKvBytes, 16u, 1024u);
+        const uint32_t at = tS + 64 * (n_s & 1);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t o = ((k >> 2) * kBlock + (k & 3) * 32u) >> 4;
-            umma_f16(tmem + 128 * t, a + o, b + o, id_qk, k > 0);
+        for (int k = 0; k < D / 16; ++k)
+          umma_ss(one, at, dq + (((k >> 2) * kBlockQ + (k & 3) * 32u) >> 4), dk + (((k >> 2) * kBlockK + (k & 3) * 32u) >> 4), id_qk,
+                  k > 0);
+        umma_commit_one(one, s_full + 16 * t + 8 * (n_s & 1));
+        if (last) umma_commit_one(one, q_empty + 8 * t);
+        ++n_s;
+      };
+      auto pv = [&](bool acc) {
+        const uint64_t dv = sdesc(sKv + (c % L::kStages) * L::kKvBytes, kBlockK, 1024u);
+        const uint32_t at = tS + 64 * (n_p & 1);
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k) umma_ts(one, tO, at + 8 * k, dv + ((k * 16u * 128u) >> 4), id_pv, acc || k > 0);
+        umma_commit_one(one, o_full + 16 * t + 8 * (n_p & 1));
+        ++n_p;
+      };
+      Job job;
+      for (int it = 0; take_job(it, job); ++it) {
+        const int top = uniform(job.top()), bottom = uniform(job.bottom()), clear_j = uniform(job.clear_j);
+        const int jlo = uniform(t ? job.jlo[1] : job.jlo[0]), jhi = uniform(t ? job.jhi[1] : job.jhi[0]);
+        if (top == 0) continue;
+        const bool has = jhi > jlo;
+        if (has && !wait(q_full + 8 * t, n_q)) break;
+        if (!wait_kv()) break;
+        if (top == jhi) qk(top - 1 == jlo);
+        free_kv();
+        for (int j = top - 1; j >= bottom && ok; --j) {
+          if (j > bottom) {
+            if (!wait_kv()) break;
+            if (j - 1 >= jlo && j - 1 < jhi) qk(j - 1 == jlo);
+            free_kv();
           }
-          umma_commit(s_full + 8 * t);
-        };
-        auto pv = [&](int t, int c, bool acc) {
-          const uint64_t b = sdesc(sKv + (c % L::kStages) * L::kTileBytes, kBlock, 1024u);
+          if (!wait_kv()) break;
+          if (j >= jlo && j < jhi) {
+            if (j == clear_j) {          // rows that are no keys of the sequence (both warps write the same zeros)
+              const uint32_t v = sKv + (c % L::kStages) * L::kKvBytes;
+              for (int x = job.clear_lo * 8 + lane; x < job.clear_hi * 8; x += 32)
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            umma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, b + ((k * 16u * 128u) >> 4), id_pv, acc || k > 0);
-        };
-        auto wait_kv = [&](int c) {
-          ok = ok && mbar_wait(kv_full + 8 * (c % L::kStages), (c / L::kStages) & 1, p.wait_ns);
-          tc_fence_after();
-        };
-        int n_p[2] = {0, 0};
-        int c = 0;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (job.jhi[t] > job.jlo[t]) ok = ok && mbar_wait(q_full + 8 * t, 0, p.wait_ns);
-        wait_kv(0);
-        if (ok) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (active(t, j_top - 1)) qk(t, 0);
-          umma_commit(kv_empty);
-        }
-        for (int j = j_top - 1; j >= j_bot && ok; --j, c += 2) {
-          wait_kv(c + 1);
-          if (clear && j == j_top - 1) ok = ok && mbar_wait(cleared, 0, p.wait_ns);
-          bool k_here = false;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (active(t, j) && ok) {
-              ok = mbar_wait(p_full + 8 * t, n_p[t] & 1, p.wait_ns);
-              tc_fence_after();
-              if (ok) {
-                pv(t, c + 1, n_p[t] > 0);
-                if (j == job.jlo[t]) umma_commit(o_full + 8 * t);
-              }
-              ++n_p[t];
+                for (int d = 0; d < D / 64; ++d) sts128(v + d * kBlockK + x * 16u, 0u, 0u, 0u, 0u);
+              fence_async_smem();
+              __syncwarp();
             }
-            if (j - 1 >= j_bot && active(t, j - 1) && ok) {
-              if (!k_here) wait_kv(c + 2);
-              k_here = true;
-              if (ok) qk(t, c + 2);
-            }
+            // the first product of a job overwrites O: the last job's must have been read
+            if (j == jhi - 1 && !wait(o_empty + 8 * t, n_q ^ 1)) break;
+            if (!wait(p_full + 16 * t + 8 * (n_p & 1), n_p >> 1)) break;
+            pv(j < jhi - 1);
           }
-          umma_commit(kv_empty + 8 * ((c + 1) % L::kStages));
-          if (j - 1 >= j_bot) umma_commit(kv_empty + 8 * ((c + 2) % L::kStages));
+          free_kv();
         }
-        umma_commit(drain);
-        ok = mbar_wait(drain, 0, p.wait_ns) && ok;
+        if (!ok) break;
+        n_q += has;
       }
-    } else if (warp == kClearWarp) {
-      // ---------------------------------------------------------------- V past the sequence's end
-      if (clear && j_top > 0) {
-        ok = mbar_wait(kv_full + 8, 0, p.wait_ns);           // the top tile's V is the ring's second tile
-        const int first = job.lk - kTile * (j_top - 1);
-        if (ok) {
-          for (int e = first * 8 + lane; e < kTile * 8; e += 32)
-#pragma unroll
-            for (int d = 0; d < D / 64; ++d) sts128(sKv + L::kTileBytes + d * kBlock + e * 16u, 0u, 0u, 0u, 0u);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(cleared);
+      umma_commit_one(one, drain + 8 * t);       // every product is done before the tensor memory is freed
+      ok = wait_bar(drain + 8 * t, 0, p.wait_ns) && ok;
+    } else {
+      // -------------------------------------------------------------- what comes next
+      const uint32_t answer = smem_u32(&s_answer);
+      uint32_t block = blockIdx.x;
+      bool more = true;
+      for (int n = 0, it = 0; more && ok; ++n) {
+        // the next block is asked for while this one's tile is looked up
+        if (lane == 0) {
+          fence_async_smem();            // the last answer has been read
+          mbar_arrive_expect_tx(answered, 16);
+          next_block_ask(answer, answered);
+        }
+        __syncwarp();
+        Job job;
+        if (find_job(p, block, block == gridDim.x - 1, job)) {
+          const int s = it % kJobSlots;
+          ok = wait_bar(job_empty + 8 * s, ((it / kJobSlots) & 1) ^ 1, p.wait_ns) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok && lane == 0) {
+            s_job[s] = job;
+            mbar_arrive(job_full + 8 * s);
+          }
+          ++it;
+        }
+        const bool got = wait_bar(answered, n & 1, p.wait_ns);
+        ok = __all_sync(0xffffffffu, got && ok);
+        more = ok && next_block_take(answer, block);
+        __syncwarp();
+        if (!more && ok) {
+          const int s = it % kJobSlots;
+          ok = wait_bar(job_empty + 8 * s, ((it / kJobSlots) & 1) ^ 1, p.wait_ns) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok && lane == 0) {
+            s_job[s].more = 0;
+            mbar_arrive(job_full + 8 * s);
+          }
         }
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---------------------------------------------------------------- softmax: one row per thread
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + 128u * t, tO = tmem + lanes + 256u + 128u * t;
-    const int tok = t * p.tt + r / p.group;
-    const bool real = r < p.tt * p.group && tok < job.n;
-    const int pos = job.i0 + tok + job.off;
-    const int hi = real ? pos + 1 : 0, lo = real && p.window > 0 ? max(pos - p.window + 1, 0) : 0;
-    // key tiles that every row of this query tile sees whole need no mask
-    const int t_first = job.i0 + t * p.tt + job.off, t_last = job.i0 + min(job.n, (t + 1) * p.tt) - 1 + job.off;
-    const int whole_hi = t_first + 1, whole_lo = p.window > 0 ? max(t_last - p.window + 1, 0) : 0;
-    float m = -INFINITY, l = 0.f;
-    const float scale = p.scale_log2, raise = kRaise / scale;
-    const uint64_t scale2 = f2_pack(scale, scale);
-    int n_s = 0;
-    for (int j = job.jhi[t] - 1; j >= job.jlo[t] && ok; --j, ++n_s) {
-      ok = mbar_wait(s_full + 8 * t, n_s & 1, p.wait_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) TMEM_LD32(tS + 32 * c, s[c]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_regs_ready(s[c]);
-      if (kTile * (j + 1) > whole_hi || kTile * j < whole_lo) {
-        const int hr = hi - kTile * j, lr = lo - kTile * j;
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= hr || c < lr) s[c >> 5][c & 31] = 0xFF800000u;   // -inf
+    // Shared memory is busy with the products' operands, so this loop keeps out of it: no exchange
+    // between warps (two warps per row, half the keys each, took 1.5 times as long), no spilled registers. What the epilogue needs of the job is
+    // read again there, and the values that follow from it are not kept across the loop.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    const int t = warp >> 2;
+    const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * t, tO = tS + 256u;
+    const float scale = p.scale_log2;
+    int n_s = 0;                         // key tiles so far
+    for (int it = 0; wait_job(it); ++it) {
+      int j, jlo, hi, lo, whole_hi, whole_lo;
+      {
+        const Job& job = s_job[it % kJobSlots];
+        const int r = (warp & 3) * 32 + lane, r_tok = t * p.tt + r / p.group;
+        const int first = job.i0 + job.off - job.kbase;                // the first token's position, from kbase on
+        const int floor = -job.kbase;                                  // key 0 (kbase < 0: with a window)
+        const bool real = r < p.tt * p.group && r_tok < job.n;
+        jlo = t ? job.jlo[1] : job.jlo[0];
+        j = (t ? job.jhi[1] : job.jhi[0]) - 1;
+        // this row's keys, and those that every row of the tile sees, from tile j's first key on
+        hi = (real ? max(first + r_tok + 1, 0) : 0) - kKeys * j;
+        lo = (real && p.window > 0 ? max(first + r_tok - p.window + 1, floor) : 0) - kKeys * j;
+        whole_hi = first + t * p.tt + 1 - kKeys * j;
+        whole_lo = (p.window > 0 ? max(first + min(job.n, (t + 1) * p.tt) - p.window, floor) : 0) - kKeys * j;
       }
-      float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+      float m = -INFINITY, l = 0.f;
+      bool later = false;                // a tile of this job has gone into O
+      const bool keys = j >= jlo;
+      for (; j >= jlo; --j, ++n_s) {
+        ok = wait_bar(s_full + 16 * t + 8 * (n_s & 1), (n_s >> 1) & 1, p.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = tS + 64 * (n_s & 1);
+        uint32_t s[2][32];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        mx0 = fmaxf(mx0, __uint_as_float(s[0][c]));
-        mx1 = fmaxf(mx1, __uint_as_float(s[1][c]));
-        mx2 = fmaxf(mx2, __uint_as_float(s[2][c]));
-        mx3 = fmaxf(mx3, __uint_as_float(s[3][c]));
-      }
-      const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-      if (__any_sync(0xffffffffu, mx > m + raise)) {
-        const float mn = fmaxf(m, mx);
-        const float f = mn == -INFINITY ? 1.f : ex2_ftz((m - mn) * scale);   // m = -inf before: 0, on sums that are 0
-        m = mn;
-        l *= f;
-        if (n_s > 0) {                   // PV of the last tile is complete: S's barrier came after it
+        for (int c = 0; c < 2; ++c) TMEM_LD32(at + 32 * c, s[c]);
+        tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            TMEM_LD32(tO + 32 * c, o);
-            tmem_wait_ld();
-            tmem_regs_ready(o);
+        for (int c = 0; c < 2; ++c) tmem_regs_ready(s[c]);
+        if (kKeys > whole_hi || 0 < whole_lo) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            TMEM_ST32(tO + 32 * c, o);
+          for (int c = 0; c < kKeys; ++c)
+            if (c >= hi || c < lo) s[c >> 5][c & 31] = 0xFF800000u;   // -inf
+        }
+        hi += kKeys;
+        lo += kKeys;
+        whole_hi += kKeys;
+        whole_lo += kKeys;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 16; c += 2)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            mx[u] = max3(mx[u], __uint_as_float(s[u >> 1][16 * (u & 1) + c]), __uint_as_float(s[u >> 1][16 * (u & 1) + c + 1]));
+        // (rows that are no queries, or see none of these keys, ask for nothing)
+        const float top = hi > kKeys ? max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) : -INFINITY;
+        if (__any_sync(0xffffffffu, (top - m) * scale > kRaise)) {     // also with m = -inf; not with top = -inf
+          const float mn = fmaxf(m, top);
+          const float f = mn == -INFINITY ? 1.f : ex2_ftz((m - mn) * scale);   // m = -inf before: 0, on sums that are 0
+          m = mn;
+          l *= f;
+          if (later) {                   // once the last tile's P V is in O
+            ok = wait_bar(o_full + 16 * t + 8 * ((n_s - 1) & 1), ((n_s - 1) >> 1) & 1, p.wait_ns) && ok;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {          // 8 columns at a time: the row of S stays in registers
+              uint32_t o[8];
+              TMEM_LD8(tO + 8 * c, o);
+              tmem_wait_ld();
+              tmem_regs_ready(o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              TMEM_ST8(tO + 8 * c, o);
+            }
           }
         }
-      }
-      const float mu = m == -INFINITY ? 0.f : m * scale;
-      const uint64_t nmu2 = f2_pack(-mu, -mu);
-      uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
+        later = true;
+        const float mu = m == -INFINITY ? 0.f : m * scale;
+        const uint64_t nmu2 = f2_pack(-mu, -mu), scale2 = f2_pack(scale, scale);
+        uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
+        for (int q = 0; q < 4; ++q) {    // 16 keys at a time, so that P takes few registers beside S
+          uint32_t pk[8];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const int e = 64 * half + 2 * c;
-          float z0, z1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1])), scale2, nmu2),
-                    z0, z1);
-          const float p0 = ex2_ftz(z0), p1 = ex2_ftz(z1);
-          if (c & 1)
-            sum1 = f2_add(sum1, f2_pack(p0, p1));
-          else
-            sum0 = f2_add(sum0, f2_pack(p0, p1));
-          pk[c] = pack2<BF16>(p0, p1);
+          for (int c = 0; c < 8; ++c) {
+            const int e = 16 * q + 2 * c;
+            float z0, z1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1])), scale2, nmu2),
+                      z0, z1);
+            const float p0 = ex2_ftz(z0), p1 = ex2_ftz(z1);
+            if (c & 1)
+              sum1 = f2_add(sum1, f2_pack(p0, p1));
+            else
+              sum0 = f2_add(sum0, f2_pack(p0, p1));
+            pk[c] = pack2<BF16>(p0, p1);
+          }
+          TMEM_ST8(at + 8 * q, pk);
         }
-        TMEM_ST32(tS + 32 * half, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * (n_s & 1));
+        float a, b;
+        f2_unpack(f2_add(sum0, sum1), a, b);
+        l += a + b;
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + 8 * t);
-      float a, b;
-      f2_unpack(f2_add(sum0, sum1), a, b);
-      l += a + b;
-    }
-    // ---------------------------------------------------------------- O / l
-    const bool keys = job.jhi[t] > job.jlo[t];
-    if (keys) {
-      ok = ok && mbar_wait(o_full + 8 * t, 0, p.wait_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
-    const int64_t row = (int64_t)job.q0 + job.i0 + tok;
-    const int hq = h * p.group + r % p.group;
-    uint16_t* out = p.out + row * p.out_stride + (int64_t)hq * D;
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    if (ok) {
+      if (!ok) break;
+      // -------------------------------------------------------------- O / l
+      if (keys) {
+        ok = wait_bar(o_full + 16 * t + 8 * ((n_s - 1) & 1), ((n_s - 1) >> 1) & 1, p.wait_ns) && ok;   // the last P V
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const Job& job = s_job[it % kJobSlots];
+      int group = p.group;               // opaque: what follows from it is computed here, not before the loop
+      asm volatile("" : "+r"(group));
+      const uint32_t stage = base + L::kOffStage + (uint32_t)warp * 2048u;
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      const int64_t row0 = (int64_t)job.q0 + job.i0;
+      uint16_t* dst[4];                  // where this lane writes its piece of rows 8 i + lane / 4; NULL: no such row
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = (warp & 3) * 32 + 8 * i + (lane >> 2), tok = t * p.tt + rr / group;
+        dst[i] = rr < p.tt * group && tok < job.n
+                     ? p.out + (row0 + tok) * p.out_stride + (int64_t)(job.h * group + rr % group) * D + 8 * (lane & 3)
+                     : nullptr;
+      }
+      if (p.lse) {
+        const int r = (warp & 3) * 32 + lane, tok = t * p.tt + r / group;
+        if (r < p.tt * group && tok < job.n)
+          p.lse[(row0 + tok) * p.heads_q + job.h * group + r % group] = l != 0.f ? (m * scale + log2f(l)) * kLn2 : -INFINITY;
+      }
+      free_job(it);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -438,22 +652,33 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
           TMEM_LD32(tO + 32 * c, o);
           tmem_wait_ld();
           tmem_regs_ready(o);
-        }
-        if (real) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t y[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float a = l != 0.f ? __uint_as_float(o[e + 2 * u]) * inv : 0.f;
-              const float b = l != 0.f ? __uint_as_float(o[e + 2 * u + 1]) * inv : 0.f;
-              y[u] = pack2<BF16>(a, b);
-            }
-            *reinterpret_cast<uint4*>(out + 32 * c + e) = make_uint4(y[0], y[1], y[2], y[3]);
+          if (c == D / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_empty + 8 * t);
           }
         }
+        // through shared memory, so that four lanes write 64 bytes of a row together
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t y[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float a = l != 0.f ? __uint_as_float(o[8 * e + 2 * u]) * inv : 0.f;
+            const float b = l != 0.f ? __uint_as_float(o[8 * e + 2 * u + 1]) * inv : 0.f;
+            y[u] = pack2<BF16>(a, b);
+          }
+          sts128(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4), y[0], y[1], y[2], y[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = 8 * i + (lane >> 2);
+          const uint4 y = lds128(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+          if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + 32 * c) = y;
+        }
+        __syncwarp();
       }
-      if (p.lse && real) p.lse[row * p.heads_q + hq] = l != 0.f ? (m * scale + log2f(l)) * kLn2 : -INFINITY;
     }
   }
   if (!ok) flag_status(p.status, HSA_FLAG_TIMEOUT);
@@ -525,11 +750,11 @@ cudaError_t launch_prompt_attn(const hsa_prompt_args& a, uint32_t* status, uint6
       return cudaErrorInvalidValue;
   }
   for (int i = 0; i < 2; ++i) {
-    // k and v as [row][key-value head][dim]: a box is 128 rows x 64 dims. Without any rows the maps
+    // k and v as [row][key-value head][dim]: a box is 64 rows x 64 dims. Without any rows the maps
     // are never used (no sequence has keys); they stand on q then.
     const cuuint64_t dims[3] = {d, (cuuint64_t)p.heads_kv, (cuuint64_t)(a.n_k > 0 ? a.n_k : 1)};
     const cuuint64_t strides[2] = {2 * d, 2 * (cuuint64_t)(i ? a.v_stride : a.k_stride)};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)kTile};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)kKeys};
     void* at = const_cast<void*>(a.n_k > 0 ? (i ? a.v : a.k) : a.q);
     if (encode(i ? &p.vm : &p.km, type, 3, at, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
