@@ -128,10 +128,23 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """Address of the current device's current stream. torch.cuda.current_stream() makes a Stream object first,
+    which costs as much as a launch, so the address is asked for directly where torch offers it."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -255,40 +268,47 @@ def hsa_schedule_step(caches, step: StepArgs, ws, stream=None):
 
 
 # ---------------------------------------------------------------- dense attention
+# The checks below run before every call, so they ask a tensor for as little as they can.
+_DTYPES = {}
+
+
 def _dtype(t):
     """The hsa_dtype of a tensor."""
-    import torch
-    try:
-        return {torch.bfloat16: HSA_BF16, torch.float16: HSA_F16, torch.float8_e4m3fn: HSA_E4M3}[t.dtype]
-    except KeyError:
-        raise ValueError(f"unsupported type {t.dtype}") from None
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: HSA_BF16, torch.float16: HSA_F16, torch.float8_e4m3fn: HSA_E4M3,
+                        "i32": torch.int32, "i64": torch.int64, "f32": torch.float32})
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported type {t.dtype}")
+    return code
 
 
 def _rows(name, t, heads, dim):
     """Row stride of [rows][heads][dim] values: rows may stand apart, a row is contiguous."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows][{heads}][{dim}]")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [rows][{heads}][{dim}]")
+    if stride[2] != 1 or (heads > 1 and stride[1] != dim):
         raise ValueError(f"{name}: a row of [{heads}][{dim}] must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return stride[0] if shape[0] > 1 else heads * dim
 
 
 def _given(name, t, dtype, shape, device):
-    """Check a contiguous tensor argument (the library takes its address alone); None passes."""
+    """Address of a contiguous tensor argument (the library takes nothing else of it); None passes."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: expected contiguous {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} "
-                         f"on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {list(shape)} on device {device}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _on_device(name, t):
-    """The library launches on the current device, so its tensors have to be there."""
+def _on_current(name, device):
+    """The library launches on the current device, so its tensors have to be there (-1: not on a GPU)."""
     import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}: expected the current CUDA device")
-    return t.device
+    if device < 0 or device != torch.cuda.current_device():
+        raise ValueError(f"{name} is on device {device}: expected the current CUDA device")
 
 
 class PagedCache:
@@ -301,13 +321,14 @@ class PagedCache:
         if k.dim() != 4 or table.dim() != 2:
             raise ValueError("k and v are [n_pages][heads][page_size][head_dim], table is [batch][max_pages]")
         self.k, self.v, self.table = k, v, table
-        _given("v", v, k.dtype, k.shape, k.device)
-        _given("k", k, k.dtype, k.shape, k.device)
-        _given("table", table, torch.int32, table.shape, k.device)
+        self.dtype, self.device = _dtype(k), k.get_device()
+        _given("k", k, k.dtype, k.shape, self.device)
+        _given("v", v, k.dtype, k.shape, self.device)
+        _given("table", table, torch.int32, table.shape, self.device)
         n_pages, self.heads, self.page_size, self.head_dim = k.shape
         self.batch, max_pages = table.shape
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
-        self.desc = hsa_paged_cache(self.batch, self.heads, self.head_dim, self.page_size, _dtype(k), 0, n_pages, max_pages,
+        self.desc = hsa_paged_cache(self.batch, self.heads, self.head_dim, self.page_size, self.dtype, 0, n_pages, max_pages,
                                     _ptr(k), _ptr(v), _ptr(table), self.k_scale, self.v_scale)
 
     @property
@@ -318,15 +339,17 @@ class PagedCache:
 def hsa_paged_cache_write(cache: PagedCache, k, v, cu=None, start=None, stream=None):
     """k, v: [n_tokens][heads][head_dim], rows at any stride; cu: int32 [batch + 1] or None (equal
     shares); start: int64 [batch] or None (0)."""
-    import torch
-    dev = _on_device("cache", cache.k)
-    k_stride, v_stride = (_rows(n, t, cache.heads, cache.head_dim) for n, t in (("k", k), ("v", v)))
-    if k.shape != v.shape or k.dtype != v.dtype or k.device != dev or v.device != dev:
+    device = cache.device
+    _on_current("cache", device)
+    k_stride, v_stride = _rows("k", k, cache.heads, cache.head_dim), _rows("v", v, cache.heads, cache.head_dim)
+    n = k.shape[0]
+    if v.shape[0] != n or k.dtype is not v.dtype or k.get_device() != device or v.get_device() != device:
         raise ValueError("k and v differ in shape or type, or are not on the cache's device")
+    dtype = _dtype(k)
     _check("hsa_paged_cache_write", load_library().hsa_paged_cache_write(
-        cache.ref, k.data_ptr(), v.data_ptr(), _dtype(k), k_stride, v_stride, k.shape[0],
-        _given("cu", cu, torch.int32, (cache.batch + 1,), dev), _given("start", start, torch.int64, (cache.batch,), dev),
-        _stream(stream)))
+        cache.ref, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride, n,
+        _given("cu", cu, _DTYPES["i32"], (cache.batch + 1,), device),
+        _given("start", start, _DTYPES["i64"], (cache.batch,), device), _stream(stream)))
 
 
 def hsa_paged_attn_workspace_bytes(cache: PagedCache, heads_q, nq, max_vis):
@@ -344,36 +367,41 @@ def new_paged_workspace(cache: PagedCache, heads_q, nq, max_vis):
 
 def hsa_paged_attn_decode(cache: PagedCache, q, vis, max_vis, sm_scale, out, ws, window=0, lse=None, stream=None):
     """q, out: [batch][nq][heads_q][head_dim]; vis: int32 [batch][nq]; lse: float32 [batch][nq][heads_q] or None."""
-    import torch
-    dev = _on_device("cache", cache.k)
-    if q.dim() != 4 or q.shape[0] != cache.batch or q.shape[3] != cache.head_dim:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected [{cache.batch}][nq][heads_q][{cache.head_dim}]")
-    _, nq, heads_q, _ = q.shape
+    device, shape = cache.device, q.shape
+    _on_current("cache", device)
+    if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.head_dim:
+        raise ValueError(f"q: shape {tuple(shape)}, expected [{cache.batch}][nq][heads_q][{cache.head_dim}]")
+    if ws is not None and (ws.get_device() != device or not ws.is_contiguous()):
+        raise ValueError("ws: expected a contiguous tensor on the cache's device")
+    _, nq, heads_q, _ = shape
+    dtype = _dtype(q)
     _check("hsa_paged_attn_decode", load_library().hsa_paged_attn_decode(
-        cache.ref, _given("q", q, q.dtype, q.shape, dev), _dtype(q), heads_q,
-        _given("vis", vis, torch.int32, (cache.batch, nq), dev), nq, max_vis, window, float(sm_scale),
-        _given("out", out, q.dtype, q.shape, dev), _given("lse", lse, torch.float32, q.shape[:3], dev), _ptr(ws),
-        ws.numel() * ws.element_size() if ws is not None and ws.device == dev else 0, _stream(stream)))
+        cache.ref, _given("q", q, q.dtype, shape, device), dtype, heads_q,
+        _given("vis", vis, _DTYPES["i32"], (cache.batch, nq), device), nq, max_vis, window, sm_scale,
+        _given("out", out, q.dtype, shape, device), _given("lse", lse, _DTYPES["f32"], shape[:3], device), _ptr(ws),
+        ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
 
 
 def hsa_prompt_attn(q, k, v, cu_q, sm_scale, out, cu_k=None, window=0, lse=None, stream=None):
     """q, out: [n_q][heads_q][head_dim], k, v: [n_k][heads_kv][head_dim], rows at any stride; cu_q,
     cu_k: int32 [batch + 1] (cu_k None: cu_q); lse: float32 [n_q][heads_q] or None."""
-    import torch
-    dev = _on_device("q", q)
+    device = q.get_device()
+    _on_current("q", device)
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k, v and out are [rows][heads][head_dim]")
     (n_q, heads_q, dim), (n_k, heads_kv, _) = q.shape, k.shape
-    q_stride, out_stride = (_rows(n, t, heads_q, dim) for n, t in (("q", q), ("out", out)))
-    k_stride, v_stride = (_rows(n, t, heads_kv, dim) for n, t in (("k", k), ("v", v)))
-    if out.shape != q.shape or k.shape != v.shape or any(t.dtype != q.dtype or t.device != dev for t in (k, v, out)):
+    q_stride, out_stride = _rows("q", q, heads_q, dim), _rows("out", out, heads_q, dim)
+    k_stride, v_stride = _rows("k", k, heads_kv, dim), _rows("v", v, heads_kv, dim)
+    if out.shape[0] != n_q or v.shape[0] != n_k or not q.dtype is k.dtype is v.dtype is out.dtype or \
+            not device == k.get_device() == v.get_device() == out.get_device():
         raise ValueError("q, k, v and out differ in type or device, q and out or k and v in shape")
-    batch = cu_q.numel() - 1
-    a = hsa_prompt_args(batch, heads_q, heads_kv, dim, _dtype(q), window, n_q, n_k, q.data_ptr(), k.data_ptr(),
-                        v.data_ptr(), q_stride, k_stride, v_stride, out_stride,
-                        _given("cu_q", cu_q, torch.int32, (batch + 1,), dev),
-                        _given("cu_k", cu_k, torch.int32, (batch + 1,), dev), float(sm_scale), out.data_ptr(),
-                        _given("lse", lse, torch.float32, (n_q, heads_q), dev))
+    dtype, i32, cu_shape = _dtype(q), _DTYPES["i32"], cu_q.shape
+    if len(cu_shape) != 1:
+        raise ValueError("cu_q is [batch + 1]")
+    a = hsa_prompt_args(cu_shape[0] - 1, heads_q, heads_kv, dim, dtype, window, n_q, n_k, q.data_ptr(), k.data_ptr(),
+                        v.data_ptr(), q_stride, k_stride, v_stride, out_stride, _given("cu_q", cu_q, i32, cu_shape, device),
+                        _given("cu_k", cu_k, i32, cu_shape, device), sm_scale, out.data_ptr(),
+                        _given("lse", lse, _DTYPES["f32"], (n_q, heads_q), device))
     _check("hsa_prompt_attn", load_library().hsa_prompt_attn(ctypes.byref(a), _stream(stream)))
 
 
