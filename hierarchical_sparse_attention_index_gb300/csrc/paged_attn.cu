@@ -35,8 +35,12 @@ constexpr float kRaise = 8.f;            // log2 of how far a logit may pass the
 
 enum KvType { kBf16 = HSA_BF16, kF16 = HSA_F16, kE4M3 = HSA_E4M3 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes, of which all but the first `bytes` are zeros and not read
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -172,36 +176,51 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   // ---------------------------------------------------------------- the ring: 16-key groups of this warp
   const uint32_t ring = smem_u32(sm) + (uint32_t)warp * T::kRing;
   const int n_groups = max(0, (end - begin + kGroup * (kWarps - warp) - 1) / (kGroup * kWarps));
-  const int64_t head_bytes = (int64_t)p.page_size * T::kRow;
   uint32_t bad = 0;                                      // bit s: the group in stage s lies on no page
-  // table entries of 32 groups at a time, one per lane, loaded a turn ahead of their use
-  auto load_pages = [&](int turn) {
+  // where 32 groups lie, one per lane, looked up a turn ahead of their use: the piece of the pools in
+  // units of 16 rows, or -1 for a bad page
+  const int64_t page_pieces = (int64_t)p.heads * (p.page_size / kGroup);
+  auto find_pieces = [&](int turn) -> int64_t {
     const int i = 32 * turn + lane;
-    return i < n_groups ? p.table[(int64_t)b * p.max_pages + (begin + kGroup * (warp + kWarps * i)) / p.page_size] : -1;
+    if (i >= n_groups) return -1;
+    const int pos = begin + kGroup * (warp + kWarps * i), pg = pos / p.page_size;
+    const int page = p.table[(int64_t)b * p.max_pages + pg];
+    if (page < 0 || page >= p.n_pages) {
+      flag_status(p.status, HSA_FLAG_INDEX_RANGE);
+      return -1;
+    }
+    return page * page_pieces + (h * p.page_size + pos - pg * p.page_size) / kGroup;
   };
-  int pages = load_pages(0), pages_next = load_pages(1);
+  int64_t pieces = find_pieces(0), pieces_next = find_pieces(1);
   auto issue = [&](int i, int stage) {                   // called with i = 0, 1, 2, ...
-    const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+    const int64_t piece = __shfl_sync(0xffffffffu, pieces, i & 31);
     if ((i & 31) == 31) {
-      pages = pages_next;
-      pages_next = load_pages((i >> 5) + 2);
+      pieces = pieces_next;
+      pieces_next = find_pieces((i >> 5) + 2);
     }
     if (i < n_groups) {
       const int pos = begin + kGroup * (warp + kWarps * i);
-      const bool ok = page >= 0 && page < p.n_pages;
-      if (!ok && lane == 0) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
-      bad = (bad & ~(1u << stage)) | ((ok ? 0u : 1u) << stage);
-      const int64_t at = ok ? ((int64_t)page * p.heads + h) * head_bytes + (int64_t)(pos % p.page_size) * T::kRow : 0;
+      const uint32_t st = (uint32_t)stage * T::kStage;
+      bad = (bad & ~(1u << stage)) | ((piece < 0 ? 1u : 0u) << stage);
+      const int64_t at = piece < 0 ? 0 : piece * (kGroup * T::kRow) + lane * 16;
       const uint8_t* k = p.k_pool + at;
       const uint8_t* v = p.v_pool + at;
-      const uint32_t dk = ring + (uint32_t)stage * T::kStage, dv = dk + T::kHalf;
+      constexpr int kCopies = kGroup * T::kChunks / 32;
+      if (piece >= 0 && pos >= sp.lo && pos + kGroup <= sp.hi) {
 #pragma unroll
-      for (int u = 0; u < kGroup * T::kChunks / 32; ++u) {
-        const int e = u * 32 + lane, r = e / T::kChunks, c = e % T::kChunks;
+        for (int u = 0; u < kCopies; ++u) {
+          cp_async16(ring + T::k_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, k + u * 512);
+          cp_async16(ring + T::kHalf + T::v_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, v + u * 512);
+        }
+      } else {
         // rows no query sees are not read: they become zeros, whatever the pool holds there
-        const uint32_t n = (ok && pos + r >= sp.lo && pos + r < sp.hi) ? 16u : 0u;
-        cp_async16(dk + T::k_at(r, c), k + (n ? e * 16 : 0), n);
-        cp_async16(dv + T::v_at(r, c), v + (n ? e * 16 : 0), n);
+#pragma unroll
+        for (int u = 0; u < kCopies; ++u) {
+          const int r = (u * 32 + lane) / T::kChunks;
+          const uint32_t n = (piece >= 0 && pos + r >= sp.lo && pos + r < sp.hi) ? 16u : 0u;
+          cp_async16z(ring + T::k_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, k + (n ? u * 512 : 0), n);
+          cp_async16z(ring + T::kHalf + T::v_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, v + (n ? u * 512 : 0), n);
+        }
       }
     }
     cp_async_commit();
@@ -323,10 +342,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       for (int j = 0; j < 2 * RT; ++j) {
         float* x0 = &s[j >> 1][0][2 * (j & 1)];
         float* x1 = &s[j >> 1][1][2 * (j & 1)];
-        x0[0] *= scale[j];
-        x0[1] *= scale[j];
-        x1[0] *= scale[j];
-        x1[1] *= scale[j];
         if (!whole) {
           const int k0 = pos + 2 * t;
           if (k0 < lo[j] || k0 >= hi[j]) x0[0] = -INFINITY;
@@ -334,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           if (k0 + 8 < lo[j] || k0 + 8 >= hi[j]) x1[0] = -INFINITY;
           if (k0 + 9 < lo[j] || k0 + 9 >= hi[j]) x1[1] = -INFINITY;
         }
-        raise |= fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x1[0], x1[1])) > m[j] + kRaise;
+        raise |= fmaf(fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x1[0], x1[1])), scale[j], -m[j]) > kRaise;   // m = -inf: any logit
       }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -344,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           float mx = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x1[0], x1[1]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          mx = fmaxf(mx, m[j]);
+          mx = fmaxf(mx * scale[j], m[j]);
           const float f = (mx == -INFINITY) ? 1.f : ex2_ftz(m[j] - mx);   // m = -inf before: 0, on sums that are 0
           m[j] = mx;
           l[j] *= f;
@@ -361,7 +376,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         const float mu = m[j] == -INFINITY ? 0.f : m[j];
         const float* x0 = &s[j >> 1][0][2 * (j & 1)];
         const float* x1 = &s[j >> 1][1][2 * (j & 1)];
-        const float p0 = ex2_ftz(x0[0] - mu), p1 = ex2_ftz(x0[1] - mu), p2 = ex2_ftz(x1[0] - mu), p3 = ex2_ftz(x1[1] - mu);
+        const float sc = scale[j];
+        const float p0 = ex2_ftz(fmaf(x0[0], sc, -mu)), p1 = ex2_ftz(fmaf(x0[1], sc, -mu)), p2 = ex2_ftz(fmaf(x1[0], sc, -mu)),
+                    p3 = ex2_ftz(fmaf(x1[1], sc, -mu));
         l[j] += (p0 + p1) + (p2 + p3);
         pa[j >> 1][j & 1] = pack2<kB>(p0, p1);
         pa[j >> 1][2 + (j & 1)] = pack2<kB>(p2, p3);
