@@ -3,17 +3,19 @@
 // cache's length and joined.
 //
 // Bound: every key and value is read once and used by nq x group query rows only, so the reads
-// from HBM decide (at 16 rows of 128 dims the products take a fifth of the time of the reads at
-// the warp MMA's rate). Hence
-//  - one CTA per (request, key-value head, 16 or 32 query rows, split of the length); the rows are
+// from HBM decide, and beside them the instructions that a warp spends on a key. Hence
+//  - one CTA per (request, key-value head, up to 32 query rows, split of the length); the rows are
 //    the queries and the heads of the group together, so that grouped heads share every load;
 //  - inside a CTA each of 4 warps streams its own 16-key groups (a group never leaves a page)
 //    through a private ring of cp.async stages: 16 rows of one head lie in one contiguous piece, no
-//    block barrier is ever needed, and two CTAs per SM keep up to 192 KB in flight;
-//  - products by the warp MMA m16n8k16 (a tile of 16 rows would fill an eighth of a tcgen05
-//    instruction). The k index is permuted so that a thread's B fragments of K are the 16-byte
-//    pieces of its row: one shared load feeds two (16-bit) or four (E4M3) k-steps. V goes through
-//    transposed matrix loads, or, in E4M3, byte permutes and converts in registers;
+//    block barrier is ever needed, and two or three CTAs per SM keep up to 192 KB in flight;
+//  - products by the warp MMA m16n8k16, transposed: S^T = K Q^T and O^T += V^T P^T, so that keys and
+//    dims fill the 16-row side and queries the 8-column side. Most calls have 8 rows or fewer; with
+//    the queries on the 16-row side half of every product, exponential and accumulator would be
+//    padding. (A tcgen05 instruction takes 128 rows.) The k index is permuted so that a thread's
+//    fragments of K are the 16-byte pieces of its rows: one shared load feeds two (16-bit) or four
+//    (E4M3) k-steps. V goes through transposed matrix loads, or, in E4M3, byte permutes and converts
+//    in registers; P^T comes from S^T's accumulators by movmatrix;
 //  - softmax in one pass with the running maximum and sum in fp32. The maximum is only raised, and
 //    the outputs rescaled, when some logit passes it by 2^8: the weights then stay below 256, which
 //    16-bit weights and fp32 sums hold, and most groups need one vote instead of shuffles;
@@ -62,6 +64,12 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
+// the 8 x 8 transpose of 16-bit values held two per lane
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (BF16) {
@@ -107,15 +115,20 @@ __device__ __forceinline__ Span request_span(const PagedAttnParams& p, int b) {
   return s;
 }
 
-template <int D, int KV>
+template <int D, int KV, int NT>
 struct Tile {
   static constexpr int kElem = KV == kE4M3 ? 1 : 2;
   static constexpr int kRow = D * kElem;                 // bytes of a key's row
   static constexpr int kChunks = kRow / 16;
   static constexpr int kHalf = kGroup * kRow;            // K, then V
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = kStage >= 8192 ? 3 : 6;
+  // CTAs per SM, as registers and shared memory (their rings, 227 KB) allow
+  static constexpr int kCtas = NT <= 2 ? 3 : 2;
+  static constexpr int kRingMax = kCtas == 3 ? 16384 : 24576;
+  static constexpr int kStages = kRingMax / kStage > 6 ? 6 : kRingMax / kStage;
   static constexpr int kRing = kStage * kStages;
+  static constexpr int kOutLd = D + 4;                   // floats from row to row when the warps merge (bank spread)
+  static_assert(8 * NT * kOutLd * 4 <= kRing, "a warp's outputs fit its ring");
   // 16-byte piece c of row r. K: pieces 4i..4i+3 of two neighbouring rows are read together; V: one
   // piece of 8 rows (matrix loads), or two pieces of rows 0, 2, 4, 6 (E4M3)
   static __device__ __forceinline__ uint32_t k_at(int r, int c) {
@@ -126,15 +139,15 @@ struct Tile {
   }
 };
 
-template <int D, int KV, int RT>
-__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
-  using T = Tile<D, KV>;
+// NT: tiles of 8 query rows
+template <int D, int KV, int NT>
+__global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+  using T = Tile<D, KV, NT>;
   constexpr bool kB = KV == kBf16;                       // products in bf16, else in f16
-  constexpr int kSteps = D / 16, kNt = D / 8;
-  constexpr int kOutRows = 16 * RT;
-  static_assert(kOutRows * D * 4 <= T::kRing, "a warp's outputs fit its ring");
+  constexpr int kSteps = D / 16, kMt = D / 16, kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ float s_m[kWarps][kOutRows], s_l[kWarps][kOutRows];
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_scale[kRows];
+  __shared__ int s_lo[kRows], s_hi[kRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
 
   griddep_wait();
@@ -149,29 +162,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   const Span sp = request_span(p, b);
   if (split >= sp.used) return;
   const int begin = sp.base + split * sp.len, end = min(begin + sp.len, sp.hi);   // keys of this CTA
-  const int rows = p.nq * p.group, row0 = chunk * kOutRows;
-
-  // this lane's rows (C layout: g and g + 8 of each 16-row tile): query, limits
-  int lo[2 * RT], hi[2 * RT];
-  int all_lo = 0, all_hi = 0x7fffffff;                   // inside [all_lo, all_hi) no row masks anything
-#pragma unroll
-  for (int j = 0; j < 2 * RT; ++j) {
-    const int r = row0 + 8 * j + g;
-    lo[j] = hi[j] = 0;
-    if (r < rows) {
-      const int raw = p.vis[(int64_t)b * p.nq + r / p.group];
-      hi[j] = clamp_vis(p, raw);
-      if (raw != hi[j] && split == 0 && h == 0) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
-      lo[j] = p.window > 0 ? max(hi[j] - p.window, 0) : 0;
-      all_lo = max(all_lo, lo[j]);
-      all_hi = min(all_hi, hi[j]);
-    }
-  }
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) {
-    all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
-    all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
-  }
+  const int rows = p.nq * p.group, row0 = chunk * p.chunk_rows, row_end = min(row0 + p.chunk_rows, rows);
 
   // ---------------------------------------------------------------- the ring: 16-key groups of this warp
   const uint32_t ring = smem_u32(sm) + (uint32_t)warp * T::kRing;
@@ -228,17 +219,39 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 #pragma unroll
   for (int s = 0; s < T::kStages - 1; ++s) issue(s, s);
 
-  // ---------------------------------------------------------------- queries into A fragments
-  // k-step ks covers, of thread t, the 4 consecutive elements q_elem(ks): the same elements that
-  // its piece of a key's row brings to that step
-  uint32_t qa[RT][kSteps][4];
-  float scale[2 * RT];
+  // ---------------------------------------------------------------- each row's keys, for masked groups
+  int all_lo = 0, all_hi = 0x7fffffff;                   // inside [all_lo, all_hi) no row masks anything
+  if (lane < kRows) {
+    const int r = row0 + lane;
+    int lo = 0, hi = 0;
+    if (r < row_end) {
+      const int raw = p.vis[(int64_t)b * p.nq + r / p.group];
+      hi = clamp_vis(p, raw);
+      if (raw != hi && split == 0 && h == 0) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
+      lo = p.window > 0 ? max(hi - p.window, 0) : 0;
+      all_lo = lo;
+      all_hi = hi;
+    }
+    if (warp == 0) {
+      s_lo[lane] = lo;
+      s_hi[lane] = hi;
+    }
+  }
+  all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+  all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+
+  // ---------------------------------------------------------------- queries into B fragments
+  // k-step ks covers, of thread t, the 4 consecutive elements that its piece of a key's row brings
+  // to that step
+  uint32_t qb[NT][kSteps][2];
+  constexpr int kScales = KV == kE4M3 ? 2 * NT : 1;
+  float scale[kScales];                                  // of rows 2t, 2t + 1 of each tile (or of all rows)
   {
     constexpr int kPer = 16 / T::kElem;                  // elements of a 16-byte piece
 #pragma unroll
-    for (int j = 0; j < 2 * RT; ++j) {
-      const int r = row0 + 8 * j + g;
-      const bool real = r < rows;
+    for (int n = 0; n < NT; ++n) {
+      const int r = row0 + 8 * n + g;
+      const bool real = r < row_end;
       const int qi = real ? r / p.group : 0, hq = h * p.group + (real ? r % p.group : 0);
       const uint16_t* q = p.q + (((int64_t)b * p.nq + qi) * p.heads_q + hq) * D;
       uint2 x[kSteps];
@@ -247,51 +260,61 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         const int piece = 4 * (ks / (kPer / 4)) + t;
         x[ks] = real ? *reinterpret_cast<const uint2*>(q + piece * kPer + 4 * (ks % (kPer / 4))) : make_uint2(0u, 0u);
       }
-      scale[j] = p.scale_log2;
-      if (KV == kE4M3 && p.q_bf16) {
-        // bf16 queries against f16 keys: to f16 after a power-of-two shift of the row, taken back in its scale
-        float amax = 0.f;
+      if constexpr (KV == kE4M3) {
+        float sc = p.scale_log2;
+        if (p.q_bf16) {
+          // bf16 queries against f16 keys: to f16 after a power-of-two shift of the row, taken back in its scale
+          float amax = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) {
-          const uint32_t w[2] = {x[ks].x, x[ks].y};
+          for (int ks = 0; ks < kSteps; ++ks) {
+            const uint32_t w[2] = {x[ks].x, x[ks].y};
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[u] << 16)), fabsf(__uint_as_float(w[u] & 0xFFFF0000u))));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        int sh = 0;
-        if (amax > 0.f && amax < INFINITY) {
-          int e;
-          frexpf(amax, &e);
-          sh = max(-120, min(120, 12 - e));              // amax 2^sh in [2^11, 2^12): products and their sums stay in fp32
-        }
-        const float mul = __uint_as_float((uint32_t)(127 + sh) << 23);
-        scale[j] *= __uint_as_float((uint32_t)(127 - sh) << 23);
+            for (int u = 0; u < 2; ++u)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[u] << 16)), fabsf(__uint_as_float(w[u] & 0xFFFF0000u))));
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          int sh = 0;
+          if (amax > 0.f && amax < INFINITY) {
+            int e;
+            frexpf(amax, &e);
+            sh = max(-120, min(120, 12 - e));            // amax 2^sh in [2^11, 2^12): products and their sums stay in fp32
+          }
+          const float mul = __uint_as_float((uint32_t)(127 + sh) << 23);
+          sc *= __uint_as_float((uint32_t)(127 - sh) << 23);
 #pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) {
-          x[ks].x = pack2<false>(__uint_as_float(x[ks].x << 16) * mul, __uint_as_float(x[ks].x & 0xFFFF0000u) * mul);
-          x[ks].y = pack2<false>(__uint_as_float(x[ks].y << 16) * mul, __uint_as_float(x[ks].y & 0xFFFF0000u) * mul);
+          for (int ks = 0; ks < kSteps; ++ks) {
+            x[ks].x = pack2<false>(__uint_as_float(x[ks].x << 16) * mul, __uint_as_float(x[ks].x & 0xFFFF0000u) * mul);
+            x[ks].y = pack2<false>(__uint_as_float(x[ks].y << 16) * mul, __uint_as_float(x[ks].y & 0xFFFF0000u) * mul);
+          }
         }
+        if (warp == 0 && t == 0) s_scale[8 * n + g] = sc;
       }
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) {              // a0, a2: row g; a1, a3: row g + 8
-        qa[j >> 1][ks][j & 1] = x[ks].x;
-        qa[j >> 1][ks][2 + (j & 1)] = x[ks].y;
+      for (int ks = 0; ks < kSteps; ++ks) {
+        qb[n][ks][0] = x[ks].x;
+        qb[n][ks][1] = x[ks].y;
       }
     }
   }
+  __syncthreads();                                       // s_lo, s_hi, s_scale
+  if constexpr (KV == kE4M3) {
+#pragma unroll
+    for (int j = 0; j < kScales; ++j) scale[j] = s_scale[8 * (j >> 1) + 2 * t + (j & 1)];
+  } else {
+    scale[0] = p.scale_log2;
+  }
 
-  float o[RT][kNt][4];
-  float m[2 * RT], l[2 * RT];
+  // rows 8 n + 2 t + e of this lane: j = 2 n + e
+  float o[kMt][NT][4], m[2 * NT], l[2 * NT];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
+  for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-    for (int n = 0; n < kNt; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[rt][n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
 #pragma unroll
-  for (int j = 0; j < 2 * RT; ++j) {
+  for (int j = 0; j < 2 * NT; ++j) {
     m[j] = -INFINITY;
     l[j] = 0.f;
   }
@@ -306,87 +329,85 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     // the stage freed by the last iteration takes the group kStages - 1 ahead
     issue(i + T::kStages - 1, stage == 0 ? T::kStages - 1 : stage - 1);
     if (!skip) {
-      // ------------------------------------------------------------ S = Q K^T
-      float s[RT][2][4];
+      // ------------------------------------------------------------ S^T = K Q^T: keys g, g + 8, rows 2t, 2t + 1
+      float s[NT][4];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[rt][n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
       for (int c4 = 0; c4 < T::kChunks / 4; ++c4) {
+        const uint4 k0 = lds128(sk + T::k_at(g, 4 * c4 + t)), k1 = lds128(sk + T::k_at(8 + g, 4 * c4 + t));
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+        if constexpr (KV == kE4M3) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const uint4 kw = lds128(sk + T::k_at(8 * n + g, 4 * c4 + t));
-          const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
-          if constexpr (KV == kE4M3) {
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)(w0[u] & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(w1[u] & 0xFFFFu)),
+                                   e4m3x2_to_f16x2((uint16_t)(w0[u] >> 16)), e4m3x2_to_f16x2((uint16_t)(w1[u] >> 16))};
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint32_t b0 = e4m3x2_to_f16x2((uint16_t)(w[u] & 0xFFFFu)), b1 = e4m3x2_to_f16x2((uint16_t)(w[u] >> 16));
+            for (int n = 0; n < NT; ++n) mma16816<kB>(s[n], a, qb[n][4 * c4 + u][0], qb[n][4 * c4 + u][1]);
+          }
+        } else {
 #pragma unroll
-              for (int rt = 0; rt < RT; ++rt) mma16816<kB>(s[rt][n], qa[rt][4 * c4 + u], b0, b1);
-            }
-          } else {
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t a[4] = {w0[2 * u], w1[2 * u], w0[2 * u + 1], w1[2 * u + 1]};
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt) mma16816<kB>(s[rt][n], qa[rt][2 * c4 + u], w[2 * u], w[2 * u + 1]);
+            for (int n = 0; n < NT; ++n) mma16816<kB>(s[n], a, qb[n][2 * c4 + u][0], qb[n][2 * c4 + u][1]);
           }
         }
       }
       // ------------------------------------------------------------ softmax, one pass
-      const bool whole = pos >= all_lo && pos + kGroup <= all_hi;
+      if (pos < all_lo || pos + kGroup > all_hi) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = 8 * n + 2 * t + (e & 1), key = pos + g + 8 * (e >> 1);
+            if (key < s_lo[r] || key >= s_hi[r]) s[n][e] = -INFINITY;
+          }
+      }
       bool raise = false;
 #pragma unroll
-      for (int j = 0; j < 2 * RT; ++j) {
-        float* x0 = &s[j >> 1][0][2 * (j & 1)];
-        float* x1 = &s[j >> 1][1][2 * (j & 1)];
-        if (!whole) {
-          const int k0 = pos + 2 * t;
-          if (k0 < lo[j] || k0 >= hi[j]) x0[0] = -INFINITY;
-          if (k0 + 1 < lo[j] || k0 + 1 >= hi[j]) x0[1] = -INFINITY;
-          if (k0 + 8 < lo[j] || k0 + 8 >= hi[j]) x1[0] = -INFINITY;
-          if (k0 + 9 < lo[j] || k0 + 9 >= hi[j]) x1[1] = -INFINITY;
-        }
-        raise |= fmaf(fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x1[0], x1[1])), scale[j], -m[j]) > kRaise;   // m = -inf: any logit
-      }
+      for (int j = 0; j < 2 * NT; ++j)                   // m = -inf: any logit raises it
+        raise |= fmaf(fmaxf(s[j >> 1][j & 1], s[j >> 1][2 + (j & 1)]), scale[j % kScales], -m[j]) > kRaise;
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int j = 0; j < 2 * RT; ++j) {
-          const float* x0 = &s[j >> 1][0][2 * (j & 1)];
-          const float* x1 = &s[j >> 1][1][2 * (j & 1)];
-          float mx = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x1[0], x1[1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          mx = fmaxf(mx * scale[j], m[j]);
+        for (int j = 0; j < 2 * NT; ++j) {
+          float mx = fmaxf(s[j >> 1][j & 1], s[j >> 1][2 + (j & 1)]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          mx = fmaxf(mx * scale[j % kScales], m[j]);
           const float f = (mx == -INFINITY) ? 1.f : ex2_ftz(m[j] - mx);   // m = -inf before: 0, on sums that are 0
           m[j] = mx;
           l[j] *= f;
 #pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            o[j >> 1][n][2 * (j & 1)] *= f;
-            o[j >> 1][n][2 * (j & 1) + 1] *= f;
+          for (int mt = 0; mt < kMt; ++mt) {
+            o[mt][j >> 1][j & 1] *= f;
+            o[mt][j >> 1][2 + (j & 1)] *= f;
           }
         }
       }
-      uint32_t pa[RT][4];
+      uint32_t pb[NT][2];                                // P^T: keys 2t, 2t + 1 and 2t + 8, 2t + 9 of row g
 #pragma unroll
-      for (int j = 0; j < 2 * RT; ++j) {
-        const float mu = m[j] == -INFINITY ? 0.f : m[j];
-        const float* x0 = &s[j >> 1][0][2 * (j & 1)];
-        const float* x1 = &s[j >> 1][1][2 * (j & 1)];
-        const float sc = scale[j];
-        const float p0 = ex2_ftz(fmaf(x0[0], sc, -mu)), p1 = ex2_ftz(fmaf(x0[1], sc, -mu)), p2 = ex2_ftz(fmaf(x1[0], sc, -mu)),
-                    p3 = ex2_ftz(fmaf(x1[1], sc, -mu));
-        l[j] += (p0 + p1) + (p2 + p3);
-        pa[j >> 1][j & 1] = pack2<kB>(p0, p1);
-        pa[j >> 1][2 + (j & 1)] = pack2<kB>(p2, p3);
+      for (int n = 0; n < NT; ++n) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = 2 * n + e;
+          const float mu = m[j] == -INFINITY ? 0.f : m[j], sc = scale[j % kScales];
+          w[e] = ex2_ftz(fmaf(s[n][e], sc, -mu));
+          w[2 + e] = ex2_ftz(fmaf(s[n][2 + e], sc, -mu));
+          l[j] += w[e] + w[2 + e];
+        }
+        pb[n][0] = movmatrix_trans(pack2<kB>(w[0], w[1]));
+        pb[n][1] = movmatrix_trans(pack2<kB>(w[2], w[3]));
       }
-      // ------------------------------------------------------------ O += P V
+      // ------------------------------------------------------------ O^T += V^T P^T
       if constexpr (KV == kE4M3) {
-        // thread column g is dims kNt g .. kNt g + kNt - 1, one per n-tile: rows 2t, 2t+1, 2t+8, 2t+9
-        uint32_t w[4][kNt / 4];
+        // thread row g of tile mt is dim kPd g + 2 mt, row g + 8 the next one: rows 2t, 2t+1, 2t+8, 2t+9 of V
+        constexpr int kPd = D / 8;
+        uint32_t w[4][kPd / 4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int r = 2 * t + (u & 1) + 8 * (u >> 1);
@@ -403,28 +424,26 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           }
         }
 #pragma unroll
-        for (int n4 = 0; n4 < kNt / 4; ++n4) {
+        for (int n4 = 0; n4 < kPd / 4; ++n4) {
           const uint32_t a01 = __byte_perm(w[0][n4], w[1][n4], 0x5140), a23 = __byte_perm(w[0][n4], w[1][n4], 0x7362);
           const uint32_t c01 = __byte_perm(w[2][n4], w[3][n4], 0x5140), c23 = __byte_perm(w[2][n4], w[3][n4], 0x7362);
-          const uint32_t b0[4] = {e4m3x2_to_f16x2((uint16_t)(a01 & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(a01 >> 16)),
-                                  e4m3x2_to_f16x2((uint16_t)(a23 & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(a23 >> 16))};
-          const uint32_t b1[4] = {e4m3x2_to_f16x2((uint16_t)(c01 & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(c01 >> 16)),
-                                  e4m3x2_to_f16x2((uint16_t)(c23 & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(c23 >> 16))};
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t x = u ? a23 : a01, y = u ? c23 : c01;
+            const uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)(x & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(x >> 16)),
+                                   e4m3x2_to_f16x2((uint16_t)(y & 0xFFFFu)), e4m3x2_to_f16x2((uint16_t)(y >> 16))};
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) mma16816<kB>(o[rt][4 * n4 + u], pa[rt], b0[u], b1[u]);
+            for (int n = 0; n < NT; ++n) mma16816<kB>(o[2 * n4 + u][n], a, pb[n][0], pb[n][1]);
+          }
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < T::kChunks; c += 2) {
+        for (int mt = 0; mt < kMt; ++mt) {
           uint32_t r4[4];
-          ldmatrix_x4_trans(sv + T::v_at(lane & 15, c + (lane >> 4)), r4);
+          ldmatrix_x4_trans(sv + T::v_at(lane & 15, 2 * mt + (lane >> 4)), r4);
+          const uint32_t a[4] = {r4[0], r4[2], r4[1], r4[3]};
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            mma16816<kB>(o[rt][c], pa[rt], r4[0], r4[1]);
-            mma16816<kB>(o[rt][c + 1], pa[rt], r4[2], r4[3]);
-          }
+          for (int n = 0; n < NT; ++n) mma16816<kB>(o[mt][n], a, pb[n][0], pb[n][1]);
         }
       }
     }
@@ -435,40 +454,29 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   // ---------------------------------------------------------------- merge the warps
   cp_async_wait<0>();
   __syncwarp();
-  float* so = reinterpret_cast<float*>(sm + (size_t)warp * T::kRing);   // [row][D]
+  float* so = reinterpret_cast<float*>(sm + (size_t)warp * T::kRing);   // [row][kOutLd]
 #pragma unroll
-  for (int j = 0; j < 2 * RT; ++j) {
-    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
-    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
-    const int r = 8 * j + g;
-    if (t == 0) {
+  for (int j = 0; j < 2 * NT; ++j) {
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 4);
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
+    const int r = 8 * (j >> 1) + 2 * t + (j & 1);
+    if (g == 0) {
       s_m[warp][r] = m[j];
       s_l[warp][r] = l[j];
     }
-    // columns 2t, 2t + 1 of n-tile n: dims 8n + 2t, + 1, or with E4M3's split columns kNt (2t) + n and kNt (2t + 1) + n
-    if constexpr (KV == kE4M3) {
 #pragma unroll
-      for (int n = 0; n < kNt; n += 4) {
+    for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int q2 = 2 * (j & 1) + e;
-          *reinterpret_cast<float4*>(so + r * D + kNt * (2 * t + e) + n) =
-              make_float4(o[j >> 1][n][q2], o[j >> 1][n + 1][q2], o[j >> 1][n + 2][q2], o[j >> 1][n + 3][q2]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int n = 0; n < kNt; ++n)
-        *reinterpret_cast<float2*>(so + r * D + 8 * n + 2 * t) =
-            make_float2(o[j >> 1][n][2 * (j & 1)], o[j >> 1][n][2 * (j & 1) + 1]);
-    }
+      for (int u = 0; u < 2; ++u)
+        so[r * T::kOutLd + (KV == kE4M3 ? D / 8 * g + 2 * mt + u : 16 * mt + g + 8 * u)] = o[mt][j >> 1][2 * u + (j & 1)];
   }
   __syncthreads();
   constexpr int kQuads = D / 4;
   const bool last = sp.used == 1;
-  for (int e = tid; e < kOutRows * kQuads; e += kThreads) {
+  for (int e = tid; e < kRows * kQuads; e += kThreads) {
     const int r = e / kQuads, d4 = e % kQuads, row = row0 + r;
-    if (row >= rows) break;
+    if (row >= row_end) break;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
@@ -477,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float f = s_m[w][r] == -INFINITY ? 0.f : ex2_ftz(s_m[w][r] - M);
-      const float4 x = *reinterpret_cast<const float4*>(sm + (size_t)w * T::kRing + ((size_t)r * D + 4 * d4) * 4);
+      const float4 x = *reinterpret_cast<const float4*>(sm + (size_t)w * T::kRing + ((size_t)r * T::kOutLd + 4 * d4) * 4);
       if (s_m[w][r] != -INFINITY || s_l[w][r] != 0.f) {  // a warp that saw no key adds nothing
         a.x += f * x.x;
         a.y += f * x.y;
@@ -565,38 +573,43 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   if (p.lse && lane == 0) p.lse[at] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
-template <int D, int KV, int RT>
+template <int D, int KV, int NT>
 cudaError_t launch(const PagedAttnParams& p, cudaStream_t s) {
-  auto kernel = paged_attn_kernel<D, KV, RT>;
-  constexpr size_t smem = (size_t)kWarps * Tile<D, KV>::kRing;
+  auto kernel = paged_attn_kernel<D, KV, NT>;
+  constexpr size_t smem = (size_t)kWarps * Tile<D, KV, NT>::kRing;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   const unsigned blocks = (unsigned)p.n_splits * p.batch * p.heads * p.chunks;
   return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, s, p);
 }
 template <int D, int KV>
-cudaError_t launch_rt(const PagedAttnParams& p, cudaStream_t s) {
-  return p.chunk_rows == 16 ? launch<D, KV, 1>(p, s) : launch<D, KV, 2>(p, s);
+cudaError_t launch_nt(const PagedAttnParams& p, cudaStream_t s) {
+  switch ((p.chunk_rows + 7) / 8) {
+    case 1: return launch<D, KV, 1>(p, s);
+    case 2: return launch<D, KV, 2>(p, s);
+    case 3: return launch<D, KV, 3>(p, s);
+    default: return launch<D, KV, 4>(p, s);
+  }
 }
 template <int D>
 cudaError_t launch_kv(const PagedAttnParams& p, int kv, cudaStream_t s) {
   switch (kv) {
-    case kBf16: return launch_rt<D, kBf16>(p, s);
-    case kF16: return launch_rt<D, kF16>(p, s);
-    default: return launch_rt<D, kE4M3>(p, s);
+    case kBf16: return launch_nt<D, kBf16>(p, s);
+    case kF16: return launch_nt<D, kF16>(p, s);
+    default: return launch_nt<D, kE4M3>(p, s);
   }
 }
 
 }  // namespace
 
-// Query rows per CTA and splits of the length. Up to 16 rows one MMA tile, above that two (a CTA of
-// 32 rows reads its keys once for both); more rows take more CTAs, whose keys then come from L2.
+// Query rows per CTA and splits of the length. Up to 32 rows one CTA reads its keys once for all of
+// them; more rows are dealt out evenly (35: 18 and 17), and the later CTAs' keys come from L2.
 // The splits fill the GPU about four times over (2 CTAs per SM on 152 SMs), so that ragged lengths
 // even out, but no split is shorter than 256 keys: 4 groups for each warp, about what the ring holds.
 PagedSplit paged_split(int32_t batch, int32_t heads, int32_t rows, int64_t max_vis, int32_t window, int32_t nq) {
   PagedSplit s;
-  s.chunk_rows = rows <= 16 ? 16 : 32;
-  s.chunks = (rows + s.chunk_rows - 1) / s.chunk_rows;
+  s.chunks = (rows + 31) / 32;
+  s.chunk_rows = (rows + s.chunks - 1) / s.chunks;
   int64_t span = max_vis;
   if (window > 0 && (int64_t)window + nq + 15 < span) span = (int64_t)window + nq + 15;   // vis one apart, as in a draft
   const int64_t ctas = (int64_t)batch * heads * s.chunks;
