@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhsa.so")
 SOURCES = ["api.cu", "index.cu", "reindex.cu", "attn.cu", "write.cu", "noalloc.cu", "paged_write.cu", "paged_attn.cu",
-           "prompt_attn.cu"]
+           "paged_rows.cu", "prompt_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

@@ -484,9 +484,9 @@ static hsa_status check_paged_query(const hsa_paged_cache* c, int32_t heads_q, i
 struct PagedWs {
   size_t off_o, off_ml, total;
 };
-static PagedWs paged_ws(const hsa_paged_cache* c, int32_t rows, int32_t n_splits) {
+static PagedWs paged_ws(const hsa_paged_cache* c, int32_t rows, const PagedSplit& sp) {
   PagedWs w;
-  const size_t parts = n_splits > 1 ? (size_t)c->batch * c->heads * n_splits * rows : 0;
+  const size_t parts = sp.joined ? (size_t)c->batch * c->heads * sp.n_splits * sp.streams * rows : 0;
   w.off_o = 0;
   w.off_ml = parts * c->head_dim * 4;
   w.total = (w.off_ml + parts * 8 + 255) / 256 * 256 + 256;
@@ -540,8 +540,8 @@ hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const void* k, co
 
 size_t hsa_paged_attn_workspace_bytes(const hsa_paged_cache* cache, int32_t heads_q, int32_t nq, int64_t max_vis) {
   if (check_paged_sizes(cache) != HSA_OK || check_paged_query(cache, heads_q, nq, max_vis) != HSA_OK) return 0;
-  const int32_t rows = nq * (heads_q / cache->heads);
-  return paged_ws(cache, rows, paged_split(cache->batch, cache->heads, rows, max_vis, 0, nq).n_splits).total;
+  const int32_t group = heads_q / cache->heads;
+  return paged_ws(cache, nq * group, paged_split(cache->batch, cache->heads, group, nq, max_vis, 0, cache->dtype)).total;
 }
 
 hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, int32_t q_dtype, int32_t heads_q,
@@ -556,9 +556,9 @@ hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, in
   if (window < 0 || !(sm_scale > 0.f) || !isfinite(sm_scale)) return HSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return HSA_ERR_ALIGN;
   const int32_t group = heads_q / cache->heads, rows = nq * group;
-  const PagedSplit sp = paged_split(cache->batch, cache->heads, rows, max_vis, window, nq);
+  const PagedSplit sp = paged_split(cache->batch, cache->heads, group, nq, max_vis, window, cache->dtype);
   if ((int64_t)sp.n_splits * sp.chunks * cache->heads * cache->batch > (int64_t)INT32_MAX) return HSA_ERR_SHAPE;
-  const PagedWs L = paged_ws(cache, rows, sp.n_splits);
+  const PagedWs L = paged_ws(cache, rows, sp);
   if (!ws || ws_bytes < L.total) return HSA_ERR_WORKSPACE;
   if (!aligned16(ws)) return HSA_ERR_ALIGN;
   uint32_t* status;
@@ -588,12 +588,14 @@ hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, in
   p.chunks = sp.chunks;
   p.n_splits = sp.n_splits;
   p.split_len = sp.split_len;
+  p.streams = sp.streams;
+  p.align = sp.align;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.off_o);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.off_ml);
   p.status = status;
-  return cuda_fail(launch_paged_attn(p, cache->head_dim, cache->dtype, (cudaStream_t)stream), "paged attention launch");
+  return cuda_fail(launch_paged_attn(p, sp, cache->head_dim, cache->dtype, wait_limit_ns(), (cudaStream_t)stream), "paged attention launch");
 }
 
 hsa_status hsa_prompt_attn(const hsa_prompt_args* a, hsa_stream_t stream) {

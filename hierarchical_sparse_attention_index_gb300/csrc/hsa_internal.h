@@ -175,14 +175,19 @@ struct PagedWriteParams {
 };
 cudaError_t launch_paged_write(const PagedWriteParams& p, bool e4m3, cudaStream_t s);
 
-// How hsa_paged_attn_decode cuts its work (host only; the workspace holds n_splits partials per row)
+// How hsa_paged_attn_decode cuts its work (host only; the workspace holds n_splits x streams partials
+// per row where a join follows)
 struct PagedSplit {
+  bool tc;                // paged_rows_kernel (tcgen05), else paged_attn_kernel
   int32_t chunk_rows;     // query rows (queries x heads of a group) per CTA
   int32_t chunks;         // CTAs that share a key-value head's rows
   int32_t n_splits;       // CTAs along the cache's length
   int32_t split_len;      // keys per split, at least
+  int32_t streams;        // partials that a CTA leaves
+  int32_t align;          // splits start at multiples of this
+  bool joined;            // paged_join_kernel follows
 };
-PagedSplit paged_split(int32_t batch, int32_t heads, int32_t rows, int64_t max_vis, int32_t window, int32_t nq);
+PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype);
 
 struct PagedAttnParams {
   int32_t batch, heads, page_size;
@@ -197,14 +202,22 @@ struct PagedAttnParams {
   int64_t max_vis;
   float scale_log2;       // sm_scale * k_scale * log2 e
   float v_scale;
-  int32_t chunk_rows, chunks, n_splits, split_len;
+  int32_t chunk_rows, chunks, n_splits, split_len, streams, align;   // PagedSplit
   uint16_t* out;
   float* lse;             // or NULL
-  float* part_o;          // workspace [B][heads][n_splits][rows][D], unnormalised
-  float* part_ml;         // workspace [B][heads][n_splits][rows] (maximum in log2 units, sum)
+  float* part_o;          // workspace [B][heads][n_splits][streams][rows][D], unnormalised
+  float* part_ml;         // workspace [B][heads][n_splits][streams][rows] (maximum in log2 units, sum)
   uint32_t* status;
 };
-cudaError_t launch_paged_attn(const PagedAttnParams& p, int32_t head_dim, int32_t kv_dtype, cudaStream_t s);
+cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedSplit& sp, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns,
+                              cudaStream_t s);
+cudaError_t launch_paged_rows(const PagedAttnParams& p, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns, cudaStream_t s);
+
+// The driver's tensor-map encoder, looked up once through the runtime (no libcuda link); NULL: none.
+using TensorMapEncoder = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                      const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                      CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+TensorMapEncoder tensor_map_encoder();
 
 // ------------------------------------------------------------------ causal attention over packed prompts
 cudaError_t launch_prompt_attn(const hsa_prompt_args& a, uint32_t* status, uint64_t wait_ns, cudaStream_t s);

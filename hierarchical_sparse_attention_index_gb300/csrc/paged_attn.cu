@@ -23,8 +23,7 @@
 //    bf16, 2^-12 in f16, independent from key to key); the sum l takes them unrounded.
 // The four warps' (m, l, O) are merged in shared memory; with one split the CTA writes the result,
 // else the partial goes to the workspace and paged_join_kernel joins the splits in their order.
-#include "hsa_common.cuh"
-#include "hsa_internal.h"
+#include "hsa_paged.cuh"
 
 namespace hsa {
 namespace {
@@ -89,30 +88,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-
-// The positions some query of request b sees, [lo, hi), and each split's share of them
-struct Span {
-  int lo, hi, base, len, used;           // split s: [base + s len, base + (s + 1) len) cut to hi; `used` of them hold any
-};
-__device__ __forceinline__ int clamp_vis(const PagedAttnParams& p, int v) {
-  return min(max(v, 0), (int)p.max_vis);
-}
-__device__ __forceinline__ Span request_span(const PagedAttnParams& p, int b) {
-  Span s;
-  s.lo = 0x7fffffff;
-  s.hi = 0;
-  for (int i = 0; i < p.nq; ++i) {
-    const int v = clamp_vis(p, p.vis[(int64_t)b * p.nq + i]);
-    s.hi = max(s.hi, v);
-    if (v > 0) s.lo = min(s.lo, p.window > 0 ? max(v - p.window, 0) : 0);
-  }
-  if (s.hi == 0) s.lo = 0;
-  s.base = s.lo & ~(kGroup - 1);
-  const int need = (s.hi - s.base + p.n_splits - 1) / p.n_splits;
-  s.len = max(p.split_len, (need + 63) & ~63);
-  s.used = max(1, (s.hi - s.base + s.len - 1) / s.len);
-  return s;
 }
 
 template <int D, int KV, int NT>
@@ -526,18 +501,19 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int64_t bh = id / rows;
   const int b = (int)(bh / p.heads), h = (int)(bh % p.heads);
   const Span sp = request_span(p, b);
-  if (sp.used == 1) return;              // written by its only split
+  const int parts = sp.used * p.streams;
+  if (parts == 1) return;                // written by its only split
   constexpr int V = D / 32;
-  const int64_t first = bh * p.n_splits * rows + row;
+  const int64_t first = bh * p.n_splits * p.streams * rows + row;
   float M = -INFINITY;
-  for (int c = lane; c < sp.used; c += 32) M = fmaxf(M, __ldcg(p.part_ml + 2 * (first + (int64_t)c * rows)));
+  for (int c = lane; c < parts; c += 32) M = fmaxf(M, __ldcg(p.part_ml + 2 * (first + (int64_t)c * rows)));
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float a[V], L = 0.f;
 #pragma unroll
   for (int e = 0; e < V; ++e) a[e] = 0.f;
 #pragma unroll 4
-  for (int c = 0; c < sp.used; ++c) {
+  for (int c = 0; c < parts; ++c) {
     const int64_t at = first + (int64_t)c * rows;
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at));
     float x[V];
@@ -602,27 +578,46 @@ cudaError_t launch_kv(const PagedAttnParams& p, int kv, cudaStream_t s) {
 
 }  // namespace
 
-// Query rows per CTA and splits of the length. Up to 32 rows one CTA reads its keys once for all of
-// them; more rows are dealt out evenly (35: 18 and 17), and the later CTAs' keys come from L2.
-// The splits fill the GPU about four times over (2 CTAs per SM on 152 SMs), so that ragged lengths
-// even out, but no split is shorter than 256 keys: 4 groups for each warp, about what the ring holds.
-PagedSplit paged_split(int32_t batch, int32_t heads, int32_t rows, int64_t max_vis, int32_t window, int32_t nq) {
+// Which kernel, query rows per CTA and splits of the length.
+// 16-bit pages and more than kTcRows query rows take the tcgen05 kernel: 128 rows (whole queries) to a CTA,
+// about four jobs per SM, so that ragged lengths even out, and no split shorter than 512 keys (a
+// stream then has four tiles). Measured at 64 requests, 4 heads, up to 4,097 keys of 128 dims, f16, ragged:
+// MEASURED.
+// Else up to 32 rows one CTA reads its keys once for all of them; more rows are dealt out evenly
+// (35: 18 and 17), and the later CTAs' keys come from L2. The splits fill the GPU about four times
+// over (2 CTAs per SM on 152 SMs), but no split is shorter than 256 keys: 4 groups for each warp,
+// about what the ring holds.
+PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype) {
+  constexpr int32_t kTcRows = 16;
   PagedSplit s;
-  s.chunks = (rows + 31) / 32;
-  s.chunk_rows = (rows + s.chunks - 1) / s.chunks;
+  const int32_t rows = nq * group;
+  s.tc = kv_dtype != HSA_E4M3 && rows > kTcRows;
+  if (s.tc) {
+    const int32_t queries = 128 / group;
+    s.chunks = (nq + queries - 1) / queries;
+    s.chunk_rows = queries * group;
+  } else {
+    s.chunks = (rows + 31) / 32;
+    s.chunk_rows = (rows + s.chunks - 1) / s.chunks;
+  }
+  s.align = s.tc ? 64 : 16;
   int64_t span = max_vis;
-  if (window > 0 && (int64_t)window + nq + 15 < span) span = (int64_t)window + nq + 15;   // vis one apart, as in a draft
-  const int64_t ctas = (int64_t)batch * heads * s.chunks;
-  int64_t n = (4 * 304 + ctas - 1) / ctas;
-  n = imax64(1, imin64(n, (span + 255) / 256));
+  if (window > 0 && (int64_t)window + nq + s.align - 1 < span) span = (int64_t)window + nq + s.align - 1;   // vis one apart, as in a draft
+  const int64_t ctas = (int64_t)batch * heads * s.chunks, fill = s.tc ? 4 * 152 : 4 * 304, least = s.tc ? 512 : 256;
+  const int64_t n = imax64(1, imin64((fill + ctas - 1) / ctas, (span + least - 1) / least));
   s.n_splits = (int32_t)n;
   s.split_len = (int32_t)imax64(64, ((span + n - 1) / n + 63) / 64 * 64);
+  s.streams = s.tc ? 2 : 1;
+  s.joined = s.tc || n > 1;
   return s;
 }
 
-cudaError_t launch_paged_attn(const PagedAttnParams& p, int32_t head_dim, int32_t kv_dtype, cudaStream_t s) {
-  cudaError_t e = head_dim == 128 ? launch_kv<128>(p, kv_dtype, s) : launch_kv<64>(p, kv_dtype, s);
-  if (e != cudaSuccess || p.n_splits == 1) return e;
+cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedSplit& sp, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns,
+                              cudaStream_t s) {
+  const cudaError_t e = sp.tc             ? launch_paged_rows(p, head_dim, kv_dtype, wait_ns, s)
+                        : head_dim == 128 ? launch_kv<128>(p, kv_dtype, s)
+                                          : launch_kv<64>(p, kv_dtype, s);
+  if (e != cudaSuccess || !sp.joined) return e;
   const int64_t ids = (int64_t)p.batch * p.heads * p.nq * p.group;
   const dim3 grid((unsigned)((ids + 3) / 4));
   return head_dim == 128 ? launch_pdl(paged_join_kernel<128>, grid, dim3(128), 0, s, p)

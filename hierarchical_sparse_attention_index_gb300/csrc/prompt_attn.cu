@@ -28,31 +28,11 @@
 // wait.
 // Measured (16,384 tokens, 32 heads over 4, 128 dims): 1,444 us, 1,523 TFLOP/s, 0.79 of the measured
 // bf16 peak; without the softmax's part 1,340 us, where shared memory bounds the products.
-#include "hsa_common.cuh"
+#include "hsa_flash.cuh"
 #include "hsa_internal.h"
-#include "hsa_tc.cuh"
 
 namespace hsa {
 namespace {
-
-// mbar_wait with a suspend hint: a waiting warp sleeps in the barrier unit instead of coming back to
-// ask, which would take shared-memory cycles from the products (4 % of a long prompt's time)
-__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-      : "=r"(done)
-      : "r"(bar), "r"(parity), "r"(20000u)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  if (mbar_sleep(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_sleep(bar, parity))
-    if (globaltimer_ns() - t0 > limit_ns) return false;
-  return true;
-}
 
 constexpr int kTile = 128;               // rows of a query tile
 constexpr int kKeys = 64;                // keys of a key tile
@@ -64,8 +44,6 @@ constexpr int kThreads = 12 * 32;
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168, "setmaxnreg draws on the launch's registers");
 constexpr uint32_t kBlockQ = kTile * 128, kBlockK = kKeys * 128;   // 64 dims of a tile, 128 bytes a row
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRaise = 8.f;            // log2 of how far a logit may pass the running maximum
 
 struct PromptParams {
   CUtensorMap qm, km, vm;
@@ -87,75 +65,6 @@ struct Shape {
   static constexpr uint32_t kOffQ = 0, kOffKv = 2 * kQBytes, kOffStage = kOffKv + kStages * kKvBytes;
   static constexpr uint32_t kSmem = kOffStage + kSoftWarps * 2048 + 1024;   // + alignment slack
 };
-
-// Products and commits issued by one lane (`one` is nonzero in it) of a warp that stays together: in
-// code that the whole warp runs, descriptors live in uniform registers, where these instructions
-// take them from; under a branch of the one lane every product would first have to move its four
-// there (88 clocks a product instead of 64 and less)
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t one;
-  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.b32 %0, 1, 0, p; }" : "=r"(one));
-  return one;
-}
-__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.ne.b32 e, %5, 0;\n"
-      "  @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one));
-}
-__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.ne.b32 e, %5, 0;\n"
-      "  @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(one));
-}
-__device__ __forceinline__ void umma_commit_one(uint32_t one, uint32_t bar) {
-  asm volatile(
-      "{ .reg .pred e; setp.ne.b32 e, %1, 0;\n"
-      "  @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
-      "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-#define TMEM_ST8(taddr, r)                                                                                      \
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),  \
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)                     \
-               : "memory")
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if constexpr (BF16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // One piece of work: tokens [i0, i0 + n) of a sequence for key-value head h, as two query tiles, and
 // the key tiles of each. Key tile j holds the keys kbase + 64 j ..; kbase is 0, or, with a window,
@@ -248,26 +157,6 @@ __device__ __forceinline__ bool find_job(const PromptParams& p, int64_t id, bool
   }
   job.more = 1;
   return true;
-}
-
-// Cluster launch control: ask the launcher for a block of this grid that has not started. The
-// 16-byte answer lands in shared memory; it holds the block's index, or nothing if none is left.
-__device__ __forceinline__ void next_block_ask(uint32_t answer, uint32_t bar) {
-  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
-               "r"(bar)
-               : "memory");
-}
-__device__ __forceinline__ bool next_block_take(uint32_t answer, uint32_t& block) {
-  uint32_t got;
-  asm volatile(
-      "{ .reg .pred p; .reg .b128 a; ld.shared.b128 a, [%2];\n"
-      "  clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n"
-      "  selp.u32 %0, 1, 0, p; mov.u32 %1, 0;\n"
-      "  @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a; }"
-      : "=r"(got), "=r"(block)
-      : "r"(answer)
-      : "memory");
-  return got != 0;
 }
 
 constexpr int kJobSlots = 2;
@@ -472,48 +361,53 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       ok = wait_bar(drain + 8 * t, 0, p.wait_ns) && ok;
     } else {
       // -------------------------------------------------------------- what comes next
+      // A block is taken only when the work before the last has been done by every role, so that no CTA
+      // holds back more than one piece of work (taking three ahead left ragged batches uneven).
       const uint32_t answer = smem_u32(&s_answer);
       uint32_t block = blockIdx.x;
-      bool more = true;
-      for (int n = 0, it = 0; more && ok; ++n) {
-        // the next block is asked for while this one's tile is looked up
+      int it = 0;
+      auto wait_slot = [&]() {
+        ok = wait_bar(job_empty + 8 * (it % kJobSlots), ((it / kJobSlots) & 1) ^ 1, p.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+      };
+      for (int n = 0; ok; ++n) {
+        Job job;
+        if (find_job(p, block, block == gridDim.x - 1, job)) {
+          if (!wait_slot()) break;
+          if (lane == 0) {
+            s_job[it % kJobSlots] = job;
+            mbar_arrive(job_full + 8 * (it % kJobSlots));
+          }
+          ++it;
+        }
+        if (!wait_slot()) break;
         if (lane == 0) {
           fence_async_smem();            // the last answer has been read
           mbar_arrive_expect_tx(answered, 16);
           next_block_ask(answer, answered);
         }
         __syncwarp();
-        Job job;
-        if (find_job(p, block, block == gridDim.x - 1, job)) {
-          const int s = it % kJobSlots;
-          ok = wait_bar(job_empty + 8 * s, ((it / kJobSlots) & 1) ^ 1, p.wait_ns) && ok;
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok && lane == 0) {
-            s_job[s] = job;
-            mbar_arrive(job_full + 8 * s);
-          }
-          ++it;
-        }
-        const bool got = wait_bar(answered, n & 1, p.wait_ns);
-        ok = __all_sync(0xffffffffu, got && ok);
-        more = ok && next_block_take(answer, block);
+        ok = wait_bar(answered, n & 1, p.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const bool more = next_block_take(answer, block);
         __syncwarp();
-        if (!more && ok) {
-          const int s = it % kJobSlots;
-          ok = wait_bar(job_empty + 8 * s, ((it / kJobSlots) & 1) ^ 1, p.wait_ns) && ok;
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok && lane == 0) {
-            s_job[s].more = 0;
-            mbar_arrive(job_full + 8 * s);
+        if (!more) {
+          if (lane == 0) {
+            s_job[it % kJobSlots].more = 0;
+            mbar_arrive(job_full + 8 * (it % kJobSlots));
           }
+          break;
         }
       }
     }
   } else {
     // ---------------------------------------------------------------- softmax: one row per thread
     // Shared memory is busy with the products' operands, so this loop keeps out of it: no exchange
-    // between warps (two warps per row, half the keys each, took 1.5 times as long), no spilled registers. What the epilogue needs of the job is
-    // read again there, and the values that follow from it are not kept across the loop.
+    // between warps (two warps per row, half the keys each, took 1.5 times as long), no spilled
+    // registers. What the epilogue needs of the job is read again there, and the values that follow
+    // from it are not kept across the loop.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int t = warp >> 2;
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * t, tO = tS + 256u;
@@ -543,79 +437,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t at = tS + 64 * (n_s & 1);
-        uint32_t s[2][32];
+        softmax_tile<D, BF16>(
+            tS + 64 * (n_s & 1), tO, hi > 0, scale, m, l, later,
+            [&](uint32_t(&s)[2][32]) {
+              if (kKeys > whole_hi || 0 < whole_lo) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) TMEM_LD32(at + 32 * c, s[c]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_regs_ready(s[c]);
-        if (kKeys > whole_hi || 0 < whole_lo) {
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            if (c >= hi || c < lo) s[c >> 5][c & 31] = 0xFF800000u;   // -inf
-        }
+                for (int c = 0; c < kKeys; ++c)
+                  if (c >= hi || c < lo) s[c >> 5][c & 31] = 0xFF800000u;   // -inf
+              }
+            },
+            [&]() {                      // the last tile's P V is in O
+              ok = wait_bar(o_full + 16 * t + 8 * ((n_s - 1) & 1), ((n_s - 1) >> 1) & 1, p.wait_ns) && ok;
+              tc_fence_after();
+            });
+        later = true;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * (n_s & 1));
         hi += kKeys;
         lo += kKeys;
         whole_hi += kKeys;
         whole_lo += kKeys;
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 16; c += 2)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            mx[u] = max3(mx[u], __uint_as_float(s[u >> 1][16 * (u & 1) + c]), __uint_as_float(s[u >> 1][16 * (u & 1) + c + 1]));
-        // (rows that are no queries, or see none of these keys, ask for nothing)
-        const float top = hi > kKeys ? max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) : -INFINITY;
-        if (__any_sync(0xffffffffu, (top - m) * scale > kRaise)) {     // also with m = -inf; not with top = -inf
-          const float mn = fmaxf(m, top);
-          const float f = mn == -INFINITY ? 1.f : ex2_ftz((m - mn) * scale);   // m = -inf before: 0, on sums that are 0
-          m = mn;
-          l *= f;
-          if (later) {                   // once the last tile's P V is in O
-            ok = wait_bar(o_full + 16 * t + 8 * ((n_s - 1) & 1), ((n_s - 1) >> 1) & 1, p.wait_ns) && ok;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) {          // 8 columns at a time: the row of S stays in registers
-              uint32_t o[8];
-              TMEM_LD8(tO + 8 * c, o);
-              tmem_wait_ld();
-              tmem_regs_ready(o);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              TMEM_ST8(tO + 8 * c, o);
-            }
-          }
-        }
-        later = true;
-        const float mu = m == -INFINITY ? 0.f : m * scale;
-        const uint64_t nmu2 = f2_pack(-mu, -mu), scale2 = f2_pack(scale, scale);
-        uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {    // 16 keys at a time, so that P takes few registers beside S
-          uint32_t pk[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int e = 16 * q + 2 * c;
-            float z0, z1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1])), scale2, nmu2),
-                      z0, z1);
-            const float p0 = ex2_ftz(z0), p1 = ex2_ftz(z1);
-            if (c & 1)
-              sum1 = f2_add(sum1, f2_pack(p0, p1));
-            else
-              sum0 = f2_add(sum0, f2_pack(p0, p1));
-            pk[c] = pack2<BF16>(p0, p1);
-          }
-          TMEM_ST8(at + 8 * q, pk);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * (n_s & 1));
-        float a, b;
-        f2_unpack(f2_add(sum0, sum1), a, b);
-        l += a + b;
       }
       if (!ok) break;
       // -------------------------------------------------------------- O / l
@@ -689,23 +530,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   if (warp == kMmaWarp) tmem_free(tmem, 512);
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// the driver's tensor-map encoder, looked up once through the runtime (no libcuda link)
-EncodeTiledFn encode_tiled() {
-  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
-}
-
 template <int D, bool BF16>
 cudaError_t launch(const PromptParams& p, unsigned blocks, cudaStream_t s) {
   auto kernel = prompt_attn_kernel<D, BF16>;
@@ -716,8 +540,20 @@ cudaError_t launch(const PromptParams& p, unsigned blocks, cudaStream_t s) {
 
 }  // namespace
 
+TensorMapEncoder tensor_map_encoder() {
+  static const TensorMapEncoder fn = []() -> TensorMapEncoder {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<TensorMapEncoder>(f);
+  }();
+  return fn;
+}
+
 cudaError_t launch_prompt_attn(const hsa_prompt_args& a, uint32_t* status, uint64_t wait_ns, cudaStream_t s) {
-  const EncodeTiledFn encode = encode_tiled();
+  const TensorMapEncoder encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
   PromptParams p;
   memset(&p, 0, sizeof(p));
@@ -732,7 +568,7 @@ cudaError_t launch_prompt_attn(const hsa_prompt_args& a, uint32_t* status, uint6
   p.out_stride = a.out_stride;
   p.cu_q = a.cu_q;
   p.cu_k = a.cu_k ? a.cu_k : a.cu_q;
-  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  p.scale_log2 = a.sm_scale * kLog2e;
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
   p.status = status;
