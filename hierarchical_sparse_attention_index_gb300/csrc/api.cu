@@ -466,7 +466,8 @@ static hsa_status check_paged(const hsa_paged_cache* c) {
   const hsa_status st = check_paged_sizes(c);
   if (st != HSA_OK) return st;
   if (!c->k || !c->v || !c->table) return HSA_ERR_INVALID_ARG;
-  if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || !isfinite(c->k_scale) || !isfinite(c->v_scale)) return HSA_ERR_INVALID_ARG;
+  for (const float scale : {c->k_scale, c->v_scale})     // with finite reciprocals and products
+    if (!(scale >= 0x1p-120f && scale <= 0x1p120f)) return HSA_ERR_INVALID_ARG;
   if (c->dtype != HSA_E4M3 && (c->k_scale != 1.f || c->v_scale != 1.f)) return HSA_ERR_INVALID_ARG;
   if (!aligned16(c->k) || !aligned16(c->v)) return HSA_ERR_ALIGN;
   return HSA_OK;
@@ -486,7 +487,7 @@ struct PagedWs {
 };
 static PagedWs paged_ws(const hsa_paged_cache* c, int32_t rows, const PagedSplit& sp) {
   PagedWs w;
-  const size_t parts = sp.joined ? (size_t)c->batch * c->heads * sp.n_splits * sp.streams * rows : 0;
+  const size_t parts = sp.joined ? (size_t)c->batch * c->heads * sp.n_splits * rows : 0;
   w.off_o = 0;
   w.off_ml = parts * c->head_dim * 4;
   w.total = (w.off_ml + parts * 8 + 255) / 256 * 256 + 256;
@@ -523,8 +524,8 @@ hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const void* k, co
   p.k_pool = static_cast<uint8_t*>(cache->k);
   p.v_pool = static_cast<uint8_t*>(cache->v);
   p.table = cache->table;
-  p.k_scale = cache->k_scale;
-  p.v_scale = cache->v_scale;
+  p.k_inv = 1.f / cache->k_scale;
+  p.v_inv = 1.f / cache->v_scale;
   p.k = static_cast<const uint16_t*>(k);
   p.v = static_cast<const uint16_t*>(v);
   p.k_stride = k_stride;
@@ -553,7 +554,8 @@ hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, in
   st = check_paged_query(cache, heads_q, nq, max_vis);
   if (st != HSA_OK) return st;
   if (!q || !vis || !out || !type_fits(q_dtype, cache->dtype)) return HSA_ERR_INVALID_ARG;
-  if (window < 0 || !(sm_scale > 0.f) || !isfinite(sm_scale)) return HSA_ERR_INVALID_ARG;
+  const float scale_log2 = sm_scale * cache->k_scale * 1.4426950408889634f;
+  if (window < 0 || !(sm_scale > 0.f) || !(scale_log2 > 0.f) || !isfinite(scale_log2)) return HSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return HSA_ERR_ALIGN;
   const int32_t group = heads_q / cache->heads, rows = nq * group;
   const PagedSplit sp = paged_split(cache->batch, cache->heads, group, nq, max_vis, window, cache->dtype);
@@ -582,14 +584,14 @@ hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, in
   p.window = window;
   p.vis = vis;
   p.max_vis = max_vis;
-  p.scale_log2 = sm_scale * cache->k_scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.v_scale = cache->v_scale;
   p.chunk_rows = sp.chunk_rows;
   p.chunks = sp.chunks;
   p.n_splits = sp.n_splits;
   p.split_len = sp.split_len;
-  p.streams = sp.streams;
   p.align = sp.align;
+  p.cluster = sp.cluster;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.off_o);
@@ -598,14 +600,17 @@ hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, in
   return cuda_fail(launch_paged_attn(p, sp, cache->head_dim, cache->dtype, wait_limit_ns(), (cudaStream_t)stream), "paged attention launch");
 }
 
+// A CTA's piece of work walks over one sequence's keys; with more, waits for it could pass the limit of 2 s.
+static constexpr int64_t kMaxRows = 1 << 27;
+
 hsa_status hsa_prompt_attn(const hsa_prompt_args* a, hsa_stream_t stream) {
   NvtxRange range("hsa_prompt_attn");
   if (!a) return HSA_ERR_INVALID_ARG;
   if (a->dtype != HSA_BF16 && a->dtype != HSA_F16) return HSA_ERR_INVALID_ARG;
-  if (a->window < 0 || !(a->sm_scale > 0.f) || !isfinite(a->sm_scale)) return HSA_ERR_INVALID_ARG;
+  if (a->window < 0 || !(a->sm_scale > 0.f) || !isfinite(a->sm_scale * 1.4426950408889634f)) return HSA_ERR_INVALID_ARG;
   if (a->batch < 1 || a->heads_kv < 1 || a->heads_kv > 1024 || (a->head_dim != 64 && a->head_dim != 128)) return HSA_ERR_SHAPE;
   if (a->heads_q < 1 || a->heads_q % a->heads_kv || a->heads_q / a->heads_kv > HSA_MAX_GROUP) return HSA_ERR_SHAPE;
-  if (a->n_q < 0 || a->n_k < 0 || a->n_q > (int64_t)INT32_MAX || a->n_k > (int64_t)INT32_MAX) return HSA_ERR_SHAPE;
+  if (a->n_q < 0 || a->n_k < 0 || a->n_q > kMaxRows || a->n_k > kMaxRows) return HSA_ERR_SHAPE;
   if (a->n_q == 0) return HSA_OK;
   if (!a->q || !a->out || !a->cu_q || (a->n_k > 0 && (!a->k || !a->v))) return HSA_ERR_INVALID_ARG;
   const int64_t row_q = (int64_t)a->heads_q * a->head_dim, row_k = (int64_t)a->heads_kv * a->head_dim;

@@ -162,7 +162,7 @@ struct PagedWriteParams {
   uint8_t* k_pool;
   uint8_t* v_pool;
   const int32_t* table;
-  float k_scale, v_scale;
+  float k_inv, v_inv;     // fp32 reciprocals of the scales
   const uint16_t* k;      // [n_tokens][heads][head_dim], k_stride elements from row to row
   const uint16_t* v;
   int64_t k_stride, v_stride, n_tokens;
@@ -175,16 +175,16 @@ struct PagedWriteParams {
 };
 cudaError_t launch_paged_write(const PagedWriteParams& p, bool e4m3, cudaStream_t s);
 
-// How hsa_paged_attn_decode cuts its work (host only; the workspace holds n_splits x streams partials
-// per row where a join follows)
+// How hsa_paged_attn_decode cuts its work (host only; the workspace holds n_splits partials per
+// row where a join follows)
 struct PagedSplit {
   bool tc;                // paged_rows_kernel (tcgen05), else paged_attn_kernel
   int32_t chunk_rows;     // query rows (queries x heads of a group) per CTA
   int32_t chunks;         // CTAs that share a key-value head's rows
   int32_t n_splits;       // CTAs along the cache's length
   int32_t split_len;      // keys per split, at least
-  int32_t streams;        // partials that a CTA leaves
   int32_t align;          // splits start at multiples of this
+  bool cluster;           // the splits are one thread-block cluster, which joins them
   bool joined;            // paged_join_kernel follows
 };
 PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype);
@@ -202,11 +202,11 @@ struct PagedAttnParams {
   int64_t max_vis;
   float scale_log2;       // sm_scale * k_scale * log2 e
   float v_scale;
-  int32_t chunk_rows, chunks, n_splits, split_len, streams, align;   // PagedSplit
+  int32_t chunk_rows, chunks, n_splits, split_len, align, cluster;   // PagedSplit
   uint16_t* out;
   float* lse;             // or NULL
-  float* part_o;          // workspace [B][heads][n_splits][streams][rows][D], unnormalised
-  float* part_ml;         // workspace [B][heads][n_splits][streams][rows] (maximum in log2 units, sum)
+  float* part_o;          // workspace [B][heads][n_splits][rows][D], unnormalised
+  float* part_ml;         // workspace [B][heads][n_splits][rows] (maximum in log2 units, sum)
   uint32_t* status;
 };
 cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedSplit& sp, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns,

@@ -21,8 +21,9 @@
 //    16-bit weights and fp32 sums hold, and most groups need one vote instead of shuffles;
 //  - the weights P are rounded to the 16-bit operand type of the product with V (relative 2^-9 in
 //    bf16, 2^-12 in f16, independent from key to key); the sum l takes them unrounded.
-// The four warps' (m, l, O) are merged in shared memory; with one split the CTA writes the result,
-// else the partial goes to the workspace and paged_join_kernel joins the splits in their order.
+// The four warps' (m, l, O) are merged in shared memory. With one split the CTA writes the result. Up to
+// 8 splits are one thread-block cluster, whose CTAs join their parts through distributed shared memory;
+// more leave their parts in the workspace, and paged_join_kernel joins them. Either joins in order.
 #include "hsa_paged.cuh"
 
 namespace hsa {
@@ -115,7 +116,8 @@ struct Tile {
 };
 
 // NT: tiles of 8 query rows
-template <int D, int KV, int NT>
+// CLUSTER: the splits of a (request, head, chunk) are one cluster
+template <int D, int KV, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
   using T = Tile<D, KV, NT>;
   constexpr bool kB = KV == kBf16;                       // products in bf16, else in f16
@@ -123,20 +125,26 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_scale[kRows];
   __shared__ int s_lo[kRows], s_hi[kRows];
+  __shared__ float2 s_part[kRows];                       // CLUSTER: (m, l) of this CTA's part of each row
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
 
   griddep_wait();
   griddep_launch_dependents();
 
-  int idx = blockIdx.x;
+  int idx = blockIdx.x, split = 0;
+  if constexpr (CLUSTER) {
+    split = idx % p.n_splits;
+    idx /= p.n_splits;
+  }
   const int chunk = idx % p.chunks;
   idx /= p.chunks;
   const int h = idx % p.heads;
   idx /= p.heads;
-  const int b = idx % p.batch, split = idx / p.batch;
+  const int b = idx % p.batch;
+  if constexpr (!CLUSTER) split = idx / p.batch;
   const Span sp = request_span(p, b);
-  if (split >= sp.used) return;
-  const int begin = sp.base + split * sp.len, end = min(begin + sp.len, sp.hi);   // keys of this CTA
+  if (!CLUSTER && split >= sp.used) return;
+  const int begin = sp.base + split * sp.len, end = max(begin, min(begin + sp.len, sp.hi));   // keys of this CTA
   const int rows = p.nq * p.group, row0 = chunk * p.chunk_rows, row_end = min(row0 + p.chunk_rows, rows);
 
   // ---------------------------------------------------------------- the ring: 16-key groups of this warp
@@ -448,7 +456,28 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
   }
   __syncthreads();
   constexpr int kQuads = D / 4;
-  const bool last = sp.used == 1;
+  auto write_out = [&](int row, int d4, float4 a, float M, float L) {
+    const int64_t at = ((int64_t)b * p.nq + row / p.group) * p.heads_q + h * p.group + row % p.group;
+    const float inv = L != 0.f ? p.v_scale / L : 0.f;
+    uint2 y;
+    if (p.q_bf16)
+      y = make_uint2(pack2<true>(a.x * inv, a.y * inv), pack2<true>(a.z * inv, a.w * inv));
+    else
+      y = make_uint2(pack2<false>(a.x * inv, a.y * inv), pack2<false>(a.z * inv, a.w * inv));
+    *reinterpret_cast<uint2*>(p.out + at * D + 4 * d4) = y;
+    if (p.lse && d4 == 0) p.lse[at] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  };
+  // a += 2^(m - M) (O, l); a part in which the row saw no key adds nothing
+  auto add = [](float4& a, float& L, float M, float m, float l, float4 x) {
+    if (m != -INFINITY || l != 0.f) {
+      const float f = m == -INFINITY ? 0.f : ex2_ftz(m - M);
+      a.x += f * x.x;
+      a.y += f * x.y;
+      a.z += f * x.z;
+      a.w += f * x.w;
+      L += f * l;
+    }
+  };
   for (int e = tid; e < kRows * kQuads; e += kThreads) {
     const int r = e / kQuads, d4 = e % kQuads, row = row0 + r;
     if (row >= row_end) break;
@@ -457,33 +486,48 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = 0.f;
+    float4* mine = reinterpret_cast<float4*>(sm + ((size_t)r * T::kOutLd + 4 * d4) * 4);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = s_m[w][r] == -INFINITY ? 0.f : ex2_ftz(s_m[w][r] - M);
-      const float4 x = *reinterpret_cast<const float4*>(sm + (size_t)w * T::kRing + ((size_t)r * T::kOutLd + 4 * d4) * 4);
-      if (s_m[w][r] != -INFINITY || s_l[w][r] != 0.f) {  // a warp that saw no key adds nothing
-        a.x += f * x.x;
-        a.y += f * x.y;
-        a.z += f * x.z;
-        a.w += f * x.w;
-        L += f * s_l[w][r];
-      }
-    }
-    if (last) {
-      const int64_t at = ((int64_t)b * p.nq + row / p.group) * p.heads_q + h * p.group + row % p.group;
-      const float inv = L != 0.f ? p.v_scale / L : 0.f;
-      uint2 y;
-      if (p.q_bf16)
-        y = make_uint2(pack2<true>(a.x * inv, a.y * inv), pack2<true>(a.z * inv, a.w * inv));
-      else
-        y = make_uint2(pack2<false>(a.x * inv, a.y * inv), pack2<false>(a.z * inv, a.w * inv));
-      *reinterpret_cast<uint2*>(p.out + at * D + 4 * d4) = y;
-      if (p.lse && d4 == 0) p.lse[at] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    for (int w = 0; w < kWarps; ++w)
+      add(a, L, M, s_m[w][r], s_l[w][r], *reinterpret_cast<const float4*>(reinterpret_cast<uint8_t*>(mine) + (size_t)w * T::kRing));
+    if (sp.used == 1) {
+      if (!CLUSTER || split == 0) write_out(row, d4, a, M, L);
+    } else if constexpr (CLUSTER) {
+      *mine = a;                         // read by this thread alone until here
+      if (d4 == 0) s_part[r] = make_float2(M, L);
     } else {
       const int64_t at = (((int64_t)b * p.heads + h) * p.n_splits + split) * rows + row;
       *reinterpret_cast<float4*>(p.part_o + at * D + 4 * d4) = a;
       if (d4 == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(M, L);
     }
+  }
+  if constexpr (CLUSTER) {
+    if (sp.used == 1) return;            // the same in every CTA of the cluster
+    cluster_sync_all();
+    // CTA `split` joins every n_splits-th element of the chunk, over the CTAs that have keys
+    const uint32_t o_at = smem_u32(sm), ml_at = smem_u32(s_part);
+    for (int e = split * kThreads + tid; e < kRows * kQuads; e += p.n_splits * kThreads) {
+      const int r = e / kQuads, d4 = e % kQuads, row = row0 + r;
+      if (row >= row_end) break;
+      float M = -INFINITY;
+      for (int c = 0; c < sp.used; ++c) M = fmaxf(M, __uint_as_float((uint32_t)ld_cluster_s32(cluster_map(ml_at + 8 * r, c))));
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      float L = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < sp.used; ++c) {
+        const uint64_t ml = ld_cluster_u64(cluster_map(ml_at + 8 * r, c));
+        const uint32_t x = cluster_map(o_at + ((uint32_t)r * T::kOutLd + 4 * d4) * 4, c);
+        const uint64_t x0 = ld_cluster_u64(x), x1 = ld_cluster_u64(x + 8);
+        float m, l;
+        float4 v;
+        f2_unpack(ml, m, l);
+        f2_unpack(x0, v.x, v.y);
+        f2_unpack(x1, v.z, v.w);
+        add(a, L, M, m, l, v);
+      }
+      write_out(row, d4, a, M, L);
+    }
+    cluster_sync_all();                  // nobody reads this CTA's shared memory any more
   }
 }
 
@@ -501,19 +545,18 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int64_t bh = id / rows;
   const int b = (int)(bh / p.heads), h = (int)(bh % p.heads);
   const Span sp = request_span(p, b);
-  const int parts = sp.used * p.streams;
-  if (parts == 1) return;                // written by its only split
+  if (sp.used == 1) return;              // written by its only split
   constexpr int V = D / 32;
-  const int64_t first = bh * p.n_splits * p.streams * rows + row;
+  const int64_t first = bh * p.n_splits * rows + row;
   float M = -INFINITY;
-  for (int c = lane; c < parts; c += 32) M = fmaxf(M, __ldcg(p.part_ml + 2 * (first + (int64_t)c * rows)));
+  for (int c = lane; c < sp.used; c += 32) M = fmaxf(M, __ldcg(p.part_ml + 2 * (first + (int64_t)c * rows)));
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float a[V], L = 0.f;
 #pragma unroll
   for (int e = 0; e < V; ++e) a[e] = 0.f;
 #pragma unroll 4
-  for (int c = 0; c < parts; ++c) {
+  for (int c = 0; c < sp.used; ++c) {
     const int64_t at = first + (int64_t)c * rows;
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at));
     float x[V];
@@ -549,22 +592,34 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   if (p.lse && lane == 0) p.lse[at] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
-template <int D, int KV, int NT>
+template <int D, int KV, int NT, bool CLUSTER>
 cudaError_t launch(const PagedAttnParams& p, cudaStream_t s) {
-  auto kernel = paged_attn_kernel<D, KV, NT>;
+  auto kernel = paged_attn_kernel<D, KV, NT, CLUSTER>;
   constexpr size_t smem = (size_t)kWarps * Tile<D, KV, NT>::kRing;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  const unsigned blocks = (unsigned)p.n_splits * p.batch * p.heads * p.chunks;
-  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, s, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.n_splits * p.batch * p.heads * p.chunks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.n_splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CLUSTER ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 template <int D, int KV>
 cudaError_t launch_nt(const PagedAttnParams& p, cudaStream_t s) {
   switch ((p.chunk_rows + 7) / 8) {
-    case 1: return launch<D, KV, 1>(p, s);
-    case 2: return launch<D, KV, 2>(p, s);
-    case 3: return launch<D, KV, 3>(p, s);
-    default: return launch<D, KV, 4>(p, s);
+    case 1: return p.cluster ? launch<D, KV, 1, true>(p, s) : launch<D, KV, 1, false>(p, s);
+    case 2: return p.cluster ? launch<D, KV, 2, true>(p, s) : launch<D, KV, 2, false>(p, s);
+    case 3: return p.cluster ? launch<D, KV, 3, true>(p, s) : launch<D, KV, 3, false>(p, s);
+    default: return p.cluster ? launch<D, KV, 4, true>(p, s) : launch<D, KV, 4, false>(p, s);
   }
 }
 template <int D>
@@ -579,16 +634,22 @@ cudaError_t launch_kv(const PagedAttnParams& p, int kv, cudaStream_t s) {
 }  // namespace
 
 // Which kernel, query rows per CTA and splits of the length.
-// 16-bit pages and more than kTcRows query rows take the tcgen05 kernel: 128 rows (whole queries) to a CTA,
-// about four jobs per SM, so that ragged lengths even out, and no split shorter than 512 keys (a
-// stream then has four tiles). Measured at 64 requests, 4 heads, up to 4,097 keys of 128 dims, f16, ragged:
-// MEASURED.
-// Else up to 32 rows one CTA reads its keys once for all of them; more rows are dealt out evenly
-// (35: 18 and 17), and the later CTAs' keys come from L2. The splits fill the GPU about four times
-// over (2 CTAs per SM on 152 SMs), but no split is shorter than 256 keys: 4 groups for each warp,
-// about what the ring holds.
+// 16-bit pages and more than 32 query rows take the tcgen05 kernel, 128 rows (whole queries) to a CTA: 35
+// rows (64 requests of up to 4,097 keys, 4 heads, f16) took 84 us there and 105 here, 32 rows 117 and
+// 110. Else up to 32 rows one CTA reads its keys once for all of them; more rows (E4M3) are dealt out
+// evenly (35: 18 and 17), and the later CTAs' keys come from L2.
+// The splits make about as many CTAs as the GPU holds at a time (3 or 2 per SM; the tcgen05 kernel's CTAs,
+// one per SM, take four each, so that ragged lengths even out): more only add starts and joins (4
+// requests of 131,072 FP8 keys: 168 us with 448 CTAs, 193 with 608, 217 with 1,216). No split is
+// shorter than 256 keys (8 per group of a warp; in a cluster 128), or 512 in the tcgen05 kernel.
+// Splits that all run at a time join in clusters (1 request of 1,000 keys: 6.7 us against 8.5); with more
+// CTAs than that, a cluster's short CTAs would hold places until its longest ends (32 ragged contexts: 99
+// us against 93).
+// A request's splits follow from max_vis and the sizes alone, so that its result does not depend on
+// where it stands in the batch. (Equal pieces of all requests' keys, one per place on the GPU, were
+// slower: 109 against 94 us for 32 ragged contexts, because SMs do not get equal shares of HBM.)
 PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype) {
-  constexpr int32_t kTcRows = 16;
+  constexpr int32_t kTcRows = 32;
   PagedSplit s;
   const int32_t rows = nq * group;
   s.tc = kv_dtype != HSA_E4M3 && rows > kTcRows;
@@ -603,12 +664,20 @@ PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, 
   s.align = s.tc ? 64 : 16;
   int64_t span = max_vis;
   if (window > 0 && (int64_t)window + nq + s.align - 1 < span) span = (int64_t)window + nq + s.align - 1;   // vis one apart, as in a draft
-  const int64_t ctas = (int64_t)batch * heads * s.chunks, fill = s.tc ? 4 * 152 : 4 * 304, least = s.tc ? 512 : 256;
-  const int64_t n = imax64(1, imin64((fill + ctas - 1) / ctas, (span + least - 1) / least));
+  const int64_t ctas = (int64_t)batch * heads * s.chunks;
+  int64_t n;
+  if (s.tc) {
+    n = imin64((4 * 152 + ctas - 1) / ctas, (span + 511) / 512);
+  } else {
+    const int64_t places = 152 * (s.chunk_rows <= 16 ? 3 : 4);
+    n = imin64((places + ctas / 2) / ctas, (span + 255) / 256);
+    if (n < 8) n = imin64(imin64((places + ctas / 2) / ctas, 8), (span + 127) / 128);
+  }
+  n = imax64(1, n);
   s.n_splits = (int32_t)n;
   s.split_len = (int32_t)imax64(64, ((span + n - 1) / n + 63) / 64 * 64);
-  s.streams = s.tc ? 2 : 1;
-  s.joined = s.tc || n > 1;
+  s.cluster = !s.tc && n > 1 && n <= 8 && ctas * n <= 152 * (s.chunk_rows <= 16 ? 3 : 2);
+  s.joined = n > 1 && !s.cluster;
   return s;
 }
 

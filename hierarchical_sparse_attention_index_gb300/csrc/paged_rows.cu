@@ -16,7 +16,9 @@
 //    times what they hold need not be zero), blocks past it, or on a bad page, come from outside the
 //    pool, where TMA fills in zeros;
 //  - CTAs stay and take the next blocks' jobs (cluster launch control), so ragged lengths even out;
-//  - each stream writes its unnormalised O and (m, l) to the workspace; paged_join_kernel joins them.
+//  - the streams' results are merged from tensor memory, where both of a row lie in the same lane: half of
+//    the dims by either stream's warps. With one split that is the result, else it goes to the
+//    workspace and paged_join_kernel joins the splits.
 #include <string.h>
 
 #include <numeric>
@@ -39,8 +41,9 @@ constexpr int kJobSlots = 2;
 template <int D>
 struct Shape {
   static constexpr uint32_t kQBytes = (D / 64) * kBlockQ, kKvBytes = (D / 64) * kBlockK;
-  static constexpr int kStages = 5;                              // tiles of K and V in a stream's ring
-  static constexpr uint32_t kOffQ = 0, kOffKv = kQBytes, kSmem = kOffKv + 2 * kStages * kKvBytes + 1024;   // + alignment slack
+  static constexpr int kStages = D == 128 ? 4 : 8;               // tiles of K and V in a stream's ring
+  static constexpr uint32_t kOffQ = 0, kOffKv = 2 * kQBytes;     // Q of two jobs
+  static constexpr uint32_t kOffStage = kOffKv + 2 * kStages * kKvBytes, kSmem = kOffStage + kSoftWarps * 2048 + 1024;   // + alignment slack
 };
 
 struct RowsParams {
@@ -54,6 +57,7 @@ struct RowsParams {
 struct Job {
   int b, h, chunk, split, lo, hi;        // [lo, hi): the positions that queries of the request see
   int j0[2], j1[2];                      // 64-key tiles [j0, j1) of stream t
+  int whole;                             // the request's only split
   int more;                              // 0: no work is left, the other fields are not set
 };
 
@@ -63,27 +67,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   const PagedAttnParams& p = rp.a;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Job s_job[kJobSlots];
+  __shared__ float2 s_ml[2][2][kTile];                   // of jobs in turn, each stream's (m in log2 units, l) of a row
   __shared__ __align__(16) uint4 s_answer;
   __shared__ uint32_t s_tmem;
-  __shared__ __align__(8) uint64_t s_bars[19 + 2 * kJobSlots + 4 * L::kStages];
+  __shared__ __align__(8) uint64_t s_bars[25 + 2 * kJobSlots + 4 * L::kStages];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t sQ = base + L::kOffQ, sKv = base + L::kOffKv;
-  // mbarriers: Q of a job loaded / read by both streams' last products; for each stream O read, every
-  // product done; two for each stream, for key tiles in turn: S computed, P written, P V added to O.
-  // Then the launcher's answer, the jobs and the rings
+  // mbarriers: Q loaded / read by both streams' last products, for jobs in turn; for each stream O read,
+  // every product done; two for each stream, for key tiles in turn: S computed, P written, P V added to O.
+  // Then the two warps of 32 rows meeting, the launcher's answer, the jobs and the rings
   const uint32_t bars = smem_u32(s_bars);
-  const uint32_t q_full = bars, q_empty = bars + 8, o_empty = bars + 16, drain = bars + 32, s_full = bars + 48, p_full = bars + 80,
-                 o_full = bars + 112, answered = bars + 144, job_full = bars + 152, job_empty = job_full + 8 * kJobSlots,
+  const uint32_t q_full = bars, q_empty = bars + 16, o_empty = bars + 32, drain = bars + 48, s_full = bars + 64, p_full = bars + 96,
+                 o_full = bars + 128, pair = bars + 160, answered = bars + 192, job_full = bars + 200, job_empty = job_full + 8 * kJobSlots,
                  kv_full = job_empty + 8 * kJobSlots, kv_empty = kv_full + 16 * L::kStages;
-  static_assert(152 + 16 * kJobSlots + 32 * L::kStages <= sizeof(s_bars), "barriers");
+  static_assert(200 + 16 * kJobSlots + 32 * L::kStages <= sizeof(s_bars), "barriers");
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), 512);
   if (tid == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 2);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(o_empty + 8 * t, 4);
+      mbar_init(q_full + 8 * t, 1);
+      mbar_init(q_empty + 8 * t, 2);
+      mbar_init(o_empty + 8 * t, kSoftWarps);
       mbar_init(drain + 8 * t, 1);
       for (int b = 0; b < 2; ++b) {
         mbar_init(s_full + 16 * t + 8 * b, 1);
@@ -91,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         mbar_init(o_full + 16 * t + 8 * b, 1);
       }
     }
+    for (int w = 0; w < 4; ++w) mbar_init(pair + 8 * w, 2);
     mbar_init(answered, 1);
     for (int s = 0; s < kJobSlots; ++s) {
       mbar_init(job_full + 8 * s, 1);
@@ -174,21 +180,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         ++c[t];
       };
       for (int it = 0; take_job(it, job); ++it) {
-        ok = wait_bar(q_empty, (n_q & 1) ^ 1, rp.wait_ns) && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(q_full, (D / 64) * (uint32_t)(rp.tt * p.group) * 128u);
-#pragma unroll
-          for (int d = 0; d < D / 64; ++d) tma_4d(sQ + d * kBlockQ, &rp.qm, 64 * d, 0, job.h, job.b * p.nq + job.chunk * rp.tt, q_full);
-        }
-        ++n_q;
-        int at[2] = {0, 0}, ahead[2] = {0, 0};       // pages of the tiles whose V and K come next
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           pages[t] = find_pages(t, 0);
           pages_next[t] = find_pages(t, 1);
         }
+        const int qs = it & 1;
+        ok = wait_bar(q_empty + 8 * qs, ((it >> 1) & 1) ^ 1, rp.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full + 8 * qs, (D / 64) * (uint32_t)(rp.tt * p.group) * 128u);
+#pragma unroll
+          for (int d = 0; d < D / 64; ++d)
+            tma_4d(sQ + qs * L::kQBytes + d * kBlockQ, &rp.qm, 64 * d, 0, job.h, job.b * p.nq + job.chunk * rp.tt, q_full + 8 * qs);
+        }
+        ++n_q;
+        int at[2] = {0, 0}, ahead[2] = {0, 0};       // pages of the tiles whose V and K come next
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (job.j0[t] < job.j1[t]) {
@@ -216,14 +224,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       for (int t = 0; t < 2; ++t)
         for (int e = max(0, c[t] - L::kStages); e < c[t]; ++e)
           ok = wait_bar(kv_full + 8 * (t * L::kStages + e % L::kStages), (e / L::kStages) & 1, rp.wait_ns) && ok;
-      if (n_q) ok = wait_bar(q_full, (n_q - 1) & 1, rp.wait_ns) && ok;
+      for (int e = max(0, n_q - 2); e < n_q; ++e) ok = wait_bar(q_full + 8 * (e & 1), (e >> 1) & 1, rp.wait_ns) && ok;
     } else if (warp < kLoadWarp) {
       // -------------------------------------------------------------- products of one stream
       const int t = warp - kMmaWarp;
       const uint32_t tS = tmem + 128 * t, tO = tmem + 256 + 128 * t, ring = sKv + t * L::kStages * L::kKvBytes;
       const uint32_t full = kv_full + 8 * t * L::kStages, empty = kv_empty + 8 * t * L::kStages;
       const uint32_t id_qk = idesc_f16(kTile, kKeys, false, false, BF16), id_pv = idesc_f16(kTile, D, false, true, BF16);
-      const uint64_t dq = sdesc(sQ, 16u, 1024u);
       const uint32_t one = elect_one();
       auto wait = [&](uint32_t bar, int n) {
         ok = wait_bar(bar, n & 1, rp.wait_ns) && ok;
@@ -231,13 +238,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         tc_fence_after();
         return ok;
       };
-      int n_o = 0, n_s = 0, n_p = 0, c = 0;      // jobs with tiles for this stream, tiles of S and P, of the ring
+      int n_s = 0, n_p = 0, c = 0;       // key tiles of S and P, tiles of the ring
       auto wait_kv = [&]() { return wait(full + 8 * (c % L::kStages), c / L::kStages); };
       auto free_kv = [&]() {
         umma_commit_one(one, empty + 8 * (c % L::kStages));
         ++c;
       };
-      auto qk = [&]() {
+      auto qk = [&](int it) {
+        const uint64_t dq = sdesc(sQ + (it & 1) * L::kQBytes, 16u, 1024u);
         const uint64_t dk = sdesc(ring + (c % L::kStages) * L::kKvBytes, 16u, 1024u);
         const uint32_t at = tS + 64 * (n_s & 1);
 #pragma unroll
@@ -259,19 +267,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       for (int it = 0; take_job(it, job); ++it) {
         const int j0 = uniform(t ? job.j0[1] : job.j0[0]), j1 = uniform(t ? job.j1[1] : job.j1[0]);
         const int lo = uniform(job.lo), hi = uniform(job.hi);
-        if (!wait(q_full, it)) break;
+        if (!wait(q_full + 8 * (it & 1), it >> 1)) break;
         if (j0 < j1) {
           if (!wait_kv()) break;
-          qk();
+          qk(it);
           free_kv();
         }
         for (int j = j0; j < j1 && ok; ++j) {
           if (j + 1 < j1) {
             if (!wait_kv()) break;
-            qk();
+            qk(it);
             free_kv();
           }
-          if (j + 1 == j1) umma_commit_one(one, q_empty);   // Q's last product is issued
+          if (j + 1 == j1) umma_commit_one(one, q_empty + 8 * (it & 1));   // Q's last product is issued
           if (!wait_kv()) break;
           const int first = max(0, lo - kKeys * j), end = min(kKeys, hi - kKeys * j);   // rows that some query sees
           if (first > 0 || end < kKeys) {
@@ -284,14 +292,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             __syncwarp();
           }
           // the first product of a job overwrites O: the last job's must have been read
-          if (j == j0 && !wait(o_empty + 8 * t, n_o ^ 1)) break;
+          if (j == j0 && !wait(o_empty + 8 * t, it ^ 1)) break;
           if (!wait(p_full + 16 * t + 8 * (n_p & 1), n_p >> 1)) break;
           pv(j > j0);
           free_kv();
         }
         if (!ok) break;
-        if (j0 == j1) umma_commit_one(one, q_empty);
-        n_o += j0 < j1;
+        if (j0 == j1) umma_commit_one(one, q_empty + 8 * (it & 1));
       }
       umma_commit_one(one, drain + 8 * t);       // every product is done before the tensor memory is freed
       ok = wait_bar(drain + 8 * t, 0, rp.wait_ns) && ok;
@@ -330,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
           job.j0[0] = begin;
           job.j1[0] = job.j0[1] = begin + half;
           job.j1[1] = max(end, begin + half);
+          job.whole = sp.used == 1;
           if (!wait_slot()) break;
           if (lane == 0) {
             s_job[it % kJobSlots] = job;
@@ -371,7 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       const int j0 = t ? job.j0[1] : job.j0[0], j1 = t ? job.j1[1] : job.j1[0], b = job.b, job_hi = job.hi;
       const int row = job.chunk * rp.tt * p.group + r;
       const bool real = r < rp.tt * p.group && row < rows;
-      const int64_t slot = (((int64_t)b * p.heads + job.h) * p.n_splits + job.split) * 2 + t;
+      const int h = job.h, partner = t ? job.j1[0] - job.j0[0] : job.j1[1] - job.j0[1];   // the other stream's tiles
+      const bool whole = job.whole;
+      const int64_t slot = ((int64_t)b * p.heads + h) * p.n_splits + job.split;
       const bool warp_real = (warp & 3) * 32 < rp.tt * p.group && job.chunk * rp.tt * p.group + (warp & 3) * 32 < rows;
       int lo = 0, hi = 0;                // this row's keys
       if (real) {
@@ -420,33 +430,90 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * (n_s & 1));
       }
       if (!ok) break;
-      // -------------------------------------------------------------- this stream's part
+      // -------------------------------------------------------------- both streams' O and (m, l)
       if (j0 < j1) {
         ok = wait_bar(o_full + 16 * t + 8 * ((n_s - 1) & 1), ((n_s - 1) >> 1) & 1, rp.wait_ns) && ok;   // the last P V
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (warp_real) {
-          float* dst = p.part_o + (slot * rows + row) * D;
+      }
+      const float m2 = m == -INFINITY ? m : m * scale;
+      s_ml[it & 1][t][r] = make_float2(m2, l);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(pair + 8 * (warp & 3));
+      ok = ok && wait_bar(pair + 8 * (warp & 3), it & 1, rp.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const float2 other = s_ml[it & 1][t ^ 1][r];
+      const bool mine_any = m2 != -INFINITY || l != 0.f, other_any = other.x != -INFINITY || other.y != 0.f;
+      const float M = fmaxf(m2, other.x);
+      const float fm = m2 == -INFINITY ? 0.f : ex2_ftz(m2 - M), fo = other.x == -INFINITY ? 0.f : ex2_ftz(other.x - M);
+      const float lsum = (mine_any ? fm * l : 0.f) + (other_any ? fo * other.y : 0.f);
+      const float gain = !whole ? 1.f : (lsum != 0.f ? p.v_scale / lsum : 0.f);
+      const uint32_t tM = tO + (D / 2) * t, tP = tM + (t ? -128 : 128);   // this warp's half of the dims, in either stream's O
+      const int row0 = row - lane, row_end = min(rows, (row - r) + rp.tt * p.group);   // this warp's first row, and past the chunk's last
+      const uint32_t stage = base + L::kOffStage + (uint32_t)warp * 2048u;
+      free_job(it);
+      if (warp_real) {
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t x[32], y[32];
+          if (j0 < j1) TMEM_LD32(tM + 32 * c, x);
+          if (partner > 0) TMEM_LD32(tP + 32 * c, y);
+          tmem_wait_ld();
+          tmem_regs_ready(x);
+          tmem_regs_ready(y);
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            TMEM_LD32(tO + 32 * c, o);
-            tmem_wait_ld();
-            tmem_regs_ready(o);
-            if (real) {
+          for (int e = 0; e < 32; ++e)
+            x[e] = __float_as_uint(((mine_any ? fm * __uint_as_float(x[e]) : 0.f) + (other_any ? fo * __uint_as_float(y[e]) : 0.f)) * gain);
+          // 64 bytes of each row at a time go through shared memory, so that four lanes write them together:
+          // this lane then holds piece lane % 4 of rows 8 i + lane / 4
+          auto flush = [&](auto&& piece, auto&& place) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4*>(dst + 32 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 4; ++e) {
+              const uint4 v = piece(e);
+              sts128(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4), v.x, v.y, v.z, v.w);
             }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int sr = 8 * i + (lane >> 2);
+              const uint4 v = lds128(stage + sr * 64 + (((lane & 3) ^ ((sr >> 1) & 3)) << 4));
+              if (row0 + sr < row_end) *place(row0 + sr) = v;
+            }
+            __syncwarp();
+          };
+          const int d = (D / 2) * t + 32 * c;
+          if (!whole) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              flush([&](int e) { return make_uint4(x[16 * u + 4 * e], x[16 * u + 4 * e + 1], x[16 * u + 4 * e + 2], x[16 * u + 4 * e + 3]); },
+                    [&](int rw) { return reinterpret_cast<uint4*>(p.part_o + (slot * rows + rw) * D + d + 16 * u) + (lane & 3); });
+          } else {
+            flush(
+                [&](int e) {
+                  auto two = [&](int i) { return pack2<BF16>(__uint_as_float(x[8 * e + 2 * i]), __uint_as_float(x[8 * e + 2 * i + 1])); };
+                  return make_uint4(two(0), two(1), two(2), two(3));
+                },
+                [&](int rw) {
+                  const int64_t at = ((int64_t)b * p.nq + rw / p.group) * p.heads_q + h * p.group + rw % p.group;
+                  return reinterpret_cast<uint4*>(p.out + at * D + d) + (lane & 3);
+                });
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_empty + 8 * t);
       }
-      if (real) *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * rows + row)) = make_float2(m == -INFINITY ? m : m * scale, l);
-      free_job(it);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(o_empty);
+        mbar_arrive(o_empty + 8);
+      }
+      if (real && t == 0) {
+        if (!whole)
+          *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * rows + row)) = make_float2(M, lsum);
+        else if (p.lse)
+          p.lse[((int64_t)b * p.nq + row / p.group) * p.heads_q + h * p.group + row % p.group] = lsum != 0.f ? (M + log2f(lsum)) * kLn2 : -INFINITY;
+      }
     }
   }
   if (!ok) flag_status(p.status, HSA_FLAG_TIMEOUT);

@@ -135,7 +135,7 @@ typedef struct {
   void* k;                /* [n_pages][heads][page_size][head_dim]                  */
   void* v;                /* [n_pages][heads][page_size][head_dim]                  */
   const int32_t* table;   /* i32 [batch][max_pages]; entries no position needs are not read */
-  float k_scale, v_scale; /* finite and > 0; 1 unless dtype is HSA_E4M3             */
+  float k_scale, v_scale; /* 2^-120 .. 2^120; 1 unless dtype is HSA_E4M3            */
 } hsa_paged_cache;
 
 /* Arguments of hsa_prompt_attn. All pointers are device memory; q, k, v and out 16-byte aligned. */
@@ -153,7 +153,7 @@ typedef struct {
   int64_t q_stride, k_stride, v_stride, out_stride; /* multiples of 8, at least a row; < 2^31 */
   const int32_t* cu_q; /* i32 [batch + 1]: rows [cu_q[b], cu_q[b+1]) of q are sequence b    */
   const int32_t* cu_k; /* i32 [batch + 1], the same for k and v; NULL: cu_q                 */
-  float sm_scale;      /* softmax scale applied to q.k; finite and > 0                      */
+  float sm_scale;      /* softmax scale applied to q.k; > 0, finite in fp32 times log2 e    */
   void* out;           /* [n_q][heads_q][head_dim], out_stride elements from row to row     */
   float* lse;          /* f32 [n_q][heads_q] or NULL                                        */
 } hsa_prompt_args;
@@ -312,8 +312,8 @@ HSA_API hsa_status hsa_schedule_step(const hsa_cache* caches, const hsa_step_arg
 
 /* Write keys and values into a paged cache. Row t of k and v belongs to the request b with
  * cu[b] <= t < cu[b+1] and becomes position start[b] + t - cu[b] of it:
- *   page value = round(x / scale): the fp32 quotient to nearest even, to HSA_E4M3 saturating at
- *   +-448 (NaN stays NaN); a 16-bit cache takes the values as they are.
+ *   page value = round(x r), r the fp32 reciprocal of the scale: the fp32 product to nearest even,
+ *   to HSA_E4M3 saturating at +-448 (NaN stays NaN); a 16-bit cache takes the values as they are.
  *   k, v      bf16 or f16 (`dtype`) [n_tokens][heads][head_dim], k_stride / v_stride elements from
  *             row to row (a multiple of 8, at least a row); 16-byte aligned. dtype must be the
  *             cache's unless the cache is HSA_E4M3
@@ -343,6 +343,7 @@ HSA_API size_t hsa_paged_attn_workspace_bytes(const hsa_paged_cache* cache, int3
  *   vis       i32 [B][nq], 0 <= vis <= max_vis; another value counts as the nearer border and is
  *             flagged HSA_FLAG_INDEX_RANGE. max_vis <= max_pages * page_size and <= HSA_MAX_VIS
  *   lse       f32 [B][nq][heads_q] or NULL
+ *   sm_scale  > 0; sm_scale * k_scale * log2 e has to be finite and not 0 in fp32
  *   ws        hsa_paged_attn_workspace_bytes bytes, 16-byte aligned; needs no initialisation
  * Positions on a page id outside [0, n_pages) are skipped and flagged HSA_FLAG_INDEX_RANGE. What
  * the pools hold at positions that no query of the request sees is never used, whatever it is. */
@@ -359,7 +360,7 @@ HSA_API hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const voi
  * Rows of q, out and lse outside [cu_q[0], cu_q[batch]) are neither read for a result nor written.
  * A sequence never uses another's rows, nor rows outside [cu_k[0], cu_k[batch]), whatever they
  * hold. A sequence whose bounds are not ascending inside [0, n_q] and [0, n_k] is skipped and
- * flagged HSA_FLAG_INDEX_RANGE. n_q and n_k < 2^31; n_q = 0 launches nothing. */
+ * flagged HSA_FLAG_INDEX_RANGE. n_q and n_k <= 2^27; n_q = 0 launches nothing. */
 HSA_API hsa_status hsa_prompt_attn(const hsa_prompt_args* args, hsa_stream_t stream);
 
 /* Limit of the kernels' bounded waits (for a copy or a tensor-core result that does not arrive),

@@ -216,9 +216,9 @@ def write_reference(pool, rows, table, cu, start, scale):
     page, n_pages = pool.shape[2], pool.shape[0]
     f8 = pool.dtype == F8
     if f8:
-        # the fp32 quotient (from 64 bits: torch divides by a number in 32 bits through its reciprocal)
-        scale = torch.tensor(scale, dtype=torch.float32).double().item()
-        vals = (rows.double() / scale).float().clamp(-448, 448).to(F8).view(torch.uint8)
+        # the fp32 product with the scale's fp32 reciprocal
+        inv = 1 / torch.tensor(scale, dtype=torch.float32)
+        vals = (rows.float() * inv.to(rows.device)).clamp(-448, 448).to(F8).view(torch.uint8)
         nan = rows.isnan()
         vals = torch.where(nan, torch.tensor(0x7F, dtype=torch.uint8, device=rows.device), vals)
         target = pool.view(torch.uint8)
