@@ -32,6 +32,17 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t
   return true;
 }
 
+// Whether the phase is complete, without waiting
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Products and commits issued by one lane (`one` is nonzero in it) of a warp that stays together: in
 // code that the whole warp runs, descriptors live in uniform registers, where these instructions
 // take them from; under a branch of the one lane every product would first have to move its four
@@ -102,6 +113,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
+// 32 bytes of 16-bit values, 32-byte aligned
+__device__ __forceinline__ void st_global_256(void* at, const uint32_t* y) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]),
+               "r"(y[5]), "r"(y[6]), "r"(y[7])
+               : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -122,6 +139,20 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)                     \
                : "memory")
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// -inf where c < lo or c >= hi: by bits, so that a column costs a predicate move and a select instead of
+// two comparisons
+__device__ __forceinline__ void mask_row(uint32_t (&s)[2][32], int lo, int hi) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int h = min(max(hi - 32 * c, 0), 32), l = min(max(lo - 32 * c, 0), 32);
+    const uint32_t below_h = h == 32 ? 0xFFFFFFFFu : (1u << h) - 1u, below_l = l == 32 ? 0xFFFFFFFFu : (1u << l) - 1u;
+    const uint32_t keep = below_h & ~below_l;
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!(keep & (1u << e))) s[c][e] = 0xFF800000u;
+  }
+}
 
 // The softmax of 64 keys, one query row per thread: S in the tensor memory columns at .. at + 63 is
 // taken into the running maximum m (in units of S) and sum l, and P = 2^((S - m) scale), rounded to the

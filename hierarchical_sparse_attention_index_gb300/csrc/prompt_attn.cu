@@ -7,7 +7,7 @@
 // head stand together (tt = 128 / group tokens per tile), so that grouped heads share every key tile
 // and a tile spans few tokens, which keeps the masked part at the diagonal small.
 //  - CTAs stay and take the next block's work themselves (cluster launch control), while the loads
-//    of the next work already run; the first work has the most keys;
+//    of the next work already run; the work with the most keys comes first;
 //  - one warp loads Q, and 64-key tiles of K and V into a ring, by TMA (128-byte swizzle);
 //  - a warp per query tile issues its tcgen05 products: S = Q K^T (128 x 64, fp32 in tensor memory,
 //    two buffers, one key tile ahead), then O += P V with P read from tensor memory and V as an
@@ -20,6 +20,8 @@
 //    independent from key to key) over S's columns. The maximum is only raised, and O rescaled in
 //    tensor memory, when a logit passes it by 2^8: weights stay below 256, and after the first
 //    tiles that hardly happens, so the rescaling needs no warps of its own;
+//  - four warps write the results, while the softmax is at the next work (in a window of 128 the writing
+//    took as long as half of the softmax);
 //  - keys come from the diagonal downwards, so the first tile already holds each row's own key;
 //  - the rows of V's tiles that are no keys of the sequence are cleared before use: their weights
 //    are zero, but zero times another sequence's infinity would not be.
@@ -36,13 +38,15 @@ namespace {
 
 constexpr int kTile = 128;               // rows of a query tile
 constexpr int kKeys = 64;                // keys of a key tile
-constexpr int kSoftWarps = 8;            // 4 per query tile: two warp groups; the third holds the other roles
+constexpr int kSoftWarps = 8;            // 4 per query tile: warp groups 0 and 1
 constexpr int kMmaWarp = 8, kLoadWarp = 10;              // a warp per query tile's products; warp 11 finds the work
-constexpr int kThreads = 12 * 32;
-// registers per thread: 168 at launch (65,536 over 384 threads, in steps of 8), then 208 for the
-// softmax groups, whose threads hold a row of 128 logits, and 88 for the third: 2 x 208 + 88 = 3 x 168
-constexpr int kSoftRegs = 208, kOtherRegs = 88;
-static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168, "setmaxnreg draws on the launch's registers");
+constexpr int kOutWarp = 12;             // warps 12..15 write the results
+constexpr int kThreads = 16 * 32;
+// registers per thread: 128 at launch (65,536 over 512 threads), then 152 for the softmax groups, whose
+// threads hold a row of 64 logits, and 104 for the other two: 2 x 152 + 2 x 104 = 4 x 128
+constexpr int kSoftRegs = 152, kOtherRegs = 104;
+static_assert(2 * kSoftRegs + 2 * kOtherRegs <= 4 * 128, "setmaxnreg draws on the launch's registers");
+constexpr int kSeqs = 512;               // batches up to this are held in shared memory and worked off by size
 constexpr uint32_t kBlockQ = kTile * 128, kBlockK = kKeys * 128;   // 64 dims of a tile, 128 bytes a row
 
 struct PromptParams {
@@ -54,6 +58,7 @@ struct PromptParams {
   float scale_log2;
   uint16_t* out;
   float* lse;
+  int32_t wide;                          // rows of out start on 32-byte boundaries
   uint32_t* status;
   uint64_t wait_ns;
 };
@@ -62,8 +67,7 @@ template <int D>
 struct Shape {
   static constexpr uint32_t kQBytes = (D / 64) * kBlockQ, kKvBytes = (D / 64) * kBlockK;
   static constexpr int kStages = 8;                              // tiles of K and V in the ring
-  static constexpr uint32_t kOffQ = 0, kOffKv = 2 * kQBytes, kOffStage = kOffKv + kStages * kKvBytes;
-  static constexpr uint32_t kSmem = kOffStage + kSoftWarps * 2048 + 1024;   // + alignment slack
+  static constexpr uint32_t kOffQ = 0, kOffKv = 2 * kQBytes, kOffSeq = kOffKv + kStages * kKvBytes, kSmem = kOffSeq + kSeqs * 24 + 1024;   // + alignment slack
 };
 
 // One piece of work: tokens [i0, i0 + n) of a sequence for key-value head h, as two query tiles, and
@@ -76,57 +80,133 @@ struct Job {
   int clear_j, clear_lo, clear_hi;       // rows [clear_lo, clear_hi) of V's tile clear_j are no keys of the sequence
   int more;                              // 0: no work is left, the other fields are not set
   __device__ bool has(int t) const { return jhi[t] > jlo[t]; }
-  __device__ bool active(int t, int j) const { return j >= jlo[t] && j < jhi[t]; }
   __device__ int top() const { return max(jhi[0], jhi[1]); }
   __device__ int bottom() const { return min(has(0) ? jlo[0] : 0x7fffffff, has(1) ? jlo[1] : 0x7fffffff); }
 };
 
-// Tiles of the sequences in order, the last tiles (the most keys) of each first. One warp; false:
-// no such tile. With `check_all`, sequences past the tile are looked at too, for their bounds.
-__device__ __forceinline__ bool find_job(const PromptParams& p, int64_t id, bool check_all, Job& job) {
-  const int lane = threadIdx.x & 31, tpc = 2 * p.tt;
-  const int64_t tile = id / p.heads_kv;
-  int64_t before = 0;
-  bool found = false;
-  job.h = (int)(id % p.heads_kv);
-  for (int base = 0; base < p.batch && (!found || check_all); base += 32) {
-    const int b = base + lane;
-    int q0 = 0, lq = 0, k0 = 0, lk = 0;
-    if (b < p.batch) {
-      const int q1 = p.cu_q[b + 1], k1 = p.cu_k[b + 1];
-      q0 = p.cu_q[b];
-      k0 = p.cu_k[b];
-      if (q0 >= 0 && q0 <= q1 && q1 <= p.n_q && k0 >= 0 && k0 <= k1 && k1 <= p.n_k) {
-        lq = q1 - q0;
-        lk = k1 - k0;
-      } else {
-        flag_status(p.status, HSA_FLAG_INDEX_RANGE);
-      }
+struct Seq {
+  int q0, lq, k0, lk;
+  int count, base;                       // pieces of work, and the level of the first
+};
+__device__ __forceinline__ Seq load_seq(const PromptParams& p, int b) {
+  Seq s = {};
+  if (b < p.batch) {
+    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
+    if (q0 >= 0 && q0 <= q1 && q1 <= p.n_q && k0 >= 0 && k0 <= k1 && k1 <= p.n_k)
+      s = Seq{q0, q1 - q0, k0, k1 - k0};
+    else
+      flag_status(p.status, HSA_FLAG_INDEX_RANGE);
+  }
+  const int tpc = 2 * p.tt;
+  s.count = (s.lq + tpc - 1) / tpc;
+  s.base = p.window > 0 ? 0 : max(0, s.lk - s.lq) / tpc;
+  return s;
+}
+
+// The order of the work. Every 2 tt tokens of a sequence are one piece; the pieces with the most keys
+// come first, so that the last ones to be taken are short. Sequence b's pieces have the levels base_b ..
+// base_b + count_b - 1 (a level is about 2 tt keys); those of one level stand in the order of the
+// sequences. One warp; the sequences lie in shared memory.
+struct Order {
+  static constexpr int kHeld = 4;        // up to 128 sequences' counts and levels stay in registers: shared memory
+  const Seq* seq;                        // answers slowly beside the products (6,000 clocks a search, 1,000 so)
+  int batch, total, levels;              // pieces in all; levels are 0 .. levels - 1
+  int count[kHeld], base[kHeld];         // of sequences lane + 32 k
+  __device__ void hold(const Seq* s, int n) {
+    const int lane = threadIdx.x & 31;
+    seq = s;
+    batch = n;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const int b = lane + 32 * k;
+      count[k] = b < n ? s[b].count : 0;
+      base[k] = b < n ? s[b].base : 0;
     }
-    const int tiles = (lq + tpc - 1) / tpc;
-    int64_t upto = tiles;
+    total = above(0);
+    int top = 0;
+    for (int b = lane; b < n; b += 32) top = max(top, s[b].base + s[b].count);
+    levels = __reduce_max_sync(0xffffffffu, top);
+  }
+  // pieces of level x and above
+  __device__ int above(int x) const {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) n += max(0, count[k] - max(0, x - base[k]));
+    for (int b = (threadIdx.x & 31) + 32 * kHeld; b < batch; b += 32) n += max(0, seq[b].count - max(0, x - seq[b].base));
+    return __reduce_add_sync(0xffffffffu, n);
+  }
+  // piece number r: the sequence, and which of its pieces
+  __device__ bool find(int r, int& which, int& i) const {
+    if (r >= total) return false;
+    which = 0;
+    i = total - 1 - r;
+    if (batch == 1) return true;
+    int x = 0, past = levels;            // above(x) > r >= above(past)
+    while (past - x > 1) {
+      const int mid = (x + past) >> 1;
+      if (above(mid) > r) x = mid; else past = mid;
+    }
+    int left = r - above(x + 1);
+    auto among = [&](int first, int c, int b) {          // of 32 sequences from `first`, this lane's with c pieces from level b on
+      uint32_t m = __ballot_sync(0xffffffffu, b <= x && x < b + c);
+      if (left >= __popc(m)) {
+        left -= __popc(m);
+        return false;
+      }
+      for (; left > 0; --left) m &= m - 1;
+      which = __ffs(m) - 1;
+      i = x - __shfl_sync(0xffffffffu, b, which);
+      which += first;
+      return true;
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (32 * k < batch && among(32 * k, count[k], base[k])) return true;
+    for (int first = 32 * kHeld; first < batch; first += 32) {
+      const int b = first + (threadIdx.x & 31);
+      if (among(first, b < batch ? seq[b].count : 0, b < batch ? seq[b].base : 0)) return true;
+    }
+    return false;
+  }
+};
+
+// Larger batches are worked off in the order of the sequences, the last piece of each first.
+__device__ __forceinline__ bool find_in_turn(const PromptParams& p, int r, Seq& out, int& i) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int first = 0; first < p.batch; first += 32) {
+    const Seq s = load_seq(p, first + lane);
+    int upto = s.count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
     upto += before;
-    const uint32_t past = __ballot_sync(0xffffffffu, upto > tile);
-    if (past && !found) {
+    const uint32_t past = __ballot_sync(0xffffffffu, upto > r);
+    if (past) {
       const int src = __ffs(past) - 1;
-      const int64_t end = __shfl_sync(0xffffffffu, upto, src);
-      job.q0 = __shfl_sync(0xffffffffu, q0, src);
-      job.k0 = __shfl_sync(0xffffffffu, k0, src);
-      job.lk = __shfl_sync(0xffffffffu, lk, src);
-      const int l = __shfl_sync(0xffffffffu, lq, src);
-      job.i0 = (int)(end - 1 - tile) * tpc;
-      job.n = min(tpc, l - job.i0);
-      job.off = job.lk - l;
-      found = true;
+      out.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+      out.lq = __shfl_sync(0xffffffffu, s.lq, src);
+      out.k0 = __shfl_sync(0xffffffffu, s.k0, src);
+      out.lk = __shfl_sync(0xffffffffu, s.lk, src);
+      i = __shfl_sync(0xffffffffu, upto, src) - 1 - r;
+      return true;
     }
     before = __shfl_sync(0xffffffffu, upto, 31);
   }
-  if (!found) return false;
+  return false;
+}
+
+__device__ __forceinline__ void make_job(const PromptParams& p, const Seq& s, int i, int h, Job& job) {
+  const int tpc = 2 * p.tt;
+  job.h = h;
+  job.q0 = s.q0;
+  job.k0 = s.k0;
+  job.lk = s.lk;
+  job.i0 = i * tpc;
+  job.n = min(tpc, s.lq - job.i0);
+  job.off = s.lk - s.lq;
   const int top = job.i0 + job.n + job.off;              // past the last position, at most lk
   const int bottom = p.window > 0 ? max(job.i0 + job.off - p.window + 1, 0) : 0;
   job.kbase = 0;
@@ -156,10 +236,10 @@ __device__ __forceinline__ bool find_job(const PromptParams& p, int64_t id, bool
     }
   }
   job.more = 1;
-  return true;
 }
 
-constexpr int kJobSlots = 2;
+constexpr int kJobSlots = 4;
+constexpr int kAhead = 8;                // key tiles left to load when the next piece of work is looked for
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptParams p) {
@@ -168,19 +248,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   __shared__ Job s_job[kJobSlots];
   __shared__ __align__(16) uint4 s_answer;
   __shared__ uint32_t s_tmem;
-  __shared__ __align__(8) uint64_t s_bars[21 + 2 * kJobSlots + 2 * L::kStages];
+  __shared__ uint16_t s_tok[kTile], s_head[kTile];       // of a query tile's rows; token 0xFFFF: no row
+  __shared__ float2 s_ml[2][kTile];                      // each query tile's (maximum, sum)
+  __shared__ __align__(8) uint64_t s_bars[23 + 3 * kJobSlots + 2 * L::kStages];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t sQ = base + L::kOffQ, sKv = base + L::kOffKv;
-  // mbarriers, one for each query tile: Q of a job loaded / read by its last product, O read, every
-  // product done; two for each query tile, for key tiles in turn: S computed, P written, P V added to
+  // mbarriers, one for each query tile: Q of a job loaded / read by its last product, O and (m, l) read,
+  // every product done, (m, l) written; two for each query tile, for key tiles in turn: S computed, P written, P V added to
   // O (one barrier for all key tiles would not do: the softmax may be two of them ahead of P V, and a
-  // parity cannot tell that). Then the launcher's answer, the jobs and the ring of K and V
+  // parity cannot tell that). Then the launcher's answer, the jobs (posted, done, loads issued) and the ring of K and V
   const uint32_t bars = smem_u32(s_bars);
   const uint32_t q_full = bars, q_empty = bars + 16, o_empty = bars + 32, drain = bars + 48, s_full = bars + 64,
-                 p_full = bars + 96, o_full = bars + 128, answered = bars + 160, job_full = bars + 168,
-                 job_empty = job_full + 8 * kJobSlots, kv_full = job_empty + 8 * kJobSlots,
+                 p_full = bars + 96, o_full = bars + 128, ml_full = bars + 160, answered = bars + 176, job_full = bars + 184,
+                 job_empty = job_full + 8 * kJobSlots, job_loaded = job_empty + 8 * kJobSlots, kv_full = job_loaded + 8 * kJobSlots,
                  kv_empty = kv_full + 8 * L::kStages;
-  static_assert(168 + 16 * kJobSlots + 16 * L::kStages <= sizeof(s_bars), "barriers");
+  static_assert(184 + 24 * kJobSlots + 16 * L::kStages <= sizeof(s_bars), "barriers");
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -195,18 +277,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         mbar_init(o_full + 16 * t + 8 * b, 1);
       }
       mbar_init(o_empty + 8 * t, 4);
+      mbar_init(ml_full + 8 * t, 4);
       mbar_init(drain + 8 * t, 1);
     }
     mbar_init(answered, 1);
     for (int s = 0; s < kJobSlots; ++s) {
       mbar_init(job_full + 8 * s, 1);
-      mbar_init(job_empty + 8 * s, kSoftWarps + 3);
+      mbar_init(job_loaded + 8 * s, 1);
+      mbar_init(job_empty + 8 * s, kSoftWarps + 3 + 4);
     }
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(kv_full + 8 * s, 1);
       mbar_init(kv_empty + 8 * s, 2);      // both tiles' products
     }
     fence_mbar_init();
+  }
+  if (tid < kTile) {
+    s_tok[tid] = tid < p.tt * p.group ? tid / p.group : 0xFFFF;
+    s_head[tid] = tid % p.group;
   }
   tc_fence_before();
   __syncthreads();
@@ -234,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     return true;
   };
 
-  if (warp >= kSoftWarps) {
+  if (warp >= kSoftWarps && warp < kOutWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
       // -------------------------------------------------------------- loads
@@ -263,11 +351,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       Job job;
       for (int it = 0; take_job(it, job); ++it) {
         if (lane == 0) {
-          const int top = job.top(), bottom = job.bottom();
+          const int top = job.top(), bottom = job.bottom(), ask = min(top - 1, bottom + kAhead);
+          if (top == 0) mbar_arrive(job_loaded + 8 * (it % kJobSlots));
           if (top > 0) load_kv(job, top - 1, &p.km);
           if (job.has(0)) load_q(job, 0);
           if (job.has(1)) load_q(job, 1);
           for (int j = top - 1; j >= bottom && ok; --j) {
+            if (j == ask) mbar_arrive(job_loaded + 8 * (it % kJobSlots));
             if (j > bottom) load_kv(job, j - 1, &p.km);
             load_kv(job, j, &p.vm);
           }
@@ -321,25 +411,60 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         umma_commit_one(one, o_full + 16 * t + 8 * (n_p & 1));
         ++n_p;
       };
-      Job job;
-      for (int it = 0; take_job(it, job); ++it) {
-        const int top = uniform(job.top()), bottom = uniform(job.bottom()), clear_j = uniform(job.clear_j);
-        const int jlo = uniform(t ? job.jlo[1] : job.jlo[0]), jhi = uniform(t ? job.jhi[1] : job.jhi[0]);
-        if (top == 0) continue;
-        const bool has = jhi > jlo;
-        if (has && !wait(q_full + 8 * t, n_q)) break;
-        if (!wait_kv()) break;
-        if (top == jhi) qk(top - 1 == jlo);
-        free_kv();
-        for (int j = top - 1; j >= bottom && ok; --j) {
-          if (j > bottom) {
+      // A job as this warp needs it
+      struct Mine {
+        int top, bottom, jlo, jhi, clear_j, clear_lo, clear_hi;
+      };
+      auto mine_of = [&](const Job& job) {
+        return Mine{uniform(job.top()), uniform(job.bottom()), uniform(t ? job.jlo[1] : job.jlo[0]), uniform(t ? job.jhi[1] : job.jhi[0]),
+                    uniform(job.clear_j), uniform(job.clear_lo), uniform(job.clear_hi)};
+      };
+      auto ready = [&](uint32_t bar, int n) { return __all_sync(0xffffffffu, mbar_test(bar, n & 1)); };
+      // The first S of the next job is computed before the last P V of this one where it can be, so that the
+      // softmax finds it when it comes there: `taken`, the next job is known; `begun`, its first S is issued.
+      bool taken = false, begun = false;
+      Mine next = {};
+      for (int it = 0;; ++it) {
+        Mine job = next;
+        if (!taken) {
+          if (!wait_job(it)) break;
+          job = mine_of(s_job[it % kJobSlots]);
+          free_job(it);
+        }
+        taken = false;
+        if (job.top == 0) continue;
+        const bool has = job.jhi > job.jlo;
+        if (!begun) {
+          if (has && !wait(q_full + 8 * t, n_q)) break;
+          if (!wait_kv()) break;
+          if (job.top == job.jhi) qk(job.top - 1 == job.jlo);
+          free_kv();
+        }
+        begun = false;
+        for (int j = job.top - 1; j >= job.bottom && ok; --j) {
+          if (j > job.bottom) {
             if (!wait_kv()) break;
-            if (j - 1 >= jlo && j - 1 < jhi) qk(j - 1 == jlo);
+            if (j - 1 >= job.jlo && j - 1 < job.jhi) qk(j - 1 == job.jlo);
             free_kv();
+          } else if (ready(job_full + 8 * ((it + 1) % kJobSlots), (it + 1) / kJobSlots) && s_job[(it + 1) % kJobSlots].more) {
+            next = mine_of(s_job[(it + 1) % kJobSlots]);
+            free_job(it + 1);
+            taken = true;
+            const int q = n_q + has, k = c + 1;          // V of this tile comes first in the ring
+            if (next.top > 0 && (next.jhi == next.jlo || ready(q_full + 8 * t, q)) &&
+                ready(kv_full + 8 * (k % L::kStages), k / L::kStages)) {
+              tc_fence_after();
+              const int v = c;
+              c = k;
+              if (next.top == next.jhi) qk(next.top - 1 == next.jlo);
+              free_kv();
+              c = v;
+              begun = true;
+            }
           }
           if (!wait_kv()) break;
-          if (j >= jlo && j < jhi) {
-            if (j == clear_j) {          // rows that are no keys of the sequence (both warps write the same zeros)
+          if (j >= job.jlo && j < job.jhi) {
+            if (j == job.clear_j) {      // rows that are no keys of the sequence (both warps write the same zeros)
               const uint32_t v = sKv + (c % L::kStages) * L::kKvBytes;
               for (int x = job.clear_lo * 8 + lane; x < job.clear_hi * 8; x += 32)
 #pragma unroll
@@ -348,21 +473,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
               __syncwarp();
             }
             // the first product of a job overwrites O: the last job's must have been read
-            if (j == jhi - 1 && !wait(o_empty + 8 * t, n_q ^ 1)) break;
+            if (j == job.jhi - 1 && !wait(o_empty + 8 * t, n_q ^ 1)) break;
             if (!wait(p_full + 16 * t + 8 * (n_p & 1), n_p >> 1)) break;
-            pv(j < jhi - 1);
+            pv(j < job.jhi - 1);
           }
           free_kv();
         }
         if (!ok) break;
+        c += begun;                      // the next job's first K
         n_q += has;
       }
       umma_commit_one(one, drain + 8 * t);       // every product is done before the tensor memory is freed
       ok = wait_bar(drain + 8 * t, 0, p.wait_ns) && ok;
     } else {
       // -------------------------------------------------------------- what comes next
-      // A block is taken only when the work before the last has been done by every role, so that no CTA
-      // holds back more than one piece of work (taking three ahead left ragged batches uneven).
+      // The next block is taken when few of this piece's key tiles are left to load: a CTA that held more
+      // would leave others without (taking a piece ahead from the start made a batch of chunks, two
+      // pieces for each SM, last 1.4 times its share), one that took it at the end would wait for it.
+      // Short pieces are posted up to four ahead: finding and starting one takes longer than its loop.
       const uint32_t answer = smem_u32(&s_answer);
       uint32_t block = blockIdx.x;
       int it = 0;
@@ -371,17 +499,44 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         ok = __all_sync(0xffffffffu, ok);
         return ok;
       };
+      Seq* seqs = reinterpret_cast<Seq*>(smem_raw + (base - raw) + L::kOffSeq);
+      Order order;
+      if (p.batch <= kSeqs) {
+        for (int b = lane; b < p.batch; b += 32) seqs[b] = load_seq(p, b);
+        __syncwarp();
+        order.hold(seqs, p.batch);
+      }
+      bool is_long = false;
       for (int n = 0; ok; ++n) {
         Job job;
-        if (find_job(p, block, block == gridDim.x - 1, job)) {
+        Seq seq;
+        int which = 0, i = 0;
+        const int h = (int)(block % (uint32_t)p.heads_kv), r = (int)(block / (uint32_t)p.heads_kv);
+        bool found;
+        if (p.batch <= kSeqs) {
+          found = order.find(r, which, i);
+          if (found) seq = seqs[which];
+        } else {
+          found = find_in_turn(p, r, seq, i);
+          if (block == gridDim.x - 1)    // every sequence's bounds are looked at once
+            for (int b = lane; b < p.batch; b += 32) load_seq(p, b);
+        }
+        if (found) {
+          make_job(p, seq, i, h, job);
           if (!wait_slot()) break;
           if (lane == 0) {
             s_job[it % kJobSlots] = job;
             mbar_arrive(job_full + 8 * (it % kJobSlots));
           }
           ++it;
+          is_long = job.top() - job.bottom() > kAhead;
         }
         if (!wait_slot()) break;
+        if (is_long) {
+          ok = wait_bar(job_loaded + 8 * ((it - 1) % kJobSlots), ((it - 1) / kJobSlots) & 1, p.wait_ns) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
         if (lane == 0) {
           fence_async_smem();            // the last answer has been read
           mbar_arrive_expect_tx(answered, 16);
@@ -402,25 +557,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         }
       }
     }
-  } else {
+  } else if (warp < kSoftWarps) {
     // ---------------------------------------------------------------- softmax: one row per thread
     // Shared memory is busy with the products' operands, so this loop keeps out of it: no exchange
-    // between warps (two warps per row, half the keys each, took 1.5 times as long), no spilled
-    // registers. What the epilogue needs of the job is read again there, and the values that follow
-    // from it are not kept across the loop.
+    // between warps (two warps per row, half the keys each, took 1.5 times as long), no spilled registers.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    const int t = warp >> 2;
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * t, tO = tS + 256u;
     const float scale = p.scale_log2;
-    int n_s = 0;                         // key tiles so far
+    int n_s = 0, n_o = 0;                // key tiles, and jobs with keys, so far
     for (int it = 0; wait_job(it); ++it) {
       int j, jlo, hi, lo, whole_hi, whole_lo;
       {
         const Job& job = s_job[it % kJobSlots];
-        const int r = (warp & 3) * 32 + lane, r_tok = t * p.tt + r / p.group;
+        const int r_tok = t * p.tt + s_tok[r];
         const int first = job.i0 + job.off - job.kbase;                // the first token's position, from kbase on
         const int floor = -job.kbase;                                  // key 0 (kbase < 0: with a window)
-        const bool real = r < p.tt * p.group && r_tok < job.n;
+        const bool real = s_tok[r] != 0xFFFF && r_tok < job.n;
         jlo = t ? job.jlo[1] : job.jlo[0];
         j = (t ? job.jhi[1] : job.jhi[0]) - 1;
         // this row's keys, and those that every row of the tile sees, from tile j's first key on
@@ -429,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         whole_hi = first + t * p.tt + 1 - kKeys * j;
         whole_lo = (p.window > 0 ? max(first + min(job.n, (t + 1) * p.tt) - p.window, floor) : 0) - kKeys * j;
       }
+      free_job(it);
       float m = -INFINITY, l = 0.f;
       bool later = false;                // a tile of this job has gone into O
       const bool keys = j >= jlo;
@@ -440,11 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         softmax_tile<D, BF16>(
             tS + 64 * (n_s & 1), tO, hi > 0, scale, m, l, later,
             [&](uint32_t(&s)[2][32]) {
-              if (kKeys > whole_hi || 0 < whole_lo) {
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c)
-                  if (c >= hi || c < lo) s[c >> 5][c & 31] = 0xFF800000u;   // -inf
-              }
+              if (kKeys > whole_hi || 0 < whole_lo) mask_row(s, lo, hi);
             },
             [&]() {                      // the last tile's P V is in O
               ok = wait_bar(o_full + 16 * t + 8 * ((n_s - 1) & 1), ((n_s - 1) >> 1) & 1, p.wait_ns) && ok;
@@ -459,66 +609,76 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         whole_lo += kKeys;
       }
       if (!ok) break;
-      // -------------------------------------------------------------- O / l
-      if (keys) {
-        ok = wait_bar(o_full + 16 * t + 8 * ((n_s - 1) & 1), ((n_s - 1) >> 1) & 1, p.wait_ns) && ok;   // the last P V
+      if (keys) {                        // (m, l) to the warps that write, when they have read the last job's
+        ok = wait_bar(o_empty + 8 * t, (n_o & 1) ^ 1, p.wait_ns) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        tc_fence_after();
+        ++n_o;
+        s_ml[t][r] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ml_full + 8 * t);
       }
-      const Job& job = s_job[it % kJobSlots];
-      int group = p.group;               // opaque: what follows from it is computed here, not before the loop
-      asm volatile("" : "+r"(group));
-      const uint32_t stage = base + L::kOffStage + (uint32_t)warp * 2048u;
-      const float inv = l != 0.f ? 1.f / l : 0.f;
-      const int64_t row0 = (int64_t)job.q0 + job.i0;
-      uint16_t* dst[4];                  // where this lane writes its piece of rows 8 i + lane / 4; NULL: no such row
+    }
+  } else {
+    // ---------------------------------------------------------------- O / l, while the softmax is at the next job
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    // Each lane writes its row, 32 bytes at a time where the rows allow it: that takes more write
+    // transactions than gathering rows in shared memory first, but shared memory is what is scarce here
+    // (a window of 128 over 32,768 tokens took 214 us that way, 187 so).
+    const int r = (warp & 3) * 32 + lane, tok = s_tok[r], head = s_head[r];
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    int n_s[2] = {0, 0}, n_o[2] = {0, 0};
+    Job job;
+    for (int it = 0; ok && take_job(it, job); ++it) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rr = (warp & 3) * 32 + 8 * i + (lane >> 2), tok = t * p.tt + rr / group;
-        dst[i] = rr < p.tt * group && tok < job.n
-                     ? p.out + (row0 + tok) * p.out_stride + (int64_t)(job.h * group + rr % group) * D + 8 * (lane & 3)
-                     : nullptr;
-      }
-      if (p.lse) {
-        const int r = (warp & 3) * 32 + lane, tok = t * p.tt + r / group;
-        if (r < p.tt * group && tok < job.n)
-          p.lse[(row0 + tok) * p.heads_q + job.h * group + r % group] = l != 0.f ? (m * scale + log2f(l)) * kLn2 : -INFINITY;
-      }
-      free_job(it);
+      for (int t = 0; t < 2; ++t) {
+        const int tiles = job.jhi[t] - job.jlo[t];
+        const bool mine = tok < job.n - t * p.tt;        // this lane has a row
+        const int64_t row = (int64_t)job.q0 + job.i0 + t * p.tt + tok;
+        const int hq = job.h * p.group + head;
+        uint16_t* dst = p.out + row * p.out_stride + hq * D;
+        float m = -INFINITY, l = 0.f;
+        if (tiles > 0) {
+          ok = ok && wait_bar(ml_full + 8 * t, n_o[t] & 1, p.wait_ns);
+          n_s[t] += tiles;
+          ++n_o[t];
+          ok = ok && wait_bar(o_full + 16 * t + 8 * ((n_s[t] - 1) & 1), ((n_s[t] - 1) >> 1) & 1, p.wait_ns);   // the last P V
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const float2 ml = s_ml[t][r];
+          m = ml.x;
+          l = ml.y;
+        }
+        const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (keys) {
-          TMEM_LD32(tO + 32 * c, o);
-          tmem_wait_ld();
-          tmem_regs_ready(o);
-          if (c == D / 32 - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(o_empty + 8 * t);
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32], y[16];
+          if (tiles > 0) {
+            TMEM_LD32(tmem + lanes + 256u + 128u * t + 32u * c, o);
+            tmem_wait_ld();
+            tmem_regs_ready(o);
+            if (c == D / 32 - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(o_empty + 8 * t);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            y[e] = pack2<BF16>(l != 0.f ? __uint_as_float(o[2 * e]) * inv : 0.f, l != 0.f ? __uint_as_float(o[2 * e + 1]) * inv : 0.f);
+          if (mine) {
+            if (p.wide) {
+              st_global_256(dst + 32 * c, y);
+              st_global_256(dst + 32 * c + 16, y + 8);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<uint4*>(dst + 32 * c + 2 * e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            }
           }
         }
-        // through shared memory, so that four lanes write 64 bytes of a row together
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t y[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float a = l != 0.f ? __uint_as_float(o[8 * e + 2 * u]) * inv : 0.f;
-            const float b = l != 0.f ? __uint_as_float(o[8 * e + 2 * u + 1]) * inv : 0.f;
-            y[u] = pack2<BF16>(a, b);
-          }
-          sts128(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4), y[0], y[1], y[2], y[3]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = 8 * i + (lane >> 2);
-          const uint4 y = lds128(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-          if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + 32 * c) = y;
-        }
-        __syncwarp();
+        if (p.lse && mine) p.lse[row * p.heads_q + hq] = l != 0.f ? (m * p.scale_log2 + log2f(l)) * kLn2 : -INFINITY;
       }
     }
   }
@@ -571,6 +731,7 @@ cudaError_t launch_prompt_attn(const hsa_prompt_args& a, uint32_t* status, uint6
   p.scale_log2 = a.sm_scale * kLog2e;
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
+  p.wide = ((uintptr_t)a.out % 32 == 0 && a.out_stride % 16 == 0) ? 1 : 0;
   p.status = status;
   p.wait_ns = wait_ns;
   const CUtensorMapDataType type = a.dtype == HSA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
