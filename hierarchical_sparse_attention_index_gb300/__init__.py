@@ -128,23 +128,24 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_raw_stream = None
+_current_device = _raw_stream = None
 
 
-def _current_stream():
-    """Address of the current device's current stream. torch.cuda.current_stream() makes a Stream object first,
-    which costs as much as a launch, so the address is asked for directly where torch offers it."""
-    global _raw_stream
+def _device_calls():
+    """torch.cuda.current_device, and the address of a device's current stream. torch.cuda.current_stream()
+    makes a Stream object first, which costs as much as a launch, so the address is asked for directly
+    where torch offers it."""
+    global _current_device, _raw_stream
     import torch
-    if _raw_stream is None:
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                              lambda device: torch.cuda.current_stream(device).cuda_stream)
-    return _raw_stream(torch.cuda.current_device())
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
+    _current_device = torch.cuda.current_device
 
 
 def _stream(stream):
     if stream is None:
-        return _current_stream()
+        if _current_device is None:
+            _device_calls()
+        return _raw_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -304,11 +305,16 @@ def _given(name, t, dtype, shape, device):
     return t.data_ptr()
 
 
-def _on_current(name, device):
-    """The library launches on the current device, so its tensors have to be there (-1: not on a GPU)."""
-    import torch
-    if device < 0 or device != torch.cuda.current_device():
-        raise ValueError(f"{name} is on device {device}: expected the current CUDA device")
+def _stream_on(name, device, stream):
+    """The stream to launch on. The library launches on the current device, so its tensors have to be
+    there (-1: not on a GPU)."""
+    if device < 0:
+        raise ValueError(f"{name} is not on a CUDA device")
+    if _current_device is None:
+        _device_calls()
+    if device != _current_device():
+        raise ValueError(f"{name} is on device {device}: expected the current one, {_current_device()}")
+    return _raw_stream(device) if stream is None else _stream(stream)
 
 
 class PagedCache:
@@ -340,7 +346,7 @@ def hsa_paged_cache_write(cache: PagedCache, k, v, cu=None, start=None, stream=N
     """k, v: [n_tokens][heads][head_dim], rows at any stride; cu: int32 [batch + 1] or None (equal
     shares); start: int64 [batch] or None (0)."""
     device = cache.device
-    _on_current("cache", device)
+    stream = _stream_on("cache", device, stream)
     k_stride, v_stride = _rows("k", k, cache.heads, cache.head_dim), _rows("v", v, cache.heads, cache.head_dim)
     n = k.shape[0]
     if v.shape[0] != n or k.dtype is not v.dtype or k.get_device() != device or v.get_device() != device:
@@ -349,7 +355,7 @@ def hsa_paged_cache_write(cache: PagedCache, k, v, cu=None, start=None, stream=N
     _check("hsa_paged_cache_write", load_library().hsa_paged_cache_write(
         cache.ref, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride, n,
         _given("cu", cu, _DTYPES["i32"], (cache.batch + 1,), device),
-        _given("start", start, _DTYPES["i64"], (cache.batch,), device), _stream(stream)))
+        _given("start", start, _DTYPES["i64"], (cache.batch,), device), stream))
 
 
 def hsa_paged_attn_workspace_bytes(cache: PagedCache, heads_q, nq, max_vis):
@@ -368,7 +374,7 @@ def new_paged_workspace(cache: PagedCache, heads_q, nq, max_vis):
 def hsa_paged_attn_decode(cache: PagedCache, q, vis, max_vis, sm_scale, out, ws, window=0, lse=None, stream=None):
     """q, out: [batch][nq][heads_q][head_dim]; vis: int32 [batch][nq]; lse: float32 [batch][nq][heads_q] or None."""
     device, shape = cache.device, q.shape
-    _on_current("cache", device)
+    stream = _stream_on("cache", device, stream)
     if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.head_dim:
         raise ValueError(f"q: shape {tuple(shape)}, expected [{cache.batch}][nq][heads_q][{cache.head_dim}]")
     if ws is not None and (ws.get_device() != device or not ws.is_contiguous()):
@@ -379,14 +385,14 @@ def hsa_paged_attn_decode(cache: PagedCache, q, vis, max_vis, sm_scale, out, ws,
         cache.ref, _given("q", q, q.dtype, shape, device), dtype, heads_q,
         _given("vis", vis, _DTYPES["i32"], (cache.batch, nq), device), nq, max_vis, window, sm_scale,
         _given("out", out, q.dtype, shape, device), _given("lse", lse, _DTYPES["f32"], shape[:3], device), _ptr(ws),
-        ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
+        ws.numel() * ws.element_size() if ws is not None else 0, stream))
 
 
 def hsa_prompt_attn(q, k, v, cu_q, sm_scale, out, cu_k=None, window=0, lse=None, stream=None):
     """q, out: [n_q][heads_q][head_dim], k, v: [n_k][heads_kv][head_dim], rows at any stride; cu_q,
     cu_k: int32 [batch + 1] (cu_k None: cu_q); lse: float32 [n_q][heads_q] or None."""
     device = q.get_device()
-    _on_current("q", device)
+    stream = _stream_on("q", device, stream)
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k, v and out are [rows][heads][head_dim]")
     (n_q, heads_q, dim), (n_k, heads_kv, _) = q.shape, k.shape
@@ -402,7 +408,7 @@ def hsa_prompt_attn(q, k, v, cu_q, sm_scale, out, cu_k=None, window=0, lse=None,
                         v.data_ptr(), q_stride, k_stride, v_stride, out_stride, _given("cu_q", cu_q, i32, cu_shape, device),
                         _given("cu_k", cu_k, i32, cu_shape, device), sm_scale, out.data_ptr(),
                         _given("lse", lse, _DTYPES["f32"], (n_q, heads_q), device))
-    _check("hsa_prompt_attn", load_library().hsa_prompt_attn(ctypes.byref(a), _stream(stream)))
+    _check("hsa_prompt_attn", load_library().hsa_prompt_attn(ctypes.byref(a), stream))
 
 
 def hsa_set_wait_limit(ns):
