@@ -12,7 +12,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "hsa_common.cuh"
-#include "hsa_internal.h"
+#include "hsa_dense.h"
 
 namespace hsa {
 

@@ -3,7 +3,7 @@
 #pragma once
 
 #include "hsa_common.cuh"
-#include "hsa_internal.h"
+#include "hsa_dense.h"
 
 namespace hsa {
 

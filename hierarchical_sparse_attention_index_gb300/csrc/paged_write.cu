@@ -9,7 +9,7 @@
 // rows' slots up while they fly (cu in shared memory: one load and a search there instead of a
 // chain of global loads), and then stores, 16 bytes per thread along a head's row.
 #include "hsa_common.cuh"
-#include "hsa_internal.h"
+#include "hsa_dense.h"
 
 namespace hsa {
 namespace {

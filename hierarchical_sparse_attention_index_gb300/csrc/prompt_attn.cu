@@ -31,7 +31,7 @@
 // Measured (16,384 tokens, 32 heads over 4, 128 dims): 1,444 us, 1,523 TFLOP/s, 0.79 of the measured
 // bf16 peak; without the softmax's part 1,340 us, where shared memory bounds the products.
 #include "hsa_flash.cuh"
-#include "hsa_internal.h"
+#include "hsa_dense.h"
 
 namespace hsa {
 namespace {
