@@ -559,7 +559,9 @@ hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, in
   if (!aligned16(q) || !aligned16(out)) return HSA_ERR_ALIGN;
   const int32_t group = heads_q / cache->heads, rows = nq * group;
   const PagedSplit sp = paged_split(cache->batch, cache->heads, group, nq, max_vis, window, cache->dtype);
-  if ((int64_t)sp.n_splits * sp.chunks * cache->heads * cache->batch > (int64_t)INT32_MAX) return HSA_ERR_SHAPE;
+  if ((int64_t)sp.n_splits * sp.chunks * cache->heads * cache->batch > (int64_t)INT32_MAX ||
+      (int64_t)rows * cache->heads * cache->batch > (int64_t)INT32_MAX)
+    return HSA_ERR_SHAPE;
   const PagedWs L = paged_ws(cache, rows, sp);
   if (!ws || ws_bytes < L.total) return HSA_ERR_WORKSPACE;
   if (!aligned16(ws)) return HSA_ERR_ALIGN;
@@ -602,13 +604,14 @@ hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, in
 
 // A CTA's piece of work walks over one sequence's keys; with more, waits for it could pass the limit of 2 s.
 static constexpr int64_t kMaxRows = 1 << 27;
+static constexpr int32_t kMaxSeqs = 1 << 20;      // so could a search through more sequences
 
 hsa_status hsa_prompt_attn(const hsa_prompt_args* a, hsa_stream_t stream) {
   NvtxRange range("hsa_prompt_attn");
   if (!a) return HSA_ERR_INVALID_ARG;
   if (a->dtype != HSA_BF16 && a->dtype != HSA_F16) return HSA_ERR_INVALID_ARG;
   if (a->window < 0 || !(a->sm_scale > 0.f) || !isfinite(a->sm_scale * 1.4426950408889634f)) return HSA_ERR_INVALID_ARG;
-  if (a->batch < 1 || a->heads_kv < 1 || a->heads_kv > 1024 || (a->head_dim != 64 && a->head_dim != 128)) return HSA_ERR_SHAPE;
+  if (a->batch < 1 || a->batch > kMaxSeqs || a->heads_kv < 1 || a->heads_kv > 1024 || (a->head_dim != 64 && a->head_dim != 128)) return HSA_ERR_SHAPE;
   if (a->heads_q < 1 || a->heads_q % a->heads_kv || a->heads_q / a->heads_kv > HSA_MAX_GROUP) return HSA_ERR_SHAPE;
   if (a->n_q < 0 || a->n_k < 0 || a->n_q > kMaxRows || a->n_k > kMaxRows) return HSA_ERR_SHAPE;
   if (a->n_q == 0) return HSA_OK;
@@ -617,6 +620,7 @@ hsa_status hsa_prompt_attn(const hsa_prompt_args* a, hsa_stream_t stream) {
   const int64_t strides[4] = {a->q_stride, a->out_stride, a->k_stride, a->v_stride};
   for (int i = 0; i < 4; ++i)
     if (strides[i] < (i < 2 ? row_q : row_k) || strides[i] % 8 || strides[i] > (int64_t)INT32_MAX) return HSA_ERR_SHAPE;
+  if (prompt_blocks(*a) > (int64_t)INT32_MAX) return HSA_ERR_SHAPE;
   if (!aligned16(a->q) || !aligned16(a->out) || !aligned16(a->k) || !aligned16(a->v)) return HSA_ERR_ALIGN;
   uint32_t* status;
   int sms;

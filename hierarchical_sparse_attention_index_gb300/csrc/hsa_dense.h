@@ -71,6 +71,7 @@ using TensorMapEncoder = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint3
 TensorMapEncoder tensor_map_encoder();
 
 // ------------------------------------------------------------------ causal attention over packed prompts
+int64_t prompt_blocks(const hsa_prompt_args& a);
 cudaError_t launch_prompt_attn(const hsa_prompt_args& a, uint32_t* status, uint64_t wait_ns, cudaStream_t s);
 
 }  // namespace hsa

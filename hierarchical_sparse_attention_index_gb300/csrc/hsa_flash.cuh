@@ -32,6 +32,9 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t
   return true;
 }
 
+// For a CTA's own copies and products in flight, before it ends: nothing may still write into its shared or
+// tensor memory then, however short the caller's limit is
+__device__ __forceinline__ bool drain_bar(uint32_t bar, uint32_t parity) { return wait_bar(bar, parity, kWaitLimitNs); }
 // Whether the phase is complete, without waiting
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t done;

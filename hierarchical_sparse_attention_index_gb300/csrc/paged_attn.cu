@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
   }
   if constexpr (CLUSTER) {
     if (sp.used == 1) return;            // the same in every CTA of the cluster
+    __syncwarp();
     cluster_sync_all();
     // CTA `split` joins every n_splits-th element of the chunk, over the CTAs that have keys
     const uint32_t o_at = smem_u32(sm), ml_at = smem_u32(s_part);
@@ -527,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
       }
       write_out(row, d4, a, M, L);
     }
+    __syncwarp();
     cluster_sync_all();                  // nobody reads this CTA's shared memory any more
   }
 }

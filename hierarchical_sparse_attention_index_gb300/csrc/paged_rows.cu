@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         for (int e = max(0, c[t] - L::kStages); e < c[t]; ++e)
-          ok = wait_bar(kv_full + 8 * (t * L::kStages + e % L::kStages), (e / L::kStages) & 1, rp.wait_ns) && ok;
-      for (int e = max(0, n_q - 2); e < n_q; ++e) ok = wait_bar(q_full + 8 * (e & 1), (e >> 1) & 1, rp.wait_ns) && ok;
+          ok = drain_bar(kv_full + 8 * (t * L::kStages + e % L::kStages), (e / L::kStages) & 1) && ok;
+      for (int e = max(0, n_q - 2); e < n_q; ++e) ok = drain_bar(q_full + 8 * (e & 1), (e >> 1) & 1) && ok;
     } else if (warp < kLoadWarp) {
       // -------------------------------------------------------------- products of one stream
       const int t = warp - kMmaWarp;
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         if (j0 == j1) umma_commit_one(one, q_empty + 8 * (it & 1));
       }
       umma_commit_one(one, drain + 8 * t);       // every product is done before the tensor memory is freed
-      ok = wait_bar(drain + 8 * t, 0, rp.wait_ns) && ok;
+      ok = drain_bar(drain + 8 * t, 0) && ok;
     } else {
       // -------------------------------------------------------------- what comes next
       // A block is taken only when the work before the last has been done by every role, so that no CTA
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
           next_block_ask(answer, answered);
         }
         __syncwarp();
-        ok = wait_bar(answered, n & 1, rp.wait_ns) && ok;
+        ok = drain_bar(answered, n & 1) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const bool more = next_block_take(answer, block);

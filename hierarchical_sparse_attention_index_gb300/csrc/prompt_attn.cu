@@ -149,7 +149,7 @@ struct Order {
     int left = r - above(x + 1);
     auto among = [&](int first, int c, int b) {          // of 32 sequences from `first`, this lane's with c pieces from level b on
       uint32_t m = __ballot_sync(0xffffffffu, b <= x && x < b + c);
-      if (left >= __popc(m)) {
+      if (!m || left >= __popc(m)) {     // (none of them: only where bounds overlap so that the count overflows)
         left -= __popc(m);
         return false;
       }
@@ -170,11 +170,13 @@ struct Order {
   }
 };
 
-// Larger batches are worked off in the order of the sequences, the last piece of each first.
-__device__ __forceinline__ bool find_in_turn(const PromptParams& p, int r, Seq& out, int& i) {
+// Larger batches are worked off in the order of the sequences, the last piece of each first. A search starts
+// at the 32 sequences where the last one ended (`first`, with `before` pieces before them): a CTA's blocks
+// come in rising order, so all its searches together pass over the batch about once.
+__device__ __forceinline__ bool find_in_turn(const PromptParams& p, int r, Seq& out, int& i, int& first, int& before) {
   const int lane = threadIdx.x & 31;
-  int before = 0;
-  for (int first = 0; first < p.batch; first += 32) {
+  if (r < before) first = before = 0;
+  for (; first < p.batch; first += 32) {
     const Seq s = load_seq(p, first + lane);
     int upto = s.count;
 #pragma unroll
@@ -367,10 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       // nothing of this CTA's may be in flight when it ends, whatever the other roles did
       if (lane == 0) {
         for (int e = max(0, c - L::kStages); e < c; ++e)
-          ok = wait_bar(kv_full + 8 * (e % L::kStages), (e / L::kStages) & 1, p.wait_ns) && ok;
+          ok = drain_bar(kv_full + 8 * (e % L::kStages), (e / L::kStages) & 1) && ok;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (n_q[t]) ok = wait_bar(q_full + 8 * t, (n_q[t] - 1) & 1, p.wait_ns) && ok;
+          if (n_q[t]) ok = drain_bar(q_full + 8 * t, (n_q[t] - 1) & 1) && ok;
       }
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       // -------------------------------------------------------------- products of one query tile
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         n_q += has;
       }
       umma_commit_one(one, drain + 8 * t);       // every product is done before the tensor memory is freed
-      ok = wait_bar(drain + 8 * t, 0, p.wait_ns) && ok;
+      ok = drain_bar(drain + 8 * t, 0) && ok;
     } else {
       // -------------------------------------------------------------- what comes next
       // The next block is taken when few of this piece's key tiles are left to load: a CTA that held more
@@ -507,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         order.hold(seqs, p.batch);
       }
       bool is_long = false;
+      int in_turn = 0, pieces = 0;       // find_in_turn's place
       for (int n = 0; ok; ++n) {
         Job job;
         Seq seq;
@@ -517,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
           found = order.find(r, which, i);
           if (found) seq = seqs[which];
         } else {
-          found = find_in_turn(p, r, seq, i);
+          found = find_in_turn(p, r, seq, i, in_turn, pieces);
           if (block == gridDim.x - 1)    // every sequence's bounds are looked at once
             for (int b = lane; b < p.batch; b += 32) load_seq(p, b);
         }
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
           next_block_ask(answer, answered);
         }
         __syncwarp();
-        ok = wait_bar(answered, n & 1, p.wait_ns) && ok;
+        ok = drain_bar(answered, n & 1) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const bool more = next_block_take(answer, block);
@@ -712,6 +715,11 @@ TensorMapEncoder tensor_map_encoder() {
   return fn;
 }
 
+// At most n_q / (2 tt) whole pieces of 2 tt tokens and one more per sequence, and no more than tokens
+int64_t prompt_blocks(const hsa_prompt_args& a) {
+  return imin64(a.n_q / (2 * (kTile / (a.heads_q / a.heads_kv))) + a.batch, a.n_q + 1) * a.heads_kv;
+}
+
 cudaError_t launch_prompt_attn(const hsa_prompt_args& a, uint32_t* status, uint64_t wait_ns, cudaStream_t s) {
   const TensorMapEncoder encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
@@ -722,7 +730,7 @@ cudaError_t launch_prompt_attn(const hsa_prompt_args& a, uint32_t* status, uint6
   p.heads_kv = a.heads_kv;
   p.group = a.heads_q / a.heads_kv;
   p.tt = kTile / p.group;
-  p.window = a.window;
+  p.window = (int32_t)imin64(a.window, 1 << 28);         // beyond every sequence, and its differences fit 32 bits
   p.n_q = a.n_q;
   p.n_k = a.n_k;
   p.out_stride = a.out_stride;
@@ -757,10 +765,7 @@ cudaError_t launch_prompt_attn(const hsa_prompt_args& a, uint32_t* status, uint6
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  // at most n_q / (2 tt) whole tiles and one more per sequence, and no more than tokens
-  const int64_t tiles = imin64(a.n_q / (2 * p.tt) + a.batch, a.n_q + 1);
-  const int64_t blocks = tiles * p.heads_kv;
-  if (blocks > (int64_t)0x7fffffff) return cudaErrorInvalidValue;
+  const int64_t blocks = prompt_blocks(a);
   if (a.head_dim == 128)
     return a.dtype == HSA_BF16 ? launch<128, true>(p, (unsigned)blocks, s) : launch<128, false>(p, (unsigned)blocks, s);
   return a.dtype == HSA_BF16 ? launch<64, true>(p, (unsigned)blocks, s) : launch<64, false>(p, (unsigned)blocks, s);

@@ -140,7 +140,7 @@ typedef struct {
 
 /* Arguments of hsa_prompt_attn. All pointers are device memory; q, k, v and out 16-byte aligned. */
 typedef struct {
-  int32_t batch;       /* sequences, >= 1                                                   */
+  int32_t batch;       /* sequences, 1..2^20                                                */
   int32_t heads_q;     /* a multiple of heads_kv, at most HSA_MAX_GROUP of it               */
   int32_t heads_kv;    /* 1..1024                                                           */
   int32_t head_dim;    /* 64 or 128                                                         */
@@ -346,7 +346,10 @@ HSA_API size_t hsa_paged_attn_workspace_bytes(const hsa_paged_cache* cache, int3
  *   sm_scale  > 0; sm_scale * k_scale * log2 e has to be finite and not 0 in fp32
  *   ws        hsa_paged_attn_workspace_bytes bytes, 16-byte aligned; needs no initialisation
  * Positions on a page id outside [0, n_pages) are skipped and flagged HSA_FLAG_INDEX_RANGE. What
- * the pools hold at positions that no query of the request sees is never used, whatever it is. */
+ * the pools hold at positions that no query of the request sees is never used, whatever it is (a
+ * value that is not finite, at a position that some queries of the request see, may reach its
+ * other queries: its weight there is 0, and 0 times it is NaN). Calls that overlap on the GPU need
+ * a workspace each. */
 HSA_API hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, int32_t q_dtype, int32_t heads_q,
                                  const int32_t* vis, int32_t nq, int64_t max_vis, int32_t window,
                                  float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
@@ -359,8 +362,10 @@ HSA_API hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const voi
  * With no keys (p < 0) o is 0 and lse is -inf. Sums are fp32; the weights are rounded to dtype.
  * Rows of q, out and lse outside [cu_q[0], cu_q[batch]) are neither read for a result nor written.
  * A sequence never uses another's rows, nor rows outside [cu_k[0], cu_k[batch]), whatever they
- * hold. A sequence whose bounds are not ascending inside [0, n_q] and [0, n_k] is skipped and
- * flagged HSA_FLAG_INDEX_RANGE. n_q and n_k <= 2^27; n_q = 0 launches nothing. */
+ * hold; a value of its own that is not finite may reach queries that do not see it, as 0 times it
+ * is NaN. A sequence whose bounds are not ascending inside [0, n_q] and [0, n_k] is skipped and
+ * flagged HSA_FLAG_INDEX_RANGE. n_q and n_k <= 2^27; n_q = 0 launches nothing. Pieces of 2 x
+ * (128 / group) tokens, times heads_kv, have to be fewer than 2^31 (HSA_ERR_SHAPE). */
 HSA_API hsa_status hsa_prompt_attn(const hsa_prompt_args* args, hsa_stream_t stream);
 
 /* Limit of the kernels' bounded waits (for a copy or a tensor-core result that does not arrive),

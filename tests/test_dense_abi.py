@@ -153,3 +153,16 @@ def test_binding_checks(H):
             H._rows("x", t, 2, 64)
     assert H._rows("x", torch.zeros(3, 6, 64)[:, 1:3], 2, 64) == 6 * 64
     assert H._rows("x", torch.zeros(1, 2, 64), 2, 64) == 128
+
+
+def test_grids_that_are_too_large(H):
+    """Sizes that are each in range but whose grid is not are refused, not left to a failing launch."""
+    lib = H.load_library()
+    wide = dict(batch=1, heads_q=131072, heads_kv=1024, head_dim=64, dtype=H.HSA_BF16, window=0, n_q=1 << 27, n_k=100, q=0x10,
+                k=0x20, v=0x30, q_stride=1 << 23, k_stride=1 << 16, v_stride=1 << 16, out_stride=1 << 23, cu_q=0x44, cu_k=None,
+                sm_scale=0.1, out=0x50, lse=None)
+    for change in (dict(), dict(n_q=100, batch=(1 << 20) + 1)):
+        assert lib.hsa_prompt_attn(ctypes.byref(H.hsa_prompt_args(*{**wide, **change}.values())), None) == SHAPE
+    c = cache(H, batch=1 << 20, heads=1024)
+    assert lib.hsa_paged_attn_decode(ctypes.byref(c), 0x10, H.HSA_BF16, 1 << 17, 0x40, 1, 1024, 0, 0.1, 0x10, None, 0x100, 1 << 62,
+                                     None) == SHAPE

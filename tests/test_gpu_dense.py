@@ -436,6 +436,96 @@ def test_prompt_bad_bounds_are_flagged(H):
             assert (out[60:] == 7).all()
 
 
+@pytest.mark.parametrize("batch", [100, 129, 300, 513, 700])
+def test_prompt_many_sequences(H, batch):
+    """Batches past what the search for work holds in registers, and in shared memory; lengths of all sizes."""
+    lens = [(7 * b * b) % 23 for b in range(batch)]
+    lens[batch // 2], lens[-1] = 400, 130
+    past = [(5 * b) % 40 for b in range(batch)]
+    heads, group, dim = 1, 4, 64
+    cu_q, cu_k = [0], [0]
+    for n, o in zip(lens, past):
+        cu_q.append(cu_q[-1] + n)
+        cu_k.append(cu_k[-1] + n + o)
+    g = torch.Generator().manual_seed(batch)
+    q = torch.randn(cu_q[-1], group, dim, generator=g).to(BF).cuda()
+    k, v = (torch.randn(cu_k[-1], heads, dim, generator=g).to(BF).cuda() for _ in range(2))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    out, lse = torch.full_like(q, 7.0), torch.full((cu_q[-1], group), 7.0, device="cuda")
+    H.hsa_prompt_attn(q, k, v, i32(cu_q), 0.125, out, cu_k=i32(cu_k), lse=lse)
+    clean(H)
+    # all sequences at once: query rows of sequence b see the keys of its own only
+    seq = torch.repeat_interleave(torch.arange(batch), torch.tensor(lens)).cuda()
+    pos = torch.arange(cu_q[-1], device="cuda") - i32(cu_q)[seq] + torch.tensor(past).cuda()[seq]
+    lo = i32(cu_k)[seq].long()
+    hi = (lo + pos + 1).repeat_interleave(group)
+    lo = lo.repeat_interleave(group)
+    o, l, A, mag = D.attention(q.reshape(-1, dim).double(), k[:, 0].double(), v[:, 0].double(), lo, hi, 0.125)
+    D.check(out.reshape(-1, dim), lse.reshape(-1), o, l, A, mag, 500, dim, BF)
+    bad = list(cu_q)
+    bad[-1] = cu_q[-1] + 1                          # the last sequence leaves the tensor: skipped, the others computed
+    again = torch.full_like(q, 7.0)
+    H.hsa_prompt_attn(q, k, v, i32(bad), 0.125, again, cu_k=i32(cu_k))
+    clean(H, H.HSA_FLAG_INDEX_RANGE)
+    assert torch.equal(again[:cu_q[-2]], out[:cu_q[-2]]) and (again[cu_q[-2]:] == 7).all()
+
+
+def test_prompt_without_keys_and_odd_strides(H):
+    """No key rows at all; and output rows that start on 16-byte, not 32-byte, boundaries."""
+    q = torch.randn(40, 4, 64).to(BF).cuda()
+    none = torch.empty(0, 2, 64, dtype=BF, device="cuda")
+    cu, zero = torch.tensor([0, 40], dtype=torch.int32).cuda(), torch.zeros(2, dtype=torch.int32).cuda()
+    out, lse = torch.full_like(q, 7.0), torch.zeros(40, 4, device="cuda")
+    H.hsa_prompt_attn(q, none, none, cu, 0.1, out, cu_k=zero, lse=lse)
+    clean(H)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    k, v = torch.randn(40, 2, 64).to(BF).cuda(), torch.randn(40, 2, 64).to(BF).cuda()
+    want = torch.empty_like(q)
+    H.hsa_prompt_attn(q, k, v, cu, 0.1, want)
+    for stride, first in ((4 * 64 + 8, 0), (4 * 64 + 8, 8), (4 * 64 + 16, 8)):
+        room = torch.full((40 * stride + first,), 7.0, dtype=BF, device="cuda")
+        odd = room[first:].as_strided((40, 4, 64), (stride, 64, 1))
+        H.hsa_prompt_attn(q, k, v, cu, 0.1, odd)
+        clean(H)
+        assert torch.equal(odd, want)
+        odd.fill_(7.0)
+        assert (room == 7).all()                    # nothing between the rows was written
+
+
+def test_waits_that_run_out(H):
+    """With a wait limit of 1 ns, work whose roles wait for each other for longer than two suspensions of a wait
+    (20 us each) gives up: both kernels end by themselves, the flag is set, the next calls are not affected."""
+    g = torch.Generator().manual_seed(9)
+    q = torch.randn(16384, 8, 128, generator=g).to(BF).cuda()
+    k, v = (torch.randn(16384, 1, 128, generator=g).to(BF).cuda() for _ in range(2))
+    cu = torch.tensor([0, 16384], dtype=torch.int32).cuda()
+    # 200 requests that share one table row's pages: one split each, 65,536 keys for a CTA
+    pk, pv, table = D.paged(1, [65536], 1, 128, 64, BF, 3)
+    cache = H.PagedCache(pk.cuda(), pv.cuda(), table.expand(200, -1).contiguous().cuda())
+    q_d = torch.randn(200, 5, 8, 128, generator=g).to(BF).cuda()    # 40 rows per key head
+    vis = torch.full((200, 5), 65536, dtype=torch.int32).cuda()
+    ws = H.new_paged_workspace(cache, 8, 5, 65536)
+
+    def calls():
+        out, out_d = torch.zeros_like(q), torch.zeros_like(q_d)
+        H.hsa_prompt_attn(q, k, v, cu, 0.1, out)
+        status_p = H.hsa_get_device_status()
+        H.hsa_paged_attn_decode(cache, q_d, vis, 65536, 0.1, out_d, ws)
+        return out, out_d, status_p, H.hsa_get_device_status()
+
+    want = calls()
+    assert want[2:] == ((0, 0), (0, 0))
+    try:
+        H.hsa_set_wait_limit(1)
+        short = calls()
+    finally:
+        H.hsa_set_wait_limit(0)
+    timeout = (H.STATUS_CODES["HSA_ERR_TIMEOUT"], H.HSA_FLAG_TIMEOUT)
+    assert short[2:] == (timeout, timeout)
+    again = calls()
+    assert again[2:] == ((0, 0), (0, 0)) and torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
 # ------------------------------------------------------------------------------------- together
 def layer(H, cache, x, cu, start, vis, scale, out_p, out_d, q_d, ws):
     H.hsa_prompt_attn(x[:, :8], x[:, 8:10], x[:, 10:12], cu, scale, out_p)
