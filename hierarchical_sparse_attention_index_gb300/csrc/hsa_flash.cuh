@@ -32,6 +32,14 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t
   return true;
 }
 
+// A kernel that hands registers from group to group (setmaxnreg) waits without a limit for more than its launch
+// holds, so what the compiler gave it is looked at before the first launch.
+template <class Kernel>
+bool launches_with(Kernel kernel, int regs) {
+  cudaFuncAttributes attr;
+  return cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(kernel)) == cudaSuccess && attr.numRegs >= regs;
+}
+
 // For a CTA's own copies and products in flight, before it ends: nothing may still write into its shared or
 // tensor memory then, however short the caller's limit is
 __device__ __forceinline__ bool drain_bar(uint32_t bar, uint32_t parity) { return wait_bar(bar, parity, kWaitLimitNs); }
@@ -108,6 +116,15 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// The same from code that the whole warp runs (`one` is nonzero in the lane that issues)
+__device__ __forceinline__ void tma_4d_one(uint32_t one, uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %7, 0;\n"
+      "@p cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6]; }" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "r"(one)
       : "memory");
 }
 

@@ -533,15 +533,17 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
   }
 }
 
-// The splits of one row, joined in their order: o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
-// A warp per row, a lane per D / 32 dims; a few KB per row, so what counts is that the loads of
-// several splits are in flight at once (unrolled by 4).
-template <int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
+// The splits of one row, joined in a fixed order: o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
+// A lane per D / 32 dims; a few KB per row and split, so what counts is that the loads of several splits are
+// in flight at once: unrolled by 4, and by W warps per row, each of which takes every W-th split.
+constexpr int kJoinWide = 8;             // warps per row for more than this many splits, else one
+template <int D, int W>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, rows = p.nq * p.group;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);       // (b, h, row)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = p.nq * p.group;
+  const int64_t id = W == 1 ? (int64_t)blockIdx.x * 4 + warp : (int64_t)blockIdx.x;         // (b, h, row)
+  const int first_split = W == 1 ? 0 : warp;
   if (id >= (int64_t)p.batch * p.heads * rows) return;
   const int row = (int)(id % rows);
   const int64_t bh = id / rows;
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
 #pragma unroll
   for (int e = 0; e < V; ++e) a[e] = 0.f;
 #pragma unroll 4
-  for (int c = 0; c < sp.used; ++c) {
+  for (int c = first_split; c < sp.used; c += W) {
     const int64_t at = first + (int64_t)c * rows;
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at));
     float x[V];
@@ -578,6 +580,20 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
       L += f * ml.y;
 #pragma unroll
       for (int e = 0; e < V; ++e) a[e] += f * x[e];
+    }
+  }
+  if constexpr (W > 1) {                 // the warps' sums, in order
+    __shared__ float s_sum[W][V + 1][32];
+#pragma unroll
+    for (int e = 0; e < V; ++e) s_sum[warp][e][lane] = a[e];
+    s_sum[warp][V][lane] = L;
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) a[e] += s_sum[w][e][lane];
+      L += s_sum[w][V][lane];
     }
   }
   const int64_t at = ((int64_t)b * p.nq + row / p.group) * p.heads_q + h * p.group + row % p.group;
@@ -690,9 +706,14 @@ cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedSplit& sp, in
                                           : launch_kv<64>(p, kv_dtype, s);
   if (e != cudaSuccess || !sp.joined) return e;
   const int64_t ids = (int64_t)p.batch * p.heads * p.nq * p.group;
+  if (p.n_splits > kJoinWide) {
+    const dim3 grid((unsigned)ids), block(32 * kJoinWide);
+    return head_dim == 128 ? launch_pdl(paged_join_kernel<128, kJoinWide>, grid, block, 0, s, p)
+                           : launch_pdl(paged_join_kernel<64, kJoinWide>, grid, block, 0, s, p);
+  }
   const dim3 grid((unsigned)((ids + 3) / 4));
-  return head_dim == 128 ? launch_pdl(paged_join_kernel<128>, grid, dim3(128), 0, s, p)
-                         : launch_pdl(paged_join_kernel<64>, grid, dim3(128), 0, s, p);
+  return head_dim == 128 ? launch_pdl(paged_join_kernel<128, 1>, grid, dim3(128), 0, s, p)
+                         : launch_pdl(paged_join_kernel<64, 1>, grid, dim3(128), 0, s, p);
 }
 
 }  // namespace hsa

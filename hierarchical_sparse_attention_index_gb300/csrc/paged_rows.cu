@@ -32,25 +32,32 @@ namespace {
 constexpr int kTile = 128;               // query rows
 constexpr int kKeys = 64;                // keys of a tile
 constexpr int kSoftWarps = 8;            // 4 per stream: two warp groups; the third holds the other roles
-constexpr int kMmaWarp = 8, kLoadWarp = 10;              // a warp per stream's products; warp 11 finds the work
-constexpr int kThreads = 12 * 32;
-constexpr int kSoftRegs = 208, kOtherRegs = 88;          // as in the prompt kernel: 2 x 208 + 88 = 3 x 168 at launch
+constexpr int kMmaWarp = 8, kLoadWarp = 10;              // a warp per stream's products, and one per stream's loads
+constexpr int kOutWarp = 12;             // warps 12..15 merge the streams and write
+constexpr int kFindWarp = 16;            // finds the work; warps 17..19 only fill its warp group
+constexpr int kThreads = 20 * 32;
+// registers per thread: 96 at launch (65,536 over 640 threads, whole groups of 8), then 136 for the softmax groups,
+// whose threads hold a row of 64 logits, 80 for the next two and 48 for the last
+constexpr int kLaunchRegs = 96, kSoftRegs = 136, kOtherRegs = 80, kFindRegs = 48;
+static_assert(2 * kSoftRegs + 2 * kOtherRegs + kFindRegs <= 5 * kLaunchRegs, "setmaxnreg draws on the launch's registers");
 constexpr uint32_t kBlockQ = kTile * 128, kBlockK = kKeys * 128;   // 64 dims of a tile, 128 bytes a row
 constexpr int kJobSlots = 2;
 
 template <int D>
 struct Shape {
-  static constexpr uint32_t kQBytes = (D / 64) * kBlockQ, kKvBytes = (D / 64) * kBlockK;
-  static constexpr int kStages = D == 128 ? 4 : 8;               // tiles of K and V in a stream's ring
-  static constexpr uint32_t kOffQ = 0, kOffKv = 2 * kQBytes;     // Q of two jobs
-  static constexpr uint32_t kOffStage = kOffKv + 2 * kStages * kKvBytes, kSmem = kOffStage + kSoftWarps * 2048 + 1024;   // + alignment slack
+  static constexpr uint32_t kKvBytes = (D / 64) * kBlockK;
+  static constexpr int kMaxStages = D == 128 ? 6 : 12;           // tiles of K and V in a stream's ring
 };
+constexpr uint32_t kSmemMost = 227 * 1024 - 4096;                // but for what is declared in the kernel
 
 struct RowsParams {
   CUtensorMap qm, km, vm;
   PagedAttnParams a;
   int32_t tt;                            // queries per chunk: 128 / group
   int32_t box;                           // rows of a box of the pools
+  int32_t q_rows;                        // rows of a query block in shared memory: tt x group, whole groups of 8
+  int32_t stages;                        // of a stream's ring: what the queries leave room for
+  int32_t wide;                          // results start on 32-byte boundaries
   uint64_t wait_ns;
 };
 
@@ -67,20 +74,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   const PagedAttnParams& p = rp.a;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Job s_job[kJobSlots];
-  __shared__ float2 s_ml[2][2][kTile];                   // of jobs in turn, each stream's (m in log2 units, l) of a row
+  __shared__ int s_pages[kJobSlots][2][32];              // pages of either stream's first tiles
+  __shared__ float2 s_ml[2][kTile];                      // each stream's (m in log2 units, l) of a row
   __shared__ __align__(16) uint4 s_answer;
   __shared__ uint32_t s_tmem;
-  __shared__ __align__(8) uint64_t s_bars[25 + 2 * kJobSlots + 4 * L::kStages];
+  __shared__ __align__(8) uint64_t s_bars[23 + 2 * kJobSlots + 4 * L::kMaxStages];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-  const uint32_t sQ = base + L::kOffQ, sKv = base + L::kOffKv;
-  // mbarriers: Q loaded / read by both streams' last products, for jobs in turn; for each stream O read,
-  // every product done; two for each stream, for key tiles in turn: S computed, P written, P V added to O.
-  // Then the two warps of 32 rows meeting, the launcher's answer, the jobs and the rings
+  // Q of two jobs, then the rings. A product reads 128 rows from a query block's start: past its own rows it
+  // reads on into what follows, and those rows of S are no one's.
+  const uint32_t q_block = (uint32_t)rp.q_rows * 128u, q_bytes = (D / 64) * q_block;
+  const uint32_t sQ = base, sKv = base + 2 * q_bytes;
+  const int stages = rp.stages;
+  // mbarriers: Q loaded / read by both streams' last products, for jobs in turn; for each stream O and (m, l)
+  // read, every product done; two for each stream, for key tiles in turn: S computed, P written, P V added
+  // to O. Then (m, l) written by each stream, the launcher's answer, the jobs and the rings
   const uint32_t bars = smem_u32(s_bars);
   const uint32_t q_full = bars, q_empty = bars + 16, o_empty = bars + 32, drain = bars + 48, s_full = bars + 64, p_full = bars + 96,
-                 o_full = bars + 128, pair = bars + 160, answered = bars + 192, job_full = bars + 200, job_empty = job_full + 8 * kJobSlots,
-                 kv_full = job_empty + 8 * kJobSlots, kv_empty = kv_full + 16 * L::kStages;
-  static_assert(200 + 16 * kJobSlots + 32 * L::kStages <= sizeof(s_bars), "barriers");
+                 o_full = bars + 128, ml_full = bars + 160, answered = bars + 176, job_full = bars + 184, job_empty = job_full + 8 * kJobSlots,
+                 kv_full = job_empty + 8 * kJobSlots, kv_empty = kv_full + 16 * L::kMaxStages;
+  static_assert(184 + 16 * kJobSlots + 32 * L::kMaxStages <= sizeof(s_bars), "barriers");
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -88,7 +100,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full + 8 * t, 1);
       mbar_init(q_empty + 8 * t, 2);
-      mbar_init(o_empty + 8 * t, kSoftWarps);
+      mbar_init(o_empty + 8 * t, 4);
+      mbar_init(ml_full + 8 * t, 4);
       mbar_init(drain + 8 * t, 1);
       for (int b = 0; b < 2; ++b) {
         mbar_init(s_full + 16 * t + 8 * b, 1);
@@ -96,13 +109,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         mbar_init(o_full + 16 * t + 8 * b, 1);
       }
     }
-    for (int w = 0; w < 4; ++w) mbar_init(pair + 8 * w, 2);
     mbar_init(answered, 1);
     for (int s = 0; s < kJobSlots; ++s) {
       mbar_init(job_full + 8 * s, 1);
-      mbar_init(job_empty + 8 * s, kSoftWarps + 3);
+      mbar_init(job_empty + 8 * s, kSoftWarps + 4 + 4);
     }
-    for (int s = 0; s < 2 * L::kStages; ++s) {
+    for (int s = 0; s < 2 * L::kMaxStages; ++s) {
       mbar_init(kv_full + 8 * s, 1);
       mbar_init(kv_empty + 8 * s, 1);
     }
@@ -134,102 +146,112 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     return true;
   };
 
-  if (warp >= kSoftWarps) {
+  // Pages of 32 / blocks tiles of a stream at a time, one block per lane, looked up a turn ahead (the first turn's
+  // when the job is posted: two reads that depend on each other, which would leave the memory idle between
+  // jobs); n_pages: no page (TMA then fills in zeros)
+  const int blocks = kKeys / rp.box, per = 32 / blocks;
+  auto find_pages = [&](const Job& job, int j0, int j1, int turn) {
+    const int j = j0 + turn * per + lane / blocks, pos = kKeys * j + rp.box * (lane % blocks);
+    int page = (int)p.n_pages;
+    if (j < j1 && pos < job.hi && pos + rp.box > job.lo) {
+      const int x = p.table[(int64_t)job.b * p.max_pages + pos / p.page_size];
+      if (x >= 0 && x < p.n_pages)
+        page = x;
+      else
+        flag_status(p.status, HSA_FLAG_INDEX_RANGE);
+    }
+    return page;
+  };
+
+  if (warp >= kSoftWarps && warp < kOutWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kLoadWarp) {
-      // -------------------------------------------------------------- loads
-      // Lane (block, part) of a tile issues one box: `box` positions x 64 dims. Both streams' rings hold
-      // K(0) K(1) V(0) K(2) V(1) ... V(n-1): the products of S run a tile ahead of those with V.
-      const int blocks = kKeys / rp.box, part = lane % (D / 64), block = lane / (D / 64);
-      int n_q = 0, c[2] = {0, 0};        // queries loaded; tiles of each ring loaded
+    if (warp >= kLoadWarp) {
+      // -------------------------------------------------------------- loads of one stream, the first's with the queries
+      // The ring holds K(0) K(1) V(0) K(2) V(1) ... V(n-1): the products of S run a tile ahead of those with V.
+      // Issuing the boxes of a 16 KB tile takes a warp 450 ns, longer than the tile's share of HBM: hence a warp per
+      // stream, and warp-uniform operands (a lane for each box: 600).
+      const int t = warp - kLoadWarp;
+      const uint32_t full = kv_full + 8 * t * L::kMaxStages, empty = kv_empty + 8 * t * L::kMaxStages, ring = sKv + t * stages * L::kKvBytes;
+      int n_q = 0, c = 0, place = 0, round = 0;      // queries loaded; tiles of the ring loaded, and its place
       Job job;
-      // Pages of 32 / blocks tiles at a time, one block per lane, looked up a turn ahead; n_pages: no page
-      // (TMA then fills in zeros)
-      const int per = 32 / blocks;
-      int pages[2], pages_next[2];
-      auto find_pages = [&](int t, int turn) {
-        const int j = job.j0[t] + turn * per + lane / blocks, pos = kKeys * j + rp.box * (lane % blocks);
-        int page = (int)p.n_pages;
-        if (j < job.j1[t] && pos < job.hi && pos + rp.box > job.lo) {
-          const int x = p.table[(int64_t)job.b * p.max_pages + pos / p.page_size];
-          if (x >= 0 && x < p.n_pages)
-            page = x;
-          else
-            flag_status(p.status, HSA_FLAG_INDEX_RANGE);
-        }
-        return page;
+      int job_h = 0, j0 = 0, j1 = 0;     // the key head, and this stream's tiles
+      int2 pages, pages_next;            // (page, row in it) of this lane's block of a turn
+      const uint32_t one = elect_one();
+      auto rows_of = [&](int turn, int page) {
+        return make_int2(page, (kKeys * (j0 + turn * per + lane / blocks) + rp.box * (lane % blocks)) % p.page_size);
       };
-      auto page_of = [&](int t, int i) {   // of this lane's block of tile j0 + i; called with i = 0, 1, 2, ...
-        if (i > 0 && i % per == 0) {
-          pages[t] = pages_next[t];
-          pages_next[t] = find_pages(t, i / per + 1);
+      auto page_of = [&](int i) {        // tile j0 + i, block `lane` of it; called with i = 0, 1, 2, ...
+        if (i > 0 && (i & (per - 1)) == 0) {
+          pages = pages_next;
+          pages_next = rows_of(i / per + 1, find_pages(job, j0, j1, i / per + 1));
         }
-        return __shfl_sync(0xffffffffu, pages[t], (i % per) * blocks + block % blocks);
+        const int src = (i & (per - 1)) * blocks + (lane & (blocks - 1));
+        return make_int2(__shfl_sync(0xffffffffu, pages.x, src), __shfl_sync(0xffffffffu, pages.y, src));
       };
-      auto load_kv = [&](int t, int j, int page, const CUtensorMap* map) {
-        const int s = c[t] % L::kStages;
-        const uint32_t bar = 8 * (t * L::kStages + s);
-        ok = ok && wait_bar(kv_empty + bar, ((c[t] / L::kStages) & 1) ^ 1, rp.wait_ns);
+      auto load_kv = [&](int2 at, const CUtensorMap* map) {
+        ok = wait_bar(empty + 8 * place, (round & 1) ^ 1, rp.wait_ns) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(kv_full + bar, L::kKvBytes);
+        const uint32_t bar = full + 8 * place, dst = ring + place * L::kKvBytes;
+        if (one) mbar_arrive_expect_tx(bar, L::kKvBytes);
         __syncwarp();
-        if (block < blocks)
-          tma_4d(sKv + (t * L::kStages + s) * L::kKvBytes + part * kBlockK + (uint32_t)(block * rp.box) * 128u, map, 64 * part,
-                 (kKeys * j + rp.box * block) % p.page_size, job.h, page, kv_full + bar);
-        ++c[t];
-      };
-      for (int it = 0; take_job(it, job); ++it) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          pages[t] = find_pages(t, 0);
-          pages_next[t] = find_pages(t, 1);
-        }
-        const int qs = it & 1;
-        ok = wait_bar(q_empty + 8 * qs, ((it >> 1) & 1) ^ 1, rp.wait_ns) && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(q_full + 8 * qs, (D / 64) * (uint32_t)(rp.tt * p.group) * 128u);
+        for (int b = 0; b < blocks; ++b) {
+          const int page = __shfl_sync(0xffffffffu, at.x, b), row = __shfl_sync(0xffffffffu, at.y, b);
 #pragma unroll
           for (int d = 0; d < D / 64; ++d)
-            tma_4d(sQ + qs * L::kQBytes + d * kBlockQ, &rp.qm, 64 * d, 0, job.h, job.b * p.nq + job.chunk * rp.tt, q_full + 8 * qs);
+            tma_4d_one(one, dst + d * kBlockK + (uint32_t)(b * rp.box) * 128u, map, 64 * d, row, job_h, page, bar);
         }
-        ++n_q;
-        int at[2] = {0, 0}, ahead[2] = {0, 0};       // pages of the tiles whose V and K come next
+        ++c;
+        if (++place == stages) {
+          place = 0;
+          ++round;
+        }
+      };
+      for (int it = 0; wait_job(it); ++it) {
+        job = s_job[it % kJobSlots];
+        job_h = uniform(job.h);
+        j0 = t ? job.j0[1] : job.j0[0];
+        j1 = t ? job.j1[1] : job.j1[0];
+        pages = rows_of(0, s_pages[it % kJobSlots][t][lane]);
+        free_job(it);
+        if (t == 0) {
+          const int qs = it & 1;
+          ok = wait_bar(q_empty + 8 * qs, ((it >> 1) & 1) ^ 1, rp.wait_ns) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (one) mbar_arrive_expect_tx(q_full + 8 * qs, (D / 64) * (uint32_t)(rp.tt * p.group) * 128u);
+          __syncwarp();
+          const int q_at = uniform(job.b * p.nq + job.chunk * rp.tt);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (job.j0[t] < job.j1[t]) {
-            at[t] = page_of(t, 0);
-            load_kv(t, job.j0[t], at[t], &rp.km);
-          }
-        const int n = max(job.j1[0] - job.j0[0], job.j1[1] - job.j0[1]);
+          for (int d = 0; d < D / 64; ++d)
+            tma_4d_one(one, sQ + qs * q_bytes + d * q_block, &rp.qm, 64 * d, 0, job_h, q_at, q_full + 8 * qs);
+          ++n_q;
+        }
+        const int n = j1 - j0;
+        int2 at = {}, ahead = {};        // pages of the tiles whose V and K come next
+        if (n > 0) {
+          at = page_of(0);
+          load_kv(at, &rp.km);
+          pages_next = rows_of(1, find_pages(job, j0, j1, 1));
+        }
         for (int i = 0; i < n && ok; ++i) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (job.j0[t] + i + 1 < job.j1[t] && ok) {
-              ahead[t] = page_of(t, i + 1);
-              load_kv(t, job.j0[t] + i + 1, ahead[t], &rp.km);
-            }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (job.j0[t] + i < job.j1[t] && ok) load_kv(t, job.j0[t] + i, at[t], &rp.vm);
-            at[t] = ahead[t];
+          if (i + 1 < n) {
+            ahead = page_of(i + 1);
+            load_kv(ahead, &rp.km);
           }
+          if (ok) load_kv(at, &rp.vm);
+          at = ahead;
         }
         if (!ok) break;
       }
       // nothing of this CTA's may be in flight when it ends, whatever the other roles did
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        for (int e = max(0, c[t] - L::kStages); e < c[t]; ++e)
-          ok = drain_bar(kv_full + 8 * (t * L::kStages + e % L::kStages), (e / L::kStages) & 1) && ok;
+      for (int e = max(0, c - stages); e < c; ++e) ok = drain_bar(full + 8 * (e % stages), (e / stages) & 1) && ok;
       for (int e = max(0, n_q - 2); e < n_q; ++e) ok = drain_bar(q_full + 8 * (e & 1), (e >> 1) & 1) && ok;
-    } else if (warp < kLoadWarp) {
+    } else {
       // -------------------------------------------------------------- products of one stream
       const int t = warp - kMmaWarp;
-      const uint32_t tS = tmem + 128 * t, tO = tmem + 256 + 128 * t, ring = sKv + t * L::kStages * L::kKvBytes;
-      const uint32_t full = kv_full + 8 * t * L::kStages, empty = kv_empty + 8 * t * L::kStages;
+      const uint32_t tS = tmem + 128 * t, tO = tmem + 256 + 128 * t, ring = sKv + t * stages * L::kKvBytes;
+      const uint32_t full = kv_full + 8 * t * L::kMaxStages, empty = kv_empty + 8 * t * L::kMaxStages;
       const uint32_t id_qk = idesc_f16(kTile, kKeys, false, false, BF16), id_pv = idesc_f16(kTile, D, false, true, BF16);
       const uint32_t one = elect_one();
       auto wait = [&](uint32_t bar, int n) {
@@ -238,25 +260,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         tc_fence_after();
         return ok;
       };
-      int n_s = 0, n_p = 0, c = 0;       // key tiles of S and P, tiles of the ring
-      auto wait_kv = [&]() { return wait(full + 8 * (c % L::kStages), c / L::kStages); };
+      int n_s = 0, n_p = 0, c = 0, turn = 0;     // key tiles of S and P; place in the ring
+      auto wait_kv = [&]() { return wait(full + 8 * c, turn); };
       auto free_kv = [&]() {
-        umma_commit_one(one, empty + 8 * (c % L::kStages));
-        ++c;
+        umma_commit_one(one, empty + 8 * c);
+        if (++c == stages) {
+          c = 0;
+          ++turn;
+        }
       };
       auto qk = [&](int it) {
-        const uint64_t dq = sdesc(sQ + (it & 1) * L::kQBytes, 16u, 1024u);
-        const uint64_t dk = sdesc(ring + (c % L::kStages) * L::kKvBytes, 16u, 1024u);
+        const uint64_t dq = sdesc(sQ + (it & 1) * q_bytes, 16u, 1024u);
+        const uint64_t dk = sdesc(ring + c * L::kKvBytes, 16u, 1024u);
         const uint32_t at = tS + 64 * (n_s & 1);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          umma_ss(one, at, dq + (((k >> 2) * kBlockQ + (k & 3) * 32u) >> 4), dk + (((k >> 2) * kBlockK + (k & 3) * 32u) >> 4), id_qk,
+          umma_ss(one, at, dq + (((k >> 2) * q_block + (k & 3) * 32u) >> 4), dk + (((k >> 2) * kBlockK + (k & 3) * 32u) >> 4), id_qk,
                   k > 0);
         umma_commit_one(one, s_full + 16 * t + 8 * (n_s & 1));
         ++n_s;
       };
       auto pv = [&](bool acc) {
-        const uint64_t dv = sdesc(ring + (c % L::kStages) * L::kKvBytes, kBlockK, 1024u);
+        const uint64_t dv = sdesc(ring + c * L::kKvBytes, kBlockK, 1024u);
         const uint32_t at = tS + 64 * (n_p & 1);
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k) umma_ts(one, tO, at + 8 * k, dv + ((k * 16u * 128u) >> 4), id_pv, acc || k > 0);
@@ -283,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
           if (!wait_kv()) break;
           const int first = max(0, lo - kKeys * j), end = min(kKeys, hi - kKeys * j);   // rows that some query sees
           if (first > 0 || end < kKeys) {
-            const uint32_t v = ring + (c % L::kStages) * L::kKvBytes;
+            const uint32_t v = ring + c * L::kKvBytes;
             for (int x = lane; x < kKeys * 8; x += 32)
               if ((x >> 3) < first || (x >> 3) >= end)
 #pragma unroll
@@ -302,71 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       }
       umma_commit_one(one, drain + 8 * t);       // every product is done before the tensor memory is freed
       ok = drain_bar(drain + 8 * t, 0) && ok;
-    } else {
-      // -------------------------------------------------------------- what comes next
-      // A block is taken only when the work before the last has been done by every role, so that no CTA
-      // holds back more than one piece of work (taking three ahead left ragged batches uneven).
-      const uint32_t answer = smem_u32(&s_answer);
-      uint32_t block = blockIdx.x;
-      int it = 0;
-      auto wait_slot = [&]() {
-        ok = wait_bar(job_empty + 8 * (it % kJobSlots), ((it / kJobSlots) & 1) ^ 1, rp.wait_ns) && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        return ok;
-      };
-      for (int n = 0; ok; ++n) {
-        Job job;
-        int idx = (int)block;
-        job.chunk = idx % p.chunks;
-        idx /= p.chunks;
-        job.h = idx % p.heads;
-        idx /= p.heads;
-        job.b = idx % p.batch;
-        job.split = idx / p.batch;
-        job.more = 1;
-        const Span sp = request_span(p, job.b);
-        job.lo = sp.lo;
-        job.hi = sp.hi;
-        if (lane < p.nq && job.split == 0 && job.h == 0) {
-          const int raw = p.vis[(int64_t)job.b * p.nq + lane];
-          if (raw != clamp_vis(p, raw)) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
-        }
-        if (job.split < sp.used) {
-          const int begin = (sp.base + job.split * sp.len) / kKeys, end = (min(sp.base + (job.split + 1) * sp.len, sp.hi) + kKeys - 1) / kKeys;
-          const int half = (max(0, end - begin) + 1) / 2;
-          job.j0[0] = begin;
-          job.j1[0] = job.j0[1] = begin + half;
-          job.j1[1] = max(end, begin + half);
-          job.whole = sp.used == 1;
-          if (!wait_slot()) break;
-          if (lane == 0) {
-            s_job[it % kJobSlots] = job;
-            mbar_arrive(job_full + 8 * (it % kJobSlots));
-          }
-          ++it;
-        }
-        if (!wait_slot()) break;
-        if (lane == 0) {
-          fence_async_smem();            // the last answer has been read
-          mbar_arrive_expect_tx(answered, 16);
-          next_block_ask(answer, answered);
-        }
-        __syncwarp();
-        ok = drain_bar(answered, n & 1) && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const bool more = next_block_take(answer, block);
-        __syncwarp();
-        if (!more) {
-          if (lane == 0) {
-            s_job[it % kJobSlots].more = 0;
-            mbar_arrive(job_full + 8 * (it % kJobSlots));
-          }
-          break;
-        }
-      }
     }
-  } else {
+  } else if (warp < kSoftWarps) {
     // ---------------------------------------------------------------- softmax: one row per thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;
@@ -379,9 +341,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       const int j0 = t ? job.j0[1] : job.j0[0], j1 = t ? job.j1[1] : job.j1[0], b = job.b, job_hi = job.hi;
       const int row = job.chunk * rp.tt * p.group + r;
       const bool real = r < rp.tt * p.group && row < rows;
-      const int h = job.h, partner = t ? job.j1[0] - job.j0[0] : job.j1[1] - job.j0[1];   // the other stream's tiles
-      const bool whole = job.whole;
-      const int64_t slot = ((int64_t)b * p.heads + h) * p.n_splits + job.split;
       const bool warp_real = (warp & 3) * 32 < rp.tt * p.group && job.chunk * rp.tt * p.group + (warp & 3) * 32 < rows;
       int lo = 0, hi = 0;                // this row's keys
       if (real) {
@@ -389,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         lo = p.window > 0 ? max(hi - p.window, 0) : 0;
       }
       const int all_lo = __reduce_max_sync(0xffffffffu, real ? lo : 0), all_hi = __reduce_min_sync(0xffffffffu, real ? hi : 0x7fffffff);
+      free_job(it);
       const bool small = p.page_size < kKeys || p.page_size % kKeys;   // a tile may lie on several pages
       float m = -INFINITY, l = 0.f;
       // pages of the tile's 16-row pieces, looked up a tile ahead by lanes 0..3: a bad one masks its keys
@@ -430,89 +390,157 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * (n_s & 1));
       }
       if (!ok) break;
-      // -------------------------------------------------------------- both streams' O and (m, l)
-      if (j0 < j1) {
-        ok = wait_bar(o_full + 16 * t + 8 * ((n_s - 1) & 1), ((n_s - 1) >> 1) & 1, rp.wait_ns) && ok;   // the last P V
-        ok = __all_sync(0xffffffffu, ok);
-      }
-      const float m2 = m == -INFINITY ? m : m * scale;
-      s_ml[it & 1][t][r] = make_float2(m2, l);
-      tc_fence_before();
+      // (m, l) to the warps that write, when they have read the last job's
+      ok = wait_bar(o_empty + 8 * t, (it & 1) ^ 1, rp.wait_ns) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      s_ml[t][r] = make_float2(m == -INFINITY ? m : m * scale, l);
       __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(pair + 8 * (warp & 3));
-      ok = ok && wait_bar(pair + 8 * (warp & 3), it & 1, rp.wait_ns);
+      if (lane == 0) mbar_arrive(ml_full + 8 * t);
+    }
+  } else if (warp < kFindWarp) {
+    // ---------------------------------------------------------------- both streams' O and (m, l), while the softmax is at the next job
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    const int r = (warp & 3) * 32 + lane, rows = p.nq * p.group;
+    const uint32_t tO = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u;
+    int n_s[2] = {0, 0};                 // key tiles of either stream so far
+    for (int it = 0; wait_job(it); ++it) {
+      const Job& job = s_job[it % kJobSlots];
+      const int tiles[2] = {job.j1[0] - job.j0[0], job.j1[1] - job.j0[1]};
+      const int row = job.chunk * rp.tt * p.group + r;
+      const bool real = r < rp.tt * p.group && row < rows, warp_real = __any_sync(0xffffffffu, real), whole = job.whole;
+      const int64_t slot = ((int64_t)job.b * p.heads + job.h) * p.n_splits + job.split;
+      const int64_t at = ((int64_t)job.b * p.nq + row / p.group) * p.heads_q + job.h * p.group + row % p.group;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        ok = ok && wait_bar(ml_full + 8 * t, it & 1, rp.wait_ns);
+        n_s[t] += tiles[t];
+        if (tiles[t] > 0) ok = ok && wait_bar(o_full + 16 * t + 8 * ((n_s[t] - 1) & 1), ((n_s[t] - 1) >> 1) & 1, rp.wait_ns);   // the last P V
+      }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const float2 other = s_ml[it & 1][t ^ 1][r];
-      const bool mine_any = m2 != -INFINITY || l != 0.f, other_any = other.x != -INFINITY || other.y != 0.f;
-      const float M = fmaxf(m2, other.x);
-      const float fm = m2 == -INFINITY ? 0.f : ex2_ftz(m2 - M), fo = other.x == -INFINITY ? 0.f : ex2_ftz(other.x - M);
-      const float lsum = (mine_any ? fm * l : 0.f) + (other_any ? fo * other.y : 0.f);
+      const float2 a = s_ml[0][r], b = s_ml[1][r];
+      const bool any_a = a.x != -INFINITY || a.y != 0.f, any_b = b.x != -INFINITY || b.y != 0.f;
+      const float M = fmaxf(a.x, b.x);
+      const float fa = a.x == -INFINITY ? 0.f : ex2_ftz(a.x - M), fb = b.x == -INFINITY ? 0.f : ex2_ftz(b.x - M);
+      const float lsum = (any_a ? fa * a.y : 0.f) + (any_b ? fb * b.y : 0.f);
       const float gain = !whole ? 1.f : (lsum != 0.f ? p.v_scale / lsum : 0.f);
-      const uint32_t tM = tO + (D / 2) * t, tP = tM + (t ? -128 : 128);   // this warp's half of the dims, in either stream's O
-      const int row0 = row - lane, row_end = min(rows, (row - r) + rp.tt * p.group);   // this warp's first row, and past the chunk's last
-      const uint32_t stage = base + L::kOffStage + (uint32_t)warp * 2048u;
-      free_job(it);
-      if (warp_real) {
-#pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t x[32], y[32];
-          if (j0 < j1) TMEM_LD32(tM + 32 * c, x);
-          if (partner > 0) TMEM_LD32(tP + 32 * c, y);
-          tmem_wait_ld();
-          tmem_regs_ready(x);
-          tmem_regs_ready(y);
+      auto done = [&]() {                // O and (m, l) are in registers
+        tc_fence_before();
+        free_job(it);
+        if (lane == 0) {
+          mbar_arrive(o_empty);
+          mbar_arrive(o_empty + 8);
+        }
+      };
+      if (!warp_real) {
+        done();
+        continue;
+      }
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            x[e] = __float_as_uint(((mine_any ? fm * __uint_as_float(x[e]) : 0.f) + (other_any ? fo * __uint_as_float(y[e]) : 0.f)) * gain);
-          // 64 bytes of each row at a time go through shared memory, so that four lanes write them together:
-          // this lane then holds piece lane % 4 of rows 8 i + lane / 4
-          auto flush = [&](auto&& piece, auto&& place) {
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t x[16], y[16];
+        if (tiles[0] > 0) TMEM_LD16(tO + 16 * c, x);
+        if (tiles[1] > 0) TMEM_LD16(tO + 128 + 16 * c, y);
+        tmem_wait_ld();
+        tmem_regs_ready(x);
+        tmem_regs_ready(y);
+        if (c == D / 16 - 1) done();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint4 v = piece(e);
-              sts128(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4), v.x, v.y, v.z, v.w);
+        for (int e = 0; e < 16; ++e)
+          x[e] = __float_as_uint(((any_a ? fa * __uint_as_float(x[e]) : 0.f) + (any_b ? fb * __uint_as_float(y[e]) : 0.f)) * gain);
+        // each lane writes its own row, 32 bytes at a time where the rows allow it
+        if (whole)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = pack2<BF16>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+        if (real) {
+          uint32_t* dst = whole ? reinterpret_cast<uint32_t*>(p.out + at * D + 16 * c) : reinterpret_cast<uint32_t*>(p.part_o + (slot * rows + row) * D + 16 * c);
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            if (e == 0 || !whole) {
+              if (rp.wide) {
+                st_global_256(dst + e, x + e);
+              } else {
+                *reinterpret_cast<uint4*>(dst + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                *reinterpret_cast<uint4*>(dst + e + 4) = make_uint4(x[e + 4], x[e + 5], x[e + 6], x[e + 7]);
+              }
             }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int sr = 8 * i + (lane >> 2);
-              const uint4 v = lds128(stage + sr * 64 + (((lane & 3) ^ ((sr >> 1) & 3)) << 4));
-              if (row0 + sr < row_end) *place(row0 + sr) = v;
-            }
-            __syncwarp();
-          };
-          const int d = (D / 2) * t + 32 * c;
-          if (!whole) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              flush([&](int e) { return make_uint4(x[16 * u + 4 * e], x[16 * u + 4 * e + 1], x[16 * u + 4 * e + 2], x[16 * u + 4 * e + 3]); },
-                    [&](int rw) { return reinterpret_cast<uint4*>(p.part_o + (slot * rows + rw) * D + d + 16 * u) + (lane & 3); });
-          } else {
-            flush(
-                [&](int e) {
-                  auto two = [&](int i) { return pack2<BF16>(__uint_as_float(x[8 * e + 2 * i]), __uint_as_float(x[8 * e + 2 * i + 1])); };
-                  return make_uint4(two(0), two(1), two(2), two(3));
-                },
-                [&](int rw) {
-                  const int64_t at = ((int64_t)b * p.nq + rw / p.group) * p.heads_q + h * p.group + rw % p.group;
-                  return reinterpret_cast<uint4*>(p.out + at * D + d) + (lane & 3);
-                });
-          }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(o_empty);
-        mbar_arrive(o_empty + 8);
-      }
-      if (real && t == 0) {
+      if (real) {
         if (!whole)
           *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * rows + row)) = make_float2(M, lsum);
         else if (p.lse)
-          p.lse[((int64_t)b * p.nq + row / p.group) * p.heads_q + h * p.group + row % p.group] = lsum != 0.f ? (M + log2f(lsum)) * kLn2 : -INFINITY;
+          p.lse[at] = lsum != 0.f ? (M + log2f(lsum)) * kLn2 : -INFINITY;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFindRegs));
+    // ---------------------------------------------------------------- what comes next
+    // A block is taken only when the work before the last has been done by every role, so that no CTA
+    // holds back more than one piece of work (taking three ahead left ragged batches uneven).
+    const uint32_t answer = smem_u32(&s_answer);
+    uint32_t block = blockIdx.x;
+    int it = 0;
+    auto wait_slot = [&]() {
+      ok = wait_bar(job_empty + 8 * (it % kJobSlots), ((it / kJobSlots) & 1) ^ 1, rp.wait_ns) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    for (int n = 0; ok && warp == kFindWarp; ++n) {
+      Job job;
+      int idx = (int)block;
+      job.chunk = idx % p.chunks;
+      idx /= p.chunks;
+      job.h = idx % p.heads;
+      idx /= p.heads;
+      job.b = idx % p.batch;
+      job.split = idx / p.batch;
+      job.more = 1;
+      const Span sp = request_span(p, job.b);
+      job.lo = sp.lo;
+      job.hi = sp.hi;
+      if (lane < p.nq && job.split == 0 && job.h == 0) {
+        const int raw = p.vis[(int64_t)job.b * p.nq + lane];
+        if (raw != clamp_vis(p, raw)) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
+      }
+      if (job.split < sp.used) {
+        const int begin = (sp.base + job.split * sp.len) / kKeys, end = (min(sp.base + (job.split + 1) * sp.len, sp.hi) + kKeys - 1) / kKeys;
+        const int half = (max(0, end - begin) + 1) / 2;
+        job.j0[0] = begin;
+        job.j1[0] = job.j0[1] = begin + half;
+        job.j1[1] = max(end, begin + half);
+        job.whole = sp.used == 1;
+        const int first[2] = {find_pages(job, job.j0[0], job.j1[0], 0), find_pages(job, job.j0[1], job.j1[1], 0)};
+        if (!wait_slot()) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) s_pages[it % kJobSlots][t][lane] = first[t];
+        __syncwarp();
+        if (lane == 0) {
+          s_job[it % kJobSlots] = job;
+          mbar_arrive(job_full + 8 * (it % kJobSlots));
+        }
+        ++it;
+      }
+      if (!wait_slot()) break;
+      if (lane == 0) {
+        fence_async_smem();            // the last answer has been read
+        mbar_arrive_expect_tx(answered, 16);
+        next_block_ask(answer, answered);
+      }
+      __syncwarp();
+      ok = drain_bar(answered, n & 1) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const bool more = next_block_take(answer, block);
+      __syncwarp();
+      if (!more) {
+        if (lane == 0) {
+          s_job[it % kJobSlots].more = 0;
+          mbar_arrive(job_full + 8 * (it % kJobSlots));
+        }
+        break;
       }
     }
   }
@@ -525,11 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
 }
 
 template <int D, bool BF16>
-cudaError_t launch(const RowsParams& p, unsigned blocks, cudaStream_t s) {
+cudaError_t launch(RowsParams& p, unsigned blocks, cudaStream_t s) {
   auto kernel = paged_rows_kernel<D, BF16>;
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), Shape<D>::kSmem);
+  static const bool fits = launches_with(kernel, kLaunchRegs);
+  if (!fits) return cudaErrorInvalidConfiguration;
+  p.q_rows = (p.tt * p.a.group + 7) / 8 * 8;
+  const uint32_t room = kSmemMost - 1024 - 2 * (D / 64) * (uint32_t)p.q_rows * 128u;
+  p.stages = (int32_t)(room / (2 * Shape<D>::kKvBytes));
+  if (p.stages > Shape<D>::kMaxStages) p.stages = Shape<D>::kMaxStages;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kSmemMost);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), Shape<D>::kSmem, s, p);
+  const uint32_t smem = 1024 + 2 * (D / 64) * (uint32_t)p.q_rows * 128u + 2 * (uint32_t)p.stages * Shape<D>::kKvBytes;   // 1024: to align
+  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, s, p);
 }
 
 }  // namespace
@@ -542,6 +577,7 @@ cudaError_t launch_paged_rows(const PagedAttnParams& a, int32_t head_dim, int32_
   p.a = a;
   p.tt = kTile / a.group;
   p.box = std::gcd(a.page_size, kKeys);
+  p.wide = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.part_o)) & 31) == 0;
   p.wait_ns = wait_ns;
   const CUtensorMapDataType type = kv_dtype == HSA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const cuuint64_t d = (cuuint64_t)head_dim;

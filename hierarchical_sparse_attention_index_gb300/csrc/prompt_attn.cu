@@ -44,8 +44,8 @@ constexpr int kOutWarp = 12;             // warps 12..15 write the results
 constexpr int kThreads = 16 * 32;
 // registers per thread: 128 at launch (65,536 over 512 threads), then 152 for the softmax groups, whose
 // threads hold a row of 64 logits, and 104 for the other two: 2 x 152 + 2 x 104 = 4 x 128
-constexpr int kSoftRegs = 152, kOtherRegs = 104;
-static_assert(2 * kSoftRegs + 2 * kOtherRegs <= 4 * 128, "setmaxnreg draws on the launch's registers");
+constexpr int kLaunchRegs = 128, kSoftRegs = 152, kOtherRegs = 104;
+static_assert(2 * kSoftRegs + 2 * kOtherRegs <= 4 * kLaunchRegs, "setmaxnreg draws on the launch's registers");
 constexpr int kSeqs = 512;               // batches up to this are held in shared memory and worked off by size
 constexpr uint32_t kBlockQ = kTile * 128, kBlockK = kKeys * 128;   // 64 dims of a tile, 128 bytes a row
 
@@ -696,6 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
 template <int D, bool BF16>
 cudaError_t launch(const PromptParams& p, unsigned blocks, cudaStream_t s) {
   auto kernel = prompt_attn_kernel<D, BF16>;
+  static const bool fits = launches_with(kernel, kLaunchRegs);
+  if (!fits) return cudaErrorInvalidConfiguration;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), Shape<D>::kSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(blocks), dim3(kThreads), Shape<D>::kSmem, s, p);
