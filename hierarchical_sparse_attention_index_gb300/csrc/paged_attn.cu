@@ -666,8 +666,29 @@ cudaError_t launch_kv(const PagedAttnParams& p, int kv, cudaStream_t s) {
 // A request's splits follow from max_vis and the sizes alone, so that its result does not depend on
 // where it stands in the batch. (Equal pieces of all requests' keys, one per place on the GPU, were
 // slower: 109 against 94 us for 32 ragged contexts, because SMs do not get equal shares of HBM.)
+// Splits for the tcgen05 kernel, one CTA to an SM: the n with the least rounds x (keys of a job + 400) + 20 n, in
+// the time of a key. A job costs what 400 keys do besides its own (its start and end), a split 20 in the join; a
+// round that is not full costs as much as a full one. 64 requests x 4 heads x 16,384 keys, ragged: n = 1, 4, 9: 246,
+// 204, 229 us; x 4,097: 73, 77, 105; 8 x 4 x 16,384: n = 3, 4, 5, 9: 54.6, 53.9, 74.5, 59.0. In w rounds the best n is
+// the largest that fits, or the square root where the two last terms meet.
+static int64_t tc_splits(int64_t ctas, int64_t span) {
+  const int64_t first = (ctas + 151) / 152, most = imax64(1, (span + 127) / 128);
+  int64_t best = 1, cost = INT64_MAX;
+  for (int64_t w = first; w < first + 8; ++w) {
+    int64_t n = imin64(152 * w / ctas, most);
+    const int64_t meet = (int64_t)sqrtf((float)(w * span) / 20.f);
+    if (n > meet) n = imax64(meet, 1);
+    const int64_t c = (ctas * n + 151) / 152 * (span / n + 400) + 20 * n;
+    if (c < cost) {
+      cost = c;
+      best = n;
+    }
+  }
+  return best;
+}
+
 PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype) {
-  constexpr int32_t kTcRows = 32;
+  constexpr int32_t kTcRows = 24;
   PagedSplit s;
   const int32_t rows = nq * group;
   s.tc = kv_dtype != HSA_E4M3 && rows > kTcRows;
@@ -685,7 +706,7 @@ PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, 
   const int64_t ctas = (int64_t)batch * heads * s.chunks;
   int64_t n;
   if (s.tc) {
-    n = imin64((4 * 152 + ctas - 1) / ctas, (span + 511) / 512);
+    n = tc_splits(ctas, span);
   } else {
     const int64_t places = 152 * (s.chunk_rows <= 16 ? 3 : 4);
     n = imin64((places + ctas / 2) / ctas, (span + 255) / 256);

@@ -331,40 +331,44 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       // The ring holds K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1), tiles counted from the top: the
       // products of S run a key tile ahead of those with V.
       int n_q[2] = {0, 0}, c = 0;        // queries loaded; tiles of the ring loaded
-      auto load_kv = [&](const Job& job, int j, const CUtensorMap* map) {
+      const uint32_t one = elect_one();
+      auto wait = [&](uint32_t bar, int n) {
+        ok = wait_bar(bar, n & 1, p.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+      };
+      auto load_kv = [&](int h, int row, const CUtensorMap* map) {
         const int s = c % L::kStages;
-        ok = ok && wait_bar(kv_empty + 8 * s, ((c / L::kStages) & 1) ^ 1, p.wait_ns);
-        if (!ok) return;
-        mbar_arrive_expect_tx(kv_full + 8 * s, L::kKvBytes);
+        if (!wait(kv_empty + 8 * s, (c / L::kStages) ^ 1)) return;
+        if (one) mbar_arrive_expect_tx(kv_full + 8 * s, L::kKvBytes);
+        __syncwarp();
 #pragma unroll
-        for (int d = 0; d < D / 64; ++d)
-          tma_3d(sKv + s * L::kKvBytes + d * kBlockK, map, 64 * d, job.h, job.k0 + job.kbase + kKeys * j, kv_full + 8 * s);
+        for (int d = 0; d < D / 64; ++d) tma_3d_one(one, sKv + s * L::kKvBytes + d * kBlockK, map, 64 * d, h, row, kv_full + 8 * s);
         ++c;
       };
-      auto load_q = [&](const Job& job, int t) {
-        ok = ok && wait_bar(q_empty + 8 * t, (n_q[t] & 1) ^ 1, p.wait_ns);
-        if (!ok) return;
-        mbar_arrive_expect_tx(q_full + 8 * t, (D / 64) * (uint32_t)(p.tt * p.group) * 128u);
+      auto load_q = [&](int h, int row, int t) {
+        if (!ok || !wait(q_empty + 8 * t, n_q[t] ^ 1)) return;
+        if (one) mbar_arrive_expect_tx(q_full + 8 * t, (D / 64) * (uint32_t)(p.tt * p.group) * 128u);
+        __syncwarp();
 #pragma unroll
         for (int d = 0; d < D / 64; ++d)
-          tma_4d(sQ + t * L::kQBytes + d * kBlockQ, &p.qm, 64 * d, 0, job.h, job.q0 + job.i0 + t * p.tt, q_full + 8 * t);
+          tma_4d_one(one, sQ + t * L::kQBytes + d * kBlockQ, &p.qm, 64 * d, 0, h, row, q_full + 8 * t);
         ++n_q[t];
       };
       Job job;
       for (int it = 0; take_job(it, job); ++it) {
-        if (lane == 0) {
-          const int top = job.top(), bottom = job.bottom(), ask = min(top - 1, bottom + kAhead);
-          if (top == 0) mbar_arrive(job_loaded + 8 * (it % kJobSlots));
-          if (top > 0) load_kv(job, top - 1, &p.km);
-          if (job.has(0)) load_q(job, 0);
-          if (job.has(1)) load_q(job, 1);
-          for (int j = top - 1; j >= bottom && ok; --j) {
-            if (j == ask) mbar_arrive(job_loaded + 8 * (it % kJobSlots));
-            if (j > bottom) load_kv(job, j - 1, &p.km);
-            load_kv(job, j, &p.vm);
-          }
+        const int top = uniform(job.top()), bottom = uniform(job.bottom()), ask = min(top - 1, bottom + kAhead);
+        const int h = uniform(job.h), row = uniform(job.k0 + job.kbase), q_row = uniform(job.q0 + job.i0);
+        if (top == 0 && lane == 0) mbar_arrive(job_loaded + 8 * (it % kJobSlots));
+        if (top > 0) load_kv(h, row + kKeys * (top - 1), &p.km);
+        if (job.has(0)) load_q(h, q_row, 0);
+        if (job.has(1)) load_q(h, q_row + p.tt, 1);
+        for (int j = top - 1; j >= bottom && ok; --j) {
+          if (j == ask && lane == 0) mbar_arrive(job_loaded + 8 * (it % kJobSlots));
+          if (j > bottom) load_kv(h, row + kKeys * (j - 1), &p.km);
+          if (ok) load_kv(h, row + kKeys * j, &p.vm);
         }
-        __syncwarp();
+        if (!ok) break;
       }
       // nothing of this CTA's may be in flight when it ends, whatever the other roles did
       if (lane == 0) {
