@@ -485,9 +485,9 @@ static hsa_status check_paged_query(const hsa_paged_cache* c, int32_t heads_q, i
 struct PagedWs {
   size_t off_o, off_ml, total;
 };
-static PagedWs paged_ws(const hsa_paged_cache* c, int32_t rows, const PagedSplit& sp) {
+static PagedWs paged_ws(const hsa_paged_cache* c, int32_t rows, int64_t splits) {
   PagedWs w;
-  const size_t parts = sp.joined ? (size_t)c->batch * c->heads * sp.n_splits * rows : 0;
+  const size_t parts = (size_t)c->batch * c->heads * splits * rows;
   w.off_o = 0;
   w.off_ml = parts * c->head_dim * 4;
   w.total = (w.off_ml + parts * 8 + 255) / 256 * 256 + 256;
@@ -542,7 +542,7 @@ hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const void* k, co
 size_t hsa_paged_attn_workspace_bytes(const hsa_paged_cache* cache, int32_t heads_q, int32_t nq, int64_t max_vis) {
   if (check_paged_sizes(cache) != HSA_OK || check_paged_query(cache, heads_q, nq, max_vis) != HSA_OK) return 0;
   const int32_t group = heads_q / cache->heads;
-  return paged_ws(cache, nq * group, paged_split(cache->batch, cache->heads, group, nq, max_vis, 0, cache->dtype)).total;
+  return paged_ws(cache, nq * group, paged_splits_most(cache->batch, cache->heads, group, nq, max_vis, cache->dtype)).total;
 }
 
 hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, int32_t q_dtype, int32_t heads_q,
@@ -562,7 +562,7 @@ hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, in
   if ((int64_t)sp.n_splits * sp.chunks * cache->heads * cache->batch > (int64_t)INT32_MAX ||
       (int64_t)rows * cache->heads * cache->batch > (int64_t)INT32_MAX)
     return HSA_ERR_SHAPE;
-  const PagedWs L = paged_ws(cache, rows, sp);
+  const PagedWs L = paged_ws(cache, rows, sp.joined ? sp.n_splits : 0);
   if (!ws || ws_bytes < L.total) return HSA_ERR_WORKSPACE;
   if (!aligned16(ws)) return HSA_ERR_ALIGN;
   uint32_t* status;

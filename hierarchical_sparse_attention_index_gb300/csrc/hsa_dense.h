@@ -39,6 +39,7 @@ struct PagedSplit {
   bool joined;            // paged_join_kernel follows
 };
 PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype);
+int64_t paged_splits_most(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t kv_dtype);
 
 struct PagedAttnParams {
   int32_t batch, heads, page_size;

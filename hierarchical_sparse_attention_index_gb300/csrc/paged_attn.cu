@@ -651,33 +651,21 @@ cudaError_t launch_kv(const PagedAttnParams& p, int kv, cudaStream_t s) {
 
 }  // namespace
 
-// Which kernel, query rows per CTA and splits of the length.
-// 16-bit pages and more than 32 query rows take the tcgen05 kernel, 128 rows (whole queries) to a CTA: 35
-// rows (64 requests of up to 4,097 keys, 4 heads, f16) took 84 us there and 105 here, 32 rows 117 and
-// 110. Else up to 32 rows one CTA reads its keys once for all of them; more rows (E4M3) are dealt out
-// evenly (35: 18 and 17), and the later CTAs' keys come from L2.
-// The splits make about as many CTAs as the GPU holds at a time (3 or 2 per SM; the tcgen05 kernel's CTAs,
-// one per SM, take four each, so that ragged lengths even out): more only add starts and joins (4
-// requests of 131,072 FP8 keys: 168 us with 448 CTAs, 193 with 608, 217 with 1,216). No split is
-// shorter than 256 keys (8 per group of a warp; in a cluster 128), or 512 in the tcgen05 kernel.
-// Splits that all run at a time join in clusters (1 request of 1,000 keys: 6.7 us against 8.5); with more
-// CTAs than that, a cluster's short CTAs would hold places until its longest ends (32 ragged contexts: 99
-// us against 93).
-// A request's splits follow from max_vis and the sizes alone, so that its result does not depend on
-// where it stands in the batch. (Equal pieces of all requests' keys, one per place on the GPU, were
-// slower: 109 against 94 us for 32 ragged contexts, because SMs do not get equal shares of HBM.)
 // Splits for the tcgen05 kernel, one CTA to an SM: the n with the least rounds x (keys of a job + 400) + 20 n, in
 // the time of a key. A job costs what 400 keys do besides its own (its start and end), a split 20 in the join; a
 // round that is not full costs as much as a full one. 64 requests x 4 heads x 16,384 keys, ragged: n = 1, 4, 9: 246,
 // 204, 229 us; x 4,097: 73, 77, 105; 8 x 4 x 16,384: n = 3, 4, 5, 9: 54.6, 53.9, 74.5, 59.0. In w rounds the best n is
 // the largest that fits, or the square root where the two last terms meet.
+static int64_t tc_splits_in(int64_t w, int64_t ctas, int64_t span) {
+  const int64_t meet = (int64_t)sqrtf((float)(w * span) / 20.f);
+  return imax64(1, imin64(imin64(152 * w / ctas, (span + 127) / 128), meet));
+}
+constexpr int64_t kRounds = 8;           // numbers of rounds looked at
 static int64_t tc_splits(int64_t ctas, int64_t span) {
-  const int64_t first = (ctas + 151) / 152, most = imax64(1, (span + 127) / 128);
+  const int64_t first = (ctas + 151) / 152;
   int64_t best = 1, cost = INT64_MAX;
-  for (int64_t w = first; w < first + 8; ++w) {
-    int64_t n = imin64(152 * w / ctas, most);
-    const int64_t meet = (int64_t)sqrtf((float)(w * span) / 20.f);
-    if (n > meet) n = imax64(meet, 1);
+  for (int64_t w = first; w < first + kRounds; ++w) {
+    const int64_t n = tc_splits_in(w, ctas, span);
     const int64_t c = (ctas * n + 151) / 152 * (span / n + 400) + 20 * n;
     if (c < cost) {
       cost = c;
@@ -687,6 +675,20 @@ static int64_t tc_splits(int64_t ctas, int64_t span) {
   return best;
 }
 
+// Which kernel, query rows per CTA and splits of the length.
+// 16-bit pages and more than 24 query rows take the tcgen05 kernel, 128 rows (whole queries) to a CTA: 30
+// rows (64 requests x 4 heads, f16, up to 4,097 keys) took 72 us there and 85 here, up to 16,384 keys 200 and 260; 24
+// rows 72 and 70, 200 and 222, but 32 requests x 8 heads x 8,192 126 and 107. Else up to 32 rows one CTA reads its keys once for all of them; more rows (E4M3) are dealt out
+// evenly (35: 18 and 17), and the later CTAs' keys come from L2.
+// The splits make about as many CTAs as the GPU holds at a time (3 or 2 per SM): more only add starts and joins (4
+// requests of 131,072 FP8 keys: 168 us with 448 CTAs, 193 with 608, 217 with 1,216). No split is
+// shorter than 256 keys (8 per group of a warp; in a cluster 128).
+// Splits that all run at a time join in clusters (1 request of 1,000 keys: 6.7 us against 8.5); with more
+// CTAs than that, a cluster's short CTAs would hold places until its longest ends (32 ragged contexts: 99
+// us against 93).
+// A request's splits follow from max_vis and the sizes alone, so that its result does not depend on
+// where it stands in the batch. (Equal pieces of all requests' keys, one per place on the GPU, were
+// slower: 109 against 94 us for 32 ragged contexts, because SMs do not get equal shares of HBM.)
 PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype) {
   constexpr int32_t kTcRows = 24;
   PagedSplit s;
@@ -718,6 +720,14 @@ PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, 
   s.cluster = !s.tc && n > 1 && n <= 8 && ctas * n <= 152 * (s.chunk_rows <= 16 ? 3 : 2);
   s.joined = n > 1 && !s.cluster;
   return s;
+}
+
+// The most splits that leave their parts in the workspace, for any length up to max_vis and any window
+int64_t paged_splits_most(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t kv_dtype) {
+  const PagedSplit s = paged_split(batch, heads, group, nq, max_vis, 0, kv_dtype);
+  if (!s.tc) return s.joined ? s.n_splits : 0;           // the longest has the most
+  const int64_t ctas = (int64_t)batch * heads * s.chunks;
+  return tc_splits_in((ctas + 151) / 152 + kRounds - 1, ctas, max_vis);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedSplit& sp, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns,

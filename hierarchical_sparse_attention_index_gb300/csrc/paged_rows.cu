@@ -5,20 +5,22 @@
 // Bound: the reads of the pages from HBM, as with few rows, as long as the products keep up. The
 // warp MMA does not: its 8-column tiles of queries are issued and softmaxed by the same few warps, and
 // past 32 rows the keys would be read again. Here up to 128 rows (queries x heads of the group) are one
-// tile of a tcgen05 product, and a 64-key tile of 32 KB takes about 700 clocks, in which an SM's share
+// tile of a tcgen05 product, and the 32 KB of 64 keys take a stream about 700 clocks, in which an SM's share
 // of HBM brings half as much. The split of a CTA's job falls into two halves, one for each stream t:
-// a ring of K and V tiles, a warp that issues the products, a warp group with a query row per thread
-// for the softmax, buffers of S and an accumulator in tensor memory; the two streams fill each other's
-// waits. A row without a query (35 rows fill 35 of 128) costs nothing but its lane: warps without any
-// skip the softmax.
-//  - one warp loads: K and V tiles as boxes of gcd(page size, 64) rows by TMA (128-byte swizzle), two
-//    lanes and more issuing; rows past the visible length inside a box are cleared before use (zero
-//    times what they hold need not be zero), blocks past it, or on a bad page, come from outside the
-//    pool, where TMA fills in zeros;
+// a ring of K and V tiles, a warp that loads it, a warp that issues the products, a warp group with a query
+// row per thread for the softmax, buffers of S and an accumulator in tensor memory; the two streams fill each
+// other's waits. A row without a query (35 rows fill 35 of 128) costs nothing but its lane: warps without any
+// skip the softmax, and the rows take no shared memory, which the rings get.
+//  - K and V tiles come as boxes of gcd(page size, 64) rows by TMA (128-byte swizzle); rows past the visible
+//    length inside a box are cleared before use (zero times what they hold need not be zero), blocks past it,
+//    or on a bad page, come from outside the pool, where TMA fills in zeros;
 //  - CTAs stay and take the next blocks' jobs (cluster launch control), so ragged lengths even out;
-//  - the streams' results are merged from tensor memory, where both of a row lie in the same lane: half of
-//    the dims by either stream's warps. With one split that is the result, else it goes to the
-//    workspace and paged_join_kernel joins the splits.
+//  - four warps merge the streams' results from tensor memory, where both of a row lie in the same lane, while the
+//    softmax is at the next job. With one split that is the result, else it goes to the workspace and
+//    paged_join_kernel joins the splits.
+// Measured: 64 requests x 4 heads x 5 queries, f16, 16,384 keys each 340 us, 0.93 of the measured copy rate; of 1 ..
+// 4,097 keys 73 us, 0.59 (the CTAs' last jobs end far apart; all with 4,097: 96 us, 0.83); 1 request x 131,072 55 us.
+// Of 64 requests of ragged lengths the longest first: 68 us, but 3 us more wherever the lengths are alike.
 #include <string.h>
 
 #include <numeric>

@@ -329,7 +329,8 @@ HSA_API hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const voi
                                  const int64_t* start, hsa_stream_t stream);
 
 /* Workspace bytes of hsa_paged_attn_decode for this cache's batch, heads and head_dim (its
- * pointers are not looked at). Host only; returns 0 for invalid sizes. */
+ * pointers are not looked at), for this max_vis, every smaller one and every window. Host only;
+ * returns 0 for invalid sizes. */
 HSA_API size_t hsa_paged_attn_workspace_bytes(const hsa_paged_cache* cache, int32_t heads_q, int32_t nq, int64_t max_vis);
 
 /* Attention of nq new tokens per request over its pages, split over the cache's length and

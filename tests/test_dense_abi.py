@@ -166,3 +166,13 @@ def test_grids_that_are_too_large(H):
     c = cache(H, batch=1 << 20, heads=1024)
     assert lib.hsa_paged_attn_decode(ctypes.byref(c), 0x10, H.HSA_BF16, 1 << 17, 0x40, 1, 1024, 0, 0.1, 0x10, None, 0x100, 1 << 62,
                                      None) == SHAPE
+
+
+@pytest.mark.parametrize("nq,group,dtype", [(5, 7, "HSA_BF16"), (1, 8, "HSA_BF16"), (5, 7, "HSA_E4M3")])
+def test_workspace_holds_for_shorter_lengths(H, nq, group, dtype):
+    """A workspace for max_vis serves every smaller one."""
+    lib = H.load_library()
+    for batch in (1, 3, 16, 64, 200):
+        c = cache(H, batch=batch, dtype=getattr(H, dtype), max_pages=10000)
+        sizes = [lib.hsa_paged_attn_workspace_bytes(ctypes.byref(c), 4 * group, nq, n) for n in range(0, 160000, 61)]
+        assert min(sizes) > 0 and sizes == sorted(sizes)

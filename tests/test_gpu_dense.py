@@ -160,6 +160,27 @@ def test_decode_large_and_small_values(H):
     D.check(out[0, 0], lse[0, 0], o, l, A, mag, n, dim, HF)
 
 
+@pytest.mark.parametrize("window", [0, 1, 50, 500, 700, 792, 860, 934])
+def test_decode_workspace_serves_every_window(H, window):
+    """A window shortens the lengths that are split, which can make more splits; the workspace is asked for without it."""
+    k, v, table = D.paged(1, [935], 4, 128, 32, BF, 21)
+    cache = H.PagedCache(k.cuda(), v.cuda(), table.cuda())
+    ws = H.new_paged_workspace(cache, 28, 5, 935)
+    q = torch.randn(1, 5, 28, 128).to(BF).cuda()
+    out = torch.empty_like(q)
+    for longest in (935, 860, 400, 77):
+        vis = torch.full((1, 5), longest, dtype=torch.int32).cuda()
+        H.hsa_paged_attn_decode(cache, q, vis, longest, 0.1, out, ws, window=window)
+        clean(H)
+        ks, vs = (D.unpage(x.cuda(), table.cuda(), 0, longest)[0] for x in (k, v))
+        lo = torch.full((35,), max(0, longest - window) if window else 0, device="cuda")
+        hi = torch.full((35,), longest, device="cuda")
+        for h in range(4):
+            mine = slice(7 * h, 7 * h + 7)
+            o, l, A, mag = D.attention(q[0, :, mine].reshape(-1, 128).double(), ks[:, h], vs[:, h], lo, hi, 0.1)
+            D.check(out[0, :, mine].reshape(-1, 128), None, o, l, A, mag, longest, 128, BF, f"window {window} of {longest}")
+
+
 def test_decode_bad_pages_and_lengths_are_flagged(H):
     """Page ids outside the pool are skipped, lengths outside [0, max_vis] cut; both set the flag."""
     def edit(table):
