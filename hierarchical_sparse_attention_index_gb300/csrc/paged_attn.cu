@@ -19,8 +19,8 @@
 //  - softmax in one pass with the running maximum and sum in fp32. The maximum is only raised, and
 //    the outputs rescaled, when some logit passes it by 2^8: the weights then stay below 256, which
 //    16-bit weights and fp32 sums hold, and most groups need one vote instead of shuffles;
-//  - the weights P are rounded to the 16-bit operand type of the product with V (relative 2^-9 in
-//    bf16, 2^-12 in f16, independent from key to key); the sum l takes them unrounded.
+//  - the weights P are rounded to the 16-bit operand type of the product with V (off by at
+//    most a relative 2^-8 in bf16, 2^-11 in f16, independent from key to key); the sum l takes them unrounded.
 // The four warps' (m, l, O) are merged in shared memory. With one split the CTA writes the result. Up to
 // 8 splits are one thread-block cluster, whose CTAs join their parts through distributed shared memory;
 // more leave their parts in the workspace, and paged_join_kernel joins them. Either joins in order.

@@ -16,7 +16,7 @@
 //    can be read; one for 128 keys reads 8 KB in 64, but leaves room for one buffer only: 16,384
 //    tokens took the same time, packed prompts 15 % more);
 //  - a warp group does the softmax of each tile, one row per thread (no shuffles): the running
-//    maximum and sum in fp32, P rounded to the operand type (a relative 2^-9 in bf16, 2^-12 in f16,
+//    maximum and sum in fp32, P rounded to the operand type (off by at most a relative 2^-8 in bf16, 2^-11 in f16,
 //    independent from key to key) over S's columns. The maximum is only raised, and O rescaled in
 //    tensor memory, when a logit passes it by 2^8: weights stay below 256, and after the first
 //    tiles that hardly happens, so the rescaling needs no warps of its own;
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // Each lane writes its row, 32 bytes at a time where the rows allow it: that takes more write
     // transactions than gathering rows in shared memory first, but shared memory is what is scarce here
-    // (a window of 128 over 32,768 tokens took 214 us that way, 187 so).
+    // (a window of 128 over 32,768 tokens took 214 us that way when it took 187 so).
     const int r = (warp & 3) * 32 + lane, tok = s_tok[r], head = s_head[r];
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int n_s[2] = {0, 0}, n_o[2] = {0, 0};
