@@ -102,6 +102,44 @@ def test_decode_window(H, kv, window):
     decode(H, 1, 3, 1, 2, 64, 16, kv, BF, [[40, 2000, 900]], window=window)
 
 
+@pytest.mark.parametrize("kv", [BF, HF])
+@pytest.mark.parametrize("dim,group,nq,page", [(128, 5, 5, 16), (64, 25, 1, 48), (128, 26, 1, 32), (64, 7, 5, 64), (128, 16, 8, 128),
+                                               (128, 128, 1, 80), (64, 127, 2, 16), (128, 1, 8, 16)])
+def test_decode_more_work_than_places(H, kv, dim, group, nq, page):
+    """Ragged batches with more pieces of work than the GPU holds at a time, empty requests among them; queries of one
+    request need not stand one behind the other."""
+    batch = 90
+    vis = [[(37 * b * b + 11 * i) % 500 if b % 7 else 0 for i in range(nq)] for b in range(batch)]
+    decode(H, batch, nq, 2, group, dim, page, kv, kv, vis, seed=group, max_vis=520)
+
+
+@pytest.mark.parametrize("kv,group,nq", [(BF, 5, 5), (HF, 8, 1), (F8, 8, 1), (BF, 1, 1)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_decode_many_splits(H, kv, group, nq, dim):
+    """One request and key head with more splits than one warp joins."""
+    decode(H, 1, nq, 1, group, dim, 64, kv, BF if kv == F8 else kv, [[20001 + i for i in range(nq)]], seed=nq, scales=(0.5, 1.5) if kv == F8 else (1., 1.))
+
+
+def test_decode_results_on_16_byte_boundaries(H):
+    """Outputs and workspaces that do not start on 32-byte boundaries give the same bits, and nothing around them changes."""
+    k, v, table = D.paged(2, [900, 300], 2, 128, 32, BF, 5)
+    cache = H.PagedCache(k.cuda(), v.cuda(), table.cuda())
+    for nq, group in ((5, 7), (1, 4)):
+        q = torch.randn(2, nq, 2 * group, 128).to(BF).cuda()
+        vis = torch.tensor([[896 + i for i in range(nq)], [296 + i for i in range(nq)]], dtype=torch.int32).cuda()
+        ws = H.new_paged_workspace(cache, 2 * group, nq, 900)
+        want = torch.empty_like(q)
+        H.hsa_paged_attn_decode(cache, q, vis, 900, 0.1, want, ws)
+        n = ws.numel()
+        room, ws_room = torch.full((q.numel() + 16,), 7.0, dtype=BF, device="cuda"), torch.full((n + 64,), 9, dtype=torch.uint8, device="cuda")
+        out = room[8:8 + q.numel()].view_as(q)
+        H.hsa_paged_attn_decode(cache, q, vis, 900, 0.1, out, ws_room[16:16 + n])
+        clean(H)
+        assert torch.equal(out, want)
+        assert (room[:8] == 7).all() and (room[8 + q.numel():] == 7).all()
+        assert (ws_room[:16] == 9).all() and (ws_room[16 + n:] == 9).all()
+
+
 def test_decode_empty_requests(H):
     """Requests and queries with nothing visible: output 0, lse -inf, also beside long ones."""
     decode(H, 4, 2, 2, 3, 128, 16, BF, BF, [[0, 0], [0, 1], [0, 900], [5, 0]], max_vis=1000)
@@ -621,6 +659,37 @@ def test_captured_and_on_other_streams(H):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out_p, ref[0]) and torch.equal(out_d, ref[1]) and torch.equal(cache.k, ref[2])
+    clean(H)
+
+
+def test_calls_at_the_same_time(H):
+    """Prompts and decodes on three streams at once, each decode with its own workspace, give the bits of calls one by one."""
+    g = torch.Generator().manual_seed(4)
+    cu = torch.tensor([0, 900, 1500, 4000], dtype=torch.int32).cuda()
+    q = torch.randn(4000, 8, 128, generator=g).to(BF).cuda()
+    k, v = (torch.randn(4000, 2, 128, generator=g).to(BF).cuda() for _ in range(2))
+    pk, pv, table = D.paged(30, [50 * b + 1 for b in range(30)], 2, 128, 32, BF, 3)
+    cache = H.PagedCache(pk.cuda(), pv.cuda(), table.cuda())
+    vis = {nq: torch.tensor([[50 * b + 1] * nq for b in range(30)], dtype=torch.int32).cuda() for nq in (1, 5)}
+    q_d = {nq: torch.randn(30, nq, 14, 128, generator=g).to(BF).cuda() for nq in (1, 5)}
+    ws = {nq: H.new_paged_workspace(cache, 14, nq, 1451) for nq in (1, 5)}
+    work = [lambda out: H.hsa_prompt_attn(q, k, v, cu, 0.1, out)]
+    work += [lambda out, nq=nq: H.hsa_paged_attn_decode(cache, q_d[nq], vis[nq], 1451, 0.1, out, ws[nq]) for nq in (1, 5)]
+    like = [q, q_d[1], q_d[5]]
+    want = [torch.empty_like(x) for x in like]
+    for w, x in zip(work, want):
+        w(x)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    for _ in range(5):
+        got = [torch.zeros_like(x) for x in like]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for w, x, s in zip(work, got, streams):
+                with torch.cuda.stream(s):
+                    w(x)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
     clean(H)
 
 
