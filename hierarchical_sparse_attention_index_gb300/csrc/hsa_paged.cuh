@@ -16,10 +16,16 @@ __device__ __forceinline__ Span request_span(const PagedAttnParams& p, int b) {
   Span s;
   s.lo = 0x7fffffff;
   s.hi = 0;
-  for (int i = 0; i < p.nq; ++i) {
-    const int v = clamp_vis(p, p.vis[(int64_t)b * p.nq + i]);
-    s.hi = max(s.hi, v);
-    if (v > 0) s.lo = min(s.lo, p.window > 0 ? max(v - p.window, 0) : 0);
+  static_assert(HSA_MAX_NQ <= 8, "one turn of loads");
+  const int32_t* vis = p.vis + (int64_t)b * p.nq;
+  int v[HSA_MAX_NQ];                     // loaded together: one after the other they would hold up the start
+#pragma unroll
+  for (int i = 0; i < HSA_MAX_NQ; ++i) v[i] = i < p.nq ? vis[i] : 0;
+#pragma unroll
+  for (int i = 0; i < HSA_MAX_NQ; ++i) {
+    const int x = clamp_vis(p, v[i]);
+    s.hi = max(s.hi, x);
+    if (x > 0) s.lo = min(s.lo, p.window > 0 ? max(x - p.window, 0) : 0);
   }
   if (s.hi == 0) s.lo = 0;
   s.base = s.lo & ~(p.align - 1);

@@ -44,6 +44,7 @@ constexpr int kLaunchRegs = 96, kSoftRegs = 136, kOtherRegs = 80, kFindRegs = 48
 static_assert(2 * kSoftRegs + 2 * kOtherRegs + kFindRegs <= 5 * kLaunchRegs, "setmaxnreg draws on the launch's registers");
 constexpr uint32_t kBlockQ = kTile * 128, kBlockK = kKeys * 128;   // 64 dims of a tile, 128 bytes a row
 constexpr int kJobSlots = 2;
+constexpr int kOrdered = 128;            // batches up to this can be worked off by length
 
 template <int D>
 struct Shape {
@@ -59,6 +60,7 @@ struct RowsParams {
   int32_t box;                           // rows of a box of the pools
   int32_t q_rows;                        // rows of a query block in shared memory: tt x group, whole groups of 8
   int32_t stages;                        // of a stream's ring: what the queries leave room for
+  int32_t ordered;                       // the longest requests come first
   int32_t wide;                          // results start on 32-byte boundaries
   uint64_t wait_ns;
 };
@@ -80,6 +82,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   __shared__ float2 s_ml[2][kTile];                      // each stream's (m in log2 units, l) of a row
   __shared__ __align__(16) uint4 s_answer;
   __shared__ uint32_t s_tmem;
+  __shared__ __align__(16) int s_len[kOrdered];          // requests' lengths
+  __shared__ uint8_t s_order[kOrdered];                  // requests, the longest first
   __shared__ __align__(8) uint64_t s_bars[23 + 2 * kJobSlots + 4 * L::kMaxStages];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   // Q of two jobs, then the rings. A product reads 128 rows from a query block's start: past its own rows it
@@ -129,6 +133,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   griddep_wait();
   griddep_launch_dependents();
   bool ok = true;
+  if (rp.ordered) {                      // four threads for each request count the longer ones
+    const int b = tid >> 2;
+    if (tid < kOrdered) {
+      s_len[tid] = -1;
+      if (tid < p.batch) {
+        const Span sp = request_span(p, tid);
+        s_len[tid] = sp.hi - sp.base;
+      }
+    }
+    __syncthreads();
+    if (b < kOrdered) {
+      const int mine = s_len[b];
+      int before = 0;
+      for (int o = 4 * (tid & 3); o < p.batch; o += 16) {
+        const int4 x = *reinterpret_cast<const int4*>(s_len + o);
+        before += (x.x > mine || (x.x == mine && o < b)) + (x.y > mine || (x.y == mine && o + 1 < b)) +
+                  (x.z > mine || (x.z == mine && o + 2 < b)) + (x.w > mine || (x.w == mine && o + 3 < b));
+      }
+      before += __shfl_xor_sync(0xffffffffu, before, 1);
+      before += __shfl_xor_sync(0xffffffffu, before, 2);
+      if (b < p.batch && (tid & 3) == 0) s_order[before] = (uint8_t)b;
+    }
+    __syncthreads();
+  }
 
   // Job `it` of this CTA, by one warp: waits for it; free_job frees its slot, once it has been read.
   auto wait_job = [&](int it) {
@@ -498,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       job.h = idx % p.heads;
       idx /= p.heads;
       job.b = idx % p.batch;
+      if (rp.ordered) job.b = s_order[job.b];
       job.split = idx / p.batch;
       job.more = 1;
       const Span sp = request_span(p, job.b);
@@ -579,6 +608,7 @@ cudaError_t launch_paged_rows(const PagedAttnParams& a, int32_t head_dim, int32_
   p.a = a;
   p.tt = kTile / a.group;
   p.box = std::gcd(a.page_size, kKeys);
+  p.ordered = a.batch <= kOrdered && a.n_splits == 1 && (int64_t)a.batch * a.heads * a.chunks > 152;
   p.wide = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.part_o)) & 31) == 0;
   p.wait_ns = wait_ns;
   const CUtensorMapDataType type = kv_dtype == HSA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
