@@ -150,37 +150,38 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
   // ---------------------------------------------------------------- the ring: 16-key groups of this warp
   const uint32_t ring = smem_u32(sm) + (uint32_t)warp * T::kRing;
   const int n_groups = max(0, (end - begin + kGroup * (kWarps - warp) - 1) / (kGroup * kWarps));
-  uint32_t bad = 0;                                      // bit s: the group in stage s lies on no page
+  uint32_t bad = 0;                                      // bit s: the group in stage s is not loaded
   // where 32 groups lie, one per lane, looked up a turn ahead of their use: the piece of the pools in
-  // units of 16 rows, or -1 for a bad page
+  // units of 16 rows, times 2^16, plus a bit for each row that some query sees; 0 for a bad page or no such row
   const int64_t page_pieces = (int64_t)p.heads * (p.page_size / kGroup);
   auto find_pieces = [&](int turn) -> int64_t {
     const int i = 32 * turn + lane;
-    if (i >= n_groups) return -1;
+    if (i >= n_groups) return 0;
     const int pos = begin + kGroup * (warp + kWarps * i), pg = pos / p.page_size;
+    const uint32_t seen = seen32(p, b, sp, pos) & 0xFFFFu;
+    if (!seen) return 0;
     const int page = p.table[(int64_t)b * p.max_pages + pg];
     if (page < 0 || page >= p.n_pages) {
       flag_status(p.status, HSA_FLAG_INDEX_RANGE);
-      return -1;
+      return 0;
     }
-    return page * page_pieces + (h * p.page_size + pos - pg * p.page_size) / kGroup;
+    return ((page * page_pieces + (h * p.page_size + pos - pg * p.page_size) / kGroup) << 16) | seen;
   };
   int64_t pieces = find_pieces(0), pieces_next = find_pieces(1);
   auto issue = [&](int i, int stage) {                   // called with i = 0, 1, 2, ...
-    const int64_t piece = __shfl_sync(0xffffffffu, pieces, i & 31);
+    const int64_t found = __shfl_sync(0xffffffffu, pieces, i & 31);
     if ((i & 31) == 31) {
       pieces = pieces_next;
       pieces_next = find_pieces((i >> 5) + 2);
     }
     if (i < n_groups) {
-      const int pos = begin + kGroup * (warp + kWarps * i);
-      const uint32_t st = (uint32_t)stage * T::kStage;
-      bad = (bad & ~(1u << stage)) | ((piece < 0 ? 1u : 0u) << stage);
-      const int64_t at = piece < 0 ? 0 : piece * (kGroup * T::kRow) + lane * 16;
+      const uint32_t st = (uint32_t)stage * T::kStage, seen = (uint32_t)found & 0xFFFFu;
+      bad = (bad & ~(1u << stage)) | ((seen ? 0u : 1u) << stage);
+      const int64_t at = seen ? (found >> 16) * (kGroup * T::kRow) + lane * 16 : 0;
       const uint8_t* k = p.k_pool + at;
       const uint8_t* v = p.v_pool + at;
       constexpr int kCopies = kGroup * T::kChunks / 32;
-      if (piece >= 0 && pos >= sp.lo && pos + kGroup <= sp.hi) {
+      if (seen == 0xFFFFu) {
 #pragma unroll
         for (int u = 0; u < kCopies; ++u) {
           cp_async16(ring + T::k_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, k + u * 512);
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
 #pragma unroll
         for (int u = 0; u < kCopies; ++u) {
           const int r = (u * 32 + lane) / T::kChunks;
-          const uint32_t n = (piece >= 0 && pos + r >= sp.lo && pos + r < sp.hi) ? 16u : 0u;
+          const uint32_t n = (seen >> r) & 1u ? 16u : 0u;
           cp_async16z(ring + T::k_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, k + (n ? u * 512 : 0), n);
           cp_async16z(ring + T::kHalf + T::v_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, v + (n ? u * 512 : 0), n);
         }

@@ -11,9 +11,10 @@
 // row per thread for the softmax, buffers of S and an accumulator in tensor memory; the two streams fill each
 // other's waits. A row without a query (35 rows fill 35 of 128) costs nothing but its lane: warps without any
 // skip the softmax, and the rows take no shared memory, which the rings get.
-//  - K and V tiles come as boxes of gcd(page size, 64) rows by TMA (128-byte swizzle); rows past the visible
-//    length inside a box are cleared before use (zero times what they hold need not be zero), blocks past it,
-//    or on a bad page, come from outside the pool, where TMA fills in zeros;
+//  - K and V tiles come as boxes of gcd(page size, 64) rows by TMA (128-byte swizzle); rows inside a box that
+//    no query sees (past the visible length, or between the windows of queries far apart) are cleared before use, as
+//    zero times what they hold need not be zero; blocks without any other row, or on a bad page, come from outside
+//    the pool, where TMA fills in zeros;
 //  - CTAs stay and take the next blocks' jobs (cluster launch control), so ragged lengths even out;
 //  - four warps merge the streams' results from tensor memory, where both of a row lie in the same lane, while the
 //    softmax is at the next job. With one split that is the result, else it goes to the workspace and
@@ -65,7 +66,8 @@ struct RowsParams {
 };
 
 struct Job {
-  int b, h, chunk, split, lo, hi;        // [lo, hi): the positions that queries of the request see
+  int b, h, chunk, split;
+  Span sp;                               // of the request's positions
   int j0[2], j1[2];                      // 64-key tiles [j0, j1) of stream t
   int whole;                             // the request's only split
   int more;                              // 0: no work is left, the other fields are not set
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   auto find_pages = [&](const Job& job, int j0, int j1, int turn) {
     const int j = j0 + turn * per + lane / blocks, pos = kKeys * j + rp.box * (lane % blocks);
     int page = (int)p.n_pages;
-    if (j < j1 && pos < job.hi && pos + rp.box > job.lo) {
+    if (j < j1 && ((seen32(p, job.b, job.sp, pos) & bits32(0, rp.box)) || (rp.box > 32 && seen32(p, job.b, job.sp, pos + 32)))) {
       const int x = p.table[(int64_t)job.b * p.max_pages + pos / p.page_size];
       if (x >= 0 && x < p.n_pages)
         page = x;
@@ -320,7 +322,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       Job job;
       for (int it = 0; take_job(it, job); ++it) {
         const int j0 = uniform(t ? job.j0[1] : job.j0[0]), j1 = uniform(t ? job.j1[1] : job.j1[0]);
-        const int lo = uniform(job.lo), hi = uniform(job.hi);
         if (!wait(q_full + 8 * (it & 1), it >> 1)) break;
         if (j0 < j1) {
           if (!wait_kv()) break;
@@ -335,11 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
           }
           if (j + 1 == j1) umma_commit_one(one, q_empty + 8 * (it & 1));   // Q's last product is issued
           if (!wait_kv()) break;
-          const int first = max(0, lo - kKeys * j), end = min(kKeys, hi - kKeys * j);   // rows that some query sees
-          if (first > 0 || end < kKeys) {
+          const uint32_t seen0 = seen32(p, job.b, job.sp, kKeys * j), seen1 = seen32(p, job.b, job.sp, kKeys * j + 32);
+          if ((seen0 & seen1) != 0xFFFFFFFFu) {          // rows that no query sees
             const uint32_t v = ring + c * L::kKvBytes;
             for (int x = lane; x < kKeys * 8; x += 32)
-              if ((x >> 3) < first || (x >> 3) >= end)
+              if (!(((x & 256 ? seen1 : seen0) >> ((x >> 3) & 31)) & 1u))
 #pragma unroll
                 for (int d = 0; d < D / 64; ++d) sts128(v + d * kBlockK + x * 16u, 0u, 0u, 0u, 0u);
             fence_async_smem();
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     int n_s = 0;                         // key tiles so far
     for (int it = 0; wait_job(it); ++it) {
       const Job& job = s_job[it % kJobSlots];
-      const int j0 = t ? job.j0[1] : job.j0[0], j1 = t ? job.j1[1] : job.j1[0], b = job.b, job_hi = job.hi;
+      const int j0 = t ? job.j0[1] : job.j0[0], j1 = t ? job.j1[1] : job.j1[0], b = job.b, job_hi = job.sp.hi;
       const int row = job.chunk * rp.tt * p.group + r;
       const bool real = r < rp.tt * p.group && row < rows;
       const bool warp_real = (warp & 3) * 32 < rp.tt * p.group && job.chunk * rp.tt * p.group + (warp & 3) * 32 < rows;
@@ -529,8 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       job.split = idx / p.batch;
       job.more = 1;
       const Span sp = request_span(p, job.b);
-      job.lo = sp.lo;
-      job.hi = sp.hi;
+      job.sp = sp;
       if (lane < p.nq && job.split == 0 && job.h == 0) {
         const int raw = p.vis[(int64_t)job.b * p.nq + lane];
         if (raw != clamp_vis(p, raw)) flag_status(p.status, HSA_FLAG_INDEX_RANGE);

@@ -134,7 +134,7 @@ typedef struct {
   int64_t max_pages;      /* table row length; max_pages * page_size <= 2^31 - 1    */
   void* k;                /* [n_pages][heads][page_size][head_dim]                  */
   void* v;                /* [n_pages][heads][page_size][head_dim]                  */
-  const int32_t* table;   /* i32 [batch][max_pages]; entries no position needs are not read */
+  const int32_t* table;   /* i32 [batch][max_pages]; entries no query needs may hold anything */
   float k_scale, v_scale; /* 2^-120 .. 2^120; 1 unless dtype is HSA_E4M3            */
 } hsa_paged_cache;
 
