@@ -58,7 +58,7 @@ struct PagedAttnParams {
   uint16_t* out;
   float* lse;             // or NULL
   float* part_o;          // workspace [B][heads][n_splits][rows][D], unnormalised
-  float* part_ml;         // workspace [B][heads][n_splits][rows] (maximum in log2 units, sum)
+  float* part_ml;         // workspace [B][heads][n_splits][rows] (log2 of the unit of the sums, sum)
   uint32_t* status;
 };
 cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedSplit& sp, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns,

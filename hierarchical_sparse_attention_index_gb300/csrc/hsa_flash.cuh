@@ -12,6 +12,10 @@ namespace hsa {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRaise = 8.f;            // log2 of how far a logit may pass the running maximum
+// Weights are 2^(x - m + kLift<BF16>). f16 holds full steps down to 2^-14 only, and keys that are 2^-17 of the largest may be
+// many: its weights take the room that kRaise leaves above (2^15 of 65,504). The factor is in the sums as well.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
 
 // mbar_wait with a suspend hint: a waiting warp sleeps in the barrier unit instead of coming back to
 // ask, which would take shared-memory cycles from the products (4 % of a long prompt's time)
@@ -183,7 +187,7 @@ __device__ __forceinline__ void mask_row(uint32_t (&s)[2][32], int lo, int hi) {
 }
 
 // The softmax of 64 keys, one query row per thread: S in the tensor memory columns at .. at + 63 is
-// taken into the running maximum m (in units of S) and sum l, and P = 2^((S - m) scale), rounded to the
+// taken into the running maximum m (in units of S) and sum l, and P = 2^((S - m) scale + kLift), rounded to the
 // operand type, goes into its first 32 columns. `mask(s)` writes -inf where a row does not see a key;
 // `sees`: this thread's row sees a key of the tile. The maximum is only raised where a logit passes
 // it by 2^8 in some row of the warp; O (D columns at tO) is then rescaled, after wait_o() if `later`
@@ -224,7 +228,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t at, uint32_t tO, bool sees
       }
     }
   }
-  const float mu = m == -INFINITY ? 0.f : m * scale;
+  const float mu = m == -INFINITY ? 0.f : fmaf(m, scale, -kLift<BF16>);
   const uint64_t nmu2 = f2_pack(-mu, -mu), scale2 = f2_pack(scale, scale);
   uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
 #pragma unroll

@@ -17,10 +17,11 @@
 //    (E4M3) k-steps. V goes through transposed matrix loads, or, in E4M3, byte permutes and converts
 //    in registers; P^T comes from S^T's accumulators by movmatrix;
 //  - softmax in one pass with the running maximum and sum in fp32. The maximum is only raised, and
-//    the outputs rescaled, when some logit passes it by 2^8: the weights then stay below 256, which
-//    16-bit weights and fp32 sums hold, and most groups need one vote instead of shuffles;
-//  - the weights P are rounded to the 16-bit operand type of the product with V (off by at
-//    most a relative 2^-8 in bf16, 2^-11 in f16, independent from key to key); the sum l takes them unrounded.
+//    the outputs rescaled, when some logit passes it by 2^8, and most groups need one vote instead of shuffles. The
+//    weights then stay below 2^8, which bf16 holds; in f16 they are 2^7 times that, as its full steps end at 2^-14;
+//  - the weights P are rounded to the 16-bit operand type of the product with V (off by at most a relative 2^-8 in
+//    bf16, in f16 2^-11 down to 2^-21 of a row's largest weight and 2^-32 of it below, independent from key to key); the
+//    sum l takes them unrounded.
 // The four warps' (m, l, O) are merged in shared memory. With one split the CTA writes the result. Up to
 // 8 splits are one thread-block cluster, whose CTAs join their parts through distributed shared memory;
 // more leave their parts in the workspace, and paged_join_kernel joins them. Either joins in order.
@@ -34,6 +35,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;               // keys per stage of a warp
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;            // log2 of how far a logit may pass the running maximum
+constexpr float kLiftF16 = 7.f;          // log2 of what f16 weights are multiplied with: 2^15 at most, of 65,504
 
 enum KvType { kBf16 = HSA_BF16, kF16 = HSA_F16, kE4M3 = HSA_E4M3 };
 
@@ -121,6 +123,7 @@ template <int D, int KV, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
   using T = Tile<D, KV, NT>;
   constexpr bool kB = KV == kBf16;                       // products in bf16, else in f16
+  constexpr float kLift = kB ? 0.f : kLiftF16;           // weights are 2^(x - m), m kLift below the running maximum
   constexpr int kSteps = D / 16, kMt = D / 16, kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_scale[kRows];
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
       bool raise = false;
 #pragma unroll
       for (int j = 0; j < 2 * NT; ++j)                   // m = -inf: any logit raises it
-        raise |= fmaf(fmaxf(s[j >> 1][j & 1], s[j >> 1][2 + (j & 1)]), scale[j % kScales], -m[j]) > kRaise;
+        raise |= fmaf(fmaxf(s[j >> 1][j & 1], s[j >> 1][2 + (j & 1)]), scale[j % kScales], -m[j]) > kRaise + kLift;
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int j = 0; j < 2 * NT; ++j) {
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          mx = fmaxf(mx * scale[j % kScales], m[j]);
+          mx = fmaxf(fmaf(mx, scale[j % kScales], -kLift), m[j]);
           const float f = (mx == -INFINITY) ? 1.f : ex2_ftz(m[j] - mx);   // m = -inf before: 0, on sums that are 0
           m[j] = mx;
           l[j] *= f;

@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       ok = wait_bar(o_empty + 8 * t, (it & 1) ^ 1, rp.wait_ns) && ok;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      s_ml[t][r] = make_float2(m == -INFINITY ? m : m * scale, l);
+      s_ml[t][r] = make_float2(m == -INFINITY ? m : fmaf(m, scale, -kLift<BF16>), l);
       __syncwarp();
       if (lane == 0) mbar_arrive(ml_full + 8 * t);
     }

@@ -16,9 +16,9 @@
 //    can be read; one for 128 keys reads 8 KB in 64, but leaves room for one buffer only: 16,384
 //    tokens took the same time, packed prompts 15 % more);
 //  - a warp group does the softmax of each tile, one row per thread (no shuffles): the running
-//    maximum and sum in fp32, P rounded to the operand type (off by at most a relative 2^-8 in bf16, 2^-11 in f16,
-//    independent from key to key) over S's columns. The maximum is only raised, and O rescaled in
-//    tensor memory, when a logit passes it by 2^8: weights stay below 256, and after the first
+//    maximum and sum in fp32, P rounded to the operand type (off by at most a relative 2^-8 in bf16, in f16 2^-11 down
+//    to 2^-21 of a row's largest weight and 2^-32 of it below, independent from key to key) over S's columns. The maximum is only
+//    raised, and O rescaled in tensor memory, when a logit passes it by 2^8: weights stay below 256 (2^15 in f16), and after the first
 //    tiles that hardly happens, so the rescaling needs no warps of its own;
 //  - four warps write the results, while the softmax is at the next work (in a window of 128 the writing
 //    took as long as half of the softmax);
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
             }
           }
         }
-        if (p.lse && mine) p.lse[row * p.heads_q + hq] = l != 0.f ? (m * p.scale_log2 + log2f(l)) * kLn2 : -INFINITY;
+        if (p.lse && mine) p.lse[row * p.heads_q + hq] = l != 0.f ? (fmaf(m, p.scale_log2, -kLift<BF16>) + log2f(l)) * kLn2 : -INFINITY;
       }
     }
   }

@@ -73,3 +73,77 @@ def test_decode_queries_further_apart_than_the_window(H, kv, qt, dim, heads, gro
                 o, l, A, mag = D.attention(q[b, :, mine].reshape(-1, dim).double(), kk[:, h], vv[:, h], lo, hi, scale)
                 D.check(out[b, :, mine].reshape(-1, dim), lse[b, :, mine].reshape(-1), o, l, A, mag, longest[b], dim,
                         BF if kv == BF else HF, f"window {window} bound {most} request {b} head {h}")
+
+
+# ------------------------------------------------------------------------------------- a long tail of weights
+def tail(n, heads, dim, kv, at, gap):
+    """Keys whose logits are alike (within about 0.5) but for those at `at`, `gap` higher and with v = 0, and a query row."""
+    g = torch.Generator().manual_seed(n)
+    k, v = torch.randn(n, heads, dim, generator=g), 1 + 0.25 * torch.randn(n, heads, dim, generator=g)
+    k[..., 0] = 0
+    k[at] = 0
+    k[at, :, 0] = 4.0
+    v[at] = 0
+    q = torch.full((dim,), 0.5)
+    q[0] = gap * math.sqrt(dim) / 4
+    return q, k.to(kv), v.to(kv)
+
+
+def with_floor(A, n, v, p_type, o_type, lse, top):
+    """A, raised so that the bound of tests/dense.py gains the absolute part of the weights' rounding: an f16 weight below
+    2^-14 is off by up to 2^-25, in units where the row's largest weight is 2^7 at least and their sum 2^7 exp(lse - top)
+    with it, for each of n keys. The bound multiplies A by u_p + u_o + 2 n 2^-23 and more."""
+    if p_type != HF:
+        return A
+    rel = 2.0 ** -11 + torch.finfo(o_type).eps / 2 + 2 * n * 2.0 ** -23
+    return A + n * 2.0 ** -32 * torch.exp(top - lse)[:, None] * v.abs().max() / rel
+
+
+@pytest.mark.parametrize("gap", [14.0, 16.0, 17.0, 17.4])
+@pytest.mark.parametrize("kv,qt", [(HF, HF), (F8, HF), (F8, BF), (BF, BF)])
+@pytest.mark.parametrize("dim,group", [(128, 8), (64, 16), (128, 28), (64, 64)])
+def test_decode_long_tail(H, kv, qt, dim, group, gap):
+    """A few keys far above 65,529 alike: the tail's weights are 2^-20 and less, and what they bring together is kept. The
+    high keys stand where each warp and each stream of a CTA meets them first."""
+    n, heads, page, batch = 65536, 4, 64, 128
+    at = [0, 16, 32, 48, n // 4, n // 2, 3 * n // 4]
+    q, k, v = tail(n, heads, dim, kv, at, gap)
+    pages = n // page
+    k, v = (x.view(torch.uint8 if kv == F8 else kv).view(pages, page, heads, -1).transpose(1, 2).contiguous().view(kv).cuda() for x in (k, v))
+    table = torch.arange(pages, dtype=torch.int32).cuda().repeat(batch, 1)
+    q = q.to(qt).cuda().expand(batch, 1, heads * group, dim).contiguous()
+    cache = H.PagedCache(k, v, table)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    vis = torch.full((batch, 1), n, dtype=torch.int32, device="cuda")
+    scale = 1 / math.sqrt(dim)
+    H.hsa_paged_attn_decode(cache, q, vis, n, scale, out, H.new_paged_workspace(cache, heads * group, 1, n), lse=lse)
+    clean(H)
+    kk, vv = (D.unpage(x, table, 0, n)[0] for x in (k, v))
+    hi = torch.full((1,), n, device="cuda")
+    p_type = BF if kv == BF else HF
+    for h in range(heads):
+        row = q[0, 0, h * group][None].double()
+        o, l, A, mag = D.attention(row, kk[:, h], vv[:, h], hi * 0, hi, scale)
+        A = with_floor(A, n, vv, p_type, qt, l, (row @ kk[:, h].T).max() * scale)
+        for r in (h * group, (h + 1) * group - 1):
+            D.check(out[0, :1, r], lse[0, :1, r], o, l, A, mag, n, dim, p_type, f"head {h}")
+    assert torch.equal(out[0], out[-1]) and torch.equal(lse[0], lse[-1])
+
+
+@pytest.mark.parametrize("gap", [14.0, 16.0, 17.0, 17.4])
+@pytest.mark.parametrize("dtype", [HF, BF])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prompt_long_tail(H, dim, dtype, gap):
+    """The same for the last rows of a prompt, whose key tiles are met from the diagonal downwards."""
+    n, group, last = 16384, 4, 256
+    q, k, v = tail(n, 1, dim, dtype, [n - last], gap)
+    q = q.to(dtype).cuda().expand(last, group, dim).contiguous()
+    k, v = k.cuda(), v.cuda()
+    out, lse = torch.empty_like(q), torch.empty(last, group, device="cuda")
+    scale = 1 / math.sqrt(dim)
+    H.hsa_prompt_attn(q, k, v, i32([0, last]), scale, out, cu_k=i32([0, n]), lse=lse)
+    clean(H)
+    hi = torch.arange(n - last + 1, n + 1, device="cuda").repeat_interleave(group)
+    o, l, A, mag = D.attention(q.reshape(-1, dim).double(), k[:, 0].double(), v[:, 0].double(), hi * 0, hi, scale)
+    top = (q[0, 0].double() @ k[:, 0].double().T).max() * scale        # every row sees it
+    D.check(out.reshape(-1, dim), lse.reshape(-1), o, l, with_floor(A, n, v.double(), dtype, dtype, l, top), mag, n, dim, dtype)
