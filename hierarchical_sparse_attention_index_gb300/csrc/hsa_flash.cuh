@@ -28,6 +28,7 @@ __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
+// Each lane has its own limit: a warp votes on the outcome before it goes on.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   if (mbar_sleep(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();

@@ -607,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
             },
             [&]() {                      // the last tile's P V is in O
               ok = wait_bar(o_full + 16 * t + 8 * ((n_s - 1) & 1), ((n_s - 1) >> 1) & 1, p.wait_ns) && ok;
+              ok = __all_sync(0xffffffffu, ok);
               tc_fence_after();
             });
         later = true;
