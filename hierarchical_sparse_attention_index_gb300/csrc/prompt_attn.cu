@@ -90,11 +90,14 @@ struct Seq {
   int q0, lq, k0, lk;
   int count, base;                       // pieces of work, and the level of the first
 };
-__device__ __forceinline__ Seq load_seq(const PromptParams& p, int b) {
+// Sequence b, empty if its own bounds are bad
+__device__ __forceinline__ Seq load_seq(const PromptParams& p, int b, bool& good) {
   Seq s = {};
+  good = true;
   if (b < p.batch) {
     const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
-    if (q0 >= 0 && q0 <= q1 && q1 <= p.n_q && k0 >= 0 && k0 <= k1 && k1 <= p.n_k)
+    good = q0 >= 0 && q0 <= q1 && q1 <= p.n_q && k0 >= 0 && k0 <= k1 && k1 <= p.n_k;
+    if (good)
       s = Seq{q0, q1 - q0, k0, k1 - k0};
     else
       flag_status(p.status, HSA_FLAG_INDEX_RANGE);
@@ -102,6 +105,32 @@ __device__ __forceinline__ Seq load_seq(const PromptParams& p, int b) {
   const int tpc = 2 * p.tt;
   s.count = (s.lq + tpc - 1) / tpc;
   s.base = p.window > 0 ? 0 : max(0, s.lk - s.lq) / tpc;
+  return s;
+}
+// Sequences first + lane, by one warp; one that starts before an earlier one ends is empty too, so that no row
+// has two and the pieces are no more than prompt_blocks counts. `high`: where the earlier ones end. Bounds that ascend
+// ask for one comparison; behind a bad one each lane needs the ends of those before it.
+__device__ __forceinline__ Seq load_seqs(const PromptParams& p, int first, int& high) {
+  const int lane = threadIdx.x & 31;
+  bool good;
+  Seq s = load_seq(p, first + lane, good);
+  const int end = s.lq > 0 ? s.q0 + s.lq : 0;
+  int before = high;
+  if (__any_sync(0xffffffffu, !good)) {
+    int upto = end;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto = max(upto, y);
+    }
+    upto = __shfl_up_sync(0xffffffffu, upto, 1);
+    if (lane > 0) before = max(before, upto);
+  }
+  high = max(high, __reduce_max_sync(0xffffffffu, end));
+  if (s.lq > 0 && s.q0 < before) {
+    flag_status(p.status, HSA_FLAG_INDEX_RANGE);
+    s.lq = s.count = 0;
+  }
   return s;
 }
 
@@ -151,7 +180,7 @@ struct Order {
     int left = r - above(x + 1);
     auto among = [&](int first, int c, int b) {          // of 32 sequences from `first`, this lane's with c pieces from level b on
       uint32_t m = __ballot_sync(0xffffffffu, b <= x && x < b + c);
-      if (!m || left >= __popc(m)) {     // (none of them: only where bounds overlap so that the count overflows)
+      if (left >= __popc(m)) {
         left -= __popc(m);
         return false;
       }
@@ -173,13 +202,14 @@ struct Order {
 };
 
 // Larger batches are worked off in the order of the sequences, the last piece of each first. A search starts
-// at the 32 sequences where the last one ended (`first`, with `before` pieces before them): a CTA's blocks
-// come in rising order, so all its searches together pass over the batch about once.
-__device__ __forceinline__ bool find_in_turn(const PromptParams& p, int r, Seq& out, int& i, int& first, int& before) {
+// at the 32 sequences where the last one ended (`first`, with `before` pieces before them, which end at `high`): a CTA's
+// blocks come in rising order, so all its searches together pass over the batch about once.
+__device__ __forceinline__ bool find_in_turn(const PromptParams& p, int r, Seq& out, int& i, int& first, int& before, int& high) {
   const int lane = threadIdx.x & 31;
-  if (r < before) first = before = 0;
+  if (r < before) first = before = high = 0;
   for (; first < p.batch; first += 32) {
-    const Seq s = load_seq(p, first + lane);
+    int end = high;
+    const Seq s = load_seqs(p, first, end);
     int upto = s.count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -198,6 +228,7 @@ __device__ __forceinline__ bool find_in_turn(const PromptParams& p, int r, Seq& 
       return true;
     }
     before = __shfl_sync(0xffffffffu, upto, 31);
+    high = end;
   }
   return false;
 }
@@ -510,12 +541,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       Seq* seqs = reinterpret_cast<Seq*>(smem_raw + (base - raw) + L::kOffSeq);
       Order order;
       if (p.batch <= kSeqs) {
-        for (int b = lane; b < p.batch; b += 32) seqs[b] = load_seq(p, b);
+        for (int first = 0, high = 0; first < p.batch; first += 32) {
+          const Seq s = load_seqs(p, first, high);
+          if (first + lane < p.batch) seqs[first + lane] = s;
+        }
         __syncwarp();
         order.hold(seqs, p.batch);
       }
       bool is_long = false;
-      int in_turn = 0, pieces = 0;       // find_in_turn's place
+      int in_turn = 0, pieces = 0, high = 0;     // find_in_turn's place
       for (int n = 0; ok; ++n) {
         Job job;
         Seq seq;
@@ -526,9 +560,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
           found = order.find(r, which, i);
           if (found) seq = seqs[which];
         } else {
-          found = find_in_turn(p, r, seq, i, in_turn, pieces);
+          found = find_in_turn(p, r, seq, i, in_turn, pieces, high);
+          bool good;
           if (block == gridDim.x - 1)    // every sequence's bounds are looked at once
-            for (int b = lane; b < p.batch; b += 32) load_seq(p, b);
+            for (int b = lane; b < p.batch; b += 32) load_seq(p, b, good);
         }
         if (found) {
           make_job(p, seq, i, h, job);

@@ -364,8 +364,9 @@ HSA_API hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const voi
  * Rows of q, out and lse outside [cu_q[0], cu_q[batch]) are neither read for a result nor written.
  * A sequence never uses another's rows, nor rows outside [cu_k[0], cu_k[batch]), whatever they
  * hold; a value of its own that is not finite may reach queries that do not see it, as 0 times it
- * is NaN. A sequence whose bounds are not ascending inside [0, n_q] and [0, n_k] is skipped and
- * flagged HSA_FLAG_INDEX_RANGE. n_q and n_k <= 2^27; n_q = 0 launches nothing. Pieces of 2 x
+ * is NaN. A sequence whose bounds are not ascending inside [0, n_q] and [0, n_k], or whose queries start
+ * before an earlier such sequence's end, is skipped and flagged HSA_FLAG_INDEX_RANGE; sequences may
+ * share rows of k and v. n_q and n_k <= 2^27; n_q = 0 launches nothing. Pieces of 2 x
  * (128 / group) tokens, times heads_kv, have to be fewer than 2^31 (HSA_ERR_SHAPE). */
 HSA_API hsa_status hsa_prompt_attn(const hsa_prompt_args* args, hsa_stream_t stream);
 

@@ -147,3 +147,44 @@ def test_prompt_long_tail(H, dim, dtype, gap):
     o, l, A, mag = D.attention(q.reshape(-1, dim).double(), k[:, 0].double(), v[:, 0].double(), hi * 0, hi, scale)
     top = (q[0, 0].double() @ k[:, 0].double().T).max() * scale        # every row sees it
     D.check(out.reshape(-1, dim), lse.reshape(-1), o, l, with_floor(A, n, v.double(), dtype, dtype, l, top), mag, n, dim, dtype)
+
+
+# ------------------------------------------------------------------------------------- sequences that overlap
+@pytest.mark.parametrize("batch", [5, 40, 600])
+@pytest.mark.parametrize("group", [1, 4])
+def test_prompt_sequences_that_overlap(H, batch, group):
+    """Bounds that go back and start again: what an earlier sequence has is not given out twice, every other sequence is
+    computed, and the flag is set."""
+    n, dim = 1500, 64
+    g = torch.Generator().manual_seed(batch)
+    q = torch.randn(n, group, dim, generator=g).to(BF).cuda()
+    k, v = (torch.randn(2 * n, 1, dim, generator=g).to(BF).cuda() for _ in range(2))
+    # [0, 1000) over and over, each time with other keys, then [1000, 1500)
+    cu_q = [0, 1000] * (batch // 2) + [1000] * (batch % 2) + [n]
+    assert len(cu_q) == batch + 1
+    cu_k = [0, 1000] + [1200 + b for b in range(batch - 2)] + [2 * n]
+    out, lse = torch.full_like(q, 7.0), torch.full((n, group), 7.0, device="cuda")
+    H.hsa_prompt_attn(q, k, v, i32(cu_q), 0.125, out, cu_k=i32(cu_k), lse=lse)
+    clean(H, H.HSA_FLAG_INDEX_RANGE)
+    first = cu_k[batch - 1]
+    for q0, q1, k0, k1 in ((0, 1000, 0, 1000), (1000, n, first, 2 * n)):
+        hi = (torch.arange(q1 - q0, device="cuda") + (k1 - k0) - (q1 - q0) + 1).repeat_interleave(group)
+        o, l, A, mag = D.attention(q[q0:q1].reshape(-1, dim).double(), k[k0:k1, 0].double(), v[k0:k1, 0].double(), hi * 0, hi, 0.125)
+        D.check(out[q0:q1].reshape(-1, dim), lse[q0:q1].reshape(-1), o, l, A, mag, k1 - k0, dim, BF, f"rows from {q0}")
+
+
+def test_prompt_sequences_that_share_keys(H):
+    """Bounds of the keys that go back: the sequence whose own keys descend is skipped, those around it are computed
+    from the same keys."""
+    n, dim = 64, 64
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(3 * n, 2, dim, generator=g).to(HF).cuda()
+    k, v = (torch.randn(2 * n, 1, dim, generator=g).to(HF).cuda() for _ in range(2))
+    out = torch.full_like(q, 7.0)
+    H.hsa_prompt_attn(q, k, v, i32([0, n, 2 * n, 3 * n]), 0.125, out, cu_k=i32([0, 2 * n, 0, 2 * n]))
+    clean(H, H.HSA_FLAG_INDEX_RANGE)
+    for q0 in (0, 2 * n):
+        hi = (torch.arange(n, device="cuda") + n + 1).repeat_interleave(2)
+        o, l, A, mag = D.attention(q[q0:q0 + n].reshape(-1, dim).double(), k[:, 0].double(), v[:, 0].double(), hi * 0, hi, 0.125)
+        D.check(out[q0:q0 + n].reshape(-1, dim), None, o, l, A, mag, 2 * n, dim, HF, f"rows from {q0}")
+    assert (out[n:2 * n] == 7).all()
