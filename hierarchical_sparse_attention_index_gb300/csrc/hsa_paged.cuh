@@ -41,9 +41,9 @@ __device__ __forceinline__ uint32_t bits32(int lo, int hi) {
   const uint32_t below_hi = hi >= 32 ? 0xFFFFFFFFu : (1u << max(hi, 0)) - 1u, below_lo = lo >= 32 ? 0xFFFFFFFFu : (1u << max(lo, 0)) - 1u;
   return below_hi & ~below_lo;
 }
-// Bit i: some query of request b sees position at + i
-__device__ __forceinline__ uint32_t seen32(const PagedAttnParams& p, int b, const Span& s, int at) {
-  if (!s.gaps) return bits32(s.lo - at, s.hi - at);
+// Bit i: some query of request b, whose Span has lo, hi and gaps, sees position at + i
+__device__ __forceinline__ uint32_t seen32(const PagedAttnParams& p, int b, int lo, int hi, bool gaps, int at) {
+  if (__builtin_expect(!gaps, 1)) return bits32(lo - at, hi - at);
   uint32_t seen = 0;
 #pragma unroll 1
   for (int i = 0; i < p.nq; ++i) {

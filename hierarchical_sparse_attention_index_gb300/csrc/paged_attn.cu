@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
     const int i = 32 * turn + lane;
     if (i >= n_groups) return 0;
     const int pos = begin + kGroup * (warp + kWarps * i), pg = pos / p.page_size;
-    const uint32_t seen = seen32(p, b, sp, pos) & 0xFFFFu;
+    const uint32_t seen = seen32(p, b, sp.lo, sp.hi, sp.gaps, pos) & 0xFFFFu;
     if (!seen) return 0;
     const int page = p.table[(int64_t)b * p.max_pages + pg];
     if (page < 0 || page >= p.n_pages) {

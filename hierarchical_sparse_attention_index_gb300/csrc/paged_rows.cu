@@ -66,8 +66,8 @@ struct RowsParams {
 };
 
 struct Job {
-  int b, h, chunk, split;
-  Span sp;                               // of the request's positions
+  int b, h, chunk, split, lo, hi;        // [lo, hi): where the positions lie that queries of the request see
+  int gaps;                              // some of them may be seen by none
   int j0[2], j1[2];                      // 64-key tiles [j0, j1) of stream t
   int whole;                             // the request's only split
   int more;                              // 0: no work is left, the other fields are not set
@@ -181,10 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   // when the job is posted: two reads that depend on each other, which would leave the memory idle between
   // jobs); n_pages: no page (TMA then fills in zeros)
   const int blocks = kKeys / rp.box, per = 32 / blocks;
+  auto seen_at = [&](const Job& job, int pos) { return seen32(p, job.b, job.lo, job.hi, job.gaps, pos); };
+  auto any_seen = [&](const Job& job, int pos) {         // of a box
+    return (seen_at(job, pos) & bits32(0, rp.box)) || (rp.box > 32 && seen_at(job, pos + 32));
+  };
   auto find_pages = [&](const Job& job, int j0, int j1, int turn) {
     const int j = j0 + turn * per + lane / blocks, pos = kKeys * j + rp.box * (lane % blocks);
     int page = (int)p.n_pages;
-    if (j < j1 && ((seen32(p, job.b, job.sp, pos) & bits32(0, rp.box)) || (rp.box > 32 && seen32(p, job.b, job.sp, pos + 32)))) {
+    if (j < j1 && pos < job.hi && pos + rp.box > job.lo && (!job.gaps || any_seen(job, pos))) {
       const int x = p.table[(int64_t)job.b * p.max_pages + pos / p.page_size];
       if (x >= 0 && x < p.n_pages)
         page = x;
@@ -322,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       Job job;
       for (int it = 0; take_job(it, job); ++it) {
         const int j0 = uniform(t ? job.j0[1] : job.j0[0]), j1 = uniform(t ? job.j1[1] : job.j1[0]);
+        const int lo = uniform(job.lo), hi = uniform(job.hi), gaps = uniform(job.gaps);
         if (!wait(q_full + 8 * (it & 1), it >> 1)) break;
         if (j0 < j1) {
           if (!wait_kv()) break;
@@ -336,8 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
           }
           if (j + 1 == j1) umma_commit_one(one, q_empty + 8 * (it & 1));   // Q's last product is issued
           if (!wait_kv()) break;
-          const uint32_t seen0 = seen32(p, job.b, job.sp, kKeys * j), seen1 = seen32(p, job.b, job.sp, kKeys * j + 32);
-          if ((seen0 & seen1) != 0xFFFFFFFFu) {          // rows that no query sees
+          if (kKeys * j < lo || kKeys * (j + 1) > hi || gaps) {        // there may be rows that no query sees
+            const uint32_t seen0 = seen_at(job, kKeys * j), seen1 = seen_at(job, kKeys * j + 32);
             const uint32_t v = ring + c * L::kKvBytes;
             for (int x = lane; x < kKeys * 8; x += 32)
               if (!(((x & 256 ? seen1 : seen0) >> ((x >> 3) & 31)) & 1u))
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     int n_s = 0;                         // key tiles so far
     for (int it = 0; wait_job(it); ++it) {
       const Job& job = s_job[it % kJobSlots];
-      const int j0 = t ? job.j0[1] : job.j0[0], j1 = t ? job.j1[1] : job.j1[0], b = job.b, job_hi = job.sp.hi;
+      const int j0 = t ? job.j0[1] : job.j0[0], j1 = t ? job.j1[1] : job.j1[0], b = job.b, job_hi = job.hi;
       const int row = job.chunk * rp.tt * p.group + r;
       const bool real = r < rp.tt * p.group && row < rows;
       const bool warp_real = (warp & 3) * 32 < rp.tt * p.group && job.chunk * rp.tt * p.group + (warp & 3) * 32 < rows;
@@ -531,7 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       job.split = idx / p.batch;
       job.more = 1;
       const Span sp = request_span(p, job.b);
-      job.sp = sp;
+      job.lo = sp.lo;
+      job.hi = sp.hi;
+      job.gaps = sp.gaps;
       if (lane < p.nq && job.split == 0 && job.h == 0) {
         const int raw = p.vis[(int64_t)job.b * p.nq + lane];
         if (raw != clamp_vis(p, raw)) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
