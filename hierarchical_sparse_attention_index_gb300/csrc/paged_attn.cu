@@ -699,7 +699,7 @@ PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, 
   const int32_t rows = nq * group;
   s.tc = kv_dtype != HSA_E4M3 && rows > kTcRows;
   if (s.tc) {
-    const int32_t queries = 128 / group;
+    const int32_t queries = nq < 128 / group ? nq : 128 / group;
     s.chunks = (nq + queries - 1) / queries;
     s.chunk_rows = queries * group;
   } else {

@@ -10,7 +10,7 @@
 // a ring of K and V tiles, a warp that loads it, a warp that issues the products, a warp group with a query
 // row per thread for the softmax, buffers of S and an accumulator in tensor memory; the two streams fill each
 // other's waits. A row without a query (35 rows fill 35 of 128) costs nothing but its lane: warps without any
-// skip the softmax, and the rows take no shared memory, which the rings get.
+// skip the softmax, no other request's queries are loaded for it, and it takes no shared memory, which the rings get.
 //  - K and V tiles come as boxes of gcd(page size, 64) rows by TMA (128-byte swizzle); rows inside a box that
 //    no query sees (past the visible length, or between the windows of queries far apart) are cleared before use, as
 //    zero times what they hold need not be zero; blocks without any other row, or on a bad page, come from outside
@@ -49,14 +49,16 @@ constexpr int kOrdered = 128;            // batches up to this can be worked off
 template <int D>
 struct Shape {
   static constexpr uint32_t kKvBytes = (D / 64) * kBlockK;
-  static constexpr int kMaxStages = D == 128 ? 6 : 12;           // tiles of K and V in a stream's ring
+  // tiles of K and V in a stream's ring, at most. 4, 5, 6 at 128 dims: 64 requests x 16,384 keys 332, 327.5, 327 us, of
+  // 1 .. 4,097 keys 61.3, 60.7, 61.7, 1 request x 131,072 53.6, 53.9, 55.7
+  static constexpr int kMaxStages = D == 128 ? 5 : 10;
 };
 constexpr uint32_t kSmemMost = 227 * 1024 - 4096;                // but for what is declared in the kernel
 
 struct RowsParams {
   CUtensorMap qm, km, vm;
   PagedAttnParams a;
-  int32_t tt;                            // queries per chunk: 128 / group
+  int32_t tt;                            // queries per chunk: as many as a request has, at most 128 / group
   int32_t box;                           // rows of a box of the pools
   int32_t q_rows;                        // rows of a query block in shared memory: tt x group, whole groups of 8
   int32_t stages;                        // of a stream's ring: what the queries leave room for
@@ -613,7 +615,7 @@ cudaError_t launch_paged_rows(const PagedAttnParams& a, int32_t head_dim, int32_
   RowsParams p;
   memset(&p, 0, sizeof(p));
   p.a = a;
-  p.tt = kTile / a.group;
+  p.tt = a.chunk_rows / a.group;
   p.box = std::gcd(a.page_size, kKeys);
   // Whole requests, more of them than SMs: the longest first, so that the last ones to be taken are short (64 requests
   // x 4 heads of 1 .. 4,097 keys 64 us, 72 in the order of the requests; 100 x 4 of up to 1,024 35 and 40; all with

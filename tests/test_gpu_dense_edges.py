@@ -188,3 +188,50 @@ def test_prompt_sequences_that_share_keys(H):
         o, l, A, mag = D.attention(q[q0:q0 + n].reshape(-1, dim).double(), k[:, 0].double(), v[:, 0].double(), hi * 0, hi, 0.125)
         D.check(out[q0:q0 + n].reshape(-1, dim), None, o, l, A, mag, 2 * n, dim, HF, f"rows from {q0}")
     assert (out[n:2 * n] == 7).all()
+
+
+# ------------------------------------------------------------------------------------- tiles of query rows
+@pytest.mark.parametrize("kv", [BF, HF])
+@pytest.mark.parametrize("dim,group,nq", [(128, 7, 5), (64, 13, 2), (128, 42, 8), (64, 33, 1), (128, 65, 3), (64, 5, 8)])
+def test_decode_tiles_of_queries(H, kv, dim, group, nq):
+    """Requests of 26 to 336 rows per key head, one of them with queries that are NaN: it is the only one that notices."""
+    vis = [[500 - i for i in range(nq)], [64] * nq, [1000] * nq]
+    k, v, table = D.paged(3, [500, 64, 1000], 2, dim, 32, kv, group)
+    cache = H.PagedCache(k.cuda(), v.cuda(), table.cuda())
+    q = torch.randn(3, nq, 2 * group, dim, generator=torch.Generator().manual_seed(nq)).to(kv).cuda()
+    q[1] = math.nan
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:3], 7.0, device="cuda")
+    H.hsa_paged_attn_decode(cache, q, i32(vis), 1000, 0.1, out, H.new_paged_workspace(cache, 2 * group, nq, 1000), lse=lse)
+    clean(H)
+    assert out[1].isnan().all()
+    for b in (0, 2):
+        kk, vv = (D.unpage(x, cache.table, b, max(vis[b]))[0] for x in (cache.k, cache.v))
+        hi = i32(vis[b]).repeat_interleave(group)
+        for h in range(2):
+            mine = slice(h * group, (h + 1) * group)
+            o, l, A, mag = D.attention(q[b, :, mine].reshape(-1, dim).double(), kk[:, h], vv[:, h], hi * 0, hi, 0.1)
+            D.check(out[b, :, mine].reshape(-1, dim), lse[b, :, mine].reshape(-1), o, l, A, mag, max(vis[b]), dim, kv, f"request {b}")
+
+
+# ------------------------------------------------------------------------------------- large pools
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_decode_many_rows_past_2_31_bytes(H, dtype):
+    """The kernel for many rows on pages that start past 2^31 bytes and 2^31 elements of their pools."""
+    heads, page, dim, group, n = 2, 64, 128, 40, 311
+    pages = (2 ** 31 + 2 ** 28) // (heads * page * dim)             # elements
+    need = -(-n // page)
+    g = torch.Generator().manual_seed(7)
+    pools = []
+    for _ in range(2):
+        pool = torch.zeros(pages, heads, page, dim, dtype=dtype, device="cuda")
+        pool[-need:] = torch.randn(need, heads, page, dim, generator=g).to(dtype).cuda()
+        pools.append(pool)
+    q = torch.randn(1, 1, heads * group, dim, generator=g).to(dtype).cuda()
+    outs = []
+    for k, v, first in ((*pools, pages - need), (*(x[-need:].clone() for x in pools), 0)):
+        cache = H.PagedCache(k, v, i32([list(range(first, first + need))]))
+        out = torch.empty_like(q)
+        H.hsa_paged_attn_decode(cache, q, i32([[n]]), n, 0.1, out, H.new_paged_workspace(cache, heads * group, 1, n))
+        outs.append(out)
+    clean(H)
+    assert torch.equal(*outs) and outs[0].isfinite().all()
