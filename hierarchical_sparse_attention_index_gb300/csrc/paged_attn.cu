@@ -93,6 +93,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// CTAs that an SM holds, for NT tiles of 8 query rows: as registers and shared memory (their rings, 227 KB) allow
+constexpr int ctas_per_sm(int nt) { return nt <= 2 ? 3 : 2; }
+
 template <int D, int KV, int NT>
 struct Tile {
   static constexpr int kElem = KV == kE4M3 ? 1 : 2;
@@ -100,8 +103,7 @@ struct Tile {
   static constexpr int kChunks = kRow / 16;
   static constexpr int kHalf = kGroup * kRow;            // K, then V
   static constexpr int kStage = 2 * kHalf;
-  // CTAs per SM, as registers and shared memory (their rings, 227 KB) allow
-  static constexpr int kCtas = NT <= 2 ? 3 : 2;
+  static constexpr int kCtas = ctas_per_sm(NT);
   static constexpr int kRingMax = kCtas == 3 ? 16384 : 24576;
   static constexpr int kStages = kRingMax / kStage > 6 ? 6 : kRingMax / kStage;
   static constexpr int kRing = kStage * kStages;
@@ -655,22 +657,33 @@ cudaError_t launch_kv(const PagedAttnParams& p, int kv, cudaStream_t s) {
 
 }  // namespace
 
-// Splits for the tcgen05 kernel, one CTA to an SM: the n with the least rounds x (keys of a job + 400) + 20 n, in
-// the time of a key. A job costs what 400 keys do besides its own (its start and end), a split 20 in the join; a
-// round that is not full costs as much as a full one. 64 requests x 4 heads x 16,384 keys, ragged: n = 1, 4, 9: 246,
-// 204, 229 us; x 4,097: 73, 77, 105; 8 x 4 x 16,384: n = 3, 4, 5, 9: 54.6, 53.9, 74.5, 59.0. In w rounds the best n is
-// the largest that fits, or the square root where the two last terms meet.
-static int64_t tc_splits_in(int64_t w, int64_t ctas, int64_t span) {
-  const int64_t meet = (int64_t)sqrtf((float)(w * span) / 20.f);
-  return imax64(1, imin64(imin64(152 * w / ctas, (span + 127) / 128), meet));
-}
-constexpr int64_t kRounds = 8;           // numbers of rounds looked at
-static int64_t tc_splits(int64_t ctas, int64_t span) {
-  const int64_t first = (ctas + 151) / 152;
+// Splits by rounds of the `places` that the GPU has for CTAs: the n with the least rounds x (keys of a job + 400) + 20 n,
+// in the time of a key. A job costs what 400 keys do besides its own (its start and end), a split 20 in the join; a
+// round that is not full costs as much as a full one. In w rounds the best n is the largest that fits.
+struct Rounds {
+  int64_t places;
+  int64_t count;                         // numbers of rounds looked at
+  bool few;                              // no more splits than where the two last terms meet
+  int64_t first(int64_t ctas) const { return (ctas + places - 1) / places; }
+  int64_t splits_in(int64_t w, int64_t ctas, int64_t span) const {
+    int64_t n = imin64(places * w / ctas, (span + 127) / 128);
+    if (few) n = imin64(n, (int64_t)sqrtf((float)(w * span) / 20.f));
+    return imax64(1, n);
+  }
+  int64_t most(int64_t ctas, int64_t span) const { return splits_in(first(ctas) + count - 1, ctas, span); }
+};
+// The tcgen05 kernel, one CTA to an SM. 64 requests x 4 heads x 16,384 keys, ragged: n = 1, 4, 9: 246, 204, 229 us;
+// x 4,097: 73, 77, 105; 8 x 4 x 16,384: n = 3, 4, 5, 9: 54.6, 53.9, 74.5, 59.0
+constexpr Rounds kTcRounds = {152, 8, true};
+// The warp MMA kernel with 17 to 32 rows, two to an SM. Against as many CTAs as four to an SM would be, in no rounds: 16
+// requests x 8 heads x 20 rows, f16, 4,097 keys 30 us (46), 16,384 97 (115); 16 x 4 x 35 rows, E4M3, 4,097 36 (40), 16,384 93 (98);
+// 64 x 4 x 24 rows, bf16, of 1 .. 16,384 keys 187 (206), all 65,536 1,240 (1,205); 4 x 4 x 35, E4M3, 4,097 17.1 (15.9)
+constexpr Rounds kWideRounds = {2 * 152, 6, false};
+static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
   int64_t best = 1, cost = INT64_MAX;
-  for (int64_t w = first; w < first + kRounds; ++w) {
-    const int64_t n = tc_splits_in(w, ctas, span);
-    const int64_t c = (ctas * n + 151) / 152 * (span / n + 400) + 20 * n;
+  for (int64_t w = r.first(ctas); w < r.first(ctas) + r.count; ++w) {
+    const int64_t n = r.splits_in(w, ctas, span);
+    const int64_t c = r.first(ctas * n) * (span / n + 400) + 20 * n;
     if (c < cost) {
       cost = c;
       best = n;
@@ -684,15 +697,16 @@ static int64_t tc_splits(int64_t ctas, int64_t span) {
 // rows (64 requests x 4 heads, f16, up to 4,097 keys) took 72 us there and 85 here, up to 16,384 keys 200 and 260; 24
 // rows 72 and 70, 200 and 222, but 32 requests x 8 heads x 8,192 126 and 107. Else up to 32 rows one CTA reads its keys once for all of them; more rows (E4M3) are dealt out
 // evenly (35: 18 and 17), and the later CTAs' keys come from L2.
-// The splits make about as many CTAs as the GPU holds at a time (3 or 2 per SM): more only add starts and joins (4
-// requests of 131,072 FP8 keys: 168 us with 448 CTAs, 193 with 608, 217 with 1,216). No split is
-// shorter than 256 keys (8 per group of a warp; in a cluster 128).
+// Up to 16 rows the splits make about as many CTAs as the GPU holds at a time, 3 per SM: more only add starts and joins (4
+// requests of 131,072 FP8 keys: 168 us with 448 CTAs, 193 with 608, 217 with 1,216); from 17 rows on rounds of 2 per SM
+// decide. No split is shorter than 256 keys (8 per group of a warp; in a cluster 128).
 // Splits that all run at a time join in clusters (1 request of 1,000 keys: 6.7 us against 8.5); with more
 // CTAs than that, a cluster's short CTAs would hold places until its longest ends (32 ragged contexts: 99
 // us against 93).
 // A request's splits follow from max_vis and the sizes alone, so that its result does not depend on
 // where it stands in the batch. (Equal pieces of all requests' keys, one per place on the GPU, were
 // slower: 109 against 94 us for 32 ragged contexts, because SMs do not get equal shares of HBM.)
+static bool wide(const PagedSplit& s) { return !s.tc && s.chunk_rows > 16; }
 PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype) {
   constexpr int32_t kTcRows = 24;
   PagedSplit s;
@@ -709,19 +723,19 @@ PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, 
   s.align = s.tc ? 64 : 16;
   int64_t span = max_vis;
   if (window > 0 && (int64_t)window + nq + s.align - 1 < span) span = (int64_t)window + nq + s.align - 1;   // vis one apart, as in a draft
-  const int64_t ctas = (int64_t)batch * heads * s.chunks;
+  const int64_t ctas = (int64_t)batch * heads * s.chunks, places = 152 * ctas_per_sm((s.chunk_rows + 7) / 8);
   int64_t n;
   if (s.tc) {
-    n = tc_splits(ctas, span);
+    n = best_splits(kTcRounds, ctas, span);
   } else {
-    const int64_t places = 152 * (s.chunk_rows <= 16 ? 3 : 4);
-    n = imin64((places + ctas / 2) / ctas, (span + 255) / 256);
-    if (n < 8) n = imin64(imin64((places + ctas / 2) / ctas, 8), (span + 127) / 128);
+    const int64_t most = wide(s) ? best_splits(kWideRounds, ctas, span) : (places + ctas / 2) / ctas;
+    n = imin64(most, (span + 255) / 256);
+    if (n < 8) n = imin64(imin64(most, 8), (span + 127) / 128);
   }
   n = imax64(1, n);
   s.n_splits = (int32_t)n;
   s.split_len = (int32_t)imax64(64, ((span + n - 1) / n + 63) / 64 * 64);
-  s.cluster = !s.tc && n > 1 && n <= 8 && ctas * n <= 152 * (s.chunk_rows <= 16 ? 3 : 2);
+  s.cluster = !s.tc && n > 1 && n <= 8 && ctas * n <= places;
   s.joined = n > 1 && !s.cluster;
   return s;
 }
@@ -729,9 +743,8 @@ PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, 
 // The most splits that leave their parts in the workspace, for any length up to max_vis and any window
 int64_t paged_splits_most(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t kv_dtype) {
   const PagedSplit s = paged_split(batch, heads, group, nq, max_vis, 0, kv_dtype);
-  if (!s.tc) return s.joined ? s.n_splits : 0;           // the longest has the most
-  const int64_t ctas = (int64_t)batch * heads * s.chunks;
-  return tc_splits_in((ctas + 151) / 152 + kRounds - 1, ctas, max_vis);
+  if (!s.tc && !wide(s)) return s.joined ? s.n_splits : 0;             // the longest has the most
+  return (s.tc ? kTcRounds : kWideRounds).most((int64_t)batch * heads * s.chunks, max_vis);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedSplit& sp, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns,
