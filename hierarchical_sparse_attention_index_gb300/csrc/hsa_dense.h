@@ -6,6 +6,8 @@
 
 namespace hsa {
 
+constexpr int kSms = 152;                // of a GB300; rules that also answer without a device go by it
+
 // ------------------------------------------------------------------ dense attention over a paged cache
 struct PagedWriteParams {
   int32_t batch, heads, head_dim, page_size;

@@ -5,17 +5,10 @@
 #include <cuda.h>
 
 #include "hsa_common.cuh"
+#include "hsa_softmax.cuh"
 #include "hsa_tc.cuh"
 
 namespace hsa {
-
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRaise = 8.f;            // log2 of how far a logit may pass the running maximum
-// Weights are 2^(x - m + kLift<BF16>). f16 holds full steps down to 2^-14 only, and keys that are 2^-17 of the largest may be
-// many: its weights take the room that kRaise leaves above (2^15 of 65,504). The factor is in the sums as well.
-template <bool BF16>
-constexpr float kLift = BF16 ? 0.f : 7.f;
 
 // mbar_wait with a suspend hint: a waiting warp sleeps in the barrier unit instead of coming back to
 // ask, which would take shared-memory cycles from the products (4 % of a long prompt's time)
@@ -109,22 +102,7 @@ __device__ __forceinline__ bool next_block_take(uint32_t answer, uint32_t& block
   return got != 0;
 }
 
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
-
-// The same from code that the whole warp runs (`one` is nonzero in the lane that issues)
+// Tensor-map copies from code that the whole warp runs (`one` is nonzero in the lane that issues)
 __device__ __forceinline__ void tma_4d_one(uint32_t one, uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
   asm volatile(
       "{ .reg .pred p; setp.ne.b32 p, %7, 0;\n"
@@ -141,11 +119,6 @@ __device__ __forceinline__ void tma_3d_one(uint32_t one, uint32_t dst, const CUt
       : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 // 32 bytes of 16-bit values, 32-byte aligned
 __device__ __forceinline__ void st_global_256(void* at, const uint32_t* y) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]),
@@ -157,16 +130,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if constexpr (BF16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 #define TMEM_ST8(taddr, r)                                                                                      \
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),  \
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)                     \

@@ -4,6 +4,7 @@
 
 #include "hsa_common.cuh"
 #include "hsa_dense.h"
+#include "hsa_softmax.cuh"
 
 namespace hsa {
 

@@ -33,9 +33,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;               // keys per stage of a warp
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRaise = 8.f;            // log2 of how far a logit may pass the running maximum
-constexpr float kLiftF16 = 7.f;          // log2 of what f16 weights are multiplied with: 2^15 at most, of 65,504
+constexpr int32_t kTcRows = 24;          // 16-bit pages: more query rows than this take the tcgen05 kernel
 
 enum KvType { kBf16 = HSA_BF16, kF16 = HSA_F16, kE4M3 = HSA_E4M3 };
 
@@ -83,16 +81,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
     mma_f16_16816(c, a[0], a[1], a[2], a[3], b0, b1);
   }
 }
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if constexpr (BF16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // CTAs that an SM holds, for NT tiles of 8 query rows: as registers and shared memory (their rings, 227 KB) allow
 constexpr int ctas_per_sm(int nt) { return nt <= 2 ? 3 : 2; }
 
@@ -125,7 +113,7 @@ template <int D, int KV, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
   using T = Tile<D, KV, NT>;
   constexpr bool kB = KV == kBf16;                       // products in bf16, else in f16
-  constexpr float kLift = kB ? 0.f : kLiftF16;           // weights are 2^(x - m), m kLift below the running maximum
+  constexpr float lift = kLift<kB>;                      // weights are 2^(x - m), m that much below the running maximum
   constexpr int kSteps = D / 16, kMt = D / 16, kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_scale[kRows];
@@ -358,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
       bool raise = false;
 #pragma unroll
       for (int j = 0; j < 2 * NT; ++j)                   // m = -inf: any logit raises it
-        raise |= fmaf(fmaxf(s[j >> 1][j & 1], s[j >> 1][2 + (j & 1)]), scale[j % kScales], -m[j]) > kRaise + kLift;
+        raise |= fmaf(fmaxf(s[j >> 1][j & 1], s[j >> 1][2 + (j & 1)]), scale[j % kScales], -m[j]) > kRaise + lift;
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int j = 0; j < 2 * NT; ++j) {
@@ -366,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          mx = fmaxf(fmaf(mx, scale[j % kScales], -kLift), m[j]);
+          mx = fmaxf(fmaf(mx, scale[j % kScales], -lift), m[j]);
           const float f = (mx == -INFINITY) ? 1.f : ex2_ftz(m[j] - mx);   // m = -inf before: 0, on sums that are 0
           m[j] = mx;
           l[j] *= f;
@@ -643,8 +631,12 @@ cudaError_t launch_nt(const PagedAttnParams& p, cudaStream_t s) {
     case 1: return p.cluster ? launch<D, KV, 1, true>(p, s) : launch<D, KV, 1, false>(p, s);
     case 2: return p.cluster ? launch<D, KV, 2, true>(p, s) : launch<D, KV, 2, false>(p, s);
     case 3: return p.cluster ? launch<D, KV, 3, true>(p, s) : launch<D, KV, 3, false>(p, s);
-    default: return p.cluster ? launch<D, KV, 4, true>(p, s) : launch<D, KV, 4, false>(p, s);
   }
+  static_assert(kTcRows <= 3 * 8, "four tiles only for E4M3");
+  if constexpr (KV == kE4M3)
+    return p.cluster ? launch<D, KV, 4, true>(p, s) : launch<D, KV, 4, false>(p, s);
+  else
+    return cudaErrorInvalidValue;
 }
 template <int D>
 cudaError_t launch_kv(const PagedAttnParams& p, int kv, cudaStream_t s) {
@@ -674,11 +666,11 @@ struct Rounds {
 };
 // The tcgen05 kernel, one CTA to an SM. 64 requests x 4 heads x 16,384 keys, ragged: n = 1, 4, 9: 246, 204, 229 us;
 // x 4,097: 73, 77, 105; 8 x 4 x 16,384: n = 3, 4, 5, 9: 54.6, 53.9, 74.5, 59.0
-constexpr Rounds kTcRounds = {152, 8, true};
+constexpr Rounds kTcRounds = {kSms, 8, true};
 // The warp MMA kernel with 17 to 32 rows, two to an SM. Against as many CTAs as four to an SM would be, in no rounds: 16
 // requests x 8 heads x 20 rows, f16, 4,097 keys 30 us (46), 16,384 97 (115); 16 x 4 x 35 rows, E4M3, 4,097 36 (40), 16,384 93 (98);
 // 64 x 4 x 24 rows, bf16, of 1 .. 16,384 keys 187 (206), all 65,536 1,240 (1,205); 4 x 4 x 35, E4M3, 4,097 17.1 (15.9)
-constexpr Rounds kWideRounds = {2 * 152, 6, false};
+constexpr Rounds kWideRounds = {2 * kSms, 6, false};
 static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
   int64_t best = 1, cost = INT64_MAX;
   for (int64_t w = r.first(ctas); w < r.first(ctas) + r.count; ++w) {
@@ -693,10 +685,11 @@ static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
 }
 
 // Which kernel, query rows per CTA and splits of the length.
-// 16-bit pages and more than 24 query rows take the tcgen05 kernel, 128 rows (whole queries) to a CTA: 30
-// rows (64 requests x 4 heads, f16, up to 4,097 keys) took 72 us there and 85 here, up to 16,384 keys 200 and 260; 24
-// rows 72 and 70, 200 and 222, but 32 requests x 8 heads x 8,192 126 and 107. Else up to 32 rows one CTA reads its keys once for all of them; more rows (E4M3) are dealt out
-// evenly (35: 18 and 17), and the later CTAs' keys come from L2.
+// 16-bit pages and more than kTcRows query rows take the tcgen05 kernel, up to 128 rows (whole queries) to a CTA. There and
+// in the warp MMA kernel, 64 requests x 4 heads of 128 dims, of 1 .. 8,192 keys: 32 rows 105 and 164 us, 24 rows 104 and 124;
+// 1,000 keys: 33.3 and 33.1, 33.5 and 28.6; 1 request x 8 heads x 1,000 keys: 13.0 and 12.4, 13.0 and 9.9; 16 x 8 x 8,192 keys of 64
+// dims: 28 rows 59.7 and 55.1, 18 rows 59.8 and 47.7. Else up to 32 rows one CTA reads its keys once for all of them; more rows
+// (E4M3) are dealt out evenly (35: 18 and 17), and the later CTAs' keys come from L2.
 // Up to 16 rows the splits make about as many CTAs as the GPU holds at a time, 3 per SM: more only add starts and joins (4
 // requests of 131,072 FP8 keys: 168 us with 448 CTAs, 193 with 608, 217 with 1,216); from 17 rows on rounds of 2 per SM
 // decide. No split is shorter than 256 keys (8 per group of a warp; in a cluster 128).
@@ -708,7 +701,6 @@ static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
 // slower: 109 against 94 us for 32 ragged contexts, because SMs do not get equal shares of HBM.)
 static bool wide(const PagedSplit& s) { return !s.tc && s.chunk_rows > 16; }
 PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype) {
-  constexpr int32_t kTcRows = 24;
   PagedSplit s;
   const int32_t rows = nq * group;
   s.tc = kv_dtype != HSA_E4M3 && rows > kTcRows;
@@ -723,7 +715,7 @@ PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, 
   s.align = s.tc ? 64 : 16;
   int64_t span = max_vis;
   if (window > 0 && (int64_t)window + nq + s.align - 1 < span) span = (int64_t)window + nq + s.align - 1;   // vis one apart, as in a draft
-  const int64_t ctas = (int64_t)batch * heads * s.chunks, places = 152 * ctas_per_sm((s.chunk_rows + 7) / 8);
+  const int64_t ctas = (int64_t)batch * heads * s.chunks, places = kSms * ctas_per_sm((s.chunk_rows + 7) / 8);
   int64_t n;
   if (s.tc) {
     n = best_splits(kTcRounds, ctas, span);

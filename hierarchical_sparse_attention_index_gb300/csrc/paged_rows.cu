@@ -3,8 +3,8 @@
 //   o = sum_j softmax_j(scale q.k_j) v_j over the positions j a query sees.
 //
 // Bound: the reads of the pages from HBM, as with few rows, as long as the products keep up. The
-// warp MMA does not: its 8-column tiles of queries are issued and softmaxed by the same few warps, and
-// past 32 rows the keys would be read again. Here up to 128 rows (queries x heads of the group) are one
+// warp MMA does not from about 25 rows on: its 8-column tiles of queries are issued and softmaxed by the same few warps.
+// Here up to 128 rows (queries x heads of the group) are one
 // tile of a tcgen05 product, and the 32 KB of 64 keys take a stream about 700 clocks, in which an SM's share
 // of HBM brings half as much. The split of a CTA's job falls into two halves, one for each stream t:
 // a ring of K and V tiles, a warp that loads it, a warp that issues the products, a warp group with a query
@@ -42,7 +42,7 @@ constexpr int kThreads = 20 * 32;
 // whose threads hold a row of 64 logits, 80 for the next two and 48 for the last
 constexpr int kLaunchRegs = 96, kSoftRegs = 136, kOtherRegs = 80, kFindRegs = 48;
 static_assert(2 * kSoftRegs + 2 * kOtherRegs + kFindRegs <= 5 * kLaunchRegs, "setmaxnreg draws on the launch's registers");
-constexpr uint32_t kBlockQ = kTile * 128, kBlockK = kKeys * 128;   // 64 dims of a tile, 128 bytes a row
+constexpr uint32_t kBlockK = kKeys * 128;                // 64 dims of a tile of keys, 128 bytes a row
 constexpr int kJobSlots = 2;
 constexpr int kOrdered = 128;            // batches up to this can be worked off by length
 
@@ -620,7 +620,7 @@ cudaError_t launch_paged_rows(const PagedAttnParams& a, int32_t head_dim, int32_
   // Whole requests, more of them than SMs: the longest first, so that the last ones to be taken are short (64 requests
   // x 4 heads of 1 .. 4,097 keys 64 us, 72 in the order of the requests; 100 x 4 of up to 1,024 35 and 40; all with
   // 4,097 95.7 and 95.2). Of requests in several splits the first are alike and few gain (within 3 % either way).
-  p.ordered = a.batch <= kOrdered && a.n_splits == 1 && (int64_t)a.batch * a.heads * a.chunks > 152;
+  p.ordered = a.batch <= kOrdered && a.n_splits == 1 && (int64_t)a.batch * a.heads * a.chunks > kSms;
   p.wide = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.part_o)) & 31) == 0;
   p.wait_ns = wait_ns;
   const CUtensorMapDataType type = kv_dtype == HSA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;

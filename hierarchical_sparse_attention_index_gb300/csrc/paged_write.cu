@@ -17,7 +17,7 @@ namespace {
 constexpr int kWriteThreads = 256;
 constexpr int kPiecesPerThread = 4;      // 16-byte pieces of K, and as many of V, in flight per thread
 constexpr int kBlockPieces = kWriteThreads * kPiecesPerThread;
-constexpr int kSpread = 2 * 152;         // blocks that a copy is spread over before one takes more than it must
+constexpr int kSpread = 2 * kSms;        // blocks that a copy is spread over before one takes more than it must
 constexpr int kCuShared = 1024;          // batches up to this search cu in shared memory
 
 __device__ __forceinline__ float half_at(uint32_t w, int hi, bool bf16) {
