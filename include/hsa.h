@@ -314,6 +314,8 @@ HSA_API hsa_status hsa_schedule_step(const hsa_cache* caches, const hsa_step_arg
  * cu[b] <= t < cu[b+1] and becomes position start[b] + t - cu[b] of it:
  *   page value = round(x r), r the fp32 reciprocal of the scale: the fp32 product to nearest even,
  *   to HSA_E4M3 saturating at +-448 (NaN stays NaN); a 16-bit cache takes the values as they are.
+ *   (For a scale that is no power of two, an x / scale within a relative 2^-23 of the middle between
+ *   two E4M3 values may go to either of them: x = 203, scale 0.875: 240, not 224.)
  *   k, v      bf16 or f16 (`dtype`) [n_tokens][heads][head_dim], k_stride / v_stride elements from
  *             row to row (a multiple of 8, at least a row); 16-byte aligned. dtype must be the
  *             cache's unless the cache is HSA_E4M3

@@ -235,3 +235,38 @@ def test_decode_many_rows_past_2_31_bytes(H, dtype):
         outs.append(out)
     clean(H)
     assert torch.equal(*outs) and outs[0].isfinite().all()
+
+
+# ------------------------------------------------------------------------------------- E4M3 codes
+@pytest.mark.parametrize("src", [BF, HF])
+@pytest.mark.parametrize("scale", [0.875, 7.0, 0.3, 0.0234375, 2.0 ** -100, 2.0 ** 100])
+def test_write_every_value_to_e4m3(H, src, scale):
+    """All 65,536 values of a 16-bit type: the code of the fp32 product with the scale's reciprocal, which is the nearest to
+    x / scale but where that lies in the middle of two E4M3 values, up to the product's two roundings (2^-23)."""
+    heads, dim, page = 8, 128, 16
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(src).view(64, heads, dim).cuda()
+    k, v, table = D.paged(1, [64], heads, dim, page, F8, 4)
+    cache = H.PagedCache(k.cuda(), v.cuda(), table.cuda(), scale, 1.0)
+    H.hsa_paged_cache_write(cache, x, x)
+    clean(H)
+    got = D.unpage(cache.k, cache.table, 0, 64)[0]
+    inv = 1 / torch.tensor(scale, dtype=torch.float32, device="cuda")
+    y = x.float() * inv
+    want = y.clamp(-448, 448).to(F8).double()
+    nan = x.isnan()
+    assert torch.equal(got.isnan(), nan) and torch.equal(got[~nan], want[~nan])
+    true = (x.double() / torch.tensor(scale, dtype=torch.float32).double().item())[~nan].clamp(-448, 448)
+    step = torch.exp2(torch.floor(torch.log2(true.abs().clamp(min=2.0 ** -6))) - 3)
+    off = (got[~nan] - true).abs()
+    assert (off <= step / 2 + true.abs() * 2.0 ** -23).all()
+
+
+def test_write_beside_a_tie(H):
+    """The example of the declaration: 203 / 0.875 is 232, in the middle of 224 and 240; the product lies above it."""
+    k, v, table = D.paged(1, [16], 1, 64, 16, F8, 4)
+    cache = H.PagedCache(k.cuda(), v.cuda(), table.cuda(), 0.875, 1.0)
+    x = torch.full((1, 1, 64), 203.0, dtype=BF, device="cuda")
+    H.hsa_paged_cache_write(cache, x, x)
+    clean(H)
+    kk, vv = (D.unpage(p, cache.table, 0, 1)[0] for p in (cache.k, cache.v))
+    assert (kk == 240).all() and (vv == 208).all()      # 203 alone goes to 208: steps of 16
