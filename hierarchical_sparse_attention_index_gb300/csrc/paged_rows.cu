@@ -19,8 +19,8 @@
 //  - four warps merge the streams' results from tensor memory, where both of a row lie in the same lane, while the
 //    softmax is at the next job. With one split that is the result, else it goes to the workspace and
 //    paged_join_kernel joins the splits.
-// Measured: 64 requests x 4 heads x 5 queries, f16, 16,384 keys each 335 us, 0.95 of the measured copy rate; of 1 ..
-// 4,097 keys 64 us, 0.67 (the CTAs' last jobs do not end together; all with 4,097: 95 us, 0.84); 1 request x 131,072 55 us.
+// Measured: 64 requests x 4 heads x 5 queries, f16, 16,384 keys each 328 us, 0.97 of the measured copy rate; of 1 ..
+// 4,097 keys 64 us, 0.67 (the CTAs' last jobs do not end together; all with 4,097: 93 us, 0.86); 1 request x 131,072 55 us.
 #include <string.h>
 
 #include <numeric>

@@ -3,8 +3,8 @@
 //
 // A copy with a gather of addresses: it is bound by HBM for prompts and by the chain of dependent
 // loads (cu, then start and the table, then the stores) for a single token per request. Measured: 65,536
-// tokens (8 heads, 128 dims, bf16) 83.2 us, 6.45 TB/s; 12,345 tokens (4 heads, 64 dims) to E4M3 4.5 us;
-// 64 single tokens 2.9 us. So a block
+// tokens (8 heads, 128 dims, bf16) 84.2 us, 6.4 TB/s, to E4M3 73.7; 12,345 tokens (4 heads, 64 dims) to E4M3 6.1 us (4.5
+// with the inputs in L2); 64 single tokens 2.7 us. So a block
 // issues the loads of its rows first, all of them 16-byte pieces of consecutive threads, looks the
 // rows' slots up while they fly (cu in shared memory: one load and a search there instead of a
 // chain of global loads), and then stores, 16 bytes per thread along a head's row.

@@ -28,9 +28,9 @@
 // TMEM: S 2 x 64 columns per query tile (P over the first half of its buffer), O head_dim columns each.
 // Every wait is bounded; a role that gives up leaves its loop, and the others follow at their next
 // wait.
-// Measured: 16,384 tokens, 32 heads over 4, 128 dims 1,436-1,457 us, 1,520 TFLOP/s, 0.79 of the measured bf16
-// peak; without the softmax's part 1,340 us, where shared memory bounds the products. 12 packed prompts, 64 heads over
-// 8, 364 us, 0.70; a window of 128 over 32,768 tokens of 64 dims 177 us. With 64 dims a key tile takes
+// Measured: 16,384 tokens, 32 heads over 4, 128 dims 1,360-1,440 us, 1,530-1,620 TFLOP/s, 0.79-0.83 of the measured bf16
+// peak (1,463-1,481 under the power cap); without the softmax's part 1,340 us, where shared memory bounds the products. 12
+// packed prompts, 64 heads over 8, 365 us, 0.70 (395-404 under the cap); a window of 128 over 32,768 tokens of 64 dims 177 us. With 64 dims a key tile takes
 // 1,200 clocks, of which the softmax's chain (logits, maximum, exponentials, P) is 1,000 and the exponentials alone are 512.
 #include "hsa_flash.cuh"
 #include "hsa_dense.h"
