@@ -340,7 +340,8 @@ HSA_API size_t hsa_paged_attn_workspace_bytes(const hsa_paged_cache* cache, int3
  * (window 0: from position 0):
  *   o = sum_j softmax_j(sm_scale * q_h . k_j) v_j,   lse = log sum_j exp(sm_scale * q_h . k_j).
  * With no positions o is 0 and lse is -inf. Sums are fp32; the weights are rounded to the
- * 16-bit type that the products use (bf16 for a bf16 cache, else f16).
+ * 16-bit type that the products use (bf16 for a bf16 cache, else f16; an f16 weight below 2^-21 of
+ * the row's largest is off by up to 2^-32 of it).
  *   q, out    bf16 or f16 (`q_dtype`) [B][nq][heads_q][head_dim], 16-byte aligned. q_dtype must
  *             be the cache's unless the cache is HSA_E4M3
  *   vis       i32 [B][nq], 0 <= vis <= max_vis; another value counts as the nearer border and is
@@ -362,7 +363,8 @@ HSA_API hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const voi
  * at position p = i + lk - lq (its keys end where its queries end: a chunk behind lk - lq
  * earlier keys) and sees the keys j of [max(0, p - window + 1), p] (window 0: from 0):
  *   o = sum_j softmax_j(sm_scale * q_h . k_j) v_j,   lse = log sum_j exp(sm_scale * q_h . k_j).
- * With no keys (p < 0) o is 0 and lse is -inf. Sums are fp32; the weights are rounded to dtype.
+ * With no keys (p < 0) o is 0 and lse is -inf. Sums are fp32; the weights are rounded to dtype,
+ * in HSA_F16 as in hsa_paged_attn_decode.
  * Rows of q, out and lse outside [cu_q[0], cu_q[batch]) are neither read for a result nor written.
  * A sequence never uses another's rows, nor rows outside [cu_k[0], cu_k[batch]), whatever they
  * hold; a value of its own that is not finite may reach queries that do not see it, as 0 times it
