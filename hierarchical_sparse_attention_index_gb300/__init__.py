@@ -20,11 +20,12 @@ HSA_MAX_NQ, HSA_MAX_VIS = 8, 1 << 20
 HSA_NOALLOC_SCRATCH_BYTES = 64 << 20
 HSA_SCALE_E8M0, HSA_SCALE_E4M3 = 0, 1
 HSA_MODE_FULL, HSA_MODE_REINDEX, HSA_MODE_REUSE = 0, 1, 2
-HSA_FLAG_INDEX_RANGE, HSA_FLAG_WRITE_RANGE, HSA_FLAG_TIMEOUT = 1, 2, 4
+HSA_FLAG_INDEX_RANGE, HSA_FLAG_WRITE_RANGE, HSA_FLAG_TIMEOUT, HSA_FLAG_NO_WEIGHT = 1, 2, 4, 8
 HSA_CACHE_ROPE, HSA_CACHE_POOL_TAIL = 1, 2
 HSA_POOL_TAIL_SLOTS = 160
 HSA_ROPE_DIMS, HSA_ROPE_THETA = 64, 160000.0
-HSA_BF16, HSA_F16, HSA_E4M3 = 0, 1, 2
+HSA_BF16, HSA_F16, HSA_E4M3, HSA_E2M1, HSA_F32 = 0, 1, 2, 3, 4
+HSA_ROPE_HALVES, HSA_ROPE_NEIGHBOURS = 0, 1
 HSA_MAX_GROUP = 128
 
 STATUS = {0: "HSA_OK", 1: "HSA_ERR_INVALID_ARG", 2: "HSA_ERR_SHAPE", 3: "HSA_ERR_ALIGN",
@@ -34,8 +35,8 @@ STATUS_CODES = {v: k for k, v in STATUS.items()}
 EXPORTS = ("hsa_abi_version", "hsa_status_string", "hsa_workspace_bytes", "hsa_workspace_init",
            "hsa_cache_write_compress", "hsa_index_full", "hsa_index_reindex", "hsa_sparse_attn_decode",
            "hsa_schedule_step", "hsa_get_device_status", "hsa_index_full_noalloc", "hsa_set_wait_limit",
-           "hsa_debug_stall_next_scan", "hsa_paged_cache_write", "hsa_paged_attn_workspace_bytes",
-           "hsa_paged_attn_decode", "hsa_prompt_attn")
+           "hsa_debug_stall_next_scan", "hsa_paged_cache_write", "hsa_paged_cache_append", "hsa_paged_cache_read",
+           "hsa_paged_attn_workspace_bytes", "hsa_paged_attn_decode", "hsa_prompt_attn", "hsa_draft_verify")
 
 
 class HsaError(RuntimeError):
@@ -65,7 +66,23 @@ class hsa_paged_cache(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
                 ("n_pages", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("k", ctypes.c_void_p),
                 ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("k_scale", ctypes.c_float),
-                ("v_scale", ctypes.c_float)]
+                ("v_scale", ctypes.c_float), ("k_s", ctypes.c_void_p), ("v_s", ctypes.c_void_p)]
+
+
+class hsa_append_args(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("rotary_at", ctypes.c_int32),
+                ("rotary_dims", ctypes.c_int32), ("pairs", ctypes.c_int32), ("n_tokens", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("cu", ctypes.c_void_p), ("start", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p)]
+
+
+class hsa_verify_args(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("nq", ctypes.c_int32), ("vocabulary", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("p", ctypes.c_void_p), ("q", ctypes.c_void_p), ("p_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("drafted", ctypes.c_void_p), ("n_draft", ctypes.c_void_p), ("u_accept", ctypes.c_void_p),
+                ("u_sample", ctypes.c_void_p), ("accepted", ctypes.c_void_p), ("tokens", ctypes.c_void_p)]
 
 
 class hsa_prompt_args(ctypes.Structure):
@@ -107,9 +124,12 @@ def load_library(path: str = LIB_PATH):
         "hsa_set_wait_limit": (I32, [ctypes.c_uint64]),
         "hsa_debug_stall_next_scan": (I32, []),
         "hsa_paged_cache_write": (I32, [G, P, P, I32, I64, I64, I64, P, P, P]),
+        "hsa_paged_cache_append": (I32, [G, ctypes.POINTER(hsa_append_args), P]),
+        "hsa_paged_cache_read": (I32, [G, P, P, I32, I64, I64, I64, P, P, P]),
         "hsa_paged_attn_workspace_bytes": (SZ, [G, I32, I32, I64]),
         "hsa_paged_attn_decode": (I32, [G, P, I32, I32, P, I32, I64, I32, F, P, P, P, SZ, P]),
         "hsa_prompt_attn": (I32, [ctypes.POINTER(hsa_prompt_args), P]),
+        "hsa_draft_verify": (I32, [ctypes.POINTER(hsa_verify_args), P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -273,13 +293,18 @@ def hsa_schedule_step(caches, step: StepArgs, ws, stream=None):
 _DTYPES = {}
 
 
-def _dtype(t):
-    """The hsa_dtype of a tensor."""
+def _types():
+    """hsa_dtype codes by torch type, and torch types by name."""
     if not _DTYPES:
         import torch
         _DTYPES.update({torch.bfloat16: HSA_BF16, torch.float16: HSA_F16, torch.float8_e4m3fn: HSA_E4M3,
                         "i32": torch.int32, "i64": torch.int64, "f32": torch.float32})
-    code = _DTYPES.get(t.dtype)
+    return _DTYPES
+
+
+def _dtype(t):
+    """The hsa_dtype of a tensor of values."""
+    code = _types().get(t.dtype)
     if code is None:
         raise ValueError(f"unsupported type {t.dtype}")
     return code
@@ -320,26 +345,46 @@ def _stream_on(name, device, stream):
 class PagedCache:
     """Caller-owned paged key-value cache of a dense attention layer: pools k and v
     [n_pages][heads][page_size][head_dim] (bfloat16, float16 or float8_e4m3fn) and an int32 table
-    [batch][max_pages] of page ids, all contiguous. A value is its stored number times its scale."""
+    [batch][max_pages] of page ids, all contiguous. A value is its stored number times its scale.
+    4-bit pages: k and v are uint8 [n_pages][heads][page_size][head_dim / 2] with scales k_s and v_s
+    [n_pages][heads][page_size][head_dim / 16] (float8_e4m3fn or uint8), in the byte order that include/hsa.h gives."""
 
-    def __init__(self, k, v, table, k_scale=1.0, v_scale=1.0):
+    def __init__(self, k, v, table, k_scale=1.0, v_scale=1.0, k_s=None, v_s=None):
         import torch
         if k.dim() != 4 or table.dim() != 2:
             raise ValueError("k and v are [n_pages][heads][page_size][head_dim], table is [batch][max_pages]")
-        self.k, self.v, self.table = k, v, table
-        self.dtype, self.device = _dtype(k), k.get_device()
+        self.k, self.v, self.table, self.k_s, self.v_s = k, v, table, k_s, v_s
+        four = k.dtype is torch.uint8
+        self.dtype, self.device = HSA_E2M1 if four else _dtype(k), k.get_device()
         _given("k", k, k.dtype, k.shape, self.device)
         _given("v", v, k.dtype, k.shape, self.device)
         _given("table", table, torch.int32, table.shape, self.device)
         n_pages, self.heads, self.page_size, self.head_dim = k.shape
+        if four:
+            self.head_dim *= 2
+            shape = (*k.shape[:3], self.head_dim // 16)
+            if k_s is None or v_s is None:
+                raise ValueError("4-bit pages need scales: k_s and v_s [n_pages][heads][page_size][head_dim / 16]")
+            for name, t in (("k_s", k_s), ("v_s", v_s)):
+                _given(name, t, t.dtype if t.dtype is torch.uint8 else torch.float8_e4m3fn, shape, self.device)
+        elif k_s is not None or v_s is not None:
+            raise ValueError("k_s and v_s are for 4-bit pages (uint8 k and v)")
         self.batch, max_pages = table.shape
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self.desc = hsa_paged_cache(self.batch, self.heads, self.head_dim, self.page_size, self.dtype, 0, n_pages, max_pages,
-                                    _ptr(k), _ptr(v), _ptr(table), self.k_scale, self.v_scale)
+                                    _ptr(k), _ptr(v), _ptr(table), self.k_scale, self.v_scale, _ptr(k_s), _ptr(v_s))
 
     @property
     def ref(self):
         return ctypes.byref(self.desc)
+
+
+def _kv_rows(cache, k, v):
+    """(type, strides) of rows of keys and values that go into or come out of a cache."""
+    k_stride, v_stride = _rows("k", k, cache.heads, cache.head_dim), _rows("v", v, cache.heads, cache.head_dim)
+    if v.shape[0] != k.shape[0] or k.dtype is not v.dtype or k.get_device() != cache.device or v.get_device() != cache.device:
+        raise ValueError("k and v differ in shape or type, or are not on the cache's device")
+    return _dtype(k), k_stride, v_stride
 
 
 def hsa_paged_cache_write(cache: PagedCache, k, v, cu=None, start=None, stream=None):
@@ -347,13 +392,49 @@ def hsa_paged_cache_write(cache: PagedCache, k, v, cu=None, start=None, stream=N
     shares); start: int64 [batch] or None (0)."""
     device = cache.device
     stream = _stream_on("cache", device, stream)
-    k_stride, v_stride = _rows("k", k, cache.heads, cache.head_dim), _rows("v", v, cache.heads, cache.head_dim)
-    n = k.shape[0]
-    if v.shape[0] != n or k.dtype is not v.dtype or k.get_device() != device or v.get_device() != device:
-        raise ValueError("k and v differ in shape or type, or are not on the cache's device")
-    dtype = _dtype(k)
+    dtype, k_stride, v_stride = _kv_rows(cache, k, v)
     _check("hsa_paged_cache_write", load_library().hsa_paged_cache_write(
-        cache.ref, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride, n,
+        cache.ref, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride, k.shape[0],
+        _given("cu", cu, _DTYPES["i32"], (cache.batch + 1,), device),
+        _given("start", start, _DTYPES["i64"], (cache.batch,), device), stream))
+
+
+def hsa_paged_cache_append(cache: PagedCache, k, v, inv_freq, q=None, q_out=None, cu=None, start=None, rotary_at=0,
+                           pairs=HSA_ROPE_HALVES, stream=None):
+    """hsa_paged_cache_write with rotated keys, and rotated queries into q_out (which may be q): k, v as there; q, q_out:
+    [n_tokens][heads_q][head_dim], rows at any stride, or None; inv_freq: float32 [rotary_dims / 2], radians per position of
+    each pair, or None (nothing turns); dims rotary_at .. rotary_at + rotary_dims - 1 of each head are rotated."""
+    device = cache.device
+    stream = _stream_on("cache", device, stream)
+    dtype, k_stride, v_stride = _kv_rows(cache, k, v)
+    n, heads_q, q_stride, out_stride, turning = k.shape[0], 0, 0, 0, 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is not None:
+        heads_q = q.shape[1] if q.dim() == 3 else 0
+        q_stride, out_stride = _rows("q", q, heads_q, cache.head_dim), _rows("q_out", q_out, heads_q, cache.head_dim)
+        if heads_q < 1 or q.shape[0] != n or q_out.shape[0] != n or not k.dtype is q.dtype is q_out.dtype or \
+                not device == q.get_device() == q_out.get_device():
+            raise ValueError("q and q_out differ from k in rows, type or device")
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq is [rotary_dims / 2]")
+        turning = 2 * inv_freq.shape[0]
+    a = hsa_append_args(dtype, heads_q, rotary_at, turning, pairs, n, _ptr(q), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
+                        out_stride, _given("cu", cu, _DTYPES["i32"], (cache.batch + 1,), device),
+                        _given("start", start, _DTYPES["i64"], (cache.batch,), device),
+                        _given("inv_freq", inv_freq, _DTYPES["f32"], (turning // 2,), device), _ptr(q_out))
+    _check("hsa_paged_cache_append", load_library().hsa_paged_cache_append(cache.ref, ctypes.byref(a), stream))
+
+
+def hsa_paged_cache_read(cache: PagedCache, k, v, cu=None, start=None, stream=None):
+    """Rows of the pages into k, v: [n_tokens][heads][head_dim], rows at any stride; cu and start as in
+    hsa_paged_cache_write."""
+    device = cache.device
+    stream = _stream_on("cache", device, stream)
+    dtype, k_stride, v_stride = _kv_rows(cache, k, v)
+    _check("hsa_paged_cache_read", load_library().hsa_paged_cache_read(
+        cache.ref, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride, k.shape[0],
         _given("cu", cu, _DTYPES["i32"], (cache.batch + 1,), device),
         _given("start", start, _DTYPES["i64"], (cache.batch,), device), stream))
 
@@ -409,6 +490,45 @@ def hsa_prompt_attn(q, k, v, cu_q, sm_scale, out, cu_k=None, window=0, lse=None,
                         _given("cu_k", cu_k, i32, cu_shape, device), sm_scale, out.data_ptr(),
                         _given("lse", lse, _DTYPES["f32"], (n_q, heads_q), device))
     _check("hsa_prompt_attn", load_library().hsa_prompt_attn(ctypes.byref(a), stream))
+
+
+def _probabilities(name, t, shape):
+    """Row stride of [batch][rows][vocabulary] probabilities: rows may stand apart, evenly."""
+    stride = t.stride()
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    batch, rows, n = shape
+    if rows > 1:
+        row, even = stride[1], batch == 1 or stride[0] == rows * stride[1]
+    else:
+        row, even = stride[0] if batch > 1 else n, True
+    if (n > 1 and stride[2] != 1) or not even:
+        raise ValueError(f"{name}: rows of {n} contiguous entries at one distance")
+    return row
+
+
+def hsa_draft_verify(p, q, drafted, u_accept, u_sample, accepted, tokens, n_draft=None, stream=None):
+    """p: [batch][nq][vocabulary] target probabilities (float32, bfloat16 or float16), q: [batch][nq - 1][vocabulary] the
+    drafter's, in the same type, or None; drafted: int32 [batch][nq - 1]; u_accept: float32 [batch][nq - 1], u_sample: float32
+    [batch]; accepted: int32 [batch], tokens: int32 [batch][nq] (written); n_draft: int32 [batch] or None (nq - 1)."""
+    device, shape = p.get_device(), p.shape
+    stream = _stream_on("p", device, stream)
+    if len(shape) != 3:
+        raise ValueError("p is [batch][nq][vocabulary]")
+    batch, nq, n = shape
+    types = _types()
+    i32, f32 = types["i32"], types["f32"]
+    dtype = HSA_F32 if p.dtype is f32 else _dtype(p)
+    q_stride = 0
+    if q is not None and nq > 1:
+        q_stride = _probabilities("q", q, (batch, nq - 1, n))
+        if q.dtype is not p.dtype or q.get_device() != device:
+            raise ValueError("p and q differ in type or device")
+    a = hsa_verify_args(batch, nq, n, dtype, p.data_ptr(), q.data_ptr() if q_stride else None, _probabilities("p", p, (batch, nq, n)), q_stride,
+                        _given("drafted", drafted, i32, (batch, nq - 1), device), _given("n_draft", n_draft, i32, (batch,), device),
+                        _given("u_accept", u_accept, f32, (batch, nq - 1), device), _given("u_sample", u_sample, f32, (batch,), device),
+                        _given("accepted", accepted, i32, (batch,), device), _given("tokens", tokens, i32, (batch, nq), device))
+    _check("hsa_draft_verify", load_library().hsa_draft_verify(ctypes.byref(a), stream))
 
 
 def hsa_set_wait_limit(ns):

@@ -454,7 +454,7 @@ hsa_status hsa_schedule_step(const hsa_cache* caches, const hsa_step_args* a, vo
 // The fields of a paged cache that sizes follow from; its pointers are checked by check_paged.
 static hsa_status check_paged_sizes(const hsa_paged_cache* c) {
   if (!c) return HSA_ERR_INVALID_ARG;
-  if (c->dtype != HSA_BF16 && c->dtype != HSA_F16 && c->dtype != HSA_E4M3) return HSA_ERR_INVALID_ARG;
+  if (c->dtype != HSA_BF16 && c->dtype != HSA_F16 && c->dtype != HSA_E4M3 && c->dtype != HSA_E2M1) return HSA_ERR_INVALID_ARG;
   if (c->flags) return HSA_ERR_INVALID_ARG;
   if (c->batch < 1 || c->heads < 1 || c->heads > 1024 || (c->head_dim != 64 && c->head_dim != 128)) return HSA_ERR_SHAPE;
   if (c->page_size < 16 || c->page_size > 4096 || c->page_size % 16) return HSA_ERR_SHAPE;
@@ -462,19 +462,21 @@ static hsa_status check_paged_sizes(const hsa_paged_cache* c) {
     return HSA_ERR_SHAPE;
   return HSA_OK;
 }
+static bool scaled(int32_t dtype) { return dtype == HSA_E4M3 || dtype == HSA_E2M1; }
 static hsa_status check_paged(const hsa_paged_cache* c) {
   const hsa_status st = check_paged_sizes(c);
   if (st != HSA_OK) return st;
   if (!c->k || !c->v || !c->table) return HSA_ERR_INVALID_ARG;
   for (const float scale : {c->k_scale, c->v_scale})     // with finite reciprocals and products
     if (!(scale >= 0x1p-120f && scale <= 0x1p120f)) return HSA_ERR_INVALID_ARG;
-  if (c->dtype != HSA_E4M3 && (c->k_scale != 1.f || c->v_scale != 1.f)) return HSA_ERR_INVALID_ARG;
-  if (!aligned16(c->k) || !aligned16(c->v)) return HSA_ERR_ALIGN;
+  if (!scaled(c->dtype) && (c->k_scale != 1.f || c->v_scale != 1.f)) return HSA_ERR_INVALID_ARG;
+  if (c->dtype == HSA_E2M1 && (!c->k_s || !c->v_s)) return HSA_ERR_INVALID_ARG;   // fields that callers of other types need not have
+  if (!aligned16(c->k) || !aligned16(c->v) || (c->dtype == HSA_E2M1 && (!aligned16(c->k_s) || !aligned16(c->v_s)))) return HSA_ERR_ALIGN;
   return HSA_OK;
 }
-// q (or new keys and values) against the cache's type: 16-bit, and the cache's own unless that is E4M3
+// q (or new keys and values) against the cache's type: 16-bit, and the cache's own unless that has fewer bits
 static bool type_fits(int32_t dtype, int32_t cache) {
-  return (dtype == HSA_BF16 || dtype == HSA_F16) && (cache == HSA_E4M3 || cache == dtype);
+  return (dtype == HSA_BF16 || dtype == HSA_F16) && (scaled(cache) || cache == dtype);
 }
 static hsa_status check_paged_query(const hsa_paged_cache* c, int32_t heads_q, int32_t nq, int64_t max_vis) {
   if (heads_q < 1 || heads_q % c->heads || heads_q / c->heads > HSA_MAX_GROUP) return HSA_ERR_SHAPE;
@@ -494,10 +496,12 @@ static PagedWs paged_ws(const hsa_paged_cache* c, int32_t rows, int64_t splits) 
   return w;
 }
 
-hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const void* k, const void* v, int32_t dtype,
-                                 int64_t k_stride, int64_t v_stride, int64_t n_tokens, const int32_t* cu,
-                                 const int64_t* start, hsa_stream_t stream) {
-  NvtxRange range("hsa_paged_cache_write");
+// What the calls between rows of tokens and pages ask of their rows (k, v and the pages), and these as the kernels take them.
+// *launch: whether there is anything to do.
+static hsa_status rows_of_tokens(const hsa_paged_cache* cache, const void* k, const void* v, int32_t dtype, int64_t k_stride,
+                                 int64_t v_stride, int64_t n_tokens, const int32_t* cu, const int64_t* start, PagedWriteParams* p,
+                                 bool* launch) {
+  *launch = false;
   const hsa_status st = check_paged(cache);
   if (st != HSA_OK) return st;
   if (!type_fits(dtype, cache->dtype)) return HSA_ERR_INVALID_ARG;
@@ -510,33 +514,105 @@ hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const void* k, co
     return HSA_ERR_SHAPE;
   if (!cu && n_tokens % cache->batch) return HSA_ERR_SHAPE;
   if (!aligned16(k) || !aligned16(v)) return HSA_ERR_ALIGN;
-  uint32_t* status;
+  memset(p, 0, sizeof(*p));
+  p->batch = cache->batch;
+  p->heads = cache->heads;
+  p->head_dim = cache->head_dim;
+  p->page_size = cache->page_size;
+  p->n_pages = cache->n_pages;
+  p->max_pages = cache->max_pages;
+  p->k_pool = static_cast<uint8_t*>(cache->k);
+  p->v_pool = static_cast<uint8_t*>(cache->v);
+  p->table = cache->table;
+  p->k_inv = 1.f / cache->k_scale;
+  p->v_inv = 1.f / cache->v_scale;
+  p->k = static_cast<const uint16_t*>(k);
+  p->v = static_cast<const uint16_t*>(v);
+  p->k_stride = k_stride;
+  p->v_stride = v_stride;
+  p->n_tokens = n_tokens;
+  p->bf16 = dtype == HSA_BF16;
+  p->cu = cu;
+  p->per_request = n_tokens / cache->batch;
+  p->start = start;
+  if (cache->dtype == HSA_E2M1) {
+    p->k_s = static_cast<uint8_t*>(cache->k_s);
+    p->v_s = static_cast<uint8_t*>(cache->v_s);
+  }
+  *launch = true;
+  return HSA_OK;
+}
+
+hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const void* k, const void* v, int32_t dtype,
+                                 int64_t k_stride, int64_t v_stride, int64_t n_tokens, const int32_t* cu,
+                                 const int64_t* start, hsa_stream_t stream) {
+  NvtxRange range("hsa_paged_cache_write");
+  PagedAppendParams p;
+  bool launch;
+  const hsa_status st = rows_of_tokens(cache, k, v, dtype, k_stride, v_stride, n_tokens, cu, start, &p.w, &launch);
+  if (st != HSA_OK || !launch) return st;
   int sms;
-  if (!device_info(&status, &sms)) return HSA_ERR_UNSUPPORTED;
-  PagedWriteParams p;
-  memset(&p, 0, sizeof(p));
-  p.batch = cache->batch;
-  p.heads = cache->heads;
-  p.head_dim = cache->head_dim;
-  p.page_size = cache->page_size;
-  p.n_pages = cache->n_pages;
-  p.max_pages = cache->max_pages;
-  p.k_pool = static_cast<uint8_t*>(cache->k);
-  p.v_pool = static_cast<uint8_t*>(cache->v);
-  p.table = cache->table;
-  p.k_inv = 1.f / cache->k_scale;
-  p.v_inv = 1.f / cache->v_scale;
-  p.k = static_cast<const uint16_t*>(k);
-  p.v = static_cast<const uint16_t*>(v);
-  p.k_stride = k_stride;
-  p.v_stride = v_stride;
-  p.n_tokens = n_tokens;
-  p.bf16 = dtype == HSA_BF16;
-  p.cu = cu;
-  p.per_request = n_tokens / cache->batch;
-  p.start = start;
-  p.status = status;
-  return cuda_fail(launch_paged_write(p, cache->dtype == HSA_E4M3, (cudaStream_t)stream), "paged write launch");
+  if (!device_info(&p.w.status, &sms)) return HSA_ERR_UNSUPPORTED;
+  if (cache->dtype != HSA_E2M1)
+    return cuda_fail(launch_paged_write(p.w, cache->dtype == HSA_E4M3, (cudaStream_t)stream), "paged write launch");
+  p.heads_q = p.rotary_at = p.rotary = p.pairs = 0;      // an append of nothing that turns
+  p.q = nullptr;
+  p.q_out = nullptr;
+  p.q_stride = p.out_stride = 0;
+  p.inv_freq = nullptr;
+  return cuda_fail(launch_paged_append(p, cache->dtype, (cudaStream_t)stream), "paged write launch");
+}
+
+hsa_status hsa_paged_cache_append(const hsa_paged_cache* cache, const hsa_append_args* a, hsa_stream_t stream) {
+  NvtxRange range("hsa_paged_cache_append");
+  if (!a) return HSA_ERR_INVALID_ARG;
+  PagedAppendParams p;
+  bool launch;
+  const hsa_status st =
+      rows_of_tokens(cache, a->k, a->v, a->dtype, a->k_stride, a->v_stride, a->n_tokens, a->cu, a->start, &p.w, &launch);
+  if (st != HSA_OK) return st;
+  if (a->pairs != HSA_ROPE_HALVES && a->pairs != HSA_ROPE_NEIGHBOURS) return HSA_ERR_INVALID_ARG;
+  if (a->heads_q < 0 || a->heads_q > 1024 * HSA_MAX_GROUP) return HSA_ERR_SHAPE;
+  if (a->rotary_at < 0 || a->rotary_at % 16 || a->rotary_dims < 0 || a->rotary_dims % 32 || a->rotary_at > cache->head_dim ||
+      a->rotary_dims > cache->head_dim - a->rotary_at)
+    return HSA_ERR_SHAPE;
+  if (!launch) return HSA_OK;
+  if (a->rotary_dims && !a->inv_freq) return HSA_ERR_INVALID_ARG;
+  if (a->heads_q) {
+    if (!a->q || !a->q_out) return HSA_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)a->heads_q * cache->head_dim;
+    for (const int64_t stride : {a->q_stride, a->out_stride})
+      if (stride < row || stride % 8 || stride > (int64_t)INT32_MAX) return HSA_ERR_SHAPE;
+    if (!aligned16(a->q) || !aligned16(a->q_out)) return HSA_ERR_ALIGN;
+  }
+  int sms;
+  if (!device_info(&p.w.status, &sms)) return HSA_ERR_UNSUPPORTED;
+  p.heads_q = a->heads_q;
+  p.rotary_at = a->rotary_at;
+  p.rotary = a->rotary_dims;
+  p.pairs = a->pairs;
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.q_out = static_cast<uint16_t*>(a->q_out);
+  p.q_stride = a->q_stride;
+  p.out_stride = a->out_stride;
+  p.inv_freq = a->inv_freq;
+  return cuda_fail(launch_paged_append(p, cache->dtype, (cudaStream_t)stream), "paged append launch");
+}
+
+hsa_status hsa_paged_cache_read(const hsa_paged_cache* cache, void* k, void* v, int32_t dtype, int64_t k_stride, int64_t v_stride,
+                                int64_t n_tokens, const int32_t* cu, const int64_t* start, hsa_stream_t stream) {
+  NvtxRange range("hsa_paged_cache_read");
+  PagedReadParams p;
+  bool launch;
+  const hsa_status st = rows_of_tokens(cache, k, v, dtype, k_stride, v_stride, n_tokens, cu, start, &p.w, &launch);
+  if (st != HSA_OK || !launch) return st;
+  int sms;
+  if (!device_info(&p.w.status, &sms)) return HSA_ERR_UNSUPPORTED;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.k = static_cast<uint16_t*>(k);
+  p.v = static_cast<uint16_t*>(v);
+  return cuda_fail(launch_paged_read(p, cache->dtype, (cudaStream_t)stream), "paged read launch");
 }
 
 size_t hsa_paged_attn_workspace_bytes(const hsa_paged_cache* cache, int32_t heads_q, int32_t nq, int64_t max_vis) {
@@ -577,6 +653,10 @@ hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, in
   p.max_pages = cache->max_pages;
   p.k_pool = static_cast<const uint8_t*>(cache->k);
   p.v_pool = static_cast<const uint8_t*>(cache->v);
+  if (cache->dtype == HSA_E2M1) {
+    p.k_s = static_cast<const uint8_t*>(cache->k_s);
+    p.v_s = static_cast<const uint8_t*>(cache->v_s);
+  }
   p.table = cache->table;
   p.q = static_cast<const uint16_t*>(q);
   p.q_bf16 = q_dtype == HSA_BF16;
@@ -626,6 +706,27 @@ hsa_status hsa_prompt_attn(const hsa_prompt_args* a, hsa_stream_t stream) {
   int sms;
   if (!device_info(&status, &sms)) return HSA_ERR_UNSUPPORTED;
   return cuda_fail(launch_prompt_attn(*a, status, wait_limit_ns(), (cudaStream_t)stream), "prompt attention launch");
+}
+
+hsa_status hsa_draft_verify(const hsa_verify_args* a, hsa_stream_t stream) {
+  NvtxRange range("hsa_draft_verify");
+  if (!a) return HSA_ERR_INVALID_ARG;
+  if (a->dtype != HSA_F32 && a->dtype != HSA_BF16 && a->dtype != HSA_F16) return HSA_ERR_INVALID_ARG;
+  if (a->batch < 1 || a->batch > 1 << 20 || a->nq < 1 || a->nq > HSA_MAX_NQ || a->vocabulary < 1 || a->vocabulary > 1 << 24)
+    return HSA_ERR_SHAPE;
+  if (!a->p || !a->u_sample || !a->accepted || !a->tokens || (a->nq > 1 && (!a->drafted || !a->u_accept))) return HSA_ERR_INVALID_ARG;
+  if (a->p_stride < a->vocabulary || a->p_stride > (int64_t)INT32_MAX ||
+      (a->q && (a->q_stride < a->vocabulary || a->q_stride > (int64_t)INT32_MAX)))
+    return HSA_ERR_SHAPE;
+  const uintptr_t size = a->dtype == HSA_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(a->p) % size || reinterpret_cast<uintptr_t>(a->q) % size) return HSA_ERR_ALIGN;
+  for (const void* x : {(const void*)a->drafted, (const void*)a->n_draft, (const void*)a->u_accept, (const void*)a->u_sample,
+                        (const void*)a->accepted, (const void*)a->tokens})
+    if (reinterpret_cast<uintptr_t>(x) % 4) return HSA_ERR_ALIGN;
+  uint32_t* status;
+  int sms;
+  if (!device_info(&status, &sms)) return HSA_ERR_UNSUPPORTED;
+  return cuda_fail(launch_draft_verify(*a, status, (cudaStream_t)stream), "draft verification launch");
 }
 
 hsa_status hsa_set_wait_limit(uint64_t ns) {

@@ -24,9 +24,30 @@ struct PagedWriteParams {
   const int32_t* cu;      // [batch + 1] or NULL: per_request rows each
   int64_t per_request;
   const int64_t* start;   // [batch] or NULL
+  uint8_t* k_s;           // scales of 4-bit pools
+  uint8_t* v_s;
   uint32_t* status;
 };
 cudaError_t launch_paged_write(const PagedWriteParams& p, bool e4m3, cudaStream_t s);
+
+struct PagedAppendParams {
+  PagedWriteParams w;
+  int32_t heads_q, rotary_at, rotary, pairs;
+  int32_t slice;          // heads of q, k and v (in that order) per block; set by the launcher
+  const uint16_t* q;      // [n_tokens][heads_q][head_dim], q_stride elements from row to row
+  uint16_t* q_out;
+  int64_t q_stride, out_stride;
+  const float* inv_freq;  // [rotary / 2]
+};
+cudaError_t launch_paged_append(const PagedAppendParams& p, int32_t kv_dtype, cudaStream_t s);
+
+struct PagedReadParams {
+  PagedWriteParams w;     // k, v, k_inv and v_inv are not looked at
+  float k_scale, v_scale;
+  uint16_t* k;            // [n_tokens][heads][head_dim], w.k_stride elements from row to row
+  uint16_t* v;
+};
+cudaError_t launch_paged_read(const PagedReadParams& p, int32_t kv_dtype, cudaStream_t s);
 
 // How hsa_paged_attn_decode cuts its work (host only; the workspace holds n_splits partials per
 // row where a join follows)
@@ -48,6 +69,8 @@ struct PagedAttnParams {
   int64_t n_pages, max_pages;
   const uint8_t* k_pool;
   const uint8_t* v_pool;
+  const uint8_t* k_s;     // scales of 4-bit pools
+  const uint8_t* v_s;
   const int32_t* table;
   const uint16_t* q;      // [B][nq][heads_q][D]
   int32_t q_bf16;         // q and out are bf16, else f16
@@ -72,6 +95,15 @@ using TensorMapEncoder = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint3
                                       const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                       CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 TensorMapEncoder tensor_map_encoder();
+
+// ------------------------------------------------------------------ verification of drafts
+struct VerifyParams {
+  hsa_verify_args a;
+  int32_t ctas;           // of the cluster that a request gets
+  int32_t wide;           // rows start on 16-byte boundaries
+  uint32_t* status;
+};
+cudaError_t launch_draft_verify(const hsa_verify_args& a, uint32_t* status, cudaStream_t s);
 
 // ------------------------------------------------------------------ causal attention over packed prompts
 int64_t prompt_blocks(const hsa_prompt_args& a);

@@ -1,0 +1,36 @@
+// 4-bit rows of paged caches (HSA_E2M1): where a row's bytes lie, and how 16 values become codes and a scale.
+#pragma once
+
+#include "hsa_common.cuh"
+
+namespace hsa {
+
+// Dims 8 c .. 8 c + 7 of a row, its bytes 4 c .. 4 c + 3, lie
+//  - in a row of K as two neighbouring pairs of bytes, at four_k_at<D>(c, 0) and four_k_at<D>(c, 1),
+//  - in a row of V as single bytes, at four_v_at<D>(c, 0) .. four_v_at<D>(c, 3).
+template <int D>
+__device__ __forceinline__ int four_k_at(int c, int half) { return D / 8 * (2 * (c & 1) + half) + 2 * (c >> 1); }
+template <int D>
+__device__ __forceinline__ int four_v_at(int c, int byte) { return D / 16 * (4 * (c & 1) + byte) + (c >> 1); }
+
+// The smallest positive E4M3 value s with 6 s >= amax (448 above 6 * 448), as its byte: the nearest one to amax / 6, or
+// the next where that is too small. (amax / 6 in fp32 may be off by 2^-23 of it, far less than a step: only where it
+// lies beside the middle of two steps can the rounding go either way, and then the comparison decides.)
+__device__ __forceinline__ uint32_t four_scale_for(float amax) {
+  uint16_t near;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(near) : "f"(0.f), "f"(amax * (1.f / 6.f)));
+  uint32_t byte = max(near & 0x7Fu, 1u);
+  if (6.f * e4m3_to_f32(byte) < amax && byte < 0x7Eu) ++byte;
+  return byte;
+}
+
+// Eight values -> four bytes of E2M1 codes of x / s (nearest even, saturating), -0 as 0
+__device__ __forceinline__ uint32_t four_codes(const float (&x)[8], float s) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w |= (f32x2_to_e2m1x2(x[2 * i + 1] / s, x[2 * i] / s) & 0xFFu) << (8 * i);
+  const uint32_t m = w & 0x77777777u;    // a sign stays where the magnitude is not 0: then, and only then, m + 7 carries into it
+  return w & (0x77777777u | ((m + 0x77777777u) & 0x88888888u));
+}
+
+}  // namespace hsa

@@ -1,0 +1,333 @@
+// New tokens into the pages of a dense layer's cache with the position rotation on the way (hsa_paged_cache_append), and
+// pages back into rows (hsa_paged_cache_read).
+//   pos = start[b] + t - cu[b];  pair i of a head of q or k: (x, y) -> (x cos - y sin, x sin + y cos) of the angle pos inv_freq[i];
+//   q_out[t] = round(rotated q[t]),  page[table[b][pos / P]][h][pos % P] = round(rotated k[t] or v[t], times 1 / scale).
+//
+// Bound: every element is read and written once, so HBM decides for prompts, the chain of dependent loads (cu, then
+// start and the table, then the stores) for single tokens. A thread's unit is two 16-byte pieces of a head, which
+// for rotated halves are the two ends of its 8 pairs, so that nothing is read twice and q may be rotated in
+// place. Loads of two units go first; while they fly, a block finds its rows' slots and the sines of
+// its rows, once for all heads. The angle is a 64-bit fraction of a turn times the position, whose wrapping product is
+// exact; what is left of a quarter turn goes through sincospif.
+#include "hsa_dense.h"
+#include "hsa_four.cuh"
+#include "hsa_rows.cuh"
+#include "hsa_softmax.cuh"
+
+namespace hsa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnits = 2;                // units in flight per thread
+constexpr int kMaxRows = 32;             // of a block
+constexpr int kMaxPairs = 64;
+
+template <bool BF16>
+__device__ __forceinline__ void widen(const uint4& a, float (&x)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = half_at(w[i], 0, BF16);
+    x[2 * i + 1] = half_at(w[i], 1, BF16);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
+  return make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
+}
+__device__ __forceinline__ uint2 e4m3x8(const float (&x)[8], float inv) {
+  uint32_t r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[4 * i + 1] * inv), "f"(x[4 * i] * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[4 * i + 3] * inv), "f"(x[4 * i + 2] * inv));
+    r[i] = (uint32_t)lo | ((uint32_t)hi << 16);
+  }
+  return make_uint2(r[0], r[1]);
+}
+
+// (cos, sin) of pos * turns / 2^64 turns
+__device__ __forceinline__ float2 cos_sin(int64_t pos, uint64_t turns) {
+  const uint64_t ph = (uint64_t)pos * turns;
+  const uint64_t quarter = (ph + (1ull << 61)) >> 62;    // the nearest quarter turn
+  float s, c;
+  sincospif((float)(int64_t)(ph - (quarter << 62)) * 0x1p-63f, &s, &c);
+  const float2 r = (quarter & 1) ? make_float2(-s, c) : make_float2(c, s);
+  return (quarter & 2) ? make_float2(-r.x, -r.y) : r;
+}
+// radians per position as a 64-bit fraction of a turn
+__device__ __forceinline__ uint64_t turns_of(float radians) {
+  const double t = (double)radians * 0.15915494309189533577;
+  return (uint64_t)__double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+}
+
+template <int D, int KV, bool BF16>
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+  constexpr int kPer = D / 16;           // units per head: pieces cA and cB of its D / 8
+  constexpr bool kFour = KV == HSA_E2M1;
+  constexpr int kRowBytes = D / 2 + 8;   // of a staged 4-bit row: codes, scales
+  __shared__ RowSlots s_rows;
+  __shared__ uint64_t s_turns[kMaxPairs];
+  __shared__ float2 s_cs[kMaxRows * kMaxPairs];          // (cos, sin) of row r, pair i at r * pairs + i
+  __shared__ __align__(16) uint8_t s_four[kFour ? kThreads / kPer * kRowBytes : 16];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int heads = p.heads_q + 2 * p.w.heads;
+  const int h0 = blockIdx.y * p.slice, nh = min(p.slice, heads - h0);
+  const int64_t t0 = (int64_t)blockIdx.x * p.w.rows_per_block;
+  const int n_rows = (int)imin64(p.w.rows_per_block, p.w.n_tokens - t0);
+  const int units = n_rows * nh * kPer;
+  const int pairs = p.rotary / 2, turned = p.rotary / 16, at0 = p.rotary_at / 8;   // units that rotate, first piece of them
+
+  for (int base = 0; base < units; base += kThreads * kUnits) {
+    uint4 x[kUnits][2];
+    int row[kUnits], head[kUnits], ca[kUnits], cb[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int e = base + i * kThreads + tid, u = e % kPer;
+      row[i] = e < units ? e / kPer / nh : -1;
+      head[i] = h0 + e / kPer % nh;
+      const int v = u - turned, half = kPer - turned;    // of the pieces that do not turn, which go around the others
+      ca[i] = v < 0 ? at0 + u : (v < at0 ? v : v + 2 * turned);
+      cb[i] = v < 0 ? at0 + u + turned : (v + half < at0 ? v + half : v + half + 2 * turned);
+      if (row[i] >= 0) {
+        const int64_t t = t0 + row[i];
+        const int hk = head[i] - p.heads_q, hv = hk - p.w.heads;
+        const uint16_t* src = hk < 0 ? p.q + t * p.q_stride + head[i] * D : hv < 0 ? p.w.k + t * p.w.k_stride + hk * D : p.w.v + t * p.w.v_stride + hv * D;
+        x[i][0] = *reinterpret_cast<const uint4*>(src + 8 * ca[i]);
+        x[i][1] = *reinterpret_cast<const uint4*>(src + 8 * cb[i]);
+      } else {
+        x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    if (base == 0) {
+      if (tid < pairs) s_turns[tid] = turns_of(p.inv_freq[tid]);
+      find_slots(p.w, t0, n_rows, s_rows, h0 == 0 ? HSA_FLAG_WRITE_RANGE : 0u);
+      for (int e = tid; e < n_rows * pairs; e += kThreads) s_cs[e] = cos_sin(s_rows.pos[e / pairs], s_turns[e % pairs]);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int r = max(row[i], 0), hk = head[i] - p.heads_q, hv = hk - p.w.heads, u = (base + i * kThreads + tid) % kPer;
+      float a[8], b[8];
+      widen<BF16>(x[i][0], a);
+      widen<BF16>(x[i][1], b);
+      if (u < turned && hv < 0) {
+        const float2* cs = s_cs + r * pairs;
+        if (p.pairs == HSA_ROPE_HALVES) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 y = cs[8 * u + j];
+            const float m = a[j], n = b[j];
+            a[j] = fmaf(m, y.x, -(n * y.y));
+            b[j] = fmaf(m, y.y, n * y.x);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = cs[4 * u + j], z = cs[4 * (u + turned) + j];
+            const float m = a[2 * j], n = a[2 * j + 1], o = b[2 * j], q = b[2 * j + 1];
+            a[2 * j] = fmaf(m, y.x, -(n * y.y));
+            a[2 * j + 1] = fmaf(m, y.y, n * y.x);
+            b[2 * j] = fmaf(o, z.x, -(q * z.y));
+            b[2 * j + 1] = fmaf(o, z.y, q * z.x);
+          }
+        }
+        x[i][0] = narrow<BF16>(a);
+        x[i][1] = narrow<BF16>(b);
+      }
+      const int64_t slot = row[i] < 0 ? -1 : s_rows.slot[r];
+      if (hk < 0) {
+        if (row[i] >= 0 && s_rows.real[r]) {
+          uint16_t* dst = p.q_out + (t0 + r) * p.out_stride + head[i] * D;
+          *reinterpret_cast<uint4*>(dst + 8 * ca[i]) = x[i][0];
+          *reinterpret_cast<uint4*>(dst + 8 * cb[i]) = x[i][1];
+        }
+      } else if (!kFour && slot >= 0) {
+        const int64_t at = slot + (int64_t)(hv < 0 ? hk : hv) * p.w.page_size;         // row of the pool
+        uint8_t* pool = hv < 0 ? p.w.k_pool : p.w.v_pool;
+        if constexpr (KV == HSA_E4M3) {
+          const float inv = hv < 0 ? p.w.k_inv : p.w.v_inv;
+          *reinterpret_cast<uint2*>(pool + at * D + 8 * ca[i]) = e4m3x8(a, inv);
+          *reinterpret_cast<uint2*>(pool + at * D + 8 * cb[i]) = e4m3x8(b, inv);
+        } else {
+          *reinterpret_cast<uint4*>(pool + (at * D + 8 * ca[i]) * 2) = x[i][0];
+          *reinterpret_cast<uint4*>(pool + (at * D + 8 * cb[i]) * 2) = x[i][1];
+        }
+      }
+      if constexpr (kFour) {
+        // codes of the pool's row, put in its order in shared memory. Two neighbouring lanes hold a group's 16 dims
+        const float inv = hv < 0 ? p.w.k_inv : p.w.v_inv;
+        uint8_t* mine = s_four + tid / kPer * kRowBytes;
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          float y[8], amax = 0.f;
+          bool nan = false;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            y[j] = (o ? b[j] : a[j]) * inv;
+            amax = fmaxf(amax, fabsf(y[j]));
+            nan |= y[j] != y[j];
+          }
+          if (nan) amax = NAN;
+          const float other = __shfl_xor_sync(0xffffffffu, amax, 1);
+          const bool none = amax != amax || other != other;
+          const uint32_t byte = none ? 0x7Fu : four_scale_for(fmaxf(amax, other));
+          const int c = o ? cb[i] : ca[i];
+          const uint32_t w = none ? 0u : four_codes(y, e4m3_to_f32(byte));
+          if (hv < 0) {
+            *reinterpret_cast<uint16_t*>(mine + four_k_at<D>(c, 0)) = (uint16_t)w;
+            *reinterpret_cast<uint16_t*>(mine + four_k_at<D>(c, 1)) = (uint16_t)(w >> 16);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mine[four_v_at<D>(c, j)] = (uint8_t)(w >> (8 * j));
+          }
+          if (!(c & 1)) mine[D / 2 + (c >> 1)] = (uint8_t)byte;
+        }
+        __syncwarp();
+        if (hk >= 0 && slot >= 0) {
+          const int64_t at = slot + (int64_t)(hv < 0 ? hk : hv) * p.w.page_size;
+          uint8_t* pool = hv < 0 ? p.w.k_pool : p.w.v_pool;
+          uint8_t* scales = hv < 0 ? p.w.k_s : p.w.v_s;
+          const int part = lane % kPer;
+          *reinterpret_cast<uint2*>(pool + at * (D / 2) + 8 * part) = *reinterpret_cast<const uint2*>(mine + 8 * part);
+          if (part == 0) {
+            if constexpr (D == 128)
+              *reinterpret_cast<uint2*>(scales + at * (D / 16)) = *reinterpret_cast<const uint2*>(mine + D / 2);
+            else
+              *reinterpret_cast<uint32_t*>(scales + at * (D / 16)) = *reinterpret_cast<const uint32_t*>(mine + D / 2);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ pages back into rows
+constexpr int kReadPieces = 4;           // 16-byte pieces of k, and as many of v, in flight per thread
+
+template <int D, int KV, bool BF16>
+__global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_constant__ PagedReadParams p) {
+  constexpr int kPer = D / 8;            // 16-byte pieces of a head's row
+  __shared__ RowSlots s_rows;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, per_row = p.w.heads * kPer;
+  const int64_t t0 = (int64_t)blockIdx.x * p.w.rows_per_block;
+  const int n_rows = (int)imin64(p.w.rows_per_block, p.w.n_tokens - t0);
+  find_slots(p.w, t0, n_rows, s_rows, HSA_FLAG_INDEX_RANGE);
+  const int pieces = n_rows * per_row;
+  for (int base = 0; base < pieces; base += kThreads * kReadPieces) {
+    uint4 x[2][kReadPieces];
+#pragma unroll
+    for (int i = 0; i < kReadPieces; ++i) {
+      const int e = base + i * kThreads + tid, r = e / per_row, rest = e - r * per_row, h = rest / kPer, c = rest % kPer;
+      const int64_t slot = e < pieces ? s_rows.slot[r] : -1;
+      if (slot < 0) continue;
+      const int64_t at = slot + (int64_t)h * p.w.page_size;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint8_t* pool = kv ? p.w.v_pool : p.w.k_pool;
+        if constexpr (KV == HSA_E2M1) {
+          const uint8_t* b = pool + at * (D / 2);
+          uint32_t w;
+          if (kv == 0) {
+            w = *reinterpret_cast<const uint16_t*>(b + four_k_at<D>(c, 0)) |
+                ((uint32_t)*reinterpret_cast<const uint16_t*>(b + four_k_at<D>(c, 1)) << 16);
+          } else {
+            w = b[four_v_at<D>(c, 0)] | ((uint32_t)b[four_v_at<D>(c, 1)] << 8) | ((uint32_t)b[four_v_at<D>(c, 2)] << 16) |
+                ((uint32_t)b[four_v_at<D>(c, 3)] << 24);
+          }
+          x[kv][i].x = w;
+          x[kv][i].y = (kv ? p.w.v_s : p.w.k_s)[at * (D / 16) + (c >> 1)];
+        } else if constexpr (KV == HSA_E4M3) {
+          const uint2 w = *reinterpret_cast<const uint2*>(pool + at * D + 8 * c);
+          x[kv][i].x = w.x;
+          x[kv][i].y = w.y;
+        } else {
+          x[kv][i] = *reinterpret_cast<const uint4*>(pool + (at * D + 8 * c) * 2);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kReadPieces; ++i) {
+      const int e = base + i * kThreads + tid, r = e / per_row, rest = e - r * per_row;
+      if (e >= pieces || s_rows.slot[r] < 0) continue;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint4 y = x[kv][i];
+        const float scale = kv ? p.v_scale : p.k_scale;
+        if constexpr (KV == HSA_E2M1 || KV == HSA_E4M3) {
+          uint32_t f[4];
+          if constexpr (KV == HSA_E2M1) {
+            e2m1x8_to_f16x2x4(y.x, f[0], f[1], f[2], f[3]);
+          } else {
+            f[0] = e4m3x2_to_f16x2((uint16_t)(y.x & 0xFFFFu));
+            f[1] = e4m3x2_to_f16x2((uint16_t)(y.x >> 16));
+            f[2] = e4m3x2_to_f16x2((uint16_t)(y.y & 0xFFFFu));
+            f[3] = e4m3x2_to_f16x2((uint16_t)(y.y >> 16));
+          }
+          const float group = KV == HSA_E2M1 ? e4m3_to_f32(y.y) : 1.f;   // code x group is exact
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float lo = half_at(f[j], 0, false), hi = half_at(f[j], 1, false);
+            o[j] = pack2<BF16>(lo * group * scale, hi * group * scale);
+          }
+          y = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        uint16_t* dst = (kv ? p.v + (t0 + r) * p.w.v_stride : p.k + (t0 + r) * p.w.k_stride) + 8 * rest;
+        __stcs(reinterpret_cast<uint4*>(dst), y);
+      }
+    }
+  }
+}
+
+template <int D, int KV, bool BF16>
+cudaError_t append(PagedAppendParams p, cudaStream_t s) {
+  constexpr int kPer = D / 16;
+  const int64_t heads = (int64_t)p.heads_q + 2 * p.w.heads, row = heads * kPer;        // units per token
+  // whole rows, about four units to a thread; fewer rows, then slices of a row's heads, while there are SMs without a block
+  const int64_t most = imin64(kMaxRows, imax64(1, 4 * kThreads / row));
+  p.w.rows_per_block = (int32_t)imax64(1, imin64(most, (p.w.n_tokens + 2 * kSms - 1) / (2 * kSms)));
+  const int64_t blocks = (p.w.n_tokens + p.w.rows_per_block - 1) / p.w.rows_per_block;
+  int64_t slices = imin64((2 * kSms + blocks - 1) / blocks, (row + kThreads - 1) / kThreads);
+  p.slice = (int32_t)((heads + slices - 1) / slices);
+  slices = (heads + p.slice - 1) / p.slice;
+  return launch_pdl(paged_append_kernel<D, KV, BF16>, dim3((unsigned)blocks, (unsigned)slices), dim3(kThreads), 0, s, p);
+}
+template <int D, int KV, bool BF16>
+cudaError_t read(PagedReadParams p, cudaStream_t s) {
+  const int64_t row = (int64_t)p.w.heads * (D / 8);
+  const int64_t most = imin64(kMaxRows, imax64(1, kThreads * kReadPieces / row)), least = imin64(kMaxRows, imax64(1, kThreads / row));
+  p.w.rows_per_block = (int32_t)imin64(most, imax64(least, (p.w.n_tokens + 2 * kSms - 1) / (2 * kSms)));
+  const int64_t blocks = (p.w.n_tokens + p.w.rows_per_block - 1) / p.w.rows_per_block;
+  return launch_pdl(paged_read_kernel<D, KV, BF16>, dim3((unsigned)blocks), dim3(kThreads), 0, s, p);
+}
+
+// the kernel of this head size, cache type and 16-bit type
+#define HSA_BY_TYPE(call, head_dim, kv, bf16, ...)                                                        \
+  switch (kv) {                                                                                           \
+    case HSA_BF16: return head_dim == 128 ? call<128, HSA_BF16, true>(__VA_ARGS__) : call<64, HSA_BF16, true>(__VA_ARGS__);   \
+    case HSA_F16: return head_dim == 128 ? call<128, HSA_F16, false>(__VA_ARGS__) : call<64, HSA_F16, false>(__VA_ARGS__);    \
+    case HSA_E4M3:                                                                                        \
+      if (bf16) return head_dim == 128 ? call<128, HSA_E4M3, true>(__VA_ARGS__) : call<64, HSA_E4M3, true>(__VA_ARGS__);      \
+      return head_dim == 128 ? call<128, HSA_E4M3, false>(__VA_ARGS__) : call<64, HSA_E4M3, false>(__VA_ARGS__);              \
+    default:                                                                                              \
+      if (bf16) return head_dim == 128 ? call<128, HSA_E2M1, true>(__VA_ARGS__) : call<64, HSA_E2M1, true>(__VA_ARGS__);      \
+      return head_dim == 128 ? call<128, HSA_E2M1, false>(__VA_ARGS__) : call<64, HSA_E2M1, false>(__VA_ARGS__);              \
+  }
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppendParams& p, int32_t kv_dtype, cudaStream_t s) {
+  HSA_BY_TYPE(append, p.w.head_dim, kv_dtype, p.w.bf16, p, s)
+}
+cudaError_t launch_paged_read(const PagedReadParams& p, int32_t kv_dtype, cudaStream_t s) {
+  HSA_BY_TYPE(read, p.w.head_dim, kv_dtype, p.w.bf16, p, s)
+}
+
+}  // namespace hsa

@@ -35,7 +35,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = 16;               // keys per stage of a warp
 constexpr int32_t kTcRows = 24;          // 16-bit pages: more query rows than this take the tcgen05 kernel
 
-enum KvType { kBf16 = HSA_BF16, kF16 = HSA_F16, kE4M3 = HSA_E4M3 };
+enum KvType { kBf16 = HSA_BF16, kF16 = HSA_F16, kE4M3 = HSA_E4M3, kE2M1 = HSA_E2M1 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -43,6 +43,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 // 16 bytes, of which all but the first `bytes` are zeros and not read
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// a row's scales of 4-bit pages, N = 4 or 8 bytes, of which all but the first `bytes` are zeros and not read
+template <int N>
+__device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -57,6 +62,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
@@ -81,28 +91,49 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
     mma_f16_16816(c, a[0], a[1], a[2], a[3], b0, b1);
   }
 }
+// 4-bit pages: the key of a 16-key group at place i of the products' key index, and back. Thread t's keys, places
+// 2t, 2t + 1, 2t + 8 and 2t + 9, are then t, t + 4, t + 8, t + 12
+__host__ __device__ __forceinline__ constexpr int four_key(int i) { return (i & 8) + ((i & 1) << 2) + ((i & 6) >> 1); }
+__host__ __device__ __forceinline__ constexpr int four_place(int r) { return (r & 8) + ((r & 3) << 1) + ((r & 4) >> 2); }
+// (x, x) of the low or the high half of an f16 pair times y
+__device__ __forceinline__ uint32_t mul_half(uint32_t x, int hi, uint32_t y) {
+  const __half2 a = *reinterpret_cast<const __half2*>(&x), b = *reinterpret_cast<const __half2*>(&y);
+  const __half2 r = __hmul2(hi ? __high2half2(a) : __low2half2(a), b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t mul_pair(uint32_t x, uint32_t y) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 // CTAs that an SM holds, for NT tiles of 8 query rows: as registers and shared memory (their rings, 227 KB) allow
 constexpr int ctas_per_sm(int nt) { return nt <= 2 ? 3 : 2; }
 
 template <int D, int KV, int NT>
 struct Tile {
   static constexpr int kElem = KV == kE4M3 ? 1 : 2;
-  static constexpr int kRow = D * kElem;                 // bytes of a key's row
+  static constexpr int kRow = KV == kE2M1 ? D / 2 : D * kElem;           // bytes of a key's row
   static constexpr int kChunks = kRow / 16;
   static constexpr int kHalf = kGroup * kRow;            // K, then V
-  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kScaleRow = KV == kE2M1 ? D / 16 : 0;             // bytes of a row's scales
+  static constexpr int kScales = kGroup * kScaleRow;     // K's behind V, then V's
+  static constexpr int kStage = 2 * kHalf + 2 * kScales;
   static constexpr int kCtas = ctas_per_sm(NT);
   static constexpr int kRingMax = kCtas == 3 ? 16384 : 24576;
-  static constexpr int kStages = kRingMax / kStage > 6 ? 6 : kRingMax / kStage;
+  static constexpr int kStagesMax = KV == kE2M1 ? (D == 128 ? 10 : 15) : 6;
+  static constexpr int kStages = kRingMax / kStage > kStagesMax ? kStagesMax : kRingMax / kStage;
   static constexpr int kRing = kStage * kStages;
   static constexpr int kOutLd = D + 4;                   // floats from row to row when the warps merge (bank spread)
   static_assert(8 * NT * kOutLd * 4 <= kRing, "a warp's outputs fit its ring");
   // 16-byte piece c of row r. K: pieces 4i..4i+3 of two neighbouring rows are read together; V: one
   // piece of 8 rows (matrix loads), or two pieces of rows 0, 2, 4, 6 (E4M3)
+  // E2M1: K's row r lies at its place in the products (four_key(place) = r), so that 8 lanes read 128 bytes in a row; V's pieces
+  // of rows t and 4 + t are read together by thread t, 8 (4) bytes of each by 8 threads
   static __device__ __forceinline__ uint32_t k_at(int r, int c) {
+    if constexpr (KV == kE2M1) return (uint32_t)(four_place(r) * kRow + c * 16);
     return (uint32_t)(r * kRow + (kChunks >= 8 ? (c ^ ((r & 1) << 2)) : c) * 16);
   }
   static __device__ __forceinline__ uint32_t v_at(int r, int c) {
+    if constexpr (KV == kE2M1) return (uint32_t)(r * kRow + (kChunks == 4 ? c ^ (r & 2) : c) * 16);
     return (uint32_t)(r * kRow + (kChunks >= 8 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3))) * 16);
   }
 };
@@ -169,6 +200,14 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
     }
     if (i < n_groups) {
       const uint32_t st = (uint32_t)stage * T::kStage, seen = (uint32_t)found & 0xFFFFu;
+      if constexpr (KV == kE2M1) {
+        // a lane for each row's scales: of K where it lies among the keys, of V in the order t, t + 4, .. of thread t
+        const int r = lane & 15;
+        const uint32_t n = (seen >> r) & 1u ? (uint32_t)T::kScaleRow : 0u;
+        const uint8_t* src = (lane < 16 ? p.k_s : p.v_s) + (n ? ((found >> 16) * kGroup + r) * T::kScaleRow : 0);
+        const uint32_t place = lane < 16 ? four_place(r) : kGroup + (r & 3) * 4 + (r >> 2);
+        cp_async_scales<(T::kScaleRow ? T::kScaleRow : 4)>(ring + st + 2 * T::kHalf + place * T::kScaleRow, src, n);
+      }
       bad = (bad & ~(1u << stage)) | ((seen ? 0u : 1u) << stage);
       const int64_t at = seen ? (found >> 16) * (kGroup * T::kRow) + lane * 16 : 0;
       const uint8_t* k = p.k_pool + at;
@@ -221,10 +260,11 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
   // k-step ks covers, of thread t, the 4 consecutive elements that its piece of a key's row brings
   // to that step
   uint32_t qb[NT][kSteps][2];
-  constexpr int kScales = KV == kE4M3 ? 2 * NT : 1;
+  constexpr bool kScaled = KV == kE4M3 || KV == kE2M1;
+  constexpr int kScales = kScaled ? 2 * NT : 1;
   float scale[kScales];                                  // of rows 2t, 2t + 1 of each tile (or of all rows)
   {
-    constexpr int kPer = 16 / T::kElem;                  // elements of a 16-byte piece
+    constexpr int kPer = KV == kE2M1 ? 4 : 16 / T::kElem;                // consecutive elements of a thread: of a 16-byte piece, 4 of a scale's group
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = row0 + 8 * n + g;
@@ -237,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
         const int piece = 4 * (ks / (kPer / 4)) + t;
         x[ks] = real ? *reinterpret_cast<const uint2*>(q + piece * kPer + 4 * (ks % (kPer / 4))) : make_uint2(0u, 0u);
       }
-      if constexpr (KV == kE4M3) {
+      if constexpr (kScaled) {
         float sc = p.scale_log2;
         if (p.q_bf16) {
           // bf16 queries against f16 keys: to f16 after a power-of-two shift of the row, taken back in its scale
@@ -275,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
     }
   }
   __syncthreads();                                       // s_lo, s_hi, s_scale
-  if constexpr (KV == kE4M3) {
+  if constexpr (kScaled) {
 #pragma unroll
     for (int j = 0; j < kScales; ++j) scale[j] = s_scale[8 * (j >> 1) + 2 * t + (j & 1)];
   } else {
@@ -312,6 +352,39 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+      if constexpr (KV == kE2M1) {
+        // a thread's bytes of a row: of each scale's group the two that hold its 4 dims, which make one k-step
+        constexpr int kW = D / 32;                       // words: two groups each
+        uint32_t w0[kW], w1[kW], c0[kW / 2], c1[kW / 2];
+        const uint32_t ss = sk + 2 * T::kHalf;
+        if constexpr (D == 128) {
+          const uint4 k0 = lds128(sk + g * T::kRow + 16 * t), k1 = lds128(sk + (8 + g) * T::kRow + 16 * t);
+          const uint2 s0 = lds64(ss + g * T::kScaleRow), s1 = lds64(ss + (8 + g) * T::kScaleRow);
+          w0[0] = k0.x, w0[1] = k0.y, w0[kW - 2] = k0.z, w0[kW - 1] = k0.w;
+          w1[0] = k1.x, w1[1] = k1.y, w1[kW - 2] = k1.z, w1[kW - 1] = k1.w;
+          c0[0] = s0.x, c0[kW / 2 - 1] = s0.y;
+          c1[0] = s1.x, c1[kW / 2 - 1] = s1.y;
+        } else {
+          const uint2 k0 = lds64(sk + g * T::kRow + 8 * t), k1 = lds64(sk + (8 + g) * T::kRow + 8 * t);
+          w0[0] = k0.x, w0[1] = k0.y;
+          w1[0] = k1.x, w1[1] = k1.y;
+          c0[0] = lds32(ss + g * T::kScaleRow);
+          c1[0] = lds32(ss + (8 + g) * T::kScaleRow);
+        }
+#pragma unroll
+        for (int j = 0; j < kW; ++j) {
+          uint32_t x[4], y[4];
+          e2m1x8_to_f16x2x4(w0[j], x[0], x[1], x[2], x[3]);
+          e2m1x8_to_f16x2x4(w1[j], y[0], y[1], y[2], y[3]);
+          const uint32_t f0 = e4m3x2_to_f16x2((uint16_t)(c0[j / 2] >> (16 * (j & 1)))), f1 = e4m3x2_to_f16x2((uint16_t)(c1[j / 2] >> (16 * (j & 1))));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {                  // code x scale has 6 bits at most and is at least 2^-10: exact in f16
+            const uint32_t a[4] = {mul_half(f0, u, x[2 * u]), mul_half(f1, u, y[2 * u]), mul_half(f0, u, x[2 * u + 1]), mul_half(f1, u, y[2 * u + 1])};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<kB>(s[n], a, qb[n][2 * j + u][0], qb[n][2 * j + u][1]);
+          }
+        }
+      } else
 #pragma unroll
       for (int c4 = 0; c4 < T::kChunks / 4; ++c4) {
         const uint4 k0 = lds128(sk + T::k_at(g, 4 * c4 + t)), k1 = lds128(sk + T::k_at(8 + g, 4 * c4 + t));
@@ -339,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int r = 8 * n + 2 * t + (e & 1), key = pos + g + 8 * (e >> 1);
+            const int place = g + 8 * (e >> 1), r = 8 * n + 2 * t + (e & 1), key = pos + (KV == kE2M1 ? four_key(place) : place);
             if (key < s_lo[r] || key >= s_hi[r]) s[n][e] = -INFINITY;
           }
       }
@@ -381,7 +454,49 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
         pb[n][1] = movmatrix_trans(pack2<kB>(w[2], w[3]));
       }
       // ------------------------------------------------------------ O^T += V^T P^T
-      if constexpr (KV == kE4M3) {
+      if constexpr (KV == kE2M1) {
+        // thread row g of tile mt is dim 16 mt + 2 g, row g + 8 the next one: byte g of each scale's group, of keys t, t + 4, t + 8, t + 12
+        constexpr int kW = D / 64;                       // words of a thread's bytes of a key: 4 groups each
+        uint32_t w[4][kW], c[4][kW];
+        const uint32_t ss = sk + 2 * T::kHalf + T::kScales + 4 * t * T::kScaleRow;
+        if constexpr (D == 128) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint2 x = lds64(sv + T::v_at(t + 4 * u, g >> 1) + 8 * (g & 1));
+            w[u][0] = x.x, w[u][kW - 1] = x.y;
+          }
+          const uint4 x = lds128(ss), y = lds128(ss + 16);
+          c[0][0] = x.x, c[0][kW - 1] = x.y, c[1][0] = x.z, c[1][kW - 1] = x.w;
+          c[2][0] = y.x, c[2][kW - 1] = y.y, c[3][0] = y.z, c[3][kW - 1] = y.w;
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) w[u][0] = lds32(sv + T::v_at(t + 4 * u, g >> 2) + 4 * (g & 3));
+          const uint4 x = lds128(ss);
+          c[0][0] = x.x, c[1][0] = x.y, c[2][0] = x.z, c[3][0] = x.w;
+        }
+#pragma unroll
+        for (int j = 0; j < kW; ++j) {
+          // codes and scales of two keys side by side, as the products take them
+          uint32_t v[4][4], f[2][4];                     // [row g, row g + 8 of keys t, t + 4; of keys t + 8, t + 12][group]
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t x = w[2 * u][j], y = w[2 * u + 1][j];
+            e2m1x8_to_f16x2x4((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), v[2 * u][0], v[2 * u][1], v[2 * u][2], v[2 * u][3]);
+            e2m1x8_to_f16x2x4(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), v[2 * u + 1][0], v[2 * u + 1][1], v[2 * u + 1][2], v[2 * u + 1][3]);
+            const uint32_t lo = __byte_perm(c[2 * u][j], c[2 * u + 1][j], 0x5140), hi = __byte_perm(c[2 * u][j], c[2 * u + 1][j], 0x7362);
+            f[u][0] = e4m3x2_to_f16x2((uint16_t)(lo & 0xFFFFu));
+            f[u][1] = e4m3x2_to_f16x2((uint16_t)(lo >> 16));
+            f[u][2] = e4m3x2_to_f16x2((uint16_t)(hi & 0xFFFFu));
+            f[u][3] = e4m3x2_to_f16x2((uint16_t)(hi >> 16));
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a[4] = {mul_pair(v[0][e], f[0][e]), mul_pair(v[1][e], f[0][e]), mul_pair(v[2][e], f[1][e]), mul_pair(v[3][e], f[1][e])};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<kB>(o[4 * j + e][n], a, pb[n][0], pb[n][1]);
+          }
+        }
+      } else if constexpr (KV == kE4M3) {
         // thread row g of tile mt is dim kPd g + 2 mt, row g + 8 the next one: rows 2t, 2t+1, 2t+8, 2t+9 of V
         constexpr int kPd = D / 8;
         uint32_t w[4][kPd / 4];
@@ -446,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        so[r * T::kOutLd + (KV == kE4M3 ? D / 8 * g + 2 * mt + u : 16 * mt + g + 8 * u)] = o[mt][j >> 1][2 * u + (j & 1)];
+        so[r * T::kOutLd + (KV == kE4M3 ? D / 8 * g + 2 * mt + u : KV == kE2M1 ? 16 * mt + 2 * g + u : 16 * mt + g + 8 * u)] = o[mt][j >> 1][2 * u + (j & 1)];
   }
   __syncthreads();
   constexpr int kQuads = D / 4;
@@ -632,8 +747,8 @@ cudaError_t launch_nt(const PagedAttnParams& p, cudaStream_t s) {
     case 2: return p.cluster ? launch<D, KV, 2, true>(p, s) : launch<D, KV, 2, false>(p, s);
     case 3: return p.cluster ? launch<D, KV, 3, true>(p, s) : launch<D, KV, 3, false>(p, s);
   }
-  static_assert(kTcRows <= 3 * 8, "four tiles only for E4M3");
-  if constexpr (KV == kE4M3)
+  static_assert(kTcRows <= 3 * 8, "four tiles only for pages of 8 and 4 bits");
+  if constexpr (KV == kE4M3 || KV == kE2M1)
     return p.cluster ? launch<D, KV, 4, true>(p, s) : launch<D, KV, 4, false>(p, s);
   else
     return cudaErrorInvalidValue;
@@ -643,7 +758,8 @@ cudaError_t launch_kv(const PagedAttnParams& p, int kv, cudaStream_t s) {
   switch (kv) {
     case kBf16: return launch_nt<D, kBf16>(p, s);
     case kF16: return launch_nt<D, kF16>(p, s);
-    default: return launch_nt<D, kE4M3>(p, s);
+    case kE4M3: return launch_nt<D, kE4M3>(p, s);
+    default: return launch_nt<D, kE2M1>(p, s);
   }
 }
 
@@ -703,7 +819,7 @@ static bool wide(const PagedSplit& s) { return !s.tc && s.chunk_rows > 16; }
 PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype) {
   PagedSplit s;
   const int32_t rows = nq * group;
-  s.tc = kv_dtype != HSA_E4M3 && rows > kTcRows;
+  s.tc = (kv_dtype == HSA_BF16 || kv_dtype == HSA_F16) && rows > kTcRows;
   if (s.tc) {
     const int32_t queries = nq < 128 / group ? nq : 128 / group;
     s.chunks = (nq + queries - 1) / queries;

@@ -10,6 +10,7 @@
 // chain of global loads), and then stores, 16 bytes per thread along a head's row.
 #include "hsa_common.cuh"
 #include "hsa_dense.h"
+#include "hsa_rows.cuh"
 
 namespace hsa {
 namespace {
@@ -20,10 +21,6 @@ constexpr int kBlockPieces = kWriteThreads * kPiecesPerThread;
 constexpr int kSpread = 2 * kSms;        // blocks that a copy is spread over before one takes more than it must
 constexpr int kCuShared = 1024;          // batches up to this search cu in shared memory
 
-__device__ __forceinline__ float half_at(uint32_t w, int hi, bool bf16) {
-  if (bf16) return __uint_as_float(hi ? (w & 0xFFFF0000u) : (w << 16));
-  return __half2float(__ushort_as_half((unsigned short)(hi ? (w >> 16) : (w & 0xFFFFu))));
-}
 // eight 16-bit values -> eight E4M3 codes of x * inv in fp32 (nearest even, saturating)
 __device__ __forceinline__ uint2 to_e4m3x8(uint4 x, float inv, bool bf16) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};

@@ -96,6 +96,7 @@ typedef enum { HSA_MODE_FULL = 0, HSA_MODE_REINDEX = 1, HSA_MODE_REUSE = 2 } hsa
 #define HSA_FLAG_INDEX_RANGE 1u   /* a top-k / pool index >= visible length or capacity was skipped */
 #define HSA_FLAG_WRITE_RANGE 2u   /* a cache write past capacity was skipped                         */
 #define HSA_FLAG_TIMEOUT 4u       /* a bounded device wait gave up                                  */
+#define HSA_FLAG_NO_WEIGHT 8u     /* hsa_draft_verify: a row of probabilities without any weight    */
 
 /* Cache flags (hsa_cache.flags) */
 #define HSA_CACHE_ROPE 1u         /* the writer applies RoPE to the main-KV latent (see hsa_cache_write_compress) */
@@ -114,15 +115,22 @@ typedef struct {
   uint8_t* ik_s;
 } hsa_cache;
 
-/* Value types of the dense attention calls and of their paged caches */
-typedef enum { HSA_BF16 = 0, HSA_F16 = 1, HSA_E4M3 = 2 } hsa_dtype;
+/* Value types of the dense attention calls and of their paged caches; HSA_E2M1 is for paged caches
+ * only (4 bits, with scales), HSA_F32 for probabilities only. */
+typedef enum { HSA_BF16 = 0, HSA_F16 = 1, HSA_E4M3 = 2, HSA_E2M1 = 3, HSA_F32 = 4 } hsa_dtype;
 
 #define HSA_MAX_GROUP 128     /* dense attention: query heads per key-value head at most      */
 
 /* Caller-owned paged key-value cache of one dense (uncompressed, grouped-head) attention layer.
  * Position t of request b lies in row t % page_size of page table[b][t / page_size]; requests
  * may share pages they only read. The pools and the table are device memory; pools 16-byte
- * aligned. A value is its stored number times k_scale or v_scale. */
+ * aligned. A value is its stored number times k_scale or v_scale.
+ * HSA_E2M1: the stored number of dim d is its E2M1 code times the E4M3 scale of its group d / 16 of the
+ * row (a NaN scale makes the group NaN). k and v are u8 [n_pages][heads][page_size][head_dim / 2], k_s and
+ * v_s u8 [n_pages][heads][page_size][head_dim / 16], one scale per group. With byte b of a row holding dim 2b
+ * in its low and 2b + 1 in its high nibble, rows are stored in the order in which the attention's threads
+ * take them: byte (head_dim / 8) t + 2 s + i of a row of k is byte 8 s + 2 t + i (t in 0..3, i in 0..1, s a group),
+ * byte (head_dim / 16) r + s of a row of v is byte 8 s + r (r in 0..7). 4.5 bits a value. */
 typedef struct {
   int32_t batch;          /* requests                                               */
   int32_t heads;          /* key-value heads, 1..1024                               */
@@ -135,8 +143,48 @@ typedef struct {
   void* k;                /* [n_pages][heads][page_size][head_dim]                  */
   void* v;                /* [n_pages][heads][page_size][head_dim]                  */
   const int32_t* table;   /* i32 [batch][max_pages]; entries no query needs may hold anything */
-  float k_scale, v_scale; /* 2^-120 .. 2^120; 1 unless dtype is HSA_E4M3            */
+  float k_scale, v_scale; /* 2^-120 .. 2^120; 1 unless dtype is HSA_E4M3 or HSA_E2M1 */
+  void* k_s;              /* HSA_E2M1: scales of k, 16-byte aligned; not looked at otherwise */
+  void* v_s;              /* HSA_E2M1: scales of v                                  */
 } hsa_paged_cache;
+
+/* Which dims of a head form the pairs that hsa_paged_cache_append rotates */
+typedef enum { HSA_ROPE_HALVES = 0, HSA_ROPE_NEIGHBOURS = 1 } hsa_rope_pairs;
+
+/* Arguments of hsa_paged_cache_append. All pointers are device memory; q, k, v and q_out 16-byte aligned. */
+typedef struct {
+  int32_t dtype;         /* HSA_BF16 or HSA_F16, of q, k, v and q_out                          */
+  int32_t heads_q;       /* query heads, at most 131,072; 0: q and q_out are not looked at     */
+  int32_t rotary_at;     /* first rotated dim, a multiple of 16                                */
+  int32_t rotary_dims;   /* rotated dims R, a multiple of 32; 0: none (inv_freq not looked at) */
+  int32_t pairs;         /* hsa_rope_pairs                                                     */
+  int64_t n_tokens;      /* rows of q, k, v and q_out                                          */
+  const void* q;         /* [n_tokens][heads_q][head_dim], q_stride elements from row to row   */
+  const void* k;         /* [n_tokens][heads][head_dim], k_stride elements from row to row     */
+  const void* v;         /* [n_tokens][heads][head_dim], v_stride elements from row to row     */
+  int64_t q_stride, k_stride, v_stride, out_stride; /* multiples of 8, at least a row; < 2^31  */
+  const int32_t* cu;     /* i32 [batch + 1] or NULL, as in hsa_paged_cache_write               */
+  const int64_t* start;  /* i64 [batch] or NULL, as in hsa_paged_cache_write                   */
+  const float* inv_freq; /* f32 [R / 2]: radians per position of pair i                        */
+  void* q_out;           /* [n_tokens][heads_q][head_dim], out_stride elements from row to row */
+} hsa_append_args;
+
+/* Arguments of hsa_draft_verify. All pointers are device memory. */
+typedef struct {
+  int32_t batch;           /* requests, 1..2^20                                                */
+  int32_t nq;              /* rows of p per request: 1..HSA_MAX_NQ, drafts of up to nq - 1     */
+  int32_t vocabulary;      /* 1..2^24                                                          */
+  int32_t dtype;           /* HSA_F32, HSA_BF16 or HSA_F16, of p and q                         */
+  const void* p;           /* [batch][nq][vocabulary], p_stride elements from row to row       */
+  const void* q;           /* [batch][nq - 1][vocabulary], q_stride elements from row to row; or NULL */
+  int64_t p_stride, q_stride; /* at least vocabulary, < 2^31                                   */
+  const int32_t* drafted;  /* i32 [batch][nq - 1]                                              */
+  const int32_t* n_draft;  /* i32 [batch] or NULL: nq - 1 for every request                    */
+  const float* u_accept;   /* f32 [batch][nq - 1], uniform in [0, 1)                           */
+  const float* u_sample;   /* f32 [batch], uniform in [0, 1)                                   */
+  int32_t* accepted;       /* i32 [batch]                                                      */
+  int32_t* tokens;         /* i32 [batch][nq]                                                  */
+} hsa_verify_args;
 
 /* Arguments of hsa_prompt_attn. All pointers are device memory; q, k, v and out 16-byte aligned. */
 typedef struct {
@@ -306,9 +354,10 @@ HSA_API hsa_status hsa_schedule_step(const hsa_cache* caches, const hsa_step_arg
 
 /* ---------------------------------------------------------------- dense attention
  * Layers without a compressed cache (dense layers, and layers with a sliding window only) keep
- * keys and values per position and key-value head. Three calls serve them: the prompt's
- * attention, the write of its keys and values into pages, and the attention of each new token
- * over the pages. Query head h belongs to key-value head h / (heads_q / heads_kv). */
+ * keys and values per position and key-value head. These calls serve them: the prompt's
+ * attention, the write of keys and values into pages, with the position rotation or without, the way
+ * back, and the attention of each new token over the pages. Query head h belongs to key-value head
+ * h / (heads_q / heads_kv). */
 
 /* Write keys and values into a paged cache. Row t of k and v belongs to the request b with
  * cu[b] <= t < cu[b+1] and becomes position start[b] + t - cu[b] of it:
@@ -316,19 +365,45 @@ HSA_API hsa_status hsa_schedule_step(const hsa_cache* caches, const hsa_step_arg
  *   to HSA_E4M3 saturating at +-448 (NaN stays NaN); a 16-bit cache takes the values as they are.
  *   (For a scale that is no power of two, an x / scale within a relative 2^-23 of the middle between
  *   two E4M3 values may go to either of them: x = 203, scale 0.875: 240, not 224.)
+ *   to HSA_E2M1, for the 16 products of a group, the smallest positive E4M3 scale s with 6 s >= their largest
+ *   magnitude (at most 448) and the codes of product / s to nearest even, saturating at +-6, -0 as 0; a group
+ *   with a NaN gets the NaN scale 0x7F.
  *   k, v      bf16 or f16 (`dtype`) [n_tokens][heads][head_dim], k_stride / v_stride elements from
  *             row to row (a multiple of 8, at least a row); 16-byte aligned. dtype must be the
- *             cache's unless the cache is HSA_E4M3
+ *             cache's unless the cache is HSA_E4M3 or HSA_E2M1
  *   n_tokens  rows of k and v, >= 0 (0: nothing is launched) and < 2^31
  *   cu        i32 [batch + 1] ascending; rows outside [cu[0], cu[batch]) are padding and not written.
  *             NULL: every request brings n_tokens / batch rows (which must divide)
  *   start     i64 [batch]; NULL means 0 for every request
  * Positions outside the table or on a page id outside [0, n_pages) are skipped and flagged
  * HSA_FLAG_WRITE_RANGE. Two rows that land on one slot (requests sharing a page they both
- * write) leave one of them there, whole 16-byte pieces of either. Everything else in the pools stays. */
+ * write) leave one of them there, whole 16-byte pieces of either (HSA_E2M1: 8-byte pieces, and scales of either).
+ * Everything else in the pools stays. */
 HSA_API hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const void* k, const void* v, int32_t dtype,
                                  int64_t k_stride, int64_t v_stride, int64_t n_tokens, const int32_t* cu,
                                  const int64_t* start, hsa_stream_t stream);
+
+/* hsa_paged_cache_write with the position rotation applied on the way: of row t, at position pos = start[b] + t -
+ * cu[b] of its request, pair i of each head of q and k turns by the angle pos inv_freq[i] (taken modulo one turn
+ * in 64-bit integers: off by at most 2^-52 of pos inv_freq / 2 pi turns) in fp32, with one rounding of the result:
+ *   (x, y) -> (x cos - y sin, x sin + y cos),
+ *   HSA_ROPE_HALVES: dims rotary_at + i and rotary_at + i + R / 2, HSA_ROPE_NEIGHBOURS: rotary_at + 2i and 2i + 1, i < R / 2.
+ * The rotated queries go to q_out, which may be q itself (the same address and stride; otherwise the two must not overlap),
+ * the rotated keys and the values to the pages as in hsa_paged_cache_write, from their fp32 values. Rows outside
+ * [cu[0], cu[batch]) are padding: neither their q_out rows nor any page is written. A row whose position is
+ * skipped (HSA_FLAG_WRITE_RANGE) has its q_out written all the same. n_tokens = 0 launches nothing. */
+HSA_API hsa_status hsa_paged_cache_append(const hsa_paged_cache* cache, const hsa_append_args* args, hsa_stream_t stream);
+
+/* Read keys and values back out of a paged cache, for instance as the earlier keys of a chunk in hsa_prompt_attn. Row t of
+ * k and v, of the request b with cu[b] <= t < cu[b+1], becomes position start[b] + t - cu[b] of that request:
+ *   row = round(stored number x scale), a 16-bit cache's values as they are.
+ *   k, v      bf16 or f16 (`dtype`) [n_tokens][heads][head_dim], strides, alignment and types as in hsa_paged_cache_write
+ *   n_tokens, cu, start   as in hsa_paged_cache_write
+ * Rows outside [cu[0], cu[batch]) and rows whose position is outside the table or on a page id outside [0, n_pages) are
+ * not written; the latter are flagged HSA_FLAG_INDEX_RANGE. */
+HSA_API hsa_status hsa_paged_cache_read(const hsa_paged_cache* cache, void* k, void* v, int32_t dtype, int64_t k_stride,
+                                int64_t v_stride, int64_t n_tokens, const int32_t* cu, const int64_t* start,
+                                hsa_stream_t stream);
 
 /* Workspace bytes of hsa_paged_attn_decode for this cache's batch, heads and head_dim (its
  * pointers are not looked at), for this max_vis, every smaller one and every window. Host only;
@@ -343,7 +418,7 @@ HSA_API size_t hsa_paged_attn_workspace_bytes(const hsa_paged_cache* cache, int3
  * 16-bit type that the products use (bf16 for a bf16 cache, else f16; an f16 weight below 2^-21 of
  * the row's largest is off by up to 2^-32 of it).
  *   q, out    bf16 or f16 (`q_dtype`) [B][nq][heads_q][head_dim], 16-byte aligned. q_dtype must
- *             be the cache's unless the cache is HSA_E4M3
+ *             be the cache's unless the cache is HSA_E4M3 or HSA_E2M1
  *   vis       i32 [B][nq], 0 <= vis <= max_vis; another value counts as the nearer border and is
  *             flagged HSA_FLAG_INDEX_RANGE. max_vis <= max_pages * page_size and <= HSA_MAX_VIS
  *   lse       f32 [B][nq][heads_q] or NULL
@@ -373,6 +448,21 @@ HSA_API hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const voi
  * share rows of k and v. n_q and n_k <= 2^27; n_q = 0 launches nothing. Pieces of 2 x
  * (128 / group) tokens, times heads_kv, have to be fewer than 2^31 (HSA_ERR_SHAPE). */
 HSA_API hsa_status hsa_prompt_attn(const hsa_prompt_args* args, hsa_stream_t stream);
+
+/* Verify a draft (speculative decoding: nq - 1 drafted tokens and nq queries per request). Row p[b][i] is the target's
+ * distribution after i drafted tokens, q[b][i] the one that token x_i = drafted[b][i] was drawn from; q = NULL
+ * stands for drafts that were not drawn (all weight on x_i). With n = n_draft[b], a is the first i < n with not
+ *   u_accept[b][i] q[b][i][x_i] < p[b][i][x_i]          (the product and the comparison are exact),
+ * or n, and the next token y is drawn from w_v = max(0, p[b][a][v] - q[b][a][v]) if a < n, else from w_v = p[b][a][v]:
+ *   y = the lowest v whose w_0 + .. + w_v passes u_sample[b] times the sum of all w.
+ * accepted[b] = a; tokens[b] = x_0 .. x_(a-1), y, then -1. Tokens then follow p, whatever q is.
+ * Sums are taken in units of 2^-46, to which each entry is rounded, so their order does not matter; the entries of a row
+ * of p sum to less than 2^16. An entry below 0 or NaN counts as 0, above 1 as 1; a u_sample as the nearer border, NaN as 0.
+ * Where all w are 0 (p = q), y is drawn from p[b][a]; where that is 0 too, y is -1 and HSA_FLAG_NO_WEIGHT set.
+ * An x_i outside [0, vocabulary) is turned down and flagged HSA_FLAG_INDEX_RANGE (with q = NULL, y is then from p[b][i]).
+ * n_draft[b] = -1 marks padding: nothing of b is written. Other values outside [0, nq - 1] do the same and
+ * are flagged HSA_FLAG_INDEX_RANGE. drafted, u_accept and q may be NULL for nq = 1. Only the rows that decide are read. */
+HSA_API hsa_status hsa_draft_verify(const hsa_verify_args* args, hsa_stream_t stream);
 
 /* Limit of the kernels' bounded waits (for a copy or a tensor-core result that does not arrive),
  * in nanoseconds, for launches made after the call from any thread, on every device. A wait that
