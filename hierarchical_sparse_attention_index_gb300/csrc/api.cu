@@ -618,7 +618,7 @@ hsa_status hsa_paged_cache_read(const hsa_paged_cache* cache, void* k, void* v, 
 size_t hsa_paged_attn_workspace_bytes(const hsa_paged_cache* cache, int32_t heads_q, int32_t nq, int64_t max_vis) {
   if (check_paged_sizes(cache) != HSA_OK || check_paged_query(cache, heads_q, nq, max_vis) != HSA_OK) return 0;
   const int32_t group = heads_q / cache->heads;
-  return paged_ws(cache, nq * group, paged_splits_most(cache->batch, cache->heads, group, nq, max_vis, cache->dtype)).total;
+  return paged_ws(cache, nq * group, paged_splits_most(cache->batch, cache->heads, cache->head_dim, group, nq, max_vis, cache->dtype)).total;
 }
 
 hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, int32_t q_dtype, int32_t heads_q,
@@ -634,7 +634,7 @@ hsa_status hsa_paged_attn_decode(const hsa_paged_cache* cache, const void* q, in
   if (window < 0 || !(sm_scale > 0.f) || !(scale_log2 > 0.f) || !isfinite(scale_log2)) return HSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return HSA_ERR_ALIGN;
   const int32_t group = heads_q / cache->heads, rows = nq * group;
-  const PagedSplit sp = paged_split(cache->batch, cache->heads, group, nq, max_vis, window, cache->dtype);
+  const PagedSplit sp = paged_split(cache->batch, cache->heads, cache->head_dim, group, nq, max_vis, window, cache->dtype);
   if ((int64_t)sp.n_splits * sp.chunks * cache->heads * cache->batch > (int64_t)INT32_MAX ||
       (int64_t)rows * cache->heads * cache->batch > (int64_t)INT32_MAX)
     return HSA_ERR_SHAPE;

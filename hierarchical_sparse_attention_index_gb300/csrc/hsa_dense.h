@@ -61,8 +61,8 @@ struct PagedSplit {
   bool cluster;           // the splits are one thread-block cluster, which joins them
   bool joined;            // paged_join_kernel follows
 };
-PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype);
-int64_t paged_splits_most(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t kv_dtype);
+PagedSplit paged_split(int32_t batch, int32_t heads, int32_t head_dim, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype);
+int64_t paged_splits_most(int32_t batch, int32_t heads, int32_t head_dim, int32_t group, int32_t nq, int64_t max_vis, int32_t kv_dtype);
 
 struct PagedAttnParams {
   int32_t batch, heads, page_size;
@@ -88,6 +88,9 @@ struct PagedAttnParams {
 };
 cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedSplit& sp, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns,
                               cudaStream_t s);
+// 4-bit pages: CTAs that an SM holds, for nt tiles of 8 query rows, as registers allow without spilling
+constexpr int four_ctas(int nt, int head_dim) { return nt == 1 && head_dim == 64 ? 4 : nt <= 2 ? 3 : 2; }
+cudaError_t launch_paged_four(const PagedAttnParams& p, int32_t head_dim, cudaStream_t s);
 cudaError_t launch_paged_rows(const PagedAttnParams& p, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns, cudaStream_t s);
 
 // The driver's tensor-map encoder, looked up once through the runtime (no libcuda link); NULL: none.

@@ -26,114 +26,40 @@
 // 8 splits are one thread-block cluster, whose CTAs join their parts through distributed shared memory;
 // more leave their parts in the workspace, and paged_join_kernel joins them. Either joins in order.
 #include "hsa_paged.cuh"
+#include "hsa_paged_warp.cuh"
 
 namespace hsa {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = kPagedWarps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kGroup = 16;               // keys per stage of a warp
+constexpr int kGroup = kPagedGroup;       // keys per stage of a warp
 constexpr int32_t kTcRows = 24;          // 16-bit pages: more query rows than this take the tcgen05 kernel
 
-enum KvType { kBf16 = HSA_BF16, kF16 = HSA_F16, kE4M3 = HSA_E4M3, kE2M1 = HSA_E2M1 };
+enum KvType { kBf16 = HSA_BF16, kF16 = HSA_F16, kE4M3 = HSA_E4M3 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// 16 bytes, of which all but the first `bytes` are zeros and not read
-__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// a row's scales of 4-bit pages, N = 4 or 8 bytes, of which all but the first `bytes` are zeros and not read
-template <int N>
-__device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-// the 8 x 8 transpose of 16-bit values held two per lane
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-template <bool BF16>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (BF16) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  } else {
-    mma_f16_16816(c, a[0], a[1], a[2], a[3], b0, b1);
-  }
-}
-// 4-bit pages: the key of a 16-key group at place i of the products' key index, and back. Thread t's keys, places
-// 2t, 2t + 1, 2t + 8 and 2t + 9, are then t, t + 4, t + 8, t + 12
-__host__ __device__ __forceinline__ constexpr int four_key(int i) { return (i & 8) + ((i & 1) << 2) + ((i & 6) >> 1); }
-__host__ __device__ __forceinline__ constexpr int four_place(int r) { return (r & 8) + ((r & 3) << 1) + ((r & 4) >> 2); }
-// (x, x) of the low or the high half of an f16 pair times y
-__device__ __forceinline__ uint32_t mul_half(uint32_t x, int hi, uint32_t y) {
-  const __half2 a = *reinterpret_cast<const __half2*>(&x), b = *reinterpret_cast<const __half2*>(&y);
-  const __half2 r = __hmul2(hi ? __high2half2(a) : __low2half2(a), b);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t mul_pair(uint32_t x, uint32_t y) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 // CTAs that an SM holds, for NT tiles of 8 query rows: as registers and shared memory (their rings, 227 KB) allow
 constexpr int ctas_per_sm(int nt) { return nt <= 2 ? 3 : 2; }
 
 template <int D, int KV, int NT>
 struct Tile {
   static constexpr int kElem = KV == kE4M3 ? 1 : 2;
-  static constexpr int kRow = KV == kE2M1 ? D / 2 : D * kElem;           // bytes of a key's row
+  static constexpr int kRow = D * kElem;                 // bytes of a key's row
   static constexpr int kChunks = kRow / 16;
   static constexpr int kHalf = kGroup * kRow;            // K, then V
-  static constexpr int kScaleRow = KV == kE2M1 ? D / 16 : 0;             // bytes of a row's scales
-  static constexpr int kScales = kGroup * kScaleRow;     // K's behind V, then V's
-  static constexpr int kStage = 2 * kHalf + 2 * kScales;
+  static constexpr int kStage = 2 * kHalf;
   static constexpr int kCtas = ctas_per_sm(NT);
   static constexpr int kRingMax = kCtas == 3 ? 16384 : 24576;
-  static constexpr int kStagesMax = KV == kE2M1 ? (D == 128 ? 10 : 15) : 6;
-  static constexpr int kStages = kRingMax / kStage > kStagesMax ? kStagesMax : kRingMax / kStage;
+  static constexpr int kStages = kRingMax / kStage > 6 ? 6 : kRingMax / kStage;
   static constexpr int kRing = kStage * kStages;
-  static constexpr int kOutLd = D + 4;                   // floats from row to row when the warps merge (bank spread)
+  static constexpr int kOutLd = kPagedOutLd<D>;
   static_assert(8 * NT * kOutLd * 4 <= kRing, "a warp's outputs fit its ring");
   // 16-byte piece c of row r. K: pieces 4i..4i+3 of two neighbouring rows are read together; V: one
   // piece of 8 rows (matrix loads), or two pieces of rows 0, 2, 4, 6 (E4M3)
-  // E2M1: K's row r lies at its place in the products (four_key(place) = r), so that 8 lanes read 128 bytes in a row; V's pieces
-  // of rows t and 4 + t are read together by thread t, 8 (4) bytes of each by 8 threads
   static __device__ __forceinline__ uint32_t k_at(int r, int c) {
-    if constexpr (KV == kE2M1) return (uint32_t)(four_place(r) * kRow + c * 16);
     return (uint32_t)(r * kRow + (kChunks >= 8 ? (c ^ ((r & 1) << 2)) : c) * 16);
   }
   static __device__ __forceinline__ uint32_t v_at(int r, int c) {
-    if constexpr (KV == kE2M1) return (uint32_t)(r * kRow + (kChunks == 4 ? c ^ (r & 2) : c) * 16);
     return (uint32_t)(r * kRow + (kChunks >= 8 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3))) * 16);
   }
 };
@@ -169,27 +95,17 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
   const Span sp = request_span(p, b);
   if (!CLUSTER && split >= sp.used) return;
   const int begin = sp.base + split * sp.len, end = max(begin, min(begin + sp.len, sp.hi));   // keys of this CTA
-  const int rows = p.nq * p.group, row0 = chunk * p.chunk_rows, row_end = min(row0 + p.chunk_rows, rows);
+  const int row0 = chunk * p.chunk_rows, row_end = min(row0 + p.chunk_rows, p.nq * p.group);
 
   // ---------------------------------------------------------------- the ring: 16-key groups of this warp
   const uint32_t ring = smem_u32(sm) + (uint32_t)warp * T::kRing;
   const int n_groups = max(0, (end - begin + kGroup * (kWarps - warp) - 1) / (kGroup * kWarps));
   uint32_t bad = 0;                                      // bit s: the group in stage s is not loaded
-  // where 32 groups lie, one per lane, looked up a turn ahead of their use: the piece of the pools in
-  // units of 16 rows, times 2^16, plus a bit for each row that some query sees; 0 for a bad page or no such row
+  // where 32 groups lie, one per lane, looked up a turn ahead of their use
   const int64_t page_pieces = (int64_t)p.heads * (p.page_size / kGroup);
   auto find_pieces = [&](int turn) -> int64_t {
     const int i = 32 * turn + lane;
-    if (i >= n_groups) return 0;
-    const int pos = begin + kGroup * (warp + kWarps * i), pg = pos / p.page_size;
-    const uint32_t seen = seen32(p, b, sp.lo, sp.hi, sp.gaps, pos) & 0xFFFFu;
-    if (!seen) return 0;
-    const int page = p.table[(int64_t)b * p.max_pages + pg];
-    if (page < 0 || page >= p.n_pages) {
-      flag_status(p.status, HSA_FLAG_INDEX_RANGE);
-      return 0;
-    }
-    return ((page * page_pieces + (h * p.page_size + pos - pg * p.page_size) / kGroup) << 16) | seen;
+    return i < n_groups ? find_piece(p, sp, b, h, page_pieces, begin + kGroup * (warp + kWarps * i)) : 0;
   };
   int64_t pieces = find_pieces(0), pieces_next = find_pieces(1);
   auto issue = [&](int i, int stage) {                   // called with i = 0, 1, 2, ...
@@ -200,14 +116,6 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
     }
     if (i < n_groups) {
       const uint32_t st = (uint32_t)stage * T::kStage, seen = (uint32_t)found & 0xFFFFu;
-      if constexpr (KV == kE2M1) {
-        // a lane for each row's scales: of K where it lies among the keys, of V in the order t, t + 4, .. of thread t
-        const int r = lane & 15;
-        const uint32_t n = (seen >> r) & 1u ? (uint32_t)T::kScaleRow : 0u;
-        const uint8_t* src = (lane < 16 ? p.k_s : p.v_s) + (n ? ((found >> 16) * kGroup + r) * T::kScaleRow : 0);
-        const uint32_t place = lane < 16 ? four_place(r) : kGroup + (r & 3) * 4 + (r >> 2);
-        cp_async_scales<(T::kScaleRow ? T::kScaleRow : 4)>(ring + st + 2 * T::kHalf + place * T::kScaleRow, src, n);
-      }
       bad = (bad & ~(1u << stage)) | ((seen ? 0u : 1u) << stage);
       const int64_t at = seen ? (found >> 16) * (kGroup * T::kRow) + lane * 16 : 0;
       const uint8_t* k = p.k_pool + at;
@@ -241,12 +149,9 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
     const int r = row0 + lane;
     int lo = 0, hi = 0;
     if (r < row_end) {
-      const int raw = p.vis[(int64_t)b * p.nq + r / p.group];
-      hi = clamp_vis(p, raw);
-      if (raw != hi && split == 0 && h == 0) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
-      lo = p.window > 0 ? max(hi - p.window, 0) : 0;
-      all_lo = lo;
-      all_hi = hi;
+      const int2 keys = row_keys(p, b, r, split == 0 && h == 0);
+      all_lo = lo = keys.x;
+      all_hi = hi = keys.y;
     }
     if (warp == 0) {
       s_lo[lane] = lo;
@@ -260,11 +165,10 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
   // k-step ks covers, of thread t, the 4 consecutive elements that its piece of a key's row brings
   // to that step
   uint32_t qb[NT][kSteps][2];
-  constexpr bool kScaled = KV == kE4M3 || KV == kE2M1;
-  constexpr int kScales = kScaled ? 2 * NT : 1;
+  constexpr int kScales = KV == kE4M3 ? 2 * NT : 1;
   float scale[kScales];                                  // of rows 2t, 2t + 1 of each tile (or of all rows)
   {
-    constexpr int kPer = KV == kE2M1 ? 4 : 16 / T::kElem;                // consecutive elements of a thread: of a 16-byte piece, 4 of a scale's group
+    constexpr int kPer = 16 / T::kElem;                  // elements of a 16-byte piece
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = row0 + 8 * n + g;
@@ -277,34 +181,9 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
         const int piece = 4 * (ks / (kPer / 4)) + t;
         x[ks] = real ? *reinterpret_cast<const uint2*>(q + piece * kPer + 4 * (ks % (kPer / 4))) : make_uint2(0u, 0u);
       }
-      if constexpr (kScaled) {
+      if constexpr (KV == kE4M3) {
         float sc = p.scale_log2;
-        if (p.q_bf16) {
-          // bf16 queries against f16 keys: to f16 after a power-of-two shift of the row, taken back in its scale
-          float amax = 0.f;
-#pragma unroll
-          for (int ks = 0; ks < kSteps; ++ks) {
-            const uint32_t w[2] = {x[ks].x, x[ks].y};
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[u] << 16)), fabsf(__uint_as_float(w[u] & 0xFFFF0000u))));
-          }
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          int sh = 0;
-          if (amax > 0.f && amax < INFINITY) {
-            int e;
-            frexpf(amax, &e);
-            sh = max(-120, min(120, 12 - e));            // amax 2^sh in [2^11, 2^12): products and their sums stay in fp32
-          }
-          const float mul = __uint_as_float((uint32_t)(127 + sh) << 23);
-          sc *= __uint_as_float((uint32_t)(127 - sh) << 23);
-#pragma unroll
-          for (int ks = 0; ks < kSteps; ++ks) {
-            x[ks].x = pack2<false>(__uint_as_float(x[ks].x << 16) * mul, __uint_as_float(x[ks].x & 0xFFFF0000u) * mul);
-            x[ks].y = pack2<false>(__uint_as_float(x[ks].y << 16) * mul, __uint_as_float(x[ks].y & 0xFFFF0000u) * mul);
-          }
-        }
+        if (p.q_bf16) queries_to_f16(x, sc);
         if (warp == 0 && t == 0) s_scale[8 * n + g] = sc;
       }
 #pragma unroll
@@ -315,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
     }
   }
   __syncthreads();                                       // s_lo, s_hi, s_scale
-  if constexpr (kScaled) {
+  if constexpr (KV == kE4M3) {
 #pragma unroll
     for (int j = 0; j < kScales; ++j) scale[j] = s_scale[8 * (j >> 1) + 2 * t + (j & 1)];
   } else {
@@ -352,39 +231,6 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-      if constexpr (KV == kE2M1) {
-        // a thread's bytes of a row: of each scale's group the two that hold its 4 dims, which make one k-step
-        constexpr int kW = D / 32;                       // words: two groups each
-        uint32_t w0[kW], w1[kW], c0[kW / 2], c1[kW / 2];
-        const uint32_t ss = sk + 2 * T::kHalf;
-        if constexpr (D == 128) {
-          const uint4 k0 = lds128(sk + g * T::kRow + 16 * t), k1 = lds128(sk + (8 + g) * T::kRow + 16 * t);
-          const uint2 s0 = lds64(ss + g * T::kScaleRow), s1 = lds64(ss + (8 + g) * T::kScaleRow);
-          w0[0] = k0.x, w0[1] = k0.y, w0[kW - 2] = k0.z, w0[kW - 1] = k0.w;
-          w1[0] = k1.x, w1[1] = k1.y, w1[kW - 2] = k1.z, w1[kW - 1] = k1.w;
-          c0[0] = s0.x, c0[kW / 2 - 1] = s0.y;
-          c1[0] = s1.x, c1[kW / 2 - 1] = s1.y;
-        } else {
-          const uint2 k0 = lds64(sk + g * T::kRow + 8 * t), k1 = lds64(sk + (8 + g) * T::kRow + 8 * t);
-          w0[0] = k0.x, w0[1] = k0.y;
-          w1[0] = k1.x, w1[1] = k1.y;
-          c0[0] = lds32(ss + g * T::kScaleRow);
-          c1[0] = lds32(ss + (8 + g) * T::kScaleRow);
-        }
-#pragma unroll
-        for (int j = 0; j < kW; ++j) {
-          uint32_t x[4], y[4];
-          e2m1x8_to_f16x2x4(w0[j], x[0], x[1], x[2], x[3]);
-          e2m1x8_to_f16x2x4(w1[j], y[0], y[1], y[2], y[3]);
-          const uint32_t f0 = e4m3x2_to_f16x2((uint16_t)(c0[j / 2] >> (16 * (j & 1)))), f1 = e4m3x2_to_f16x2((uint16_t)(c1[j / 2] >> (16 * (j & 1))));
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {                  // code x scale has 6 bits at most and is at least 2^-10: exact in f16
-            const uint32_t a[4] = {mul_half(f0, u, x[2 * u]), mul_half(f1, u, y[2 * u]), mul_half(f0, u, x[2 * u + 1]), mul_half(f1, u, y[2 * u + 1])};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<kB>(s[n], a, qb[n][2 * j + u][0], qb[n][2 * j + u][1]);
-          }
-        }
-      } else
 #pragma unroll
       for (int c4 = 0; c4 < T::kChunks / 4; ++c4) {
         const uint4 k0 = lds128(sk + T::k_at(g, 4 * c4 + t)), k1 = lds128(sk + T::k_at(8 + g, 4 * c4 + t));
@@ -412,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int place = g + 8 * (e >> 1), r = 8 * n + 2 * t + (e & 1), key = pos + (KV == kE2M1 ? four_key(place) : place);
+            const int r = 8 * n + 2 * t + (e & 1), key = pos + g + 8 * (e >> 1);
             if (key < s_lo[r] || key >= s_hi[r]) s[n][e] = -INFINITY;
           }
       }
@@ -454,49 +300,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
         pb[n][1] = movmatrix_trans(pack2<kB>(w[2], w[3]));
       }
       // ------------------------------------------------------------ O^T += V^T P^T
-      if constexpr (KV == kE2M1) {
-        // thread row g of tile mt is dim 16 mt + 2 g, row g + 8 the next one: byte g of each scale's group, of keys t, t + 4, t + 8, t + 12
-        constexpr int kW = D / 64;                       // words of a thread's bytes of a key: 4 groups each
-        uint32_t w[4][kW], c[4][kW];
-        const uint32_t ss = sk + 2 * T::kHalf + T::kScales + 4 * t * T::kScaleRow;
-        if constexpr (D == 128) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint2 x = lds64(sv + T::v_at(t + 4 * u, g >> 1) + 8 * (g & 1));
-            w[u][0] = x.x, w[u][kW - 1] = x.y;
-          }
-          const uint4 x = lds128(ss), y = lds128(ss + 16);
-          c[0][0] = x.x, c[0][kW - 1] = x.y, c[1][0] = x.z, c[1][kW - 1] = x.w;
-          c[2][0] = y.x, c[2][kW - 1] = y.y, c[3][0] = y.z, c[3][kW - 1] = y.w;
-        } else {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) w[u][0] = lds32(sv + T::v_at(t + 4 * u, g >> 2) + 4 * (g & 3));
-          const uint4 x = lds128(ss);
-          c[0][0] = x.x, c[1][0] = x.y, c[2][0] = x.z, c[3][0] = x.w;
-        }
-#pragma unroll
-        for (int j = 0; j < kW; ++j) {
-          // codes and scales of two keys side by side, as the products take them
-          uint32_t v[4][4], f[2][4];                     // [row g, row g + 8 of keys t, t + 4; of keys t + 8, t + 12][group]
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t x = w[2 * u][j], y = w[2 * u + 1][j];
-            e2m1x8_to_f16x2x4((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), v[2 * u][0], v[2 * u][1], v[2 * u][2], v[2 * u][3]);
-            e2m1x8_to_f16x2x4(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), v[2 * u + 1][0], v[2 * u + 1][1], v[2 * u + 1][2], v[2 * u + 1][3]);
-            const uint32_t lo = __byte_perm(c[2 * u][j], c[2 * u + 1][j], 0x5140), hi = __byte_perm(c[2 * u][j], c[2 * u + 1][j], 0x7362);
-            f[u][0] = e4m3x2_to_f16x2((uint16_t)(lo & 0xFFFFu));
-            f[u][1] = e4m3x2_to_f16x2((uint16_t)(lo >> 16));
-            f[u][2] = e4m3x2_to_f16x2((uint16_t)(hi & 0xFFFFu));
-            f[u][3] = e4m3x2_to_f16x2((uint16_t)(hi >> 16));
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t a[4] = {mul_pair(v[0][e], f[0][e]), mul_pair(v[1][e], f[0][e]), mul_pair(v[2][e], f[1][e]), mul_pair(v[3][e], f[1][e])};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<kB>(o[4 * j + e][n], a, pb[n][0], pb[n][1]);
-          }
-        }
-      } else if constexpr (KV == kE4M3) {
+      if constexpr (KV == kE4M3) {
         // thread row g of tile mt is dim kPd g + 2 mt, row g + 8 the next one: rows 2t, 2t+1, 2t+8, 2t+9 of V
         constexpr int kPd = D / 8;
         uint32_t w[4][kPd / 4];
@@ -561,85 +365,10 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        so[r * T::kOutLd + (KV == kE4M3 ? D / 8 * g + 2 * mt + u : KV == kE2M1 ? 16 * mt + 2 * g + u : 16 * mt + g + 8 * u)] = o[mt][j >> 1][2 * u + (j & 1)];
+        so[r * T::kOutLd + (KV == kE4M3 ? D / 8 * g + 2 * mt + u : 16 * mt + g + 8 * u)] = o[mt][j >> 1][2 * u + (j & 1)];
   }
   __syncthreads();
-  constexpr int kQuads = D / 4;
-  auto write_out = [&](int row, int d4, float4 a, float M, float L) {
-    const int64_t at = ((int64_t)b * p.nq + row / p.group) * p.heads_q + h * p.group + row % p.group;
-    const float inv = L != 0.f ? p.v_scale / L : 0.f;
-    uint2 y;
-    if (p.q_bf16)
-      y = make_uint2(pack2<true>(a.x * inv, a.y * inv), pack2<true>(a.z * inv, a.w * inv));
-    else
-      y = make_uint2(pack2<false>(a.x * inv, a.y * inv), pack2<false>(a.z * inv, a.w * inv));
-    *reinterpret_cast<uint2*>(p.out + at * D + 4 * d4) = y;
-    if (p.lse && d4 == 0) p.lse[at] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
-  };
-  // a += 2^(m - M) (O, l); a part in which the row saw no key adds nothing
-  auto add = [](float4& a, float& L, float M, float m, float l, float4 x) {
-    if (m != -INFINITY || l != 0.f) {
-      const float f = m == -INFINITY ? 0.f : ex2_ftz(m - M);
-      a.x += f * x.x;
-      a.y += f * x.y;
-      a.z += f * x.z;
-      a.w += f * x.w;
-      L += f * l;
-    }
-  };
-  for (int e = tid; e < kRows * kQuads; e += kThreads) {
-    const int r = e / kQuads, d4 = e % kQuads, row = row0 + r;
-    if (row >= row_end) break;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-    float4* mine = reinterpret_cast<float4*>(sm + ((size_t)r * T::kOutLd + 4 * d4) * 4);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      add(a, L, M, s_m[w][r], s_l[w][r], *reinterpret_cast<const float4*>(reinterpret_cast<uint8_t*>(mine) + (size_t)w * T::kRing));
-    if (sp.used == 1) {
-      if (!CLUSTER || split == 0) write_out(row, d4, a, M, L);
-    } else if constexpr (CLUSTER) {
-      *mine = a;                         // read by this thread alone until here
-      if (d4 == 0) s_part[r] = make_float2(M, L);
-    } else {
-      const int64_t at = (((int64_t)b * p.heads + h) * p.n_splits + split) * rows + row;
-      *reinterpret_cast<float4*>(p.part_o + at * D + 4 * d4) = a;
-      if (d4 == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(M, L);
-    }
-  }
-  if constexpr (CLUSTER) {
-    if (sp.used == 1) return;            // the same in every CTA of the cluster
-    __syncwarp();
-    cluster_sync_all();
-    // CTA `split` joins every n_splits-th element of the chunk, over the CTAs that have keys
-    const uint32_t o_at = smem_u32(sm), ml_at = smem_u32(s_part);
-    for (int e = split * kThreads + tid; e < kRows * kQuads; e += p.n_splits * kThreads) {
-      const int r = e / kQuads, d4 = e % kQuads, row = row0 + r;
-      if (row >= row_end) break;
-      float M = -INFINITY;
-      for (int c = 0; c < sp.used; ++c) M = fmaxf(M, __uint_as_float((uint32_t)ld_cluster_s32(cluster_map(ml_at + 8 * r, c))));
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      float L = 0.f;
-#pragma unroll 4
-      for (int c = 0; c < sp.used; ++c) {
-        const uint64_t ml = ld_cluster_u64(cluster_map(ml_at + 8 * r, c));
-        const uint32_t x = cluster_map(o_at + ((uint32_t)r * T::kOutLd + 4 * d4) * 4, c);
-        const uint64_t x0 = ld_cluster_u64(x), x1 = ld_cluster_u64(x + 8);
-        float m, l;
-        float4 v;
-        f2_unpack(ml, m, l);
-        f2_unpack(x0, v.x, v.y);
-        f2_unpack(x1, v.z, v.w);
-        add(a, L, M, m, l, v);
-      }
-      write_out(row, d4, a, M, L);
-    }
-    __syncwarp();
-    cluster_sync_all();                  // nobody reads this CTA's shared memory any more
-  }
+  merge_warps<D, NT, CLUSTER>(p, sp, b, h, split, row0, row_end, sm, T::kRing, s_m, s_l, s_part);
 }
 
 // The splits of one row, joined in a fixed order: o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
@@ -721,24 +450,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) paged_join_kernel(const
 
 template <int D, int KV, int NT, bool CLUSTER>
 cudaError_t launch(const PagedAttnParams& p, cudaStream_t s) {
-  auto kernel = paged_attn_kernel<D, KV, NT, CLUSTER>;
-  constexpr size_t smem = (size_t)kWarps * Tile<D, KV, NT>::kRing;
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.n_splits * p.batch * p.heads * p.chunks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)p.n_splits;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = CLUSTER ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return launch_splits<CLUSTER>(paged_attn_kernel<D, KV, NT, CLUSTER>, p, (size_t)kWarps * Tile<D, KV, NT>::kRing, s);
 }
 template <int D, int KV>
 cudaError_t launch_nt(const PagedAttnParams& p, cudaStream_t s) {
@@ -747,8 +459,8 @@ cudaError_t launch_nt(const PagedAttnParams& p, cudaStream_t s) {
     case 2: return p.cluster ? launch<D, KV, 2, true>(p, s) : launch<D, KV, 2, false>(p, s);
     case 3: return p.cluster ? launch<D, KV, 3, true>(p, s) : launch<D, KV, 3, false>(p, s);
   }
-  static_assert(kTcRows <= 3 * 8, "four tiles only for pages of 8 and 4 bits");
-  if constexpr (KV == kE4M3 || KV == kE2M1)
+  static_assert(kTcRows <= 3 * 8, "four tiles only for E4M3");
+  if constexpr (KV == kE4M3)
     return p.cluster ? launch<D, KV, 4, true>(p, s) : launch<D, KV, 4, false>(p, s);
   else
     return cudaErrorInvalidValue;
@@ -758,20 +470,20 @@ cudaError_t launch_kv(const PagedAttnParams& p, int kv, cudaStream_t s) {
   switch (kv) {
     case kBf16: return launch_nt<D, kBf16>(p, s);
     case kF16: return launch_nt<D, kF16>(p, s);
-    case kE4M3: return launch_nt<D, kE4M3>(p, s);
-    default: return launch_nt<D, kE2M1>(p, s);
+    default: return launch_nt<D, kE4M3>(p, s);
   }
 }
 
 }  // namespace
 
-// Splits by rounds of the `places` that the GPU has for CTAs: the n with the least rounds x (keys of a job + 400) + 20 n,
-// in the time of a key. A job costs what 400 keys do besides its own (its start and end), a split 20 in the join; a
+// Splits by rounds of the `places` that the GPU has for CTAs: the n with the least rounds x (keys of a job + start) + 20 n,
+// in the time of a key. A job costs what `start` keys do besides its own (its start and end), a split 20 in the join; a
 // round that is not full costs as much as a full one. In w rounds the best n is the largest that fits.
 struct Rounds {
   int64_t places;
   int64_t count;                         // numbers of rounds looked at
   bool few;                              // no more splits than where the two last terms meet
+  int64_t start;
   int64_t first(int64_t ctas) const { return (ctas + places - 1) / places; }
   int64_t splits_in(int64_t w, int64_t ctas, int64_t span) const {
     int64_t n = imin64(places * w / ctas, (span + 127) / 128);
@@ -782,16 +494,19 @@ struct Rounds {
 };
 // The tcgen05 kernel, one CTA to an SM. 64 requests x 4 heads x 16,384 keys, ragged: n = 1, 4, 9: 246, 204, 229 us;
 // x 4,097: 73, 77, 105; 8 x 4 x 16,384: n = 3, 4, 5, 9: 54.6, 53.9, 74.5, 59.0
-constexpr Rounds kTcRounds = {kSms, 8, true};
+constexpr Rounds kTcRounds = {kSms, 8, true, 400};
 // The warp MMA kernel with 17 to 32 rows, two to an SM. Against as many CTAs as four to an SM would be, in no rounds: 16
 // requests x 8 heads x 20 rows, f16, 4,097 keys 30 us (46), 16,384 97 (115); 16 x 4 x 35 rows, E4M3, 4,097 36 (40), 16,384 93 (98);
 // 64 x 4 x 24 rows, bf16, of 1 .. 16,384 keys 187 (206), all 65,536 1,240 (1,205); 4 x 4 x 35, E4M3, 4,097 17.1 (15.9)
-constexpr Rounds kWideRounds = {2 * kSms, 6, false};
+constexpr Rounds kWideRounds = {2 * kSms, 6, false, 400};
+// 4-bit pages. 8 query rows, 128 dims, 32 x 8 heads of 1 .. 8,192 keys: n = 1, 2, 3, 5, 8: 74, 52.6, 42.1, 47.8, 45.7 us; 16 x 8 of 8,192: n = 3, 4, 6: 38.8,
+// 46.3, 43.3; 4 x 8 of 131,072: n = 13, 14, 19, 28: 120, 114, 126, 117; 16 rows, 64 x 8 of 4,096: n = 1, 2, 4: 112, 105, 115
+static Rounds four_rounds(int32_t chunk_rows, int32_t head_dim) { return {kSms * four_ctas((chunk_rows + 7) / 8, head_dim), 6, false, 700}; }
 static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
   int64_t best = 1, cost = INT64_MAX;
   for (int64_t w = r.first(ctas); w < r.first(ctas) + r.count; ++w) {
     const int64_t n = r.splits_in(w, ctas, span);
-    const int64_t c = r.first(ctas * n) * (span / n + 400) + 20 * n;
+    const int64_t c = r.first(ctas * n) * (span / n + r.start) + 20 * n;
     if (c < cost) {
       cost = c;
       best = n;
@@ -815,8 +530,18 @@ static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
 // A request's splits follow from max_vis and the sizes alone, so that its result does not depend on
 // where it stands in the batch. (Equal pieces of all requests' keys, one per place on the GPU, were
 // slower: 109 against 94 us for 32 ragged contexts, because SMs do not get equal shares of HBM.)
-static bool wide(const PagedSplit& s) { return !s.tc && s.chunk_rows > 16; }
-PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype) {
+static bool rounds_of(const PagedSplit& s, int32_t head_dim, int32_t kv_dtype, Rounds* r) {
+  if (s.tc)
+    *r = kTcRounds;
+  else if (kv_dtype == HSA_E2M1)
+    *r = four_rounds(s.chunk_rows, head_dim);
+  else if (s.chunk_rows > 16)
+    *r = kWideRounds;
+  else
+    return false;
+  return true;
+}
+PagedSplit paged_split(int32_t batch, int32_t heads, int32_t head_dim, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype) {
   PagedSplit s;
   const int32_t rows = nq * group;
   s.tc = (kv_dtype == HSA_BF16 || kv_dtype == HSA_F16) && rows > kTcRows;
@@ -831,12 +556,15 @@ PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, 
   s.align = s.tc ? 64 : 16;
   int64_t span = max_vis;
   if (window > 0 && (int64_t)window + nq + s.align - 1 < span) span = (int64_t)window + nq + s.align - 1;   // vis one apart, as in a draft
-  const int64_t ctas = (int64_t)batch * heads * s.chunks, places = kSms * ctas_per_sm((s.chunk_rows + 7) / 8);
-  int64_t n;
+  const int64_t ctas = (int64_t)batch * heads * s.chunks;
+  int64_t n, places = kSms * ctas_per_sm((s.chunk_rows + 7) / 8);
+  Rounds rounds;
+  const bool in_rounds = rounds_of(s, head_dim, kv_dtype, &rounds);
   if (s.tc) {
-    n = best_splits(kTcRounds, ctas, span);
+    n = best_splits(rounds, ctas, span);
   } else {
-    const int64_t most = wide(s) ? best_splits(kWideRounds, ctas, span) : (places + ctas / 2) / ctas;
+    if (kv_dtype == HSA_E2M1) places = rounds.places;
+    const int64_t most = in_rounds ? best_splits(rounds, ctas, span) : (places + ctas / 2) / ctas;
     n = imin64(most, (span + 255) / 256);
     if (n < 8) n = imin64(imin64(most, 8), (span + 127) / 128);
   }
@@ -849,17 +577,19 @@ PagedSplit paged_split(int32_t batch, int32_t heads, int32_t group, int32_t nq, 
 }
 
 // The most splits that leave their parts in the workspace, for any length up to max_vis and any window
-int64_t paged_splits_most(int32_t batch, int32_t heads, int32_t group, int32_t nq, int64_t max_vis, int32_t kv_dtype) {
-  const PagedSplit s = paged_split(batch, heads, group, nq, max_vis, 0, kv_dtype);
-  if (!s.tc && !wide(s)) return s.joined ? s.n_splits : 0;             // the longest has the most
-  return (s.tc ? kTcRounds : kWideRounds).most((int64_t)batch * heads * s.chunks, max_vis);
+int64_t paged_splits_most(int32_t batch, int32_t heads, int32_t head_dim, int32_t group, int32_t nq, int64_t max_vis, int32_t kv_dtype) {
+  const PagedSplit s = paged_split(batch, heads, head_dim, group, nq, max_vis, 0, kv_dtype);
+  Rounds rounds;
+  if (!rounds_of(s, head_dim, kv_dtype, &rounds)) return s.joined ? s.n_splits : 0;            // the longest has the most
+  return rounds.most((int64_t)batch * heads * s.chunks, max_vis);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedSplit& sp, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns,
                               cudaStream_t s) {
-  const cudaError_t e = sp.tc             ? launch_paged_rows(p, head_dim, kv_dtype, wait_ns, s)
-                        : head_dim == 128 ? launch_kv<128>(p, kv_dtype, s)
-                                          : launch_kv<64>(p, kv_dtype, s);
+  const cudaError_t e = sp.tc                    ? launch_paged_rows(p, head_dim, kv_dtype, wait_ns, s)
+                        : kv_dtype == HSA_E2M1 ? launch_paged_four(p, head_dim, s)
+                        : head_dim == 128      ? launch_kv<128>(p, kv_dtype, s)
+                                               : launch_kv<64>(p, kv_dtype, s);
   if (e != cudaSuccess || !sp.joined) return e;
   const int64_t ids = (int64_t)p.batch * p.heads * p.nq * p.group;
   if (p.n_splits > kJoinWide) {
