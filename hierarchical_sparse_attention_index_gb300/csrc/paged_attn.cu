@@ -571,7 +571,9 @@ PagedSplit paged_split(int32_t batch, int32_t heads, int32_t head_dim, int32_t g
   n = imax64(1, n);
   s.n_splits = (int32_t)n;
   s.split_len = (int32_t)imax64(64, ((span + n - 1) / n + 63) / 64 * 64);
-  s.cluster = !s.tc && n > 1 && n <= 8 && ctas * n <= places;
+  // 4-bit pages: as many clusters as run at a time, where the SMs of each of about eight parts of the GPU hold some 54 CTAs, of
+  // which up to n - 1 are left over (64 x 65,536 keys, 7 splits: 172 us in clusters, 116 joined by the kernel)
+  s.cluster = !s.tc && n > 1 && n <= 8 && ctas * n <= places - (kv_dtype == HSA_E2M1 ? places * n / 48 : 0);
   s.joined = n > 1 && !s.cluster;
   return s;
 }
