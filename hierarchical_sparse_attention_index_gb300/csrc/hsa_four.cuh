@@ -33,4 +33,11 @@ __device__ __forceinline__ uint32_t four_codes(const float (&x)[8], float s) {
   return w & (0x77777777u | ((m + 0x77777777u) & 0x88888888u));
 }
 
+// (x, x) of the low or the high half of an f16 pair times y
+__device__ __forceinline__ uint32_t mul_half(uint32_t x, int hi, uint32_t y) {
+  const __half2 a = *reinterpret_cast<const __half2*>(&x), b = *reinterpret_cast<const __half2*>(&y);
+  const __half2 r = __hmul2(hi ? __high2half2(a) : __low2half2(a), b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 }  // namespace hsa

@@ -18,6 +18,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+// a row's scales of 4-bit pages, N = 4 or 8 bytes, of which all but the first `bytes` are zeros and not read
+template <int N>
+__device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -82,9 +87,9 @@ __device__ __forceinline__ int2 row_keys(const PagedAttnParams& p, int b, int r,
   return make_int2(p.window > 0 ? max(hi - p.window, 0) : 0, hi);
 }
 
-// bf16 queries against f16 keys: a thread's four consecutive elements for each k-step to f16, after a power-of-two shift of
-// the row (four lanes hold it), which is taken back in its scale
-template <int STEPS>
+// bf16 queries against f16 keys: a thread's elements of a row, which LANES neighbouring lanes hold, to f16, after a power-of-two
+// shift of the row, which is taken back in its scale
+template <int STEPS, int LANES = 4>
 __device__ __forceinline__ void queries_to_f16(uint2 (&x)[STEPS], float& scale) {
   float amax = 0.f;
 #pragma unroll
@@ -94,8 +99,8 @@ __device__ __forceinline__ void queries_to_f16(uint2 (&x)[STEPS], float& scale) 
     for (int u = 0; u < 2; ++u)
       amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[u] << 16)), fabsf(__uint_as_float(w[u] & 0xFFFF0000u))));
   }
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   int sh = 0;
   if (amax > 0.f && amax < INFINITY) {
     int e;

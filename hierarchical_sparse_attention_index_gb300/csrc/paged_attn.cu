@@ -34,6 +34,7 @@ namespace {
 constexpr int kWarps = kPagedWarps;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = kPagedGroup;       // keys per stage of a warp
+constexpr int32_t kTcRowsFour = 16;      // of 4-bit pages
 constexpr int32_t kTcRows = 24;          // 16-bit pages: more query rows than this take the tcgen05 kernel
 
 enum KvType { kBf16 = HSA_BF16, kF16 = HSA_F16, kE4M3 = HSA_E4M3 };
@@ -544,7 +545,7 @@ static bool rounds_of(const PagedSplit& s, int32_t head_dim, int32_t kv_dtype, R
 PagedSplit paged_split(int32_t batch, int32_t heads, int32_t head_dim, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype) {
   PagedSplit s;
   const int32_t rows = nq * group;
-  s.tc = (kv_dtype == HSA_BF16 || kv_dtype == HSA_F16) && rows > kTcRows;
+  s.tc = kv_dtype != HSA_E4M3 && rows > (kv_dtype == HSA_E2M1 ? kTcRowsFour : kTcRows);
   if (s.tc) {
     const int32_t queries = nq < 128 / group ? nq : 128 / group;
     s.chunks = (nq + queries - 1) / queries;

@@ -15,6 +15,7 @@
 //    in pairs of keys as the products take them, and come from shared memory;
 //  - the keys of a piece are taken in the order t, t + 4 (four_key), so that every shared load is free of bank conflicts;
 //  - two pieces of 16 keys go through a turn of the loop together: two independent chains, one vote and one wait for both.
+#include "hsa_four.cuh"
 #include "hsa_paged_warp.cuh"
 
 namespace hsa {
@@ -27,12 +28,6 @@ constexpr int kWarps = kPagedWarps, kThreads = kWarps * 32, kGroup = kPagedGroup
 __host__ __device__ __forceinline__ constexpr int four_key(int i) { return (i & 8) + ((i & 1) << 2) + ((i & 6) >> 1); }
 __host__ __device__ __forceinline__ constexpr int four_place(int r) { return (r & 8) + ((r & 3) << 1) + ((r & 4) >> 2); }
 
-// (x, x) of the low or the high half of an f16 pair times y
-__device__ __forceinline__ uint32_t mul_half(uint32_t x, int hi, uint32_t y) {
-  const __half2 a = *reinterpret_cast<const __half2*>(&x), b = *reinterpret_cast<const __half2*>(&y);
-  const __half2 r = __hmul2(hi ? __high2half2(a) : __low2half2(a), b);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 __device__ __forceinline__ uint32_t mul_pair(uint32_t x, uint32_t y) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -40,12 +35,6 @@ __device__ __forceinline__ uint32_t mul_pair(uint32_t x, uint32_t y) {
 __device__ __forceinline__ void sts128v(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// a row's scales, N = 4 or 8 bytes, of which all but the first `bytes` are zeros and not read
-template <int N>
-__device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
-}
-
 // Bytes of a warp's ring slot (one piece): K's codes, a row at its place in the products; V's codes, whose 16-byte chunks of rows
 // t and t + 4 lie apart; K's and V's scales in the same orders. Behind the slots, the scales in f16 of the pieces of a turn.
 template <int D, int NT>

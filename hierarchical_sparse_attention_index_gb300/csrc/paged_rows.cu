@@ -26,7 +26,8 @@
 #include <numeric>
 
 #include "hsa_flash.cuh"
-#include "hsa_paged.cuh"
+#include "hsa_four.cuh"
+#include "hsa_paged_warp.cuh"
 
 namespace hsa {
 namespace {
@@ -36,12 +37,21 @@ constexpr int kKeys = 64;                // keys of a tile
 constexpr int kSoftWarps = 8;            // 4 per stream: two warp groups; the third holds the other roles
 constexpr int kMmaWarp = 8, kLoadWarp = 10;              // a warp per stream's products, and one per stream's loads
 constexpr int kOutWarp = 12;             // warps 12..15 merge the streams and write
-constexpr int kFindWarp = 16;            // finds the work; warps 17..19 only fill its warp group
-constexpr int kThreads = 20 * 32;
-// registers per thread: 96 at launch (65,536 over 640 threads, whole groups of 8), then 136 for the softmax groups,
-// whose threads hold a row of 64 logits, 80 for the next two and 48 for the last
-constexpr int kLaunchRegs = 96, kSoftRegs = 136, kOtherRegs = 80, kFindRegs = 48;
-static_assert(2 * kSoftRegs + 2 * kOtherRegs + kFindRegs <= 5 * kLaunchRegs, "setmaxnreg draws on the launch's registers");
+// The roles of the other warps, and registers per thread: at launch (65,536 over the threads, whole groups of 8), then for the
+// softmax groups, whose threads hold a row of 64 logits, for the group of the products, the one that writes, and the rest
+template <bool FOUR>
+struct Roles {                           // 16-bit pages: warps 10 and 11 load, 16 finds the work, 17..19 only fill its warp group
+  static constexpr int kFindWarp = 16, kThreads = 20 * 32, kJobReaders = kSoftWarps + 4 + 4, kFilled = 1;
+  static constexpr int kLaunchRegs = 96, kSoftRegs = 136, kIssueRegs = 80, kOutRegs = 80, kLastRegs = 48;
+  static_assert(2 * kSoftRegs + kIssueRegs + kOutRegs + kLastRegs <= 5 * kLaunchRegs, "setmaxnreg draws on the launch's registers");
+};
+template <>
+struct Roles<true> {                     // 4-bit pages: warp 10 fills its group, 11 finds the work, 16..23 load and convert, four for each stream
+  static constexpr int kFindWarp = 11, kThreads = 24 * 32, kJobReaders = kSoftWarps + 2 + 4 + 8, kFilled = 4;
+  static constexpr int kLaunchRegs = 80, kSoftRegs = 128, kIssueRegs = 56, kOutRegs = 72, kLastRegs = 48;
+  static_assert(2 * kSoftRegs + kIssueRegs + kOutRegs + 2 * kLastRegs <= 6 * kLaunchRegs, "setmaxnreg draws on the launch's registers");
+};
+constexpr int kConvertWarp = 16;
 constexpr uint32_t kBlockK = kKeys * 128;                // 64 dims of a tile of keys, 128 bytes a row
 constexpr int kJobSlots = 2;
 constexpr int kOrdered = 128;            // batches up to this can be worked off by length
@@ -52,8 +62,11 @@ struct Shape {
   // tiles of K and V in a stream's ring, at most. 4, 5, 6 at 128 dims: 64 requests x 16,384 keys 332, 327.5, 327 us, of
   // 1 .. 4,097 keys 61.3, 60.7, 61.7, 1 request x 131,072 53.6, 53.9, 55.7
   static constexpr int kMaxStages = D == 128 ? 5 : 10;
+  // 4-bit pages: a converting warp's slots of a piece of 16 keys, K or V: codes and scales
+  static constexpr int kRawSlots = 6, kRawBytes = kPagedGroup * (D / 2 + D / 16);
 };
-constexpr uint32_t kSmemMost = 227 * 1024 - 4096;                // but for what is declared in the kernel
+
+constexpr uint32_t smem_most(bool four) { return 227 * 1024 - (four ? 4608 : 4096); }      // but for what is declared in the kernel
 
 struct RowsParams {
   CUtensorMap qm, km, vm;
@@ -75,13 +88,15 @@ struct Job {
   int more;                              // 0: no work is left, the other fields are not set
 };
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_constant__ RowsParams rp) {
+template <int D, bool BF16, bool FOUR>
+__global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(const __grid_constant__ RowsParams rp) {
   using L = Shape<D>;
+  using R = Roles<FOUR>;
   const PagedAttnParams& p = rp.a;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Job s_job[kJobSlots];
-  __shared__ int s_pages[kJobSlots][2][32];              // pages of either stream's first tiles
+  __shared__ int s_pages[FOUR ? 1 : kJobSlots][2][FOUR ? 1 : 32];   // pages of either stream's first tiles
+  __shared__ float s_query[2][FOUR ? kTile : 1];         // 4-bit pages: 2^-shift of each row's queries in f16
   __shared__ float2 s_ml[2][kTile];                      // each stream's (m in log2 units, l) of a row
   __shared__ __align__(16) uint4 s_answer;
   __shared__ uint32_t s_tmem;
@@ -94,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   const uint32_t q_block = (uint32_t)rp.q_rows * 128u, q_bytes = (D / 64) * q_block;
   const uint32_t sQ = base, sKv = base + 2 * q_bytes;
   const int stages = rp.stages;
+  const uint32_t sRaw = sKv + 2 * (uint32_t)stages * L::kKvBytes;        // 4-bit pages: pieces as they lie in the pools
   // mbarriers: Q loaded / read by both streams' last products, for jobs in turn; for each stream O and (m, l)
   // read, every product done; two for each stream, for key tiles in turn: S computed, P written, P V added
   // to O. Then (m, l) written by each stream, the launcher's answer, the jobs and the rings
@@ -107,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), 512);
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
-      mbar_init(q_full + 8 * t, 1);
+      mbar_init(q_full + 8 * t, FOUR ? 8 : 1);
       mbar_init(q_empty + 8 * t, 2);
       mbar_init(o_empty + 8 * t, 4);
       mbar_init(ml_full + 8 * t, 4);
@@ -121,10 +137,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     mbar_init(answered, 1);
     for (int s = 0; s < kJobSlots; ++s) {
       mbar_init(job_full + 8 * s, 1);
-      mbar_init(job_empty + 8 * s, kSoftWarps + 4 + 4);
+      mbar_init(job_empty + 8 * s, R::kJobReaders);
     }
     for (int s = 0; s < 2 * L::kMaxStages; ++s) {
-      mbar_init(kv_full + 8 * s, 1);
+      mbar_init(kv_full + 8 * s, R::kFilled);
       mbar_init(kv_empty + 8 * s, 1);
     }
     fence_mbar_init();
@@ -200,9 +216,243 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     return page;
   };
 
+  // ---------------------------------------------------------------- what comes next
+  auto find_work = [&]() {
+    // A block is taken only when the work before the last has been done by every role, so that no CTA
+    // holds back more than one piece of work (taking three ahead left ragged batches uneven).
+    const uint32_t answer = smem_u32(&s_answer);
+    uint32_t block = blockIdx.x;
+    int it = 0;
+    auto wait_slot = [&]() {
+      ok = wait_bar(job_empty + 8 * (it % kJobSlots), ((it / kJobSlots) & 1) ^ 1, rp.wait_ns) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    for (int n = 0; ok; ++n) {
+      Job job;
+      int idx = (int)block;
+      job.chunk = idx % p.chunks;
+      idx /= p.chunks;
+      job.h = idx % p.heads;
+      idx /= p.heads;
+      job.b = idx % p.batch;
+      if (rp.ordered) job.b = s_order[job.b];
+      job.split = idx / p.batch;
+      job.more = 1;
+      const Span sp = request_span(p, job.b);
+      job.lo = sp.lo;
+      job.hi = sp.hi;
+      job.gaps = sp.gaps;
+      if (lane < p.nq && job.split == 0 && job.h == 0) {
+        const int raw = p.vis[(int64_t)job.b * p.nq + lane];
+        if (raw != clamp_vis(p, raw)) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
+      }
+      if (job.split < sp.used) {
+        const int begin = (sp.base + job.split * sp.len) / kKeys, end = (min(sp.base + (job.split + 1) * sp.len, sp.hi) + kKeys - 1) / kKeys;
+        const int half = (max(0, end - begin) + 1) / 2;
+        job.j0[0] = begin;
+        job.j1[0] = job.j0[1] = begin + half;
+        job.j1[1] = max(end, begin + half);
+        job.whole = sp.used == 1;
+        int first[2] = {0, 0};
+        if constexpr (!FOUR)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) first[t] = find_pages(job, job.j0[t], job.j1[t], 0);
+        if (!wait_slot()) break;
+        if constexpr (!FOUR)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) s_pages[it % kJobSlots][t][lane] = first[t];
+        __syncwarp();
+        if (lane == 0) {
+          s_job[it % kJobSlots] = job;
+          mbar_arrive(job_full + 8 * (it % kJobSlots));
+        }
+        ++it;
+      }
+      if (!wait_slot()) break;
+      if (lane == 0) {
+        fence_async_smem();            // the last answer has been read
+        mbar_arrive_expect_tx(answered, 16);
+        next_block_ask(answer, answered);
+      }
+      __syncwarp();
+      ok = drain_bar(answered, n & 1) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const bool more = next_block_take(answer, block);
+      __syncwarp();
+      if (!more) {
+        if (lane == 0) {
+          s_job[it % kJobSlots].more = 0;
+          mbar_arrive(job_full + 8 * (it % kJobSlots));
+        }
+        break;
+      }
+    }
+  };
+
+  // ---------------------------------------------------------------- 4-bit pages: loads, and codes to f16
+  // A warp takes 16 keys of each tile of its stream: pieces come into its own slots by asynchronous copies, up to
+  // kRawSlots ahead, and go from there, converted, into the tiles that the products read. Half a row for each lane, whose bytes
+  // are 8 neighbouring dims of every scale's group, in K as in V (the pages' orders): one 16-byte piece of the tile each.
+  // Rows no query sees become zeros. At a job's start the eight warps bring its queries, too.
+  auto convert = [&]() {
+    constexpr int kRow = D / 2, kScaleRow = D / 16, kChunks = kRow / 16, kHalf = kPagedGroup * kRow, kCopies = kPagedGroup * kChunks / 32;
+    constexpr int kSlots = L::kRawSlots;
+    const int cw = warp - kConvertWarp, t = cw >> 2, part = cw & 3;
+    const uint32_t full = kv_full + 8 * t * L::kMaxStages, empty = kv_empty + 8 * t * L::kMaxStages, ring = sKv + t * stages * L::kKvBytes;
+    const uint32_t raw = sRaw + cw * kSlots * L::kRawBytes;
+    const int64_t page_pieces = (int64_t)p.heads * (p.page_size / kPagedGroup);
+    // 16-byte chunk c of row r of a piece: four lanes' worth of banks apart from row to row
+    auto raw_at = [](int r, int c) { return (uint32_t)(r * kRow + (kChunks == 4 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1)) * 16); };
+    const int r0 = lane / kChunks, c0 = lane % kChunks, r = lane & 15, half = lane >> 4;
+    const uint32_t copy0 = raw_at(r0, c0);
+    int place = 0, round = 0;            // of the ring
+    for (int it = 0; wait_job(it); ++it) {
+      const Job& job = s_job[it % kJobSlots];
+      const int b = uniform(job.b), h = uniform(job.h), chunk = uniform(job.chunk), j0 = uniform(t ? job.j0[1] : job.j0[0]),
+                n = uniform(t ? job.j1[1] : job.j1[0]) - j0;
+      Span sp;
+      sp.lo = job.lo;
+      sp.hi = job.hi;
+      sp.gaps = job.gaps;
+      free_job(it);
+      auto find_pieces = [&](int of) -> int64_t {
+        const int i = 32 * of + lane;
+        return i < n ? find_piece(p, sp, b, h, page_pieces, kKeys * (j0 + i) + kPagedGroup * part) : 0;
+      };
+      int64_t pieces = find_pieces(0), pieces_next = find_pieces(1), now = 0, before = 0;
+      // step u of 2 n: K(0) K(1) V(0) K(2) V(1) .. V(n - 1)
+      auto issue = [&](int u) {          // called with u = 0, 1, 2, ...
+        if (u < 2 * n) {
+          const bool keys = u == 0 || ((u & 1) && u != 2 * n - 1);
+          if (keys) {
+            const int i = (u + 1) >> 1;
+            before = now;
+            now = __shfl_sync(0xffffffffu, pieces, i & 31);
+            if ((i & 31) == 31) {
+              pieces = pieces_next;
+              pieces_next = find_pieces((i >> 5) + 2);
+            }
+          }
+          const int64_t found = keys || u == 2 * n - 1 ? now : before;
+          const uint32_t seen = (uint32_t)found & 0xFFFFu, at = raw + (uint32_t)(u % kSlots) * L::kRawBytes;
+          const uint64_t piece = (uint32_t)(found >> 16);
+          const uint8_t* pool = keys ? p.k_pool : p.v_pool;
+          const uint8_t* scales = keys ? p.k_s : p.v_s;
+          if (lane < 16) {
+            const bool some = (seen >> lane) & 1u;
+            cp_async_scales<kScaleRow>(at + kHalf + lane * kScaleRow, some ? scales + (piece * kPagedGroup + lane) * kScaleRow : scales,
+                                       some ? (uint32_t)kScaleRow : 0u);
+          }
+#pragma unroll
+          for (int v = 0; v < kCopies; ++v) {
+            const uint32_t some = (seen >> (r0 + 8 * v)) & 1u ? 16u : 0u;
+            cp_async16z(at + copy0 + v * 512, some ? pool + piece * kHalf + lane * 16 + v * 512 : pool, some);
+          }
+        }
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int u = 0; u < kSlots - 1; ++u) issue(u);
+
+      // ---- queries: 16 (8) lanes to a row, rows in turn over the eight warps
+      {
+        constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;
+        const int qs = it & 1, rows = p.nq * p.group, first = chunk * rp.tt * p.group;
+        ok = wait_bar(q_empty + 8 * qs, ((it >> 1) & 1) ^ 1, rp.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        for (int base_row = cw * kRowsAt; base_row < rp.q_rows; base_row += 8 * kRowsAt) {
+          const int row = base_row + lane / kLanes, c = lane % kLanes, at = first + row;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (row < rp.tt * p.group && at < rows)
+            x = *reinterpret_cast<const uint4*>(p.q + (((int64_t)b * p.nq + at / p.group) * p.heads_q + h * p.group + at % p.group) * D + 8 * c);
+          float shift = 1.f;
+          if (p.q_bf16) {
+            uint2 y[2] = {make_uint2(x.x, x.y), make_uint2(x.z, x.w)};
+            queries_to_f16<2, kLanes>(y, shift);
+            x = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
+          }
+          if (row < rp.q_rows) {
+            sts128(sQ + qs * q_bytes + (c >> 3) * q_block + row * 128 + ((c & 7) ^ (row & 7)) * 16, x.x, x.y, x.z, x.w);
+            if (c == 0) s_query[qs][row] = shift;
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full + 8 * qs);
+      }
+
+      // ---- tiles
+      const uint32_t to = (uint32_t)(kPagedGroup * part + r) * 128u;
+      for (int u = 0; u < 2 * n; ++u) {
+        issue(u + kSlots - 1);
+        cp_async_wait<kSlots - 1>();
+        __syncwarp();
+        const uint32_t at = raw + (uint32_t)(u % kSlots) * L::kRawBytes, dst = ring + place * L::kKvBytes + to;
+        const bool keys = u == 0 || ((u & 1) && u != 2 * n - 1);
+        uint32_t w[D / 16];              // this lane's codes
+#pragma unroll
+        for (int v = 0; v < D / 64; ++v) {
+          const uint4 x = lds128(at + raw_at(r, D / 64 * half + v));
+          w[4 * v] = x.x, w[4 * v + 1] = x.y, w[4 * v + 2] = x.z, w[4 * v + 3] = x.w;
+        }
+        uint32_t c[D / 64];              // the row's scales
+        if constexpr (D == 128) {
+          const uint2 x = lds64(at + kHalf + r * kScaleRow);
+          c[0] = x.x, c[D / 64 - 1] = x.y;
+        } else {
+          c[0] = lds32(at + kHalf + r * kScaleRow);
+        }
+        ok = wait_bar(empty + 8 * place, (round & 1) ^ 1, rp.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        auto store = [&](int s, uint32_t f, int hi, uint32_t y0, uint32_t y1, uint32_t y2, uint32_t y3) {      // the 8 dims of group s
+          sts128(dst + (s >> 2) * kBlockK + (((2 * (s & 3) + half) ^ (r & 7)) * 16), mul_half(f, hi, y0), mul_half(f, hi, y1), mul_half(f, hi, y2),
+                 mul_half(f, hi, y3));
+        };
+        if (keys) {
+          // words j and D / 32 + j: dims 0 .. 3 and 4 .. 7 of the lane's eight, of groups 2 j and 2 j + 1
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            uint32_t x[4], y[4];
+            e2m1x8_to_f16x2x4(w[j], x[0], x[1], x[2], x[3]);
+            e2m1x8_to_f16x2x4(w[D / 32 + j], y[0], y[1], y[2], y[3]);
+            const uint32_t f = e4m3x2_to_f16x2((uint16_t)(c[j >> 1] >> (16 * (j & 1))));
+            store(2 * j, f, 0, x[0], x[1], y[0], y[1]);
+            store(2 * j + 1, f, 1, x[2], x[3], y[2], y[3]);
+          }
+        } else {
+          // word D / 64 q + j: dims 2 q, 2 q + 1 of the lane's eight, of groups 4 j .. 4 j + 3
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            uint32_t x[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) e2m1x8_to_f16x2x4(w[D / 64 * q + j], x[q][0], x[q][1], x[q][2], x[q][3]);
+            const uint32_t f0 = e4m3x2_to_f16x2((uint16_t)(c[j] & 0xFFFFu)), f1 = e4m3x2_to_f16x2((uint16_t)(c[j] >> 16));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) store(4 * j + e, e < 2 ? f0 : f1, e & 1, x[0][e], x[1][e], x[2][e], x[3][e]);
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + 8 * place);
+        if (++place == stages) {
+          place = 0;
+          ++round;
+        }
+      }
+      if (!ok) break;
+    }
+    cp_async_wait<0>();
+  };
+
   if (warp >= kSoftWarps && warp < kOutWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp >= kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kIssueRegs));
+    if (FOUR && warp >= kLoadWarp) {
+      if (warp == R::kFindWarp) find_work();
+    } else if (warp >= kLoadWarp) {
       // -------------------------------------------------------------- loads of one stream, the first's with the queries
       // The ring holds K(0) K(1) V(0) K(2) V(1) ... V(n-1): the products of S run a tile ahead of those with V.
       // Issuing the boxes of a 16 KB tile takes a warp 450 ns, longer than the tile's share of HBM: hence a warp per
@@ -343,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
           }
           if (j + 1 == j1) umma_commit_one(one, q_empty + 8 * (it & 1));   // Q's last product is issued
           if (!wait_kv()) break;
-          if (kKeys * j < lo || kKeys * (j + 1) > hi || gaps) {        // there may be rows that no query sees
+          if (!FOUR && (kKeys * j < lo || kKeys * (j + 1) > hi || gaps)) {   // there may be rows that no query sees
             const uint32_t seen0 = seen_at(job, kKeys * j), seen1 = seen_at(job, kKeys * j + 32);
             const uint32_t v = ring + c * L::kKvBytes;
             for (int x = lane; x < kKeys * 8; x += 32)
@@ -367,10 +617,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     }
   } else if (warp < kSoftWarps) {
     // ---------------------------------------------------------------- softmax: one row per thread
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftRegs));
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * t, tO = tS + 256u;
-    const float scale = p.scale_log2;
+    float scale = p.scale_log2;
     const int rows = p.nq * p.group;
     int n_s = 0;                         // key tiles so far
     for (int it = 0; wait_job(it); ++it) {
@@ -385,6 +635,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         lo = p.window > 0 ? max(hi - p.window, 0) : 0;
       }
       const int all_lo = __reduce_max_sync(0xffffffffu, real ? lo : 0), all_hi = __reduce_min_sync(0xffffffffu, real ? hi : 0x7fffffff);
+      if constexpr (FOUR) {              // before the job is freed: job it + 2 then waits with its queries
+        ok = wait_bar(q_full + 8 * (it & 1), (it >> 1) & 1, rp.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        scale = r < rp.q_rows ? p.scale_log2 * s_query[it & 1][r] : p.scale_log2;
+      }
       free_job(it);
       const bool small = p.page_size < kKeys || p.page_size % kKeys;   // a tile may lie on several pages
       float m = -INFINITY, l = 0.f;
@@ -436,9 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(ml_full + 8 * t);
     }
-  } else if (warp < kFindWarp) {
+  } else if (warp < kOutWarp + 4) {
     // ---------------------------------------------------------------- both streams' O and (m, l), while the softmax is at the next job
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kOutRegs));
     const int r = (warp & 3) * 32 + lane, rows = p.nq * p.group;
     const uint32_t tO = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u;
     int n_s[2] = {0, 0};                 // key tiles of either stream so far
@@ -491,7 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         // each lane writes its own row, 32 bytes at a time where the rows allow it
         if (whole)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = pack2<BF16>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+          for (int e = 0; e < 8; ++e)
+            x[e] = BF16 || (FOUR && p.q_bf16) ? pack2<true>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]))
+                                              : pack2<false>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
         if (real) {
           uint32_t* dst = whole ? reinterpret_cast<uint32_t*>(p.out + at * D + 16 * c) : reinterpret_cast<uint32_t*>(p.part_o + (slot * rows + row) * D + 16 * c);
 #pragma unroll
@@ -514,75 +772,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFindRegs));
-    // ---------------------------------------------------------------- what comes next
-    // A block is taken only when the work before the last has been done by every role, so that no CTA
-    // holds back more than one piece of work (taking three ahead left ragged batches uneven).
-    const uint32_t answer = smem_u32(&s_answer);
-    uint32_t block = blockIdx.x;
-    int it = 0;
-    auto wait_slot = [&]() {
-      ok = wait_bar(job_empty + 8 * (it % kJobSlots), ((it / kJobSlots) & 1) ^ 1, rp.wait_ns) && ok;
-      ok = __all_sync(0xffffffffu, ok);
-      return ok;
-    };
-    for (int n = 0; ok && warp == kFindWarp; ++n) {
-      Job job;
-      int idx = (int)block;
-      job.chunk = idx % p.chunks;
-      idx /= p.chunks;
-      job.h = idx % p.heads;
-      idx /= p.heads;
-      job.b = idx % p.batch;
-      if (rp.ordered) job.b = s_order[job.b];
-      job.split = idx / p.batch;
-      job.more = 1;
-      const Span sp = request_span(p, job.b);
-      job.lo = sp.lo;
-      job.hi = sp.hi;
-      job.gaps = sp.gaps;
-      if (lane < p.nq && job.split == 0 && job.h == 0) {
-        const int raw = p.vis[(int64_t)job.b * p.nq + lane];
-        if (raw != clamp_vis(p, raw)) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
-      }
-      if (job.split < sp.used) {
-        const int begin = (sp.base + job.split * sp.len) / kKeys, end = (min(sp.base + (job.split + 1) * sp.len, sp.hi) + kKeys - 1) / kKeys;
-        const int half = (max(0, end - begin) + 1) / 2;
-        job.j0[0] = begin;
-        job.j1[0] = job.j0[1] = begin + half;
-        job.j1[1] = max(end, begin + half);
-        job.whole = sp.used == 1;
-        const int first[2] = {find_pages(job, job.j0[0], job.j1[0], 0), find_pages(job, job.j0[1], job.j1[1], 0)};
-        if (!wait_slot()) break;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) s_pages[it % kJobSlots][t][lane] = first[t];
-        __syncwarp();
-        if (lane == 0) {
-          s_job[it % kJobSlots] = job;
-          mbar_arrive(job_full + 8 * (it % kJobSlots));
-        }
-        ++it;
-      }
-      if (!wait_slot()) break;
-      if (lane == 0) {
-        fence_async_smem();            // the last answer has been read
-        mbar_arrive_expect_tx(answered, 16);
-        next_block_ask(answer, answered);
-      }
-      __syncwarp();
-      ok = drain_bar(answered, n & 1) && ok;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const bool more = next_block_take(answer, block);
-      __syncwarp();
-      if (!more) {
-        if (lane == 0) {
-          s_job[it % kJobSlots].more = 0;
-          mbar_arrive(job_full + 8 * (it % kJobSlots));
-        }
-        break;
-      }
-    }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kLastRegs));
+    if constexpr (FOUR)
+      convert();
+    else if (warp == R::kFindWarp)
+      find_work();
   }
   if (!ok) flag_status(p.status, HSA_FLAG_TIMEOUT);
   __syncwarp();
@@ -592,26 +786,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
   if (warp == kMmaWarp) tmem_free(tmem, 512);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool FOUR = false>
 cudaError_t launch(RowsParams& p, unsigned blocks, cudaStream_t s) {
-  auto kernel = paged_rows_kernel<D, BF16>;
-  static const bool fits = launches_with(kernel, kLaunchRegs);
+  auto kernel = paged_rows_kernel<D, BF16, FOUR>;
+  static const bool fits = launches_with(kernel, Roles<FOUR>::kLaunchRegs);
   if (!fits) return cudaErrorInvalidConfiguration;
   p.q_rows = (p.tt * p.a.group + 7) / 8 * 8;
-  const uint32_t room = kSmemMost - 1024 - 2 * (D / 64) * (uint32_t)p.q_rows * 128u;
+  const uint32_t raw = FOUR ? 8 * Shape<D>::kRawSlots * Shape<D>::kRawBytes : 0;
+  const uint32_t room = smem_most(FOUR) - 1024 - raw - 2 * (D / 64) * (uint32_t)p.q_rows * 128u;
   p.stages = (int32_t)(room / (2 * Shape<D>::kKvBytes));
   if (p.stages > Shape<D>::kMaxStages) p.stages = Shape<D>::kMaxStages;
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), kSmemMost);
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem_most(FOUR));
   if (e != cudaSuccess) return e;
-  const uint32_t smem = 1024 + 2 * (D / 64) * (uint32_t)p.q_rows * 128u + 2 * (uint32_t)p.stages * Shape<D>::kKvBytes;   // 1024: to align
-  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, s, p);
+  const uint32_t smem = 1024 + 2 * (D / 64) * (uint32_t)p.q_rows * 128u + 2 * (uint32_t)p.stages * Shape<D>::kKvBytes + raw;   // 1024: to align
+  return launch_pdl(kernel, dim3(blocks), dim3(Roles<FOUR>::kThreads), smem, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_rows(const PagedAttnParams& a, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns, cudaStream_t s) {
-  const TensorMapEncoder encode = tensor_map_encoder();
-  if (!encode) return cudaErrorNotSupported;
   RowsParams p;
   memset(&p, 0, sizeof(p));
   p.a = a;
@@ -623,6 +816,11 @@ cudaError_t launch_paged_rows(const PagedAttnParams& a, int32_t head_dim, int32_
   p.ordered = a.batch <= kOrdered && a.n_splits == 1 && (int64_t)a.batch * a.heads * a.chunks > kSms;
   p.wide = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.part_o)) & 31) == 0;
   p.wait_ns = wait_ns;
+  const unsigned blocks = (unsigned)a.n_splits * a.batch * a.heads * a.chunks;
+  if (kv_dtype == HSA_E2M1)              // queries and pages are loaded without tensor maps
+    return head_dim == 128 ? launch<128, false, true>(p, blocks, s) : launch<64, false, true>(p, blocks, s);
+  const TensorMapEncoder encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
   const CUtensorMapDataType type = kv_dtype == HSA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const cuuint64_t d = (cuuint64_t)head_dim;
   const cuuint32_t ones[4] = {1, 1, 1, 1};
@@ -645,7 +843,6 @@ cudaError_t launch_paged_rows(const PagedAttnParams& a, int32_t head_dim, int32_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  const unsigned blocks = (unsigned)a.n_splits * a.batch * a.heads * a.chunks;
   if (head_dim == 128) return kv_dtype == HSA_BF16 ? launch<128, true>(p, blocks, s) : launch<128, false>(p, blocks, s);
   return kv_dtype == HSA_BF16 ? launch<64, true>(p, blocks, s) : launch<64, false>(p, blocks, s);
 }
