@@ -48,7 +48,7 @@ struct Roles {                           // 16-bit pages: warps 10 and 11 load, 
 template <>
 struct Roles<true> {                     // 4-bit pages: warp 10 fills its group, 11 finds the work, 16..23 load and convert, four for each stream
   static constexpr int kFindWarp = 11, kThreads = 24 * 32, kJobReaders = kSoftWarps + 2 + 4 + 8, kFilled = 4;
-  static constexpr int kLaunchRegs = 80, kSoftRegs = 128, kIssueRegs = 56, kOutRegs = 72, kLastRegs = 48;
+  static constexpr int kLaunchRegs = 80, kSoftRegs = 120, kIssueRegs = 40, kOutRegs = 56, kLastRegs = 72;
   static_assert(2 * kSoftRegs + kIssueRegs + kOutRegs + 2 * kLastRegs <= 6 * kLaunchRegs, "setmaxnreg draws on the launch's registers");
 };
 constexpr int kConvertWarp = 16;
@@ -62,8 +62,8 @@ struct Shape {
   // tiles of K and V in a stream's ring, at most. 4, 5, 6 at 128 dims: 64 requests x 16,384 keys 332, 327.5, 327 us, of
   // 1 .. 4,097 keys 61.3, 60.7, 61.7, 1 request x 131,072 53.6, 53.9, 55.7
   static constexpr int kMaxStages = D == 128 ? 5 : 10;
-  // 4-bit pages: a converting warp's slots of a piece of 16 keys, K or V: codes and scales
-  static constexpr int kRawSlots = 6, kRawBytes = kPagedGroup * (D / 2 + D / 16);
+  // 4-bit pages: a converting warp's slots of a piece of 16 keys, K and V: codes, then scales
+  static constexpr int kRawSlots = 4, kRawBytes = 2 * kPagedGroup * (D / 2 + D / 16);
 };
 
 constexpr uint32_t smem_most(bool four) { return 227 * 1024 - (four ? 4608 : 4096); }      // but for what is declared in the kernel
@@ -97,6 +97,9 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
   __shared__ Job s_job[kJobSlots];
   __shared__ int s_pages[FOUR ? 1 : kJobSlots][2][FOUR ? 1 : 32];   // pages of either stream's first tiles
   __shared__ float s_query[2][FOUR ? kTile : 1];         // 4-bit pages: 2^-shift of each row's queries in f16
+  // 4-bit pages: which 16-key pieces of a tile are on bad pages or seen by no query, of each stream's tiles in turn. A tile is written 8 after it
+  // is read: the rings and S hold 5 key tiles between the two at most
+  __shared__ __align__(4) uint8_t s_bad[2][8][4];
   __shared__ float2 s_ml[2][kTile];                      // each stream's (m in log2 units, l) of a row
   __shared__ __align__(16) uint4 s_answer;
   __shared__ uint32_t s_tmem;
@@ -292,156 +295,202 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
   };
 
   // ---------------------------------------------------------------- 4-bit pages: loads, and codes to f16
-  // A warp takes 16 keys of each tile of its stream: pieces come into its own slots by asynchronous copies, up to
+  // A warp takes 16 keys of each tile of its stream: pieces of K and V come into its own slots by asynchronous copies, up to
   // kRawSlots ahead, and go from there, converted, into the tiles that the products read. Half a row for each lane, whose bytes
   // are 8 neighbouring dims of every scale's group, in K as in V (the pages' orders): one 16-byte piece of the tile each.
-  // Rows no query sees become zeros. At a job's start the eight warps bring its queries, too.
+  // Rows no query sees become zeros. The eight warps bring a job's queries, too.
   auto convert = [&]() {
-    constexpr int kRow = D / 2, kScaleRow = D / 16, kChunks = kRow / 16, kHalf = kPagedGroup * kRow, kCopies = kPagedGroup * kChunks / 32;
-    constexpr int kSlots = L::kRawSlots;
+    constexpr int kRow = D / 2, kScaleRow = D / 16, kChunks = kRow / 16, kHalf = kPagedGroup * kRow, kScales = kPagedGroup * kScaleRow;
+    constexpr int kCopies = kPagedGroup * kChunks / 32, kSlots = L::kRawSlots;
     const int cw = warp - kConvertWarp, t = cw >> 2, part = cw & 3;
     const uint32_t full = kv_full + 8 * t * L::kMaxStages, empty = kv_empty + 8 * t * L::kMaxStages, ring = sKv + t * stages * L::kKvBytes;
     const uint32_t raw = sRaw + cw * kSlots * L::kRawBytes;
     const int64_t page_pieces = (int64_t)p.heads * (p.page_size / kPagedGroup);
-    // 16-byte chunk c of row r of a piece: four lanes' worth of banks apart from row to row
+    // 16-byte chunk c of row r of a piece: eight lanes' rows lie apart in the banks
     auto raw_at = [](int r, int c) { return (uint32_t)(r * kRow + (kChunks == 4 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1)) * 16); };
-    const int r0 = lane / kChunks, c0 = lane % kChunks, r = lane & 15, half = lane >> 4;
-    const uint32_t copy0 = raw_at(r0, c0);
-    int place = 0, round = 0;            // of the ring
-    for (int it = 0; wait_job(it); ++it) {
+    const int r0 = lane / kChunks, r = lane & 15, half = lane >> 4;
+    // this lane's copies of a piece: 16 bytes of every 32 / kChunks-th row of K and V, and one row's scales, of K or of V
+    const uint8_t* const k_src = p.k_pool + lane * 16;
+    const uint8_t* const v_src = p.v_pool + lane * 16;
+    const uint8_t* const s_src = (lane < 16 ? p.k_s : p.v_s) + r * kScaleRow;
+    const uint32_t copy_at = raw_at(r0, lane % kChunks), scale_at = 2 * kHalf + lane * kScaleRow;
+    // this lane's chunks of a slot, and where its pieces of a tile go: those of group s to to[s % 4] of its 64 dims
+    uint32_t from[D / 64], to[4];
+#pragma unroll
+    for (int v = 0; v < D / 64; ++v) from[v] = raw_at(r, D / 64 * half + v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) to[e] = (uint32_t)(kPagedGroup * part + r) * 128u + ((2 * e + half) ^ (r & 7)) * 16;
+    // ---- the job whose pieces are being loaded: the one that is converted, or already the next
+    int b = 0, h = 0, j0 = 0, n_load = 0, loads = 0;     // its tiles, and calls of load() for it
+    Span sp = {};
+    int64_t pieces = 0, pieces_next = 0;
+    uint32_t load_slot = 0, gone = 0;    // slot that the next piece takes; bit s: the piece in slot s is on a bad page or seen by no query
+    auto find_pieces = [&](int of) -> int64_t {
+      const int i = 32 * of + lane;
+      return i < n_load ? find_piece(p, sp, b, h, page_pieces, kKeys * (j0 + i) + kPagedGroup * part) : 0;
+    };
+    // the next tile's piece; every call is one group of copies
+    auto load = [&]() {
+      if (loads < n_load) {
+        const int64_t found = __shfl_sync(0xffffffffu, pieces, loads & 31);
+        if ((loads & 31) == 31) {
+          pieces = pieces_next;
+          pieces_next = find_pieces((loads >> 5) + 2);
+        }
+        const uint32_t seen = (uint32_t)found & 0xFFFFu, at = raw + load_slot * L::kRawBytes;
+        const uint64_t piece = (uint32_t)(found >> 16);
+        const uint8_t* k = k_src + piece * kHalf;
+        const uint8_t* v = v_src + piece * kHalf;
+        const uint8_t* sc = s_src + piece * kScales;
+        gone = seen ? gone & ~(1u << load_slot) : gone | 1u << load_slot;
+        if (seen == 0xFFFFu) {
+          cp_async_scales<kScaleRow>(at + scale_at, sc, kScaleRow);
+#pragma unroll
+          for (int u = 0; u < kCopies; ++u) {
+            cp_async16(at + copy_at + u * 512, k + u * 512);
+            cp_async16(at + kHalf + copy_at + u * 512, v + u * 512);
+          }
+        } else {
+          const bool some = (seen >> r) & 1u;
+          cp_async_scales<kScaleRow>(at + scale_at, some ? sc : p.k_s, some ? (uint32_t)kScaleRow : 0u);
+#pragma unroll
+          for (int u = 0; u < kCopies; ++u) {
+            const uint32_t m = (seen >> (r0 + 8 * u)) & 1u ? 16u : 0u;
+            cp_async16z(at + copy_at + u * 512, m ? k + u * 512 : p.k_pool, m);
+            cp_async16z(at + kHalf + copy_at + u * 512, m ? v + u * 512 : p.v_pool, m);
+          }
+        }
+        load_slot = load_slot + 1 == kSlots ? 0 : load_slot + 1;
+      }
+      ++loads;
+      cp_async_commit();
+    };
+    // job `it` from here on: its pieces, its queries (16 or 8 lanes to a row, rows in turn over the eight warps)
+    auto open = [&](int it) {
       const Job& job = s_job[it % kJobSlots];
-      const int b = uniform(job.b), h = uniform(job.h), chunk = uniform(job.chunk), j0 = uniform(t ? job.j0[1] : job.j0[0]),
-                n = uniform(t ? job.j1[1] : job.j1[0]) - j0;
-      Span sp;
+      const int chunk = job.chunk, first = chunk * rp.tt * p.group;
+      b = job.b;
+      h = job.h;
+      j0 = t ? job.j0[1] : job.j0[0];
+      n_load = (t ? job.j1[1] : job.j1[0]) - j0;
       sp.lo = job.lo;
       sp.hi = job.hi;
       sp.gaps = job.gaps;
       free_job(it);
-      auto find_pieces = [&](int of) -> int64_t {
-        const int i = 32 * of + lane;
-        return i < n ? find_piece(p, sp, b, h, page_pieces, kKeys * (j0 + i) + kPagedGroup * part) : 0;
-      };
-      int64_t pieces = find_pieces(0), pieces_next = find_pieces(1), now = 0, before = 0;
-      // step u of 2 n: K(0) K(1) V(0) K(2) V(1) .. V(n - 1)
-      auto issue = [&](int u) {          // called with u = 0, 1, 2, ...
-        if (u < 2 * n) {
-          const bool keys = u == 0 || ((u & 1) && u != 2 * n - 1);
-          if (keys) {
-            const int i = (u + 1) >> 1;
-            before = now;
-            now = __shfl_sync(0xffffffffu, pieces, i & 31);
-            if ((i & 31) == 31) {
-              pieces = pieces_next;
-              pieces_next = find_pieces((i >> 5) + 2);
-            }
-          }
-          const int64_t found = keys || u == 2 * n - 1 ? now : before;
-          const uint32_t seen = (uint32_t)found & 0xFFFFu, at = raw + (uint32_t)(u % kSlots) * L::kRawBytes;
-          const uint64_t piece = (uint32_t)(found >> 16);
-          const uint8_t* pool = keys ? p.k_pool : p.v_pool;
-          const uint8_t* scales = keys ? p.k_s : p.v_s;
-          if (lane < 16) {
-            const bool some = (seen >> lane) & 1u;
-            cp_async_scales<kScaleRow>(at + kHalf + lane * kScaleRow, some ? scales + (piece * kPagedGroup + lane) * kScaleRow : scales,
-                                       some ? (uint32_t)kScaleRow : 0u);
-          }
-#pragma unroll
-          for (int v = 0; v < kCopies; ++v) {
-            const uint32_t some = (seen >> (r0 + 8 * v)) & 1u ? 16u : 0u;
-            cp_async16z(at + copy0 + v * 512, some ? pool + piece * kHalf + lane * 16 + v * 512 : pool, some);
-          }
+      loads = 0;
+      pieces = find_pieces(0);
+      pieces_next = find_pieces(1);
+      constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;
+      const int qs = it & 1, rows = p.nq * p.group;
+      ok = wait_bar(q_empty + 8 * qs, ((it >> 1) & 1) ^ 1, rp.wait_ns) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      for (int base_row = cw * kRowsAt; base_row < rp.q_rows; base_row += 8 * kRowsAt) {
+        const int row = base_row + lane / kLanes, c = lane % kLanes, at = first + row;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (row < rp.tt * p.group && at < rows)
+          x = *reinterpret_cast<const uint4*>(p.q + (((int64_t)b * p.nq + at / p.group) * p.heads_q + h * p.group + at % p.group) * D + 8 * c);
+        float shift = 1.f;
+        if (p.q_bf16) {
+          uint2 y[2] = {make_uint2(x.x, x.y), make_uint2(x.z, x.w)};
+          queries_to_f16<2, kLanes>(y, shift);
+          x = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
         }
-        cp_async_commit();
-      };
-#pragma unroll
-      for (int u = 0; u < kSlots - 1; ++u) issue(u);
-
-      // ---- queries: 16 (8) lanes to a row, rows in turn over the eight warps
-      {
-        constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;
-        const int qs = it & 1, rows = p.nq * p.group, first = chunk * rp.tt * p.group;
-        ok = wait_bar(q_empty + 8 * qs, ((it >> 1) & 1) ^ 1, rp.wait_ns) && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        for (int base_row = cw * kRowsAt; base_row < rp.q_rows; base_row += 8 * kRowsAt) {
-          const int row = base_row + lane / kLanes, c = lane % kLanes, at = first + row;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (row < rp.tt * p.group && at < rows)
-            x = *reinterpret_cast<const uint4*>(p.q + (((int64_t)b * p.nq + at / p.group) * p.heads_q + h * p.group + at % p.group) * D + 8 * c);
-          float shift = 1.f;
-          if (p.q_bf16) {
-            uint2 y[2] = {make_uint2(x.x, x.y), make_uint2(x.z, x.w)};
-            queries_to_f16<2, kLanes>(y, shift);
-            x = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
-          }
-          if (row < rp.q_rows) {
-            sts128(sQ + qs * q_bytes + (c >> 3) * q_block + row * 128 + ((c & 7) ^ (row & 7)) * 16, x.x, x.y, x.z, x.w);
-            if (c == 0) s_query[qs][row] = shift;
-          }
+        if (row < rp.q_rows) {
+          sts128(sQ + qs * q_bytes + (c >> 3) * q_block + row * 128 + ((c & 7) ^ (row & 7)) * 16, x.x, x.y, x.z, x.w);
+          if (c == 0) s_query[qs][row] = shift;
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full + 8 * qs);
       }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full + 8 * qs);
+    };
 
-      // ---- tiles
-      const uint32_t to = (uint32_t)(kPagedGroup * part + r) * 128u;
-      for (int u = 0; u < 2 * n; ++u) {
-        issue(u + kSlots - 1);
-        cp_async_wait<kSlots - 1>();
-        __syncwarp();
-        const uint32_t at = raw + (uint32_t)(u % kSlots) * L::kRawBytes, dst = ring + place * L::kKvBytes + to;
-        const bool keys = u == 0 || ((u & 1) && u != 2 * n - 1);
-        uint32_t w[D / 16];              // this lane's codes
+    // ---- tiles, in the order of the products: K(0) K(1) V(0) K(2) V(1) .. V(n - 1)
+    int place = 0, round = 0, tiles = 0; // of the ring; key tiles so far
+    auto convert_tile = [&](uint32_t at, bool keys) {    // the slot at `at` to the next place of the ring
+      uint32_t w[D / 16];                // this lane's codes
 #pragma unroll
-        for (int v = 0; v < D / 64; ++v) {
-          const uint4 x = lds128(at + raw_at(r, D / 64 * half + v));
-          w[4 * v] = x.x, w[4 * v + 1] = x.y, w[4 * v + 2] = x.z, w[4 * v + 3] = x.w;
+      for (int v = 0; v < D / 64; ++v) {
+        const uint4 x = lds128(at + (keys ? 0 : kHalf) + from[v]);
+        w[4 * v] = x.x, w[4 * v + 1] = x.y, w[4 * v + 2] = x.z, w[4 * v + 3] = x.w;
+      }
+      uint32_t c[D / 64];                // the row's scales
+      const uint32_t c_at = at + 2 * kHalf + (keys ? 0 : kScales) + r * kScaleRow;
+      if constexpr (D == 128) {
+        const uint2 x = lds64(c_at);
+        c[0] = x.x, c[D / 64 - 1] = x.y;
+      } else {
+        c[0] = lds32(c_at);
+      }
+      ok = wait_bar(empty + 8 * place, (round & 1) ^ 1, rp.wait_ns) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      const uint32_t dst = ring + place * L::kKvBytes;
+      auto store = [&](int s, uint32_t f, int hi, uint32_t y0, uint32_t y1, uint32_t y2, uint32_t y3) {        // the 8 dims of group s
+        sts128(dst + to[s & 3] + (s >> 2) * kBlockK, mul_half(f, hi, y0), mul_half(f, hi, y1), mul_half(f, hi, y2), mul_half(f, hi, y3));
+      };
+      if (keys) {
+        // words j and D / 32 + j: dims 0 .. 3 and 4 .. 7 of the lane's eight, of groups 2 j and 2 j + 1
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          uint32_t x[4], y[4];
+          e2m1x8_to_f16x2x4(w[j], x[0], x[1], x[2], x[3]);
+          e2m1x8_to_f16x2x4(w[D / 32 + j], y[0], y[1], y[2], y[3]);
+          const uint32_t f = e4m3x2_to_f16x2((uint16_t)(c[j >> 1] >> (16 * (j & 1))));
+          store(2 * j, f, 0, x[0], x[1], y[0], y[1]);
+          store(2 * j + 1, f, 1, x[2], x[3], y[2], y[3]);
         }
-        uint32_t c[D / 64];              // the row's scales
-        if constexpr (D == 128) {
-          const uint2 x = lds64(at + kHalf + r * kScaleRow);
-          c[0] = x.x, c[D / 64 - 1] = x.y;
-        } else {
-          c[0] = lds32(at + kHalf + r * kScaleRow);
+      } else {
+        // word D / 64 q + j: dims 2 q, 2 q + 1 of the lane's eight, of groups 4 j .. 4 j + 3
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          uint32_t x[4][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) e2m1x8_to_f16x2x4(w[D / 64 * q + j], x[q][0], x[q][1], x[q][2], x[q][3]);
+          const uint32_t f0 = e4m3x2_to_f16x2((uint16_t)(c[j] & 0xFFFFu)), f1 = e4m3x2_to_f16x2((uint16_t)(c[j] >> 16));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) store(4 * j + e, e < 2 ? f0 : f1, e & 1, x[0][e], x[1][e], x[2][e], x[3][e]);
         }
-        ok = wait_bar(empty + 8 * place, (round & 1) ^ 1, rp.wait_ns) && ok;
-        ok = __all_sync(0xffffffffu, ok);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8 * place);
+      if (++place == stages) {
+        place = 0;
+        ++round;
+      }
+    };
+    uint32_t slot = 0;                   // of the tile to be converted
+    bool opened = false;
+    for (int it = 0; opened || wait_job(it); ++it) {
+      if (!opened) open(it);
+      if (!ok) break;
+      while (loads < kSlots) load();
+      opened = false;
+      const int n = n_load;
+      for (int i = 0; i <= n; ++i) {     // K(i), then V(i - 1)
+        const uint32_t last = slot == 0 ? kSlots - 1 : slot - 1;
+        if (i < n) {
+          cp_async_wait<kSlots - 2>();
+          __syncwarp();
+          if (lane == 0) s_bad[t][tiles & 7][part] = (gone >> slot) & 1u;
+          ++tiles;
+          convert_tile(raw + slot * L::kRawBytes, true);
+        }
+        if (i > 0 && ok) {
+          convert_tile(raw + last * L::kRawBytes, false);
+          // Into the slot of V(i - 1), which every lane has read. Behind this job's last tile come the next job's, if it is there:
+          // its pieces and queries are then on their way while the products are at this one
+          if (ok && !opened && loads >= n && __all_sync(0xffffffffu, mbar_test(job_full + 8 * ((it + 1) % kJobSlots), ((it + 1) / kJobSlots) & 1)) &&
+              s_job[(it + 1) % kJobSlots].more) {
+            open(it + 1);
+            opened = true;
+          }
+          if (ok) load();
+        }
         if (!ok) break;
-        auto store = [&](int s, uint32_t f, int hi, uint32_t y0, uint32_t y1, uint32_t y2, uint32_t y3) {      // the 8 dims of group s
-          sts128(dst + (s >> 2) * kBlockK + (((2 * (s & 3) + half) ^ (r & 7)) * 16), mul_half(f, hi, y0), mul_half(f, hi, y1), mul_half(f, hi, y2),
-                 mul_half(f, hi, y3));
-        };
-        if (keys) {
-          // words j and D / 32 + j: dims 0 .. 3 and 4 .. 7 of the lane's eight, of groups 2 j and 2 j + 1
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            uint32_t x[4], y[4];
-            e2m1x8_to_f16x2x4(w[j], x[0], x[1], x[2], x[3]);
-            e2m1x8_to_f16x2x4(w[D / 32 + j], y[0], y[1], y[2], y[3]);
-            const uint32_t f = e4m3x2_to_f16x2((uint16_t)(c[j >> 1] >> (16 * (j & 1))));
-            store(2 * j, f, 0, x[0], x[1], y[0], y[1]);
-            store(2 * j + 1, f, 1, x[2], x[3], y[2], y[3]);
-          }
-        } else {
-          // word D / 64 q + j: dims 2 q, 2 q + 1 of the lane's eight, of groups 4 j .. 4 j + 3
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            uint32_t x[4][4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) e2m1x8_to_f16x2x4(w[D / 64 * q + j], x[q][0], x[q][1], x[q][2], x[q][3]);
-            const uint32_t f0 = e4m3x2_to_f16x2((uint16_t)(c[j] & 0xFFFFu)), f1 = e4m3x2_to_f16x2((uint16_t)(c[j] >> 16));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) store(4 * j + e, e < 2 ? f0 : f1, e & 1, x[0][e], x[1][e], x[2][e], x[3][e]);
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full + 8 * place);
-        if (++place == stages) {
-          place = 0;
-          ++round;
-        }
+        slot = i < n ? (slot + 1 == kSlots ? 0 : slot + 1) : slot;
       }
       if (!ok) break;
     }
@@ -644,31 +693,36 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
       free_job(it);
       const bool small = p.page_size < kKeys || p.page_size % kKeys;   // a tile may lie on several pages
       float m = -INFINITY, l = 0.f;
-      // pages of the tile's 16-row pieces, looked up a tile ahead by lanes 0..3: a bad one masks its keys
-      auto good_of = [&](int j) {
-        bool good = true;
+      // pages of the tile's 16-row pieces, looked up a tile ahead by lanes 0..3: a bad one masks its keys. Only the id is
+      // read ahead: compared where it is read, it would hold up the tile for as long as the table takes to answer
+      auto page_of = [&](int j) {
+        int page = 0;
         const int pos = kKeys * j + 16 * lane;
-        if (warp_real && lane < (small ? 4 : 1) && pos < job_hi) {
-          const int x = p.table[(int64_t)b * p.max_pages + pos / p.page_size];
-          good = x >= 0 && x < p.n_pages;
-        }
-        return good;
+        if (warp_real && lane < (small ? 4 : 1) && pos < job_hi) page = p.table[(int64_t)b * p.max_pages + pos / p.page_size];
+        return page;
       };
-      bool good = j0 < j1 ? good_of(j0) : true;
+      int page = !FOUR && j0 < j1 ? page_of(j0) : 0;
       for (int j = j0; j < j1; ++j, ++n_s) {
-        const uint32_t bad = __ballot_sync(0xffffffffu, !good);
-        if (j + 1 < j1) good = good_of(j + 1);
+        uint32_t bad = 0;
+        if constexpr (!FOUR) {
+          bad = __ballot_sync(0xffffffffu, page < 0 || page >= p.n_pages);
+          if (j + 1 < j1) page = page_of(j + 1);
+        }
         ok = wait_bar(s_full + 16 * t + 8 * (n_s & 1), (n_s >> 1) & 1, rp.wait_ns) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        if constexpr (FOUR) {
+          bad = *reinterpret_cast<const volatile uint32_t*>(s_bad[t][n_s & 7]);
+          if (bad) bad = (bad & 1) | (bad >> 7 & 2) | (bad >> 14 & 4) | (bad >> 21 & 8);
+        }
         if (warp_real) {
           const int hr = hi - kKeys * j, lr = lo - kKeys * j;
           softmax_tile<D, BF16>(
               tS + 64 * (n_s & 1), tO, hr > 0 && lr < kKeys, scale, m, l, j > j0,
               [&](uint32_t(&s)[2][32]) {
                 if (kKeys * (j + 1) > all_hi || kKeys * j < all_lo || bad) {
-                  const uint32_t hidden = small ? bad : (bad ? 15u : 0u);
+                  const uint32_t hidden = FOUR || small ? bad : (bad ? 15u : 0u);
 #pragma unroll
                   for (int c = 0; c < kKeys; ++c)
                     if (c >= hr || c < lr || ((hidden >> (c >> 4)) & 1u)) s[c >> 5][c & 31] = 0xFF800000u;   // -inf
