@@ -19,10 +19,8 @@
 namespace hsa {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kStep = 128;               // pieces are multiples of this many entries
-constexpr int kFlush = 128;              // entries of a lane between 64-bit sums: 128 low parts, of at most 2^22 for p and for q
+constexpr int kFlush = 128;              // entries of a lane between 64-bit sums, at most: low parts are 2^22 for p and for q
 
 __device__ __forceinline__ float value_of(float x) { return x; }
 __device__ __forceinline__ float value_of(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -40,20 +38,27 @@ __device__ __forceinline__ Fixed fixed_of(float x) {
   return {__float_as_int(a), __float_as_int(__fadd_rn(rest, kLo))};
 }
 constexpr Fixed kZero = {0x3F800000, 0x34400000};        // fixed_of(0): the bits of kHi and kLo
+// Two at a time, by the packed additions (which round like the single ones)
+__device__ __forceinline__ void fixed_of2(float x, float y, Fixed& f, Fixed& g) {
+  const uint64_t v = f2_pack(x, y), a = f2_add(v, f2_pack(kHi, kHi));
+  const uint64_t b = f2_add(f2_fma(f2_add(a, f2_pack(-kHi, -kHi)), f2_pack(-1.f, -1.f), v), f2_pack(kLo, kLo));
+  float lo, hi;
+  f2_unpack(a, lo, hi);
+  f.hi = __float_as_int(lo);
+  g.hi = __float_as_int(hi);
+  f2_unpack(b, lo, hi);
+  f.lo = __float_as_int(lo);
+  g.lo = __float_as_int(hi);
+}
 
-// What the next token is drawn from: entry v weighs p[v] - q[v] (q given), p[v] but for v = without, as far as above 0
-template <typename T>
+// What the next token is drawn from: entry v weighs p[v] - q[v] (Q), p[v] but for v = without (else), as far as above 0
+template <typename T, bool Q>
 struct Weights {
   const T* p;
   const T* q;
   int without;
-  // adds the weight of v, whose entries are a and b, in two parts
-  __device__ __forceinline__ void add(T a, T b, int v, int& hi, int& lo) const {
-    const float x = __saturatef(value_of(a));            // NaN: 0
-    const Fixed f = fixed_of(x);
-    if (q) {
-      const float y = __saturatef(value_of(b));
-      const Fixed g = fixed_of(y);
+  __device__ __forceinline__ void add(float x, Fixed f, float y, Fixed g, int v, int& hi, int& lo) const {
+    if constexpr (Q) {
       if (x > y) {
         hi += f.hi - g.hi;
         lo += f.lo - g.lo;
@@ -63,9 +68,24 @@ struct Weights {
       lo += f.lo - kZero.lo;
     }
   }
+  // adds the weight of v, whose entries are a and b, in two parts
+  __device__ __forceinline__ void add(T a, T b, int v, int& hi, int& lo) const {
+    const float x = __saturatef(value_of(a)), y = Q ? __saturatef(value_of(b)) : 0.f;          // NaN: 0
+    add(x, fixed_of(x), y, Q ? fixed_of(y) : kZero, v, hi, lo);
+  }
+  // the same for v and v + 1
+  __device__ __forceinline__ void add2(T a0, T a1, T b0, T b1, int v, int& hi, int& lo) const {
+    const float x0 = __saturatef(value_of(a0)), x1 = __saturatef(value_of(a1));
+    const float y0 = Q ? __saturatef(value_of(b0)) : 0.f, y1 = Q ? __saturatef(value_of(b1)) : 0.f;
+    Fixed f0, f1, g0 = kZero, g1 = kZero;
+    fixed_of2(x0, x1, f0, f1);
+    if constexpr (Q) fixed_of2(y0, y1, g0, g1);
+    add(x0, f0, y0, g0, v, hi, lo);
+    add(x1, f1, y1, g1, v + 1, hi, lo);
+  }
   __device__ __forceinline__ int64_t at(int v) const {
     int hi = 0, lo = 0;
-    add(p[v], q ? q[v] : p[v], v, hi, lo);
+    add(p[v], Q ? q[v] : p[v], v, hi, lo);
     return ((int64_t)hi << 23) + lo;
   }
 };
@@ -85,43 +105,57 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
   return x;
 }
 
-// The sum of the weights of [lo, hi), by a warp
-template <typename T, bool WIDE>
-__device__ __forceinline__ int64_t sum_piece(const Weights<T>& w, int lo, int hi, int lane) {
+// The sum of the weights of [lo, hi), by a warp. The loads of a batch go before anything that needs them.
+template <typename T, bool WIDE, bool Q>
+__device__ __forceinline__ int64_t sum_piece(const Weights<T, Q>& w, int lo, int hi, int lane) {
   int64_t sum = 0;
   if constexpr (WIDE) {                  // 16 bytes at a time; lo is a multiple of kStep
-    constexpr int kPer = 16 / sizeof(T), kTurn = kFlush / kPer;
+    constexpr int kPer = 16 / sizeof(T), kBatch = sizeof(T);             // 2 batches of 16-bit entries hold as many as 4 of fp32
+    static_assert(kPer * kBatch <= kFlush, "low parts");
     const int n = (hi - lo) / kPer;
     const uint4* p = reinterpret_cast<const uint4*>(w.p + lo);
-    const uint4* q = w.q ? reinterpret_cast<const uint4*>(w.q + lo) : nullptr;
-    for (int first = 0; first < n; first += 32 * kTurn) {
-      int h = 0, l = 0;
-      const int last = min(n, first + 32 * kTurn);
-#pragma unroll 4
-      for (int i = first + lane; i < last; i += 32) {
-        const uint4 a = __ldcg(p + i), b = q ? __ldcg(q + i) : a;
-        T x[kPer], y[kPer];
-        memcpy(x, &a, 16);
-        memcpy(y, &b, 16);
+    const uint4* q = reinterpret_cast<const uint4*>(w.q + lo);
+    for (int first = lane; first < n; first += 32 * kBatch) {
+      uint4 a[kBatch], b[kBatch];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) w.add(x[e], y[e], lo + i * kPer + e, h, l);
+      for (int i = 0; i < kBatch; ++i) {
+        const int k = first + 32 * i;
+        a[i] = k < n ? p[k] : make_uint4(0u, 0u, 0u, 0u);
+        b[i] = Q && k < n ? q[k] : make_uint4(0u, 0u, 0u, 0u);
+      }
+      int h = 0, l = 0;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        T x[kPer], y[kPer];
+        memcpy(x, &a[i], 16);
+        memcpy(y, &b[i], 16);
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) w.add2(x[e], x[e + 1], y[e], y[e + 1], lo + (first + 32 * i) * kPer + e, h, l);
       }
       sum += ((int64_t)h << 23) + l;
     }
     lo += n * kPer;
   }
-  for (int first = lo; first < hi; first += 32 * kFlush) {
+  constexpr int kBatch = 16;
+  for (int first = lo + lane; first < hi; first += 32 * kBatch) {
+    T x[kBatch], y[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int v = first + 32 * i;
+      x[i] = v < hi ? w.p[v] : T(0.f);
+      y[i] = Q && v < hi ? w.q[v] : T(0.f);
+    }
     int h = 0, l = 0;
-    const int last = min(hi, first + 32 * kFlush);
-#pragma unroll 8
-    for (int v = first + lane; v < last; v += 32) w.add(w.p[v], w.q ? w.q[v] : w.p[v], v, h, l);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) w.add(x[i], y[i], first + 32 * i, h, l);
     sum += ((int64_t)h << 23) + l;
   }
   return warp_sum(sum);
 }
 
-template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kThreads) draft_verify_kernel(const __grid_constant__ VerifyParams vp) {
+template <typename T, bool WIDE, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) draft_verify_kernel(const __grid_constant__ VerifyParams vp) {
+  constexpr int kWarps = kThreads / 32;
   const hsa_verify_args& p = vp.a;
   __shared__ int s_kept, s_without;
   __shared__ int64_t s_piece[kWarps], s_scan[kWarps];    // sums of the warps' pieces; of the warps' parts of one piece
@@ -130,7 +164,15 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const __grid_con
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas, most = p.nq - 1;
+  // everything that depends on nothing is asked for at once
   const int n = p.n_draft ? p.n_draft[b] : most;
+  const float u_sample = p.u_sample[b];
+  int x = -1;
+  float u = 0.f;
+  if (warp == 0 && lane < most) {
+    x = p.drafted[(int64_t)b * most + lane];
+    u = p.u_accept[(int64_t)b * most + lane];
+  }
   if (n < 0 || n > most) {               // the same in every CTA of the cluster
     if (n != -1 && rank == 0 && tid == 0) flag_status(vp.status, HSA_FLAG_INDEX_RANGE);
     return;
@@ -139,18 +181,11 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const __grid_con
   const T* rows_q = p.q ? static_cast<const T*>(p.q) + (int64_t)b * most * p.q_stride : nullptr;
   // ---------------------------------------------------------------- how many stay
   if (warp == 0) {
-    bool turned = false, known = true;
-    int x = -1;
-    if (lane < n) {
-      x = p.drafted[(int64_t)b * most + lane];
-      const float u = p.u_accept[(int64_t)b * most + lane];
-      known = x >= 0 && x < p.vocabulary;
-      turned = true;
-      if (known) {
-        const float px = __saturatef(value_of(rows_p[lane * p.p_stride + x]));
-        const float qx = rows_q ? __saturatef(value_of(rows_q[lane * p.q_stride + x])) : 1.f;
-        turned = !((double)u * (double)qx < (double)px);
-      }
+    const bool known = lane >= n || (x >= 0 && x < p.vocabulary);
+    bool turned = lane < n;
+    if (lane < n && known) {
+      const T tp = rows_p[lane * p.p_stride + x], tq = rows_q ? rows_q[lane * p.q_stride + x] : T(1.f);
+      turned = !((double)u * (double)__saturatef(value_of(tq)) < (double)__saturatef(value_of(tp)));
     }
     const uint32_t all = __ballot_sync(0xffffffffu, turned);
     const int kept = all ? __ffs(all) - 1 : n;
@@ -167,43 +202,37 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const __grid_con
   }
   __syncthreads();
   const int kept = s_kept;
-  Weights<T> w{rows_p + kept * p.p_stride, rows_q && kept < n ? rows_q + kept * p.q_stride : nullptr, s_without};
+  const T* row_p = rows_p + kept * p.p_stride;
   const int per = ((p.vocabulary + ctas * kWarps - 1) / (ctas * kWarps) + kStep - 1) / kStep * kStep;
   auto begin_of = [&](int piece) { return min(p.vocabulary, (rank * kWarps + piece) * per); };
 
-  // ---------------------------------------------------------------- the sums: of pieces, shares, the row
-  uint64_t before = 0, total = 0;        // of the CTAs before this one, of all
-  for (int turn = 0;; ++turn) {
+  // The sums, of pieces, shares and the row, then the piece and the entry that pass the border; false if the row weighs nothing
+  bool waiting = false;                  // the others may still read this CTA's sum
+  auto sample = [&](auto w) -> bool {
     const int64_t sum = sum_piece<T, WIDE>(w, begin_of(warp), begin_of(warp + 1), lane);
+    if (waiting) cluster_wait();
+    __syncthreads();                     // s_piece of an earlier turn has been read
     if (lane == 0) s_piece[warp] = sum;
     __syncthreads();
-    uint64_t mine = 0;
+    uint64_t before = 0, total = 0;      // of the CTAs before this one, of all
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) mine += (uint64_t)s_piece[i];
+    for (int i = 0; i < kWarps; ++i) total += (uint64_t)s_piece[i];
     if (ctas > 1) {
-      if (tid == 0) s_cta = mine;
+      if (tid == 0) s_cta = total;
       __syncthreads();
       cluster_sync_all();
-      before = total = 0;
+      total = 0;
       for (int c = 0; c < ctas; ++c) {
-        const uint64_t x = ld_cluster_u64(cluster_map(smem_u32(&s_cta), c));
-        if (c < rank) before += x;
-        total += x;
+        const uint64_t y = ld_cluster_u64(cluster_map(smem_u32(&s_cta), c));
+        if (c < rank) before += y;
+        total += y;
       }
       __syncwarp();
-      cluster_arrive();                  // waited for below: until then the others may read this CTA's sum
-    } else {
-      total = mine;
+      cluster_arrive();
+      waiting = true;
     }
-    if (total || turn) break;
-    w.q = nullptr;                       // nothing is left of p: p itself
-    w.without = -1;
-    if (ctas > 1) cluster_wait();
-    __syncthreads();
-  }
-  // ---------------------------------------------------------------- the piece and the entry that pass the border
-  if (total) {
-    const uint32_t bits = __float_as_uint(fminf(fmaxf(p.u_sample[b], 0.f), 0x1.fffffep-1f));   // NaN: 0
+    if (!total) return false;
+    const uint32_t bits = __float_as_uint(fminf(fmaxf(u_sample, 0.f), 0x1.fffffep-1f));        // NaN: 0
     const int left = (int)(bits >> 23) - 86;             // 2^(e - 150) in units of 2^-64
     const uint64_t m = (bits & 0x7FFFFFu) | 0x800000u;
     const uint64_t border = __umul64hi(total, left >= 0 ? m << left : left > -24 ? m >> -left : 0ull);
@@ -222,6 +251,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const __grid_con
       const int lo = begin_of(piece), hi = begin_of(piece + 1), each = (per + kThreads - 1) / kThreads;
       const int v0 = min(hi, lo + tid * each), v1 = min(hi, v0 + each);
       int64_t own = 0;
+#pragma unroll 4
       for (int v = v0; v < v1; ++v) own += w.at(v);
       const int64_t upto = warp_scan(own, lane);
       if (lane == 31) s_scan[warp] = upto;
@@ -238,20 +268,28 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const __grid_con
         }
       }
     }
-  } else if (rank == 0 && tid == 0) {
+    return true;
+  };
+  bool found;
+  if (rows_q && kept < n)
+    found = sample(Weights<T, true>{row_p, rows_q + kept * p.q_stride, -1});
+  else
+    found = sample(Weights<T, false>{row_p, nullptr, s_without});
+  if (!found && kept < n) found = sample(Weights<T, false>{row_p, nullptr, -1});   // nothing is left of p: p itself
+  if (!found && rank == 0 && tid == 0) {
     p.tokens[(int64_t)b * p.nq + kept] = -1;
     flag_status(vp.status, HSA_FLAG_NO_WEIGHT);
   }
   __syncwarp();
-  if (ctas > 1) cluster_wait();
+  if (waiting) cluster_wait();
 }
 
-template <typename T>
+template <typename T, int THREADS>
 cudaError_t launch(const VerifyParams& p, cudaStream_t s) {
-  auto kernel = p.wide ? draft_verify_kernel<T, true> : draft_verify_kernel<T, false>;
+  auto kernel = p.wide ? draft_verify_kernel<T, true, THREADS> : draft_verify_kernel<T, false, THREADS>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.a.batch * p.ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -263,6 +301,10 @@ cudaError_t launch(const VerifyParams& p, cudaStream_t s) {
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
+template <typename T>
+cudaError_t launch(const VerifyParams& p, bool few, cudaStream_t s) {
+  return few ? launch<T, 512>(p, s) : launch<T, 256>(p, s);
+}
 
 }  // namespace
 
@@ -270,16 +312,19 @@ cudaError_t launch_draft_verify(const hsa_verify_args& a, uint32_t* status, cuda
   VerifyParams p;
   p.a = a;
   p.status = status;
-  // as many CTAs to a request as give every SM two, while each has 2,048 entries
+  // Clusters of 8 CTAs as long as every SM has a CTA at most, of 512 threads; else CTAs of 256, as many as run at a time, four to
+  // an SM, while each has 2,048 entries. 1 and 8 requests of 131,072 entries: 6.2 and 7.3 us, with 256 threads 7.3 and 9.4; 64: 22
+  // and 16.2
+  const bool few = (int64_t)a.batch * 8 <= kSms;
   p.ctas = 1;
-  while (p.ctas < 8 && (int64_t)p.ctas * a.batch < 2 * kSms && a.vocabulary / p.ctas > 2048) p.ctas *= 2;
+  while (p.ctas < 8 && (int64_t)2 * p.ctas * a.batch <= 4 * kSms && a.vocabulary / p.ctas > 2048) p.ctas *= 2;
   const int size = a.dtype == HSA_F32 ? 4 : 2;
   p.wide = ((reinterpret_cast<uintptr_t>(a.p) | reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.p_stride * size) |
              (uintptr_t)(a.q ? a.q_stride * size : 0)) & 15) == 0;
   switch (a.dtype) {
-    case HSA_F32: return launch<float>(p, s);
-    case HSA_BF16: return launch<__nv_bfloat16>(p, s);
-    default: return launch<__half>(p, s);
+    case HSA_F32: return launch<float>(p, few, s);
+    case HSA_BF16: return launch<__nv_bfloat16>(p, few, s);
+    default: return launch<__half>(p, few, s);
   }
 }
 

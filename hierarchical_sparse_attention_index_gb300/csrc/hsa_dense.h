@@ -88,6 +88,7 @@ struct PagedAttnParams {
 };
 cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedSplit& sp, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns,
                               cudaStream_t s);
+constexpr int32_t kPagedTcRows = 24;     // pages of 16 or 4 bits: more query rows than this take the tcgen05 kernel
 // 4-bit pages: CTAs that an SM holds, for nt tiles of 8 query rows, as registers allow without spilling
 constexpr int four_ctas(int nt, int head_dim) { return nt == 1 && head_dim == 64 ? 4 : nt <= 2 ? 3 : 2; }
 cudaError_t launch_paged_four(const PagedAttnParams& p, int32_t head_dim, cudaStream_t s);

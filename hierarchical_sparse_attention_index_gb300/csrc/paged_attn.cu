@@ -34,8 +34,6 @@ namespace {
 constexpr int kWarps = kPagedWarps;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroup = kPagedGroup;       // keys per stage of a warp
-constexpr int32_t kTcRowsFour = 16;      // of 4-bit pages
-constexpr int32_t kTcRows = 24;          // 16-bit pages: more query rows than this take the tcgen05 kernel
 
 enum KvType { kBf16 = HSA_BF16, kF16 = HSA_F16, kE4M3 = HSA_E4M3 };
 
@@ -460,7 +458,7 @@ cudaError_t launch_nt(const PagedAttnParams& p, cudaStream_t s) {
     case 2: return p.cluster ? launch<D, KV, 2, true>(p, s) : launch<D, KV, 2, false>(p, s);
     case 3: return p.cluster ? launch<D, KV, 3, true>(p, s) : launch<D, KV, 3, false>(p, s);
   }
-  static_assert(kTcRows <= 3 * 8, "four tiles only for E4M3");
+  static_assert(kPagedTcRows <= 3 * 8, "four tiles only for E4M3");
   if constexpr (KV == kE4M3)
     return p.cluster ? launch<D, KV, 4, true>(p, s) : launch<D, KV, 4, false>(p, s);
   else
@@ -517,7 +515,7 @@ static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
 }
 
 // Which kernel, query rows per CTA and splits of the length.
-// 16-bit pages and more than kTcRows query rows take the tcgen05 kernel, up to 128 rows (whole queries) to a CTA. There and
+// 16-bit pages and more than kPagedTcRows query rows take the tcgen05 kernel, up to 128 rows (whole queries) to a CTA. There and
 // in the warp MMA kernel, 64 requests x 4 heads of 128 dims, of 1 .. 8,192 keys: 32 rows 105 and 164 us, 24 rows 104 and 124;
 // 1,000 keys: 33.3 and 33.1, 33.5 and 28.6; 1 request x 8 heads x 1,000 keys: 13.0 and 12.4, 13.0 and 9.9; 16 x 8 x 8,192 keys of 64
 // dims: 28 rows 59.7 and 55.1, 18 rows 59.8 and 47.7. Else up to 32 rows one CTA reads its keys once for all of them; more rows
@@ -545,7 +543,7 @@ static bool rounds_of(const PagedSplit& s, int32_t head_dim, int32_t kv_dtype, R
 PagedSplit paged_split(int32_t batch, int32_t heads, int32_t head_dim, int32_t group, int32_t nq, int64_t max_vis, int32_t window, int32_t kv_dtype) {
   PagedSplit s;
   const int32_t rows = nq * group;
-  s.tc = kv_dtype != HSA_E4M3 && rows > (kv_dtype == HSA_E2M1 ? kTcRowsFour : kTcRows);
+  s.tc = kv_dtype != HSA_E4M3 && rows > kPagedTcRows;
   if (s.tc) {
     const int32_t queries = nq < 128 / group ? nq : 128 / group;
     s.chunks = (nq + queries - 1) / queries;

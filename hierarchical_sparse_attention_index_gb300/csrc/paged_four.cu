@@ -427,8 +427,8 @@ cudaError_t launch_nt(const PagedAttnParams& p, cudaStream_t s) {
     case 1: return p.cluster ? launch<D, 1, true>(p, s) : launch<D, 1, false>(p, s);
     case 2: return p.cluster ? launch<D, 2, true>(p, s) : launch<D, 2, false>(p, s);
     case 3: return p.cluster ? launch<D, 3, true>(p, s) : launch<D, 3, false>(p, s);
-    case 4: return p.cluster ? launch<D, 4, true>(p, s) : launch<D, 4, false>(p, s);
   }
+  static_assert(kPagedTcRows <= 3 * 8, "no more tiles");
   return cudaErrorInvalidValue;
 }
 
