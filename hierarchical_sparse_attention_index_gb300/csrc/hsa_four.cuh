@@ -24,11 +24,16 @@ __device__ __forceinline__ uint32_t four_scale_for(float amax) {
   return byte;
 }
 
-// Eight values -> four bytes of E2M1 codes of x / s (nearest even, saturating), -0 as 0
+// Eight values -> four bytes of E2M1 codes of x / s (nearest even, saturating), -0 as 0. |x| <= 7 s, s > 0. The quotient is x r
+// with r = 1 / s, plus the exact remainder's part (P. Markstein, 1990), so that one that lies between two codes stays there
 __device__ __forceinline__ uint32_t four_codes(const float (&x)[8], float s) {
+  const float r = 1.f / s;
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w |= (f32x2_to_e2m1x2(x[2 * i + 1] / s, x[2 * i] / s) & 0xFFu) << (8 * i);
+  for (int i = 0; i < 4; ++i) {
+    const float a = x[2 * i] * r, b = x[2 * i + 1] * r;
+    w |= (f32x2_to_e2m1x2(fmaf(fmaf(-b, s, x[2 * i + 1]), r, b), fmaf(fmaf(-a, s, x[2 * i]), r, a)) & 0xFFu) << (8 * i);
+  }
   const uint32_t m = w & 0x77777777u;    // a sign stays where the magnitude is not 0: then, and only then, m + 7 carries into it
   return w & (0x77777777u | ((m + 0x77777777u) & 0x88888888u));
 }

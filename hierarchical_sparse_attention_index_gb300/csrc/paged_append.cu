@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
   constexpr int kRowBytes = D / 2 + 8;   // of a staged 4-bit row: codes, scales
   __shared__ RowSlots s_rows;
   __shared__ uint64_t s_turns[kMaxPairs];
-  __shared__ float2 s_cs[kMaxRows * kMaxPairs];          // (cos, sin) of row r, pair i at r * pairs + i
+  __shared__ __align__(16) float2 s_cs[kMaxRows * kMaxPairs];            // (cos, sin) of row r's pairs, from r * pairs on (pair_at)
   __shared__ __align__(16) uint8_t s_four[kFour ? kThreads / kPer * kRowBytes : 16];
   griddep_wait();
   griddep_launch_dependents();
@@ -80,24 +80,38 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
   const int n_rows = (int)imin64(p.w.rows_per_block, p.w.n_tokens - t0);
   const int units = n_rows * nh * kPer;
   const int pairs = p.rotary / 2, turned = p.rotary / 16, at0 = p.rotary_at / 8;   // units that rotate, first piece of them
+  // Pair i's place: two neighbouring pairs are 16 bytes, which the threads of a head read side by side. A piece has 8 pairs, halves
+  // sharing them, or 4
+  const bool halves = p.pairs == HSA_ROPE_HALVES;
+  const int piece_pairs = halves ? 8 : 4, lines = pairs / piece_pairs;
+  auto pair_at = [&](int i) { return 2 * ((i % piece_pairs >> 1) * lines + i / piece_pairs) + (i & 1); };
+  // a thread's next unit is kThreads further: no division on the way
+  int e = tid, row_at = tid / kPer / nh, head_at = tid / kPer % nh;
+  const int row_step = kThreads / kPer / nh, head_step = kThreads / kPer % nh, u = tid % kPer;
 
+  const int after = u - turned, half = kPer - turned;    // of the pieces that do not turn, which go around the others
+  const int ca = after < 0 ? at0 + u : (after < at0 ? after : after + 2 * turned);
+  const int cb = after < 0 ? at0 + u + turned : (after + half < at0 ? after + half : after + half + 2 * turned);
   for (int base = 0; base < units; base += kThreads * kUnits) {
     uint4 x[kUnits][2];
-    int row[kUnits], head[kUnits], ca[kUnits], cb[kUnits];
+    int row[kUnits], head[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int e = base + i * kThreads + tid, u = e % kPer;
-      row[i] = e < units ? e / kPer / nh : -1;
-      head[i] = h0 + e / kPer % nh;
-      const int v = u - turned, half = kPer - turned;    // of the pieces that do not turn, which go around the others
-      ca[i] = v < 0 ? at0 + u : (v < at0 ? v : v + 2 * turned);
-      cb[i] = v < 0 ? at0 + u + turned : (v + half < at0 ? v + half : v + half + 2 * turned);
+      row[i] = e < units ? row_at : -1;
+      head[i] = h0 + head_at;
+      e += kThreads;
+      row_at += row_step;
+      head_at += head_step;
+      if (head_at >= nh) {
+        head_at -= nh;
+        ++row_at;
+      }
       if (row[i] >= 0) {
         const int64_t t = t0 + row[i];
         const int hk = head[i] - p.heads_q, hv = hk - p.w.heads;
         const uint16_t* src = hk < 0 ? p.q + t * p.q_stride + head[i] * D : hv < 0 ? p.w.k + t * p.w.k_stride + hk * D : p.w.v + t * p.w.v_stride + hv * D;
-        x[i][0] = *reinterpret_cast<const uint4*>(src + 8 * ca[i]);
-        x[i][1] = *reinterpret_cast<const uint4*>(src + 8 * cb[i]);
+        x[i][0] = *reinterpret_cast<const uint4*>(src + 8 * ca);
+        x[i][1] = *reinterpret_cast<const uint4*>(src + 8 * cb);
       } else {
         x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
       }
@@ -105,34 +119,44 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
     if (base == 0) {
       if (tid < pairs) s_turns[tid] = turns_of(p.inv_freq[tid]);
       find_slots(p.w, t0, n_rows, s_rows, h0 == 0 ? HSA_FLAG_WRITE_RANGE : 0u);
-      for (int e = tid; e < n_rows * pairs; e += kThreads) s_cs[e] = cos_sin(s_rows.pos[e / pairs], s_turns[e % pairs]);
+      for (int k = tid; k < n_rows * pairs; k += kThreads) {
+        const int r = k / pairs, i = k - r * pairs;
+        s_cs[r * pairs + pair_at(i)] = cos_sin(s_rows.pos[r], s_turns[i]);
+      }
       __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int r = max(row[i], 0), hk = head[i] - p.heads_q, hv = hk - p.w.heads, u = (base + i * kThreads + tid) % kPer;
+      const int r = max(row[i], 0), hk = head[i] - p.heads_q, hv = hk - p.w.heads;
       float a[8], b[8];
       widen<BF16>(x[i][0], a);
       widen<BF16>(x[i][1], b);
       if (u < turned && hv < 0) {
-        const float2* cs = s_cs + r * pairs;
-        if (p.pairs == HSA_ROPE_HALVES) {
+        const float4* cs = reinterpret_cast<const float4*>(s_cs + r * pairs) + u;      // (cos, sin) of two pairs
+        if (halves) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 y = cs[8 * u + j];
-            const float m = a[j], n = b[j];
-            a[j] = fmaf(m, y.x, -(n * y.y));
-            b[j] = fmaf(m, y.y, n * y.x);
+          for (int j = 0; j < 4; ++j) {
+            const float4 y = cs[j * lines];
+            const float m = a[2 * j], n = b[2 * j], o = a[2 * j + 1], q = b[2 * j + 1];
+            a[2 * j] = fmaf(m, y.x, -(n * y.y));
+            b[2 * j] = fmaf(m, y.y, n * y.x);
+            a[2 * j + 1] = fmaf(o, y.z, -(q * y.w));
+            b[2 * j + 1] = fmaf(o, y.w, q * y.z);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 y = cs[4 * u + j], z = cs[4 * (u + turned) + j];
-            const float m = a[2 * j], n = a[2 * j + 1], o = b[2 * j], q = b[2 * j + 1];
-            a[2 * j] = fmaf(m, y.x, -(n * y.y));
-            a[2 * j + 1] = fmaf(m, y.y, n * y.x);
-            b[2 * j] = fmaf(o, z.x, -(q * z.y));
-            b[2 * j + 1] = fmaf(o, z.y, q * z.x);
+          for (int j = 0; j < 2; ++j) {
+            const float4 y = cs[j * lines], z = cs[j * lines + turned];
+            const float m = a[4 * j], n = a[4 * j + 1], o = a[4 * j + 2], q = a[4 * j + 3];
+            a[4 * j] = fmaf(m, y.x, -(n * y.y));
+            a[4 * j + 1] = fmaf(m, y.y, n * y.x);
+            a[4 * j + 2] = fmaf(o, y.z, -(q * y.w));
+            a[4 * j + 3] = fmaf(o, y.w, q * y.z);
+            const float m2 = b[4 * j], n2 = b[4 * j + 1], o2 = b[4 * j + 2], q2 = b[4 * j + 3];
+            b[4 * j] = fmaf(m2, z.x, -(n2 * z.y));
+            b[4 * j + 1] = fmaf(m2, z.y, n2 * z.x);
+            b[4 * j + 2] = fmaf(o2, z.z, -(q2 * z.w));
+            b[4 * j + 3] = fmaf(o2, z.w, q2 * z.z);
           }
         }
         x[i][0] = narrow<BF16>(a);
@@ -142,19 +166,19 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
       if (hk < 0) {
         if (row[i] >= 0 && s_rows.real[r]) {
           uint16_t* dst = p.q_out + (t0 + r) * p.out_stride + head[i] * D;
-          *reinterpret_cast<uint4*>(dst + 8 * ca[i]) = x[i][0];
-          *reinterpret_cast<uint4*>(dst + 8 * cb[i]) = x[i][1];
+          *reinterpret_cast<uint4*>(dst + 8 * ca) = x[i][0];
+          *reinterpret_cast<uint4*>(dst + 8 * cb) = x[i][1];
         }
       } else if (!kFour && slot >= 0) {
         const int64_t at = slot + (int64_t)(hv < 0 ? hk : hv) * p.w.page_size;         // row of the pool
         uint8_t* pool = hv < 0 ? p.w.k_pool : p.w.v_pool;
         if constexpr (KV == HSA_E4M3) {
           const float inv = hv < 0 ? p.w.k_inv : p.w.v_inv;
-          *reinterpret_cast<uint2*>(pool + at * D + 8 * ca[i]) = e4m3x8(a, inv);
-          *reinterpret_cast<uint2*>(pool + at * D + 8 * cb[i]) = e4m3x8(b, inv);
+          *reinterpret_cast<uint2*>(pool + at * D + 8 * ca) = e4m3x8(a, inv);
+          *reinterpret_cast<uint2*>(pool + at * D + 8 * cb) = e4m3x8(b, inv);
         } else {
-          *reinterpret_cast<uint4*>(pool + (at * D + 8 * ca[i]) * 2) = x[i][0];
-          *reinterpret_cast<uint4*>(pool + (at * D + 8 * cb[i]) * 2) = x[i][1];
+          *reinterpret_cast<uint4*>(pool + (at * D + 8 * ca) * 2) = x[i][0];
+          *reinterpret_cast<uint4*>(pool + (at * D + 8 * cb) * 2) = x[i][1];
         }
       }
       if constexpr (kFour) {
@@ -175,7 +199,10 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
           const float other = __shfl_xor_sync(0xffffffffu, amax, 1);
           const bool none = amax != amax || other != other;
           const uint32_t byte = none ? 0x7Fu : four_scale_for(fmaxf(amax, other));
-          const int c = o ? cb[i] : ca[i];
+          const int c = o ? cb : ca;
+          if (byte == 0x7Eu)             // the largest scale may be too small
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = fminf(fmaxf(y[j], -3136.f), 3136.f);
           const uint32_t w = none ? 0u : four_codes(y, e4m3_to_f32(byte));
           if (hv < 0) {
             *reinterpret_cast<uint16_t*>(mine + four_k_at<D>(c, 0)) = (uint16_t)w;
@@ -290,8 +317,8 @@ template <int D, int KV, bool BF16>
 cudaError_t append(PagedAppendParams p, cudaStream_t s) {
   constexpr int kPer = D / 16;
   const int64_t heads = (int64_t)p.heads_q + 2 * p.w.heads, row = heads * kPer;        // units per token
-  // whole rows, about four units to a thread; fewer rows, then slices of a row's heads, while there are SMs without a block
-  const int64_t most = imin64(kMaxRows, imax64(1, 4 * kThreads / row));
+  // whole rows, about eight units to a thread; fewer rows, then slices of a row's heads, while there are SMs without a block
+  const int64_t most = imin64(kMaxRows, imax64(1, 8 * kThreads / row));
   p.w.rows_per_block = (int32_t)imax64(1, imin64(most, (p.w.n_tokens + 2 * kSms - 1) / (2 * kSms)));
   const int64_t blocks = (p.w.n_tokens + p.w.rows_per_block - 1) / p.w.rows_per_block;
   int64_t slices = imin64((2 * kSms + blocks - 1) / blocks, (row + kThreads - 1) / kThreads);
