@@ -156,3 +156,13 @@ def test_plain_forms():
             four.check_group(b, s, x[:, :dim], torch.zeros_like(x[:, :dim]), keys)
     assert four.scale_of(torch.tensor([0.0, 6 * 2.0 ** -9, 6 * 2.0 ** -9 + 1e-9, 6.0, 1e9])).tolist() == [1, 1, 2, 0x38, 0x7E]
     assert four.code_of(torch.tensor([0.25, 0.75, 2.5, -3.5, 5.0, 5.1, -9.0])).tolist() == [0, 2, 4, -6, 6, 7, -7]
+
+
+def test_records_as_bytes(H):  # noqa: F811
+    """The records that the binding writes as bytes are those of the structures, field by field."""
+    for layout, record in ((H._APPEND_ARGS, H.hsa_append_args), (H._VERIFY_ARGS, H.hsa_verify_args)):
+        values = [100 + i for i in range(len(record._fields_))]
+        raw = layout.pack(*values)
+        assert len(raw) == ctypes.sizeof(record)
+        r = record.from_buffer_copy(raw)
+        assert [getattr(r, name) for name, _ in record._fields_] == values
