@@ -66,25 +66,32 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
   }
 }
 
-// Where 16 keys from position pos on lie: the piece of the pools in units of 16 rows, times 2^16, plus a bit for each row
-// that some query sees; 0 for a bad page or no such row. page_pieces: heads x 16-row pieces of a page
-__device__ __forceinline__ int64_t find_piece(const PagedAttnParams& p, const Span& sp, int b, int h, int64_t page_pieces, int pos) {
-  const int pg = pos / p.page_size;
+// Where 16 keys from position pos on lie, in page number pg of request b, which is `page`: the piece of the pools in units of 16
+// rows, times 2^16, plus a bit for each row that some query sees; 0 for a bad page or no such row. page_pieces: heads x 16-row
+// pieces of a page
+__device__ __forceinline__ int64_t piece_at(const PagedAttnParams& p, const Span& sp, int b, int h, int64_t page_pieces, int pos, int pg, int page) {
   const uint32_t seen = seen32(p, b, sp.lo, sp.hi, sp.gaps, pos) & 0xFFFFu;
   if (!seen) return 0;
-  const int page = p.table[(int64_t)b * p.max_pages + pg];
   if (page < 0 || page >= p.n_pages) {
     flag_status(p.status, HSA_FLAG_INDEX_RANGE);
     return 0;
   }
   return ((page * page_pieces + (h * p.page_size + pos - pg * p.page_size) / kPagedGroup) << 16) | seen;
 }
+__device__ __forceinline__ int64_t find_piece(const PagedAttnParams& p, const Span& sp, int b, int h, int64_t page_pieces, int pos) {
+  const int pg = pos / p.page_size;
+  if (pos >= sp.hi) return 0;            // past the table, it may be
+  return piece_at(p, sp, b, h, page_pieces, pos, pg, p.table[(int64_t)b * p.max_pages + pg]);
+}
 
-// The keys [lo, hi) that row r of request b sees
-__device__ __forceinline__ int2 row_keys(const PagedAttnParams& p, int b, int r, bool flag) {
-  const int raw = p.vis[(int64_t)b * p.nq + r / p.group], hi = clamp_vis(p, raw);
+// The keys [lo, hi) that a query of length `raw` sees, and those of row r of request b
+__device__ __forceinline__ int2 keys_of(const PagedAttnParams& p, int raw, bool flag) {
+  const int hi = clamp_vis(p, raw);
   if (raw != hi && flag) flag_status(p.status, HSA_FLAG_INDEX_RANGE);
   return make_int2(p.window > 0 ? max(hi - p.window, 0) : 0, hi);
+}
+__device__ __forceinline__ int2 row_keys(const PagedAttnParams& p, int b, int r, bool flag) {
+  return keys_of(p, p.vis[(int64_t)b * p.nq + r / p.group], flag);
 }
 
 // bf16 queries against f16 keys: a thread's elements of a row, which LANES neighbouring lanes hold, to f16, after a power-of-two

@@ -80,10 +80,27 @@ __global__ void __launch_bounds__(kThreads, (Slot<D, NT>::kCtas)) paged_four_ker
   idx /= p.heads;
   const int b = idx % p.batch;
   if constexpr (!CLUSTER) split = idx / p.batch;
+  // Everything that depends on nothing but the block is asked for at once, before the first answer is needed: one wait on memory
+  // before the first copies, not four: the rows' queries and lengths, the request's
+  // lengths, and the pages of the warp's first pieces as they are unless a window or a length past max_vis moves them
+  const int row0 = chunk * p.chunk_rows, row_end = min(row0 + p.chunk_rows, p.nq * p.group);
+  uint2 qx[NT][kSteps];                  // k-step ks covers, of thread t, dims 16 ks + 4 t .. + 3
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = row0 + 8 * n + g;
+    const bool real = r < row_end;
+    const int qi = real ? r / p.group : 0, hq = h * p.group + (real ? r % p.group : 0);
+    const uint16_t* q = p.q + (((int64_t)b * p.nq + qi) * p.heads_q + hq) * D;
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) qx[n][ks] = real ? *reinterpret_cast<const uint2*>(q + 16 * ks + 4 * t) : make_uint2(0u, 0u);
+  }
+  const bool real_row = lane < kRows && row0 + lane < row_end;
+  const int raw_vis = real_row ? p.vis[(int64_t)b * p.nq + (row0 + lane) / p.group] : 0;
+  const int likely = split * p.split_len, likely_pg = (likely + kGroup * (warp + kWarps * lane)) / p.page_size;
+  const int likely_page = likely_pg < p.max_pages ? p.table[(int64_t)b * p.max_pages + likely_pg] : -1;
   const Span sp = request_span(p, b);
   if (!CLUSTER && split >= sp.used) return;
   const int begin = sp.base + split * sp.len, end = max(begin, min(begin + sp.len, sp.hi));   // keys of this CTA
-  const int row0 = chunk * p.chunk_rows, row_end = min(row0 + p.chunk_rows, p.nq * p.group);
 
   // ---------------------------------------------------------------- the ring: 16-key pieces of this warp, 64 keys apart
   const uint32_t ring = smem_u32(sm) + (uint32_t)warp * T::kWarpBytes, wide = ring + T::kSlots * T::kBytes;
@@ -91,12 +108,18 @@ __global__ void __launch_bounds__(kThreads, (Slot<D, NT>::kCtas)) paged_four_ker
   const int turns = (n_pieces + kP - 1) / kP;
   uint32_t bad = 0;                                      // bit i % 32: piece i is zeros
   const int64_t page_pieces = (int64_t)p.heads * (p.page_size / kGroup);
-  // where 32 pieces lie, one per lane, looked up a turn ahead of their use
-  auto find_pieces = [&](int of) -> int64_t {
+  // where 32 pieces lie, one per lane. Their pages are read a turn ahead of their use, and only read: looked at where they are
+  // read, they would hold up the warp for as long as the table takes to answer
+  auto page_of = [&](int of) {
     const int i = 32 * of + lane;
-    return i < n_pieces ? find_piece(p, sp, b, h, page_pieces, begin + kGroup * (warp + kWarps * i)) : 0;
+    return i < n_pieces ? p.table[(int64_t)b * p.max_pages + (begin + kGroup * (warp + kWarps * i)) / p.page_size] : -1;
   };
-  int64_t pieces = find_pieces(0), pieces_next = find_pieces(1);
+  auto pieces_of = [&](int of, int page) -> int64_t {
+    const int i = 32 * of + lane, pos = begin + kGroup * (warp + kWarps * i);
+    return i < n_pieces ? piece_at(p, sp, b, h, page_pieces, pos, pos / p.page_size, page) : 0;
+  };
+  int64_t pieces = pieces_of(0, begin == likely ? likely_page : page_of(0));
+  int next_page = page_of(1);
   // this lane's copies of a piece: 16 bytes of every 32 / kChunks-th row of K and of V, and one row's scales, of K or of V
   constexpr int kCopies = kGroup * T::kChunks / 32;
   const int r0 = lane / T::kChunks, c0 = lane % T::kChunks, rs = lane & 15;
@@ -105,13 +128,14 @@ __global__ void __launch_bounds__(kThreads, (Slot<D, NT>::kCtas)) paged_four_ker
   const uint8_t* const s_src = (lane < 16 ? p.k_s : p.v_s) + rs * T::kScaleRow;
   const uint32_t k_dst = T::k_at(r0, c0), v_dst = T::kHalf + T::v_at(r0, c0);
   const uint32_t s_dst = 2 * T::kHalf + (uint32_t)(lane < 16 ? four_place(rs) : kGroup + rs) * T::kScaleRow;
+  static_assert(T::kSlots - kP < 32, "the first copies are of the first 32 pieces");
   static_assert(kCopies == 1 || (T::k_at(8, 0) == 512 && T::v_at(8, 0) == 512), "rows 8 apart lie 512 bytes apart");
   const int issued = turns * kP;                         // the last turn's second piece may be none: zeros
   auto issue = [&](int i, uint32_t at) {                 // called with i = 0, 1, 2, ...; at: its slot
     const int64_t found = __shfl_sync(0xffffffffu, pieces, i & 31);
     if ((i & 31) == 31) {
-      pieces = pieces_next;
-      pieces_next = find_pieces((i >> 5) + 2);
+      pieces = pieces_of((i >> 5) + 1, next_page);
+      next_page = page_of((i >> 5) + 2);
     }
     if (i < issued) {
       const uint32_t seen = (uint32_t)found & 0xFFFFu;
@@ -148,10 +172,9 @@ __global__ void __launch_bounds__(kThreads, (Slot<D, NT>::kCtas)) paged_four_ker
   // ---------------------------------------------------------------- each row's keys, for masked pieces
   int all_lo = 0, all_hi = 0x7fffffff;                   // inside [all_lo, all_hi) no row masks anything
   if (lane < kRows) {
-    const int r = row0 + lane;
     int2 keys = make_int2(0, 0);
-    if (r < row_end) {
-      keys = row_keys(p, b, r, split == 0 && h == 0);
+    if (real_row) {
+      keys = keys_of(p, raw_vis, split == 0 && h == 0);
       all_lo = keys.x;
       all_hi = keys.y;
     }
@@ -164,24 +187,16 @@ __global__ void __launch_bounds__(kThreads, (Slot<D, NT>::kCtas)) paged_four_ker
   all_hi = __reduce_min_sync(0xffffffffu, all_hi);
 
   // ---------------------------------------------------------------- queries into B fragments
-  // k-step ks covers, of thread t, dims 16 ks + 4 t .. + 3
   uint32_t qb[NT][kSteps][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int r = row0 + 8 * n + g;
-    const bool real = r < row_end;
-    const int qi = real ? r / p.group : 0, hq = h * p.group + (real ? r % p.group : 0);
-    const uint16_t* q = p.q + (((int64_t)b * p.nq + qi) * p.heads_q + hq) * D;
-    uint2 x[kSteps];
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) x[ks] = real ? *reinterpret_cast<const uint2*>(q + 16 * ks + 4 * t) : make_uint2(0u, 0u);
     float sc = p.scale_log2;
-    if (p.q_bf16) queries_to_f16(x, sc);
+    if (p.q_bf16) queries_to_f16(qx[n], sc);
     if (warp == 0 && t == 0) s_scale[8 * n + g] = sc;
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks) {
-      qb[n][ks][0] = x[ks].x;
-      qb[n][ks][1] = x[ks].y;
+      qb[n][ks][0] = qx[n][ks].x;
+      qb[n][ks][1] = qx[n][ks].y;
     }
   }
   __syncthreads();                                       // s_lo, s_hi, s_scale

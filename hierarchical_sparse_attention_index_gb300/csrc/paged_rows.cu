@@ -323,19 +323,24 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
     // ---- the job whose pieces are being loaded: the one that is converted, or already the next
     int b = 0, h = 0, j0 = 0, n_load = 0, loads = 0;     // its tiles, and calls of load() for it
     Span sp = {};
-    int64_t pieces = 0, pieces_next = 0;
+    int64_t pieces = 0;                  // where 32 tiles' pieces lie, one per lane
+    int next_page = 0;                   // pages of the 32 after them, read and not yet looked at
     uint32_t load_slot = 0, gone = 0;    // slot that the next piece takes; bit s: the piece in slot s is on a bad page or seen by no query
-    auto find_pieces = [&](int of) -> int64_t {
-      const int i = 32 * of + lane;
-      return i < n_load ? find_piece(p, sp, b, h, page_pieces, kKeys * (j0 + i) + kPagedGroup * part) : 0;
+    auto page_of = [&](int of) {
+      const int i = 32 * of + lane, pos = kKeys * (j0 + i) + kPagedGroup * part;
+      return i < n_load && pos < sp.hi ? p.table[(int64_t)b * p.max_pages + pos / p.page_size] : -1;
+    };
+    auto pieces_of = [&](int of, int page) -> int64_t {
+      const int i = 32 * of + lane, pos = kKeys * (j0 + i) + kPagedGroup * part;
+      return i < n_load ? piece_at(p, sp, b, h, page_pieces, pos, pos / p.page_size, page) : 0;
     };
     // the next tile's piece; every call is one group of copies
     auto load = [&]() {
       if (loads < n_load) {
         const int64_t found = __shfl_sync(0xffffffffu, pieces, loads & 31);
         if ((loads & 31) == 31) {
-          pieces = pieces_next;
-          pieces_next = find_pieces((loads >> 5) + 2);
+          pieces = pieces_of((loads >> 5) + 1, next_page);
+          next_page = page_of((loads >> 5) + 2);
         }
         const uint32_t seen = (uint32_t)found & 0xFFFFu, at = raw + load_slot * L::kRawBytes;
         const uint64_t piece = (uint32_t)(found >> 16);
@@ -378,8 +383,8 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
       sp.gaps = job.gaps;
       free_job(it);
       loads = 0;
-      pieces = find_pieces(0);
-      pieces_next = find_pieces(1);
+      pieces = pieces_of(0, page_of(0));
+      next_page = page_of(1);
       constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;
       const int qs = it & 1, rows = p.nq * p.group;
       ok = wait_bar(q_empty + 8 * qs, ((it >> 1) & 1) ^ 1, rp.wait_ns) && ok;
