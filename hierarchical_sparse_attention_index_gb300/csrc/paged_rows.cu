@@ -48,10 +48,20 @@ struct Roles {                           // 16-bit pages: warps 10 and 11 load, 
 template <>
 struct Roles<true> {                     // 4-bit pages: warp 10 fills its group, 11 finds the work, 16..23 load and convert, four for each stream
   static constexpr int kFindWarp = 11, kThreads = 24 * 32, kJobReaders = kSoftWarps + 2 + 4 + 8, kFilled = 4;
-  static constexpr int kLaunchRegs = 80, kSoftRegs = 120, kIssueRegs = 40, kOutRegs = 56, kLastRegs = 72;
+  static constexpr int kLaunchRegs = 80, kSoftRegs = 112, kIssueRegs = 40, kOutRegs = 88, kLastRegs = 64;
   static_assert(2 * kSoftRegs + kIssueRegs + kOutRegs + 2 * kLastRegs <= 6 * kLaunchRegs, "setmaxnreg draws on the launch's registers");
 };
+// A warp group goes on with REGS registers per thread, of the LAUNCH that it was launched with
+template <int REGS, int LAUNCH>
+__device__ __forceinline__ void take_registers() {
+  static_assert(REGS % 8 == 0 && REGS >= 24 && REGS <= 256, "setmaxnreg");
+  if constexpr (REGS > LAUNCH)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
 constexpr int kConvertWarp = 16;
+constexpr uint32_t kSumRow = 80;         // bytes from lane to lane of 16 columns that a writing warp hands over (bank spread)
 constexpr uint32_t kBlockK = kKeys * 128;                // 64 dims of a tile of keys, 128 bytes a row
 constexpr int kJobSlots = 2;
 constexpr int kOrdered = 128;            // batches up to this can be worked off by length
@@ -63,7 +73,7 @@ struct Shape {
   // 1 .. 4,097 keys 61.3, 60.7, 61.7, 1 request x 131,072 53.6, 53.9, 55.7
   static constexpr int kMaxStages = D == 128 ? 5 : 10;
   // 4-bit pages: a converting warp's slots of a piece of 16 keys, K and V: codes, then scales
-  static constexpr int kRawSlots = 4, kRawBytes = 2 * kPagedGroup * (D / 2 + D / 16);
+  static constexpr int kRawSlots = 3, kRawBytes = 2 * kPagedGroup * (D / 2 + D / 16);
 };
 
 constexpr uint32_t smem_most(bool four) { return 227 * 1024 - (four ? 4608 : 4096); }      // but for what is declared in the kernel
@@ -76,6 +86,7 @@ struct RowsParams {
   int32_t q_rows;                        // rows of a query block in shared memory: tt x group, whole groups of 8
   int32_t stages;                        // of a stream's ring: what the queries leave room for
   int32_t ordered;                       // the longest requests come first
+  int32_t shift;                         // 4-bit pages: rows that the second stream's queries lie lower in the products, 64 or 0
   int32_t wide;                          // results start on 32-byte boundaries
   uint64_t wait_ns;
 };
@@ -105,22 +116,26 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
   __shared__ uint32_t s_tmem;
   __shared__ __align__(16) int s_len[kOrdered];          // requests' lengths
   __shared__ uint8_t s_order[kOrdered];                  // requests, the longest first
-  __shared__ __align__(8) uint64_t s_bars[23 + 2 * kJobSlots + 4 * L::kMaxStages];
+  __shared__ __align__(8) uint64_t s_bars[23 + 2 * kJobSlots + 4 * L::kMaxStages + 8];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   // Q of two jobs, then the rings. A product reads 128 rows from a query block's start: past its own rows it
   // reads on into what follows, and those rows of S are no one's.
   const uint32_t q_block = (uint32_t)rp.q_rows * 128u, q_bytes = (D / 64) * q_block;
-  const uint32_t sQ = base, sKv = base + 2 * q_bytes;
+  // (4-bit pages: the rings come first, so that products may start `shift` rows before a block.)
   const int stages = rp.stages;
-  const uint32_t sRaw = sKv + 2 * (uint32_t)stages * L::kKvBytes;        // 4-bit pages: pieces as they lie in the pools
+  const uint32_t rings = 2 * (uint32_t)stages * L::kKvBytes;
+  const uint32_t sQ = FOUR ? base + rings : base, sKv = FOUR ? base : base + 2 * q_bytes;
+  const uint32_t sRaw = sQ + 2 * q_bytes;                                // 4-bit pages: pieces as they lie in the pools, and
+  const uint32_t sSum = sRaw + 8 * L::kRawSlots * L::kRawBytes;          // what one writing warp hands to another
   // mbarriers: Q loaded / read by both streams' last products, for jobs in turn; for each stream O and (m, l)
   // read, every product done; two for each stream, for key tiles in turn: S computed, P written, P V added
   // to O. Then (m, l) written by each stream, the launcher's answer, the jobs and the rings
   const uint32_t bars = smem_u32(s_bars);
   const uint32_t q_full = bars, q_empty = bars + 16, o_empty = bars + 32, drain = bars + 48, s_full = bars + 64, p_full = bars + 96,
                  o_full = bars + 128, ml_full = bars + 160, answered = bars + 176, job_full = bars + 184, job_empty = job_full + 8 * kJobSlots,
-                 kv_full = job_empty + 8 * kJobSlots, kv_empty = kv_full + 16 * L::kMaxStages;
-  static_assert(184 + 16 * kJobSlots + 32 * L::kMaxStages <= sizeof(s_bars), "barriers");
+                 kv_full = job_empty + 8 * kJobSlots, kv_empty = kv_full + 16 * L::kMaxStages,
+                 sum_full = kv_empty + 16 * L::kMaxStages, sum_empty = sum_full + 32;
+  static_assert(184 + 16 * kJobSlots + 32 * L::kMaxStages + 64 <= sizeof(s_bars), "barriers");
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -146,6 +161,8 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
       mbar_init(kv_full + 8 * s, R::kFilled);
       mbar_init(kv_empty + 8 * s, 1);
     }
+    if constexpr (FOUR)
+      for (int s = 0; s < 8; ++s) mbar_init(sum_full + 8 * s, 1);
     fence_mbar_init();
   }
   tc_fence_before();
@@ -503,7 +520,7 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
   };
 
   if (warp >= kSoftWarps && warp < kOutWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kIssueRegs));
+    take_registers<R::kIssueRegs, R::kLaunchRegs>();
     if (FOUR && warp >= kLoadWarp) {
       if (warp == R::kFindWarp) find_work();
     } else if (warp >= kLoadWarp) {
@@ -611,7 +628,7 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
         }
       };
       auto qk = [&](int it) {
-        const uint64_t dq = sdesc(sQ + (it & 1) * q_bytes, 16u, 1024u);
+        const uint64_t dq = sdesc(sQ + (it & 1) * q_bytes - (FOUR && t ? rp.shift * 128u : 0u), 16u, 1024u);
         const uint64_t dk = sdesc(ring + c * L::kKvBytes, 16u, 1024u);
         const uint32_t at = tS + 64 * (n_s & 1);
 #pragma unroll
@@ -671,8 +688,8 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
     }
   } else if (warp < kSoftWarps) {
     // ---------------------------------------------------------------- softmax: one row per thread
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftRegs));
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    take_registers<R::kSoftRegs, R::kLaunchRegs>();
+    const int t = warp >> 2, r0 = (warp & 3) * 32 - (FOUR && t ? rp.shift : 0), r = r0 + lane;
     const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * t, tO = tS + 256u;
     float scale = p.scale_log2;
     const int rows = p.nq * p.group;
@@ -681,8 +698,8 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
       const Job& job = s_job[it % kJobSlots];
       const int j0 = t ? job.j0[1] : job.j0[0], j1 = t ? job.j1[1] : job.j1[0], b = job.b, job_hi = job.hi;
       const int row = job.chunk * rp.tt * p.group + r;
-      const bool real = r < rp.tt * p.group && row < rows;
-      const bool warp_real = (warp & 3) * 32 < rp.tt * p.group && job.chunk * rp.tt * p.group + (warp & 3) * 32 < rows;
+      const bool real = r >= 0 && r < rp.tt * p.group && row < rows;
+      const bool warp_real = r0 >= 0 && r0 < rp.tt * p.group && job.chunk * rp.tt * p.group + r0 < rows;
       int lo = 0, hi = 0;                // this row's keys
       if (real) {
         hi = clamp_vis(p, p.vis[(int64_t)b * p.nq + row / p.group]);
@@ -693,7 +710,7 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
         ok = wait_bar(q_full + 8 * (it & 1), (it >> 1) & 1, rp.wait_ns) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        scale = r < rp.q_rows ? p.scale_log2 * s_query[it & 1][r] : p.scale_log2;
+        scale = r >= 0 && r < rp.q_rows ? p.scale_log2 * s_query[it & 1][r] : p.scale_log2;
       }
       free_job(it);
       const bool small = p.page_size < kKeys || p.page_size % kKeys;   // a tile may lie on several pages
@@ -747,16 +764,18 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
       ok = wait_bar(o_empty + 8 * t, (it & 1) ^ 1, rp.wait_ns) && ok;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      s_ml[t][r] = make_float2(m == -INFINITY ? m : fmaf(m, scale, -kLift<BF16>), l);
+      if (!FOUR || r >= 0) s_ml[t][r] = make_float2(m == -INFINITY ? m : fmaf(m, scale, -kLift<BF16>), l);
       __syncwarp();
       if (lane == 0) mbar_arrive(ml_full + 8 * t);
     }
   } else if (warp < kOutWarp + 4) {
     // ---------------------------------------------------------------- both streams' O and (m, l), while the softmax is at the next job
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kOutRegs));
-    const int r = (warp & 3) * 32 + lane, rows = p.nq * p.group;
+    take_registers<R::kOutRegs, R::kLaunchRegs>();
+    // `apart`: the second stream's rows are 64 lower, so in the lanes of warps 2 and 3, which hand their part to warps 0 and 1
+    const bool apart = FOUR && rp.shift, hands = apart && (warp & 2);
+    const int r = (warp & 3) * 32 + lane - (hands ? 64 : 0), rows = p.nq * p.group;
     const uint32_t tO = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u;
-    int n_s[2] = {0, 0};                 // key tiles of either stream so far
+    int n_s[2] = {0, 0}, n_c = 0;        // key tiles of either stream so far; pieces handed over
     for (int it = 0; wait_job(it); ++it) {
       const Job& job = s_job[it % kJobSlots];
       const int tiles[2] = {job.j1[0] - job.j0[0], job.j1[1] - job.j0[1]};
@@ -791,18 +810,7 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
         done();
         continue;
       }
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t x[16], y[16];
-        if (tiles[0] > 0) TMEM_LD16(tO + 16 * c, x);
-        if (tiles[1] > 0) TMEM_LD16(tO + 128 + 16 * c, y);
-        tmem_wait_ld();
-        tmem_regs_ready(x);
-        tmem_regs_ready(y);
-        if (c == D / 16 - 1) done();
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          x[e] = __float_as_uint(((any_a ? fa * __uint_as_float(x[e]) : 0.f) + (any_b ? fb * __uint_as_float(y[e]) : 0.f)) * gain);
+      auto write = [&](int c, uint32_t (&x)[16]) {       // columns 16 c .. of this row
         // each lane writes its own row, 32 bytes at a time where the rows allow it
         if (whole)
 #pragma unroll
@@ -822,6 +830,57 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
               }
             }
         }
+      };
+      if (apart) {
+        const bool any = hands ? any_b : any_a;
+        const float f = hands ? fb : fa;
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c, ++n_c) {
+          uint32_t x[16];
+          if (tiles[hands ? 1 : 0] > 0) TMEM_LD16(tO + (hands ? 128 : 0) + 16 * c, x);
+          tmem_wait_ld();
+          tmem_regs_ready(x);
+          if (c == D / 16 - 1) done();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = any ? __float_as_uint(f * __uint_as_float(x[e])) : 0u;
+          const int turn = 2 * (warp & 1) + (n_c & 1);   // pair of warps, and its buffers in turn
+          const uint32_t mine = sSum + (uint32_t)(32 * turn + lane) * kSumRow;
+          ok = (hands ? wait_bar(sum_empty + 8 * turn, ((n_c >> 1) & 1) ^ 1, rp.wait_ns) : wait_bar(sum_full + 8 * turn, (n_c >> 1) & 1, rp.wait_ns)) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (hands) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) sts128(mine + 4 * e, x[e], x[e + 1], x[e + 2], x[e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const uint4 y = lds128(mine + 4 * e);
+              const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[e + k] = __float_as_uint((__uint_as_float(x[e + k]) + __uint_as_float(w[k])) * gain);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive((hands ? sum_full : sum_empty) + 8 * turn);
+          if (!hands) write(c, x);
+        }
+        if (!ok) break;
+        if (hands) continue;
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t x[16], y[16];
+          if (tiles[0] > 0) TMEM_LD16(tO + 16 * c, x);
+          if (tiles[1] > 0) TMEM_LD16(tO + 128 + 16 * c, y);
+          tmem_wait_ld();
+          tmem_regs_ready(x);
+          tmem_regs_ready(y);
+          if (c == D / 16 - 1) done();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            x[e] = __float_as_uint(((any_a ? fa * __uint_as_float(x[e]) : 0.f) + (any_b ? fb * __uint_as_float(y[e]) : 0.f)) * gain);
+          write(c, x);
+        }
       }
       if (real) {
         if (!whole)
@@ -831,7 +890,7 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kLastRegs));
+    take_registers<R::kLastRegs, R::kLaunchRegs>();
     if constexpr (FOUR)
       convert();
     else if (warp == R::kFindWarp)
@@ -851,7 +910,9 @@ cudaError_t launch(RowsParams& p, unsigned blocks, cudaStream_t s) {
   static const bool fits = launches_with(kernel, Roles<FOUR>::kLaunchRegs);
   if (!fits) return cudaErrorInvalidConfiguration;
   p.q_rows = (p.tt * p.a.group + 7) / 8 * 8;
-  const uint32_t raw = FOUR ? 8 * Shape<D>::kRawSlots * Shape<D>::kRawBytes : 0;
+  // Up to 64 rows lie in two warps' lanes. The second stream's lie 64 lower, in the others', whose schedulers have no softmax else
+  p.shift = FOUR && p.q_rows <= 64 ? 64 : 0;
+  const uint32_t raw = FOUR ? 8 * Shape<D>::kRawSlots * Shape<D>::kRawBytes + 4 * 32 * kSumRow : 0;
   const uint32_t room = smem_most(FOUR) - 1024 - raw - 2 * (D / 64) * (uint32_t)p.q_rows * 128u;
   p.stages = (int32_t)(room / (2 * Shape<D>::kKvBytes));
   if (p.stages > Shape<D>::kMaxStages) p.stages = Shape<D>::kMaxStages;
