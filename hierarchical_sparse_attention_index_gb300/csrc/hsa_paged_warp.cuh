@@ -66,22 +66,26 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
   }
 }
 
-// Where 16 keys from position pos on lie, in page number pg of request b, which is `page`: the piece of the pools in units of 16
-// rows, times 2^16, plus a bit for each row that some query sees; 0 for a bad page or no such row. page_pieces: heads x 16-row
-// pieces of a page
-__device__ __forceinline__ int64_t piece_at(const PagedAttnParams& p, const Span& sp, int b, int h, int64_t page_pieces, int pos, int pg, int page) {
+// Where 16 keys from position pos on lie: the piece of the pools in units of 16 rows, times 2^16, plus a bit for each row
+// that some query sees; 0 for a bad page or no such row. page_pieces: heads x 16-row pieces of a page; piece_at: where the page,
+// number pg of the request, is known to be `page`
+template <typename Page>
+__device__ __forceinline__ int64_t piece_in(const PagedAttnParams& p, const Span& sp, int b, int h, int64_t page_pieces, int pos, int pg, Page&& page_of) {
   const uint32_t seen = seen32(p, b, sp.lo, sp.hi, sp.gaps, pos) & 0xFFFFu;
   if (!seen) return 0;
+  const int page = page_of();
   if (page < 0 || page >= p.n_pages) {
     flag_status(p.status, HSA_FLAG_INDEX_RANGE);
     return 0;
   }
   return ((page * page_pieces + (h * p.page_size + pos - pg * p.page_size) / kPagedGroup) << 16) | seen;
 }
+__device__ __forceinline__ int64_t piece_at(const PagedAttnParams& p, const Span& sp, int b, int h, int64_t page_pieces, int pos, int pg, int page) {
+  return piece_in(p, sp, b, h, page_pieces, pos, pg, [&]() { return page; });
+}
 __device__ __forceinline__ int64_t find_piece(const PagedAttnParams& p, const Span& sp, int b, int h, int64_t page_pieces, int pos) {
   const int pg = pos / p.page_size;
-  if (pos >= sp.hi) return 0;            // past the table, it may be
-  return piece_at(p, sp, b, h, page_pieces, pos, pg, p.table[(int64_t)b * p.max_pages + pg]);
+  return piece_in(p, sp, b, h, page_pieces, pos, pg, [&]() { return p.table[(int64_t)b * p.max_pages + pg]; });
 }
 
 // The keys [lo, hi) that a query of length `raw` sees, and those of row r of request b
