@@ -24,15 +24,27 @@ __device__ __forceinline__ uint32_t four_scale_for(float amax) {
   return byte;
 }
 
-// Eight values -> four bytes of E2M1 codes of x / s (nearest even, saturating), -0 as 0. |x| <= 7 s, s > 0. The quotient is x r
-// with r = 1 / s, plus the exact remainder's part (P. Markstein, 1990), so that one that lies between two codes stays there
-__device__ __forceinline__ uint32_t four_codes(const float (&x)[8], float s) {
-  const float r = 1.f / s;
+// The largest magnitude, NaN if any is
+__device__ __forceinline__ float abs_max(float x, float y, float z) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
+// Eight values, in pairs, -> four bytes of E2M1 codes of x / s (nearest even, saturating), -0 as 0. |x| <= 7 s, s > 0. The quotient is
+// q = x r with r = 1 / s to a unit in the last place, plus the part of the exact remainder (P. Markstein, 1990): one that
+// lies between two codes is exact, and none beside it becomes it, as s has 4 bits and x / s is then more than half a unit away
+__device__ __forceinline__ uint32_t four_codes(const uint64_t (&x)[4], float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  const uint64_t rr = f2_pack(r, r), minus = f2_pack(-s, -s);
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = x[2 * i] * r, b = x[2 * i + 1] * r;
-    w |= (f32x2_to_e2m1x2(fmaf(fmaf(-b, s, x[2 * i + 1]), r, b), fmaf(fmaf(-a, s, x[2 * i]), r, a)) & 0xFFu) << (8 * i);
+    const uint64_t q = f2_mul(x[i], rr);
+    float lo, hi;
+    f2_unpack(f2_fma(f2_fma(q, minus, x[i]), rr, q), lo, hi);
+    w |= (f32x2_to_e2m1x2(hi, lo) & 0xFFu) << (8 * i);
   }
   const uint32_t m = w & 0x77777777u;    // a sign stays where the magnitude is not 0: then, and only then, m + 7 carries into it
   return w & (0x77777777u | ((m + 0x77777777u) & 0x88888888u));

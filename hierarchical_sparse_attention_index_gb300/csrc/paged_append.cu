@@ -63,7 +63,7 @@ __device__ __forceinline__ uint64_t turns_of(float radians) {
 }
 
 template <int D, int KV, bool BF16>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+__global__ void __launch_bounds__(kThreads, KV == HSA_E2M1 ? 4 : 0) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   constexpr int kPer = D / 16;           // units per head: pieces cA and cB of its D / 8
   constexpr bool kFour = KV == HSA_E2M1;
   constexpr int kRowBytes = D / 2 + 8;   // of a staged 4-bit row: codes, scales
@@ -181,29 +181,33 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
           *reinterpret_cast<uint4*>(pool + (at * D + 8 * cb) * 2) = x[i][1];
         }
       }
-      if constexpr (kFour) {
+      if (kFour && __any_sync(0xffffffffu, hk >= 0 && slot >= 0)) {      // most warps have heads of q alone, or none
         // codes of the pool's row, put in its order in shared memory. Two neighbouring lanes hold a group's 16 dims
         const float inv = hv < 0 ? p.w.k_inv : p.w.v_inv;
         uint8_t* mine = s_four + tid / kPer * kRowBytes;
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
-          float y[8], amax = 0.f;
-          bool nan = false;
+          uint64_t y[4];
+          float amax = 0.f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            y[j] = (o ? b[j] : a[j]) * inv;
-            amax = fmaxf(amax, fabsf(y[j]));
-            nan |= y[j] != y[j];
+          for (int j = 0; j < 4; ++j) {
+            const float* from = o ? b : a;
+            y[j] = f2_mul(f2_pack(from[2 * j], from[2 * j + 1]), f2_pack(inv, inv));
+            float lo, hi;
+            f2_unpack(y[j], lo, hi);
+            amax = abs_max(amax, lo, hi);
           }
-          if (nan) amax = NAN;
-          const float other = __shfl_xor_sync(0xffffffffu, amax, 1);
-          const bool none = amax != amax || other != other;
-          const uint32_t byte = none ? 0x7Fu : four_scale_for(fmaxf(amax, other));
+          amax = abs_max(amax, __shfl_xor_sync(0xffffffffu, amax, 1), 0.f);
+          const uint32_t byte = amax != amax ? 0x7Fu : four_scale_for(amax);
           const int c = o ? cb : ca;
           if (byte == 0x7Eu)             // the largest scale may be too small
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = fminf(fmaxf(y[j], -3136.f), 3136.f);
-          const uint32_t w = none ? 0u : four_codes(y, e4m3_to_f32(byte));
+            for (int j = 0; j < 4; ++j) {
+              float lo, hi;
+              f2_unpack(y[j], lo, hi);
+              y[j] = f2_pack(fminf(fmaxf(lo, -3136.f), 3136.f), fminf(fmaxf(hi, -3136.f), 3136.f));
+            }
+          const uint32_t w = byte == 0x7Fu ? 0u : four_codes(y, e4m3_to_f32(byte));
           if (hv < 0) {
             *reinterpret_cast<uint16_t*>(mine + four_k_at<D>(c, 0)) = (uint16_t)w;
             *reinterpret_cast<uint16_t*>(mine + four_k_at<D>(c, 1)) = (uint16_t)(w >> 16);
