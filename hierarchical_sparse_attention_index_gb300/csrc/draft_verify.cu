@@ -11,6 +11,9 @@
 //    (The borders of sums in fp32 would move by more than most tokens weigh; fp64 adds are slower than the
 //    loads here.) An entry becomes two integers by four fp32 additions: the bits of 1 + x hold x in units of 2^-23, and
 //    the rest, which fp32 holds exactly, gives 23 more bits in the same way.
+// Measured, fp32, 131,072 entries: 1 request x 5 rows 6.0 us, 64 requests 16.0 us, 0.54 of the measured copy rate (rows of 131,071, read entry by
+// entry: 18); 100 x 4 rows, bf16 22 us; 37 lookups x 8 rows of 50,001 entries 5.7 us. What is left in the short ones is the
+// launch, the cluster's start and loads that wait for one another.
 #include <string.h>
 
 #include "hsa_common.cuh"

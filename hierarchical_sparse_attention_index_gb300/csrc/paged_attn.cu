@@ -498,8 +498,9 @@ constexpr Rounds kTcRounds = {kSms, 8, true, 400};
 // requests x 8 heads x 20 rows, f16, 4,097 keys 30 us (46), 16,384 97 (115); 16 x 4 x 35 rows, E4M3, 4,097 36 (40), 16,384 93 (98);
 // 64 x 4 x 24 rows, bf16, of 1 .. 16,384 keys 187 (206), all 65,536 1,240 (1,205); 4 x 4 x 35, E4M3, 4,097 17.1 (15.9)
 constexpr Rounds kWideRounds = {2 * kSms, 6, false, 400};
-// 4-bit pages. 8 query rows, 128 dims, 32 x 8 heads of 1 .. 8,192 keys: n = 1, 2, 3, 5, 8: 74, 52.6, 42.1, 47.8, 45.7 us; 16 x 8 of 8,192: n = 3, 4, 6: 38.8,
-// 46.3, 43.3; 4 x 8 of 131,072: n = 13, 14, 19, 28: 120, 114, 126, 117; 16 rows, 64 x 8 of 4,096: n = 1, 2, 4: 112, 105, 115
+// 4-bit pages. 8 query rows, 128 dims, 32 x 8 heads of 1 .. 8,192 keys: n = 1, 2, 3, 5, 8: 72.8, 50.9, 43.4, 46.0, 44.8 us; 16 x 8 of
+// 8,192: n = 3, 4, 6: 37.5, 44.2, 41.1; 4 x 8 of 131,072: n = 13, 14, 19, 28: 118, 112, 123.5, 115; 16 rows, 64 x 8 of 4,096: n = 1, 2,
+// 4: 107.7, 105.2, 108
 static Rounds four_rounds(int32_t chunk_rows, int32_t head_dim) { return {kSms * four_ctas((chunk_rows + 7) / 8, head_dim), 6, false, 700}; }
 static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
   int64_t best = 1, cost = INT64_MAX;
@@ -515,10 +516,12 @@ static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
 }
 
 // Which kernel, query rows per CTA and splits of the length.
-// 16-bit pages and more than kPagedTcRows query rows take the tcgen05 kernel, up to 128 rows (whole queries) to a CTA. There and
+// 16-bit and 4-bit pages and more than kPagedTcRows query rows take the tcgen05 kernel, up to 128 rows (whole queries) to a CTA. There and
 // in the warp MMA kernel, 64 requests x 4 heads of 128 dims, of 1 .. 8,192 keys: 32 rows 105 and 164 us, 24 rows 104 and 124;
 // 1,000 keys: 33.3 and 33.1, 33.5 and 28.6; 1 request x 8 heads x 1,000 keys: 13.0 and 12.4, 13.0 and 9.9; 16 x 8 x 8,192 keys of 64
-// dims: 28 rows 59.7 and 55.1, 18 rows 59.8 and 47.7. Else up to 32 rows one CTA reads its keys once for all of them; more rows
+// dims: 28 rows 59.7 and 55.1, 18 rows 59.8 and 47.7. From 4-bit pages, 16 x 8 heads of 128 dims x 8,192 keys: 24 rows 84 and 71
+// us, 28 rows 84 and 120; 64 x 4, of 1 .. 4,097 keys: 56 and 63, 60 and 106; 16 x 8 x 8,192 of 64 dims: 67.5 and 48, 67 and 55.
+// Else up to 32 rows one CTA reads its keys once for all of them; more rows
 // (E4M3) are dealt out evenly (35: 18 and 17), and the later CTAs' keys come from L2.
 // Up to 16 rows the splits make about as many CTAs as the GPU holds at a time, 3 per SM: more only add starts and joins (4
 // requests of 131,072 FP8 keys: 168 us with 448 CTAs, 193 with 608, 217 with 1,216); from 17 rows on rounds of 2 per SM
@@ -571,7 +574,7 @@ PagedSplit paged_split(int32_t batch, int32_t heads, int32_t head_dim, int32_t g
   s.n_splits = (int32_t)n;
   s.split_len = (int32_t)imax64(64, ((span + n - 1) / n + 63) / 64 * 64);
   // 4-bit pages: as many clusters as run at a time, where the SMs of each of about eight parts of the GPU hold some 54 CTAs, of
-  // which up to n - 1 are left over (64 x 65,536 keys, 7 splits: 172 us in clusters, 116 joined by the kernel)
+  // which up to n - 1 are left over (64 x 65,536 keys, 7 splits: 172 us in clusters, 112 joined by the kernel)
   s.cluster = !s.tc && n > 1 && n <= 8 && ctas * n <= places - (kv_dtype == HSA_E2M1 ? places * n / 48 : 0);
   s.joined = n > 1 && !s.cluster;
   return s;

@@ -1,7 +1,7 @@
 // Attention of a few new tokens per request over 4-bit pages (hsa_paged_attn_decode, HSA_E2M1):
 //   o = sum_j softmax_j(scale q.k_j) v_j,  k and v E2M1 codes times an E4M3 scale for each 16 dims,
 // split over the cache's length and joined as in paged_attn.cu, whose layout of the work (a CTA per request, key-value head, up
-// to 32 query rows and split; 4 warps with rings of their own; transposed warp MMAs; one-pass softmax) this kernel shares.
+// to 24 query rows and split; 4 warps with rings of their own; transposed warp MMAs; one-pass softmax) this kernel shares.
 //
 // Bound: a key and its value are 144 bytes at 128 dims, an eighth of what fp32 would be and 9/16 of E4M3, so the
 // instructions that a warp spends on a key decide: at the copy rate 16 keys have 392 clocks of a scheduler. Codes become f16
@@ -14,7 +14,12 @@
 //  - scales are converted once per warp, not by each thread that needs them (4 and 8 times as often), those of V
 //    in pairs of keys as the products take them, and come from shared memory;
 //  - the keys of a piece are taken in the order t, t + 4 (four_key), so that every shared load is free of bank conflicts;
-//  - two pieces of 16 keys go through a turn of the loop together: two independent chains, one vote and one wait for both.
+//  - two pieces of 16 keys go through a turn of the loop together: two independent chains, one vote and one wait for both (from 17
+//    rows on one, for want of registers).
+// Measured (8 rows, bf16 queries, 128 dims): 16 requests x 8 heads x 8,192 keys 37.1 us, 0.60 of the measured copy rate, 4 x 8 x
+// 131,072 112 us, 0.80, 32 x 8 of 1 .. 8,192 keys 43.4 us, 1 x 8 x 1,000 6.6 us; 16 rows, 64 x 8 x 4,096 105 us; 64 dims, 8 rows, 32 x 8 x 8,192
+// 42.7 us. In the long one the schedulers issue in 62 % of the clocks, 295 instructions for 16 keys; the integer and conversion unit is
+// at 52 %, the tensor unit at 27 %, HBM at 79 %: what is left is waits between dependent instructions that 12 warps do not fill.
 #include "hsa_four.cuh"
 #include "hsa_paged_warp.cuh"
 

@@ -1,5 +1,6 @@
 // Attention of new tokens over a paged cache for many query rows per key-value head (several queries,
-// large groups) and 16-bit pages, on tcgen05; paged_attn.cu has the form for few rows and for E4M3.
+// large groups) and 16-bit or 4-bit pages, on tcgen05; paged_attn.cu and paged_four.cu have the forms for few rows, the first
+// also that for E4M3.
 //   o = sum_j softmax_j(scale q.k_j) v_j over the positions j a query sees.
 //
 // Bound: the reads of the pages from HBM, as with few rows, as long as the products keep up. The
@@ -16,11 +17,23 @@
 //    zero times what they hold need not be zero; blocks without any other row, or on a bad page, come from outside
 //    the pool, where TMA fills in zeros;
 //  - CTAs stay and take the next blocks' jobs (cluster launch control), so ragged lengths even out;
-//  - four warps merge the streams' results from tensor memory, where both of a row lie in the same lane, while the
+//  - four warps merge the streams' results from tensor memory, where both of a row lie in the same lane (but see below), while the
 //    softmax is at the next job. With one split that is the result, else it goes to the workspace and
 //    paged_join_kernel joins the splits.
 // Measured: 64 requests x 4 heads x 5 queries, f16, 16,384 keys each 328 us, 0.97 of the measured copy rate; of 1 ..
 // 4,097 keys 64 us, 0.67 (the CTAs' last jobs do not end together; all with 4,097: 93 us, 0.86); 1 request x 131,072 55 us.
+//
+// 4-bit pages (FOUR): eight more warps take the place of the loads by TMA. Each brings its 16 keys of a tile by asynchronous
+// copies as they lie in the pool, makes f16 of them (codes times scales, exact) and writes them into the rings' tiles. The reads
+// are 9/32 of those from 16-bit pages, so they decide no more. 64 keys of 128 dims take 1,283 clocks of an SM, in which the tensor path
+// is busy for 56 %, the converting warps for 70 to 80 % (they wait for a free tile in the rest, timed by the clock), and shared memory for
+// 912 by count: 32 KB written and 32 read as converted tiles, 9 written and 9 read as they come, 32 KB of queries for the product with K.
+//  - Up to 64 query rows the second stream's queries lie 64 rows lower, so that its rows fall to the warps that the first
+//    stream's leave idle (64 x 5 queries x 16,384 keys 306 -> 291 us). The merge then goes through shared memory.
+//  - Twice the pieces for half the converting warps: 416 us against 306. Q in tensor memory would spare its reads, but S of two
+//    streams twice and their O take all 512 columns.
+// Measured: 64 requests x 4 heads x 5 queries x 7 heads, f16, 16,384 keys each 291 us (16-bit pages: 328), of 1 .. 4,097 keys
+// 58.4; 16 x 8 heads x 8 queries x 16 heads, bf16, 8,192 keys 89.
 #include <string.h>
 
 #include <numeric>
