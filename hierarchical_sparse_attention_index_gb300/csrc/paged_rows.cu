@@ -30,10 +30,11 @@
 // 912 by count: 32 KB written and 32 read as converted tiles, 9 written and 9 read as they come, 32 KB of queries for the product with K.
 //  - Up to 64 query rows the second stream's queries lie 64 rows lower, so that its rows fall to the warps that the first
 //    stream's leave idle (64 x 5 queries x 16,384 keys 306 -> 291 us). The merge then goes through shared memory.
-//  - Twice the pieces for half the converting warps: 416 us against 306. Q in tensor memory would spare its reads, but S of two
+//  - Rings of 2, 3, 4 tiles 311, 293, 291 us; 2, 3, 4, 6 slots for what a converting warp brings 348, 291, 295, 309 (the last two take
+//    tiles from the rings); twice the pieces for half the converting warps: 416 against 306. Q in tensor memory would spare its reads, but S of two
 //    streams twice and their O take all 512 columns.
 // Measured: 64 requests x 4 heads x 5 queries x 7 heads, f16, 16,384 keys each 291 us (16-bit pages: 328), of 1 .. 4,097 keys
-// 58.4; 16 x 8 heads x 8 queries x 16 heads, bf16, 8,192 keys 89.
+// 58.4; 16 x 8 heads x 8 queries x 16 heads, bf16, 8,192 keys 85.
 #include <string.h>
 
 #include <numeric>
@@ -925,7 +926,7 @@ cudaError_t launch(RowsParams& p, unsigned blocks, cudaStream_t s) {
   p.q_rows = (p.tt * p.a.group + 7) / 8 * 8;
   // Up to 64 rows lie in two warps' lanes. The second stream's lie 64 lower, in the others', whose schedulers have no softmax else
   p.shift = FOUR && p.q_rows <= 64 ? 64 : 0;
-  const uint32_t raw = FOUR ? 8 * Shape<D>::kRawSlots * Shape<D>::kRawBytes + 4 * 32 * kSumRow : 0;
+  const uint32_t raw = FOUR ? 8 * Shape<D>::kRawSlots * Shape<D>::kRawBytes + (p.shift ? 4 * 32 * kSumRow : 0) : 0;
   const uint32_t room = smem_most(FOUR) - 1024 - raw - 2 * (D / 64) * (uint32_t)p.q_rows * 128u;
   p.stages = (int32_t)(room / (2 * Shape<D>::kKvBytes));
   if (p.stages > Shape<D>::kMaxStages) p.stages = Shape<D>::kMaxStages;
