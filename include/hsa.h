@@ -130,7 +130,8 @@ typedef enum { HSA_BF16 = 0, HSA_F16 = 1, HSA_E4M3 = 2, HSA_E2M1 = 3, HSA_F32 = 
  * v_s u8 [n_pages][heads][page_size][head_dim / 16], one scale per group. With byte b of a row holding dim 2b
  * in its low and 2b + 1 in its high nibble, rows are stored in the order in which the attention's threads
  * take them: byte (head_dim / 8) t + 2 s + i of a row of k is byte 8 s + 2 t + i (t in 0..3, i in 0..1, s a group),
- * byte (head_dim / 16) r + s of a row of v is byte 8 s + r (r in 0..7). 4.5 bits a value. */
+ * byte (head_dim / 16) r + s of a row of v is byte 8 s + r (r in 0..7). 4.5 bits a value. A caller compiled
+ * against a struct without the last two members, which cannot hold HSA_E2M1, is served as before. */
 typedef struct {
   int32_t batch;          /* requests                                               */
   int32_t heads;          /* key-value heads, 1..1024                               */
@@ -396,7 +397,7 @@ HSA_API hsa_status hsa_paged_cache_append(const hsa_paged_cache* cache, const hs
 
 /* Read keys and values back out of a paged cache, for instance as the earlier keys of a chunk in hsa_prompt_attn. Row t of
  * k and v, of the request b with cu[b] <= t < cu[b+1], becomes position start[b] + t - cu[b] of that request:
- *   row = round(stored number x scale), a 16-bit cache's values as they are.
+ *   row = round(stored number x scale), the fp32 product to nearest even, a 16-bit cache's values as they are.
  *   k, v      bf16 or f16 (`dtype`) [n_tokens][heads][head_dim], strides, alignment and types as in hsa_paged_cache_write
  *   n_tokens, cu, start   as in hsa_paged_cache_write
  * Rows outside [cu[0], cu[batch]) and rows whose position is outside the table or on a page id outside [0, n_pages) are
