@@ -524,13 +524,14 @@ def hsa_draft_verify(p, q, drafted, u_accept, u_sample, accepted, tokens, n_draf
     types = _types()
     i32, f32 = types["i32"], types["f32"]
     dtype = HSA_F32 if p.dtype is f32 else _dtype(p)
-    q_stride = 0
+    q_stride = at_q = 0
     if q is not None and nq > 1:
+        at_q = q.data_ptr()
         q_stride = _probabilities("q", q, (batch, nq - 1, n))
         if q.dtype is not p.dtype or q.get_device() != device:
             raise ValueError("p and q differ in type or device")
     one, drafts = (batch,), (batch, nq - 1)
-    a = _VERIFY_ARGS.pack(batch, nq, n, dtype, p.data_ptr(), q.data_ptr() if q_stride else 0, _probabilities("p", p, shape), q_stride,
+    a = _VERIFY_ARGS.pack(batch, nq, n, dtype, p.data_ptr(), at_q, _probabilities("p", p, shape), q_stride,
                           _given("drafted", drafted, i32, drafts, device) or 0, _given("n_draft", n_draft, i32, one, device) or 0,
                           _given("u_accept", u_accept, f32, drafts, device) or 0, _given("u_sample", u_sample, f32, one, device) or 0,
                           _given("accepted", accepted, i32, one, device) or 0, _given("tokens", tokens, i32, (batch, nq), device) or 0)

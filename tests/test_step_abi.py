@@ -166,3 +166,15 @@ def test_records_as_bytes(H):  # noqa: F811
         assert len(raw) == ctypes.sizeof(record)
         r = record.from_buffer_copy(raw)
         assert [getattr(r, name) for name, _ in record._fields_] == values
+
+
+def test_rows_on_top_of_one_another(H, monkeypatch):  # noqa: F811
+    """Expanded probabilities (rows 0 entries apart) are refused; those of a drafter are not taken for none."""
+    monkeypatch.setattr(H, "_stream_on", lambda *_: None)
+    i, f = dict(dtype=torch.int32), dict(dtype=torch.float32)
+    for nq in (2, 4):
+        args = [torch.zeros(2, nq - 1, **i), torch.zeros(2, nq - 1, **f), torch.zeros(2, **f), torch.zeros(2, **i), torch.zeros(2, nq, **i)]
+        p, q = torch.zeros(2, nq, 10), torch.zeros(2, nq - 1, 10)
+        for a, b in ((p, q[:1, :1].expand(2, nq - 1, 10)), (p[:1, :1].expand(2, nq, 10), q), (p[:1, :1].expand(2, nq, 10), None)):
+            with pytest.raises(H.HsaError, match="HSA_ERR_SHAPE"):
+                H.hsa_draft_verify(a, b, *args)
