@@ -25,7 +25,7 @@
 //
 // 4-bit pages (FOUR): eight more warps take the place of the loads by TMA. Each brings its 16 keys of a tile by asynchronous
 // copies as they lie in the pool, makes f16 of them (codes times scales, exact) and writes them into the rings' tiles. The reads
-// are 9/32 of those from 16-bit pages, so they decide no more. 64 keys of 128 dims take 1,283 clocks of an SM, in which the tensor path
+// are 9/32 of those from 16-bit pages, so they decide no more. 64 keys of 128 dims take 1,215 clocks of an SM, in which the tensor path
 // is busy for 56 %, the converting warps for 70 to 80 % (they wait for a free tile in the rest, timed by the clock), and shared memory for
 // 912 by count: 32 KB written and 32 read as converted tiles, 9 written and 9 read as they come, 32 KB of queries for the product with K.
 //  - Up to 64 query rows the second stream's queries lie 64 rows lower, so that its rows fall to the warps that the first
@@ -33,8 +33,8 @@
 //  - Rings of 2, 3, 4 tiles 311, 293, 291 us; 2, 3, 4, 6 slots for what a converting warp brings 348, 291, 295, 309 (the last two take
 //    tiles from the rings); twice the pieces for half the converting warps: 416 against 306. Q in tensor memory would spare its reads, but S of two
 //    streams twice and their O take all 512 columns.
-// Measured: 64 requests x 4 heads x 5 queries x 7 heads, f16, 16,384 keys each 291 us (16-bit pages: 328), of 1 .. 4,097 keys
-// 58.4; 16 x 8 heads x 8 queries x 16 heads, bf16, 8,192 keys 85.
+// Measured: 64 requests x 4 heads x 5 queries x 7 heads, f16, 16,384 keys each 276 us (16-bit pages: 328), of 1 .. 4,097 keys
+// 56.6; 16 x 8 heads x 8 queries x 16 heads, bf16, 8,192 keys 82.
 #include <string.h>
 
 #include <numeric>
@@ -62,7 +62,9 @@ struct Roles {                           // 16-bit pages: warps 10 and 11 load, 
 template <>
 struct Roles<true> {                     // 4-bit pages: warp 10 fills its group, 11 finds the work, 16..23 load and convert, four for each stream
   static constexpr int kFindWarp = 11, kThreads = 24 * 32, kJobReaders = kSoftWarps + 2 + 4 + 8, kFilled = 4;
-  static constexpr int kLaunchRegs = 80, kSoftRegs = 112, kIssueRegs = 40, kOutRegs = 88, kLastRegs = 64;
+  // (48 for the converting warps keep their conversions between the stores: 276 us against 283 with 56 and 291 with 64, 64 requests x 5
+  // queries x 16,384 keys; with 40 they spill, 307)
+  static constexpr int kLaunchRegs = 80, kSoftRegs = 112, kIssueRegs = 40, kOutRegs = 104, kLastRegs = 48;
   static_assert(2 * kSoftRegs + kIssueRegs + kOutRegs + 2 * kLastRegs <= 6 * kLaunchRegs, "setmaxnreg draws on the launch's registers");
 };
 // A warp group goes on with REGS registers per thread, of the LAUNCH that it was launched with
@@ -414,28 +416,46 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
       sp.gaps = job.gaps;
       free_job(it);
       loads = 0;
-      pieces = pieces_of(0, page_of(0));
+      // what reads global memory goes first: pages, queries of kBatch turns, the first piece
+      const int page = page_of(0);
       next_page = page_of(1);
-      constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;
-      const int qs = it & 1, rows = p.nq * p.group;
+      constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = 2, kStep = 8 * kRowsAt;
+      const int qs = it & 1, rows = p.nq * p.group, c = lane % kLanes;
+      uint4 x[kBatch];
+      auto fetch = [&](int base_row) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int row = base_row + i * kStep + lane / kLanes, at = first + row;
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (row < rp.tt * p.group && at < rows)
+            x[i] = *reinterpret_cast<const uint4*>(p.q + (((int64_t)b * p.nq + at / p.group) * p.heads_q + h * p.group + at % p.group) * D + 8 * c);
+        }
+      };
+      int base_row = cw * kRowsAt;
+      fetch(base_row);
+      pieces = pieces_of(0, page);
+      load();
       ok = wait_bar(q_empty + 8 * qs, ((it >> 1) & 1) ^ 1, rp.wait_ns) && ok;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
-      for (int base_row = cw * kRowsAt; base_row < rp.q_rows; base_row += 8 * kRowsAt) {
-        const int row = base_row + lane / kLanes, c = lane % kLanes, at = first + row;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (row < rp.tt * p.group && at < rows)
-          x = *reinterpret_cast<const uint4*>(p.q + (((int64_t)b * p.nq + at / p.group) * p.heads_q + h * p.group + at % p.group) * D + 8 * c);
-        float shift = 1.f;
-        if (p.q_bf16) {
-          uint2 y[2] = {make_uint2(x.x, x.y), make_uint2(x.z, x.w)};
-          queries_to_f16<2, kLanes>(y, shift);
-          x = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
+      while (base_row < rp.q_rows) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int row = base_row + i * kStep + lane / kLanes;
+          if (base_row + i * kStep >= rp.q_rows) break;
+          float shift = 1.f;
+          if (p.q_bf16) {
+            uint2 y[2] = {make_uint2(x[i].x, x[i].y), make_uint2(x[i].z, x[i].w)};
+            queries_to_f16<2, kLanes>(y, shift);
+            x[i] = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y);
+          }
+          if (row < rp.q_rows) {
+            sts128(sQ + qs * q_bytes + (c >> 3) * q_block + row * 128 + ((c & 7) ^ (row & 7)) * 16, x[i].x, x[i].y, x[i].z, x[i].w);
+            if (c == 0) s_query[qs][row] = shift;
+          }
         }
-        if (row < rp.q_rows) {
-          sts128(sQ + qs * q_bytes + (c >> 3) * q_block + row * 128 + ((c & 7) ^ (row & 7)) * 16, x.x, x.y, x.z, x.w);
-          if (c == 0) s_query[qs][row] = shift;
-        }
+        base_row += kBatch * kStep;
+        if (base_row < rp.q_rows) fetch(base_row);
       }
       fence_async_smem();
       __syncwarp();
@@ -522,8 +542,9 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
               s_job[(it + 1) % kJobSlots].more) {
             open(it + 1);
             opened = true;
+          } else if (ok) {
+            load();
           }
-          if (ok) load();
         }
         if (!ok) break;
         slot = i < n ? (slot + 1 == kSlots ? 0 : slot + 1) : slot;
