@@ -89,8 +89,9 @@ struct PagedAttnParams {
 cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedSplit& sp, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns,
                               cudaStream_t s);
 constexpr int32_t kPagedTcRows = 24;     // pages of 16 or 4 bits: more query rows than this take the tcgen05 kernel
-// 4-bit pages: CTAs that an SM holds, for nt tiles of 8 query rows, as registers allow without spilling
-constexpr int four_ctas(int nt, int head_dim) { return nt == 1 && head_dim == 64 ? 4 : nt <= 2 ? 3 : 2; }
+// 4-bit pages: CTAs that an SM holds, for nt tiles of 8 query rows, as registers allow without spilling. Two and three with 16 rows: 64 x 8
+// heads x 4,096 keys 91.5 and 106 us, of 1 .. 4,096 68 and 73; 32 x 8 x 8,192 86.5 and 104.6, of 1 .. 8,192 77 and 69.5
+constexpr int four_ctas(int nt, int head_dim) { return nt > 1 ? 2 : head_dim == 64 ? 4 : 3; }
 cudaError_t launch_paged_four(const PagedAttnParams& p, int32_t head_dim, cudaStream_t s);
 cudaError_t launch_paged_rows(const PagedAttnParams& p, int32_t head_dim, int32_t kv_dtype, uint64_t wait_ns, cudaStream_t s);
 

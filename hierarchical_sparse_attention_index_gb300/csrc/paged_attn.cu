@@ -500,7 +500,7 @@ constexpr Rounds kTcRounds = {kSms, 8, true, 400};
 constexpr Rounds kWideRounds = {2 * kSms, 6, false, 400};
 // 4-bit pages. 8 query rows, 128 dims, 32 x 8 heads of 1 .. 8,192 keys: n = 1, 2, 3, 5, 8: 72.8, 50.9, 43.4, 46.0, 44.8 us; 16 x 8 of
 // 8,192: n = 3, 4, 6: 37.5, 44.2, 41.1; 4 x 8 of 131,072: n = 13, 14, 19, 28: 118, 112, 123.5, 115; 16 rows, 64 x 8 of 4,096: n = 1, 2,
-// 4: 107.7, 105.2, 108
+// 4: 91.5, 104, 111, of 1 .. 4,096: 68, 70, 75; 8 x 8 of 16,384: n = 3, 4, 5: 62.6, 48.5, 75.7; 32 x 8 of 1 .. 8,192: n = 1, 4: 77, 64
 static Rounds four_rounds(int32_t chunk_rows, int32_t head_dim) { return {kSms * four_ctas((chunk_rows + 7) / 8, head_dim), 6, false, 700}; }
 static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
   int64_t best = 1, cost = INT64_MAX;
@@ -519,8 +519,8 @@ static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
 // 16-bit and 4-bit pages and more than kPagedTcRows query rows take the tcgen05 kernel, up to 128 rows (whole queries) to a CTA. There and
 // in the warp MMA kernel, 64 requests x 4 heads of 128 dims, of 1 .. 8,192 keys: 32 rows 105 and 164 us, 24 rows 104 and 124;
 // 1,000 keys: 33.3 and 33.1, 33.5 and 28.6; 1 request x 8 heads x 1,000 keys: 13.0 and 12.4, 13.0 and 9.9; 16 x 8 x 8,192 keys of 64
-// dims: 28 rows 59.7 and 55.1, 18 rows 59.8 and 47.7. From 4-bit pages, 16 x 8 heads of 128 dims x 8,192 keys: 24 rows 84 and 71
-// us, 28 rows 84 and 120; 64 x 4, of 1 .. 4,097 keys: 56 and 63, 60 and 106; 16 x 8 x 8,192 of 64 dims: 67.5 and 48, 67 and 55.
+// dims: 28 rows 59.7 and 55.1, 18 rows 59.8 and 47.7. From 4-bit pages, 16 x 8 heads of 128 dims x 8,192 keys: 24 rows 73 and 65
+// us, 28 rows 73 and 120; 64 x 4, of 1 .. 4,097 keys: 60.5 and 60, 60 and 106; 16 x 8 x 8,192 of 64 dims: 63 and 40, 63 and 55.
 // Else up to 32 rows one CTA reads its keys once for all of them; more rows
 // (E4M3) are dealt out evenly (35: 18 and 17), and the later CTAs' keys come from L2.
 // Up to 16 rows the splits make about as many CTAs as the GPU holds at a time, 3 per SM: more only add starts and joins (4

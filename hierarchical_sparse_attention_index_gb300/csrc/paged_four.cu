@@ -14,10 +14,9 @@
 //  - scales are converted once per warp, not by each thread that needs them (4 and 8 times as often), those of V
 //    in pairs of keys as the products take them, and come from shared memory;
 //  - the keys of a piece are taken in the order t, t + 4 (four_key), so that every shared load is free of bank conflicts;
-//  - two pieces of 16 keys go through a turn of the loop together: two independent chains, one vote and one wait for both (from 17
-//    rows on one, for want of registers).
+//  - two pieces of 16 keys go through a turn of the loop together: two independent chains, one vote and one wait for both.
 // Measured (8 rows, bf16 queries, 128 dims): 16 requests x 8 heads x 8,192 keys 37.1 us, 0.60 of the measured copy rate, 4 x 8 x
-// 131,072 112 us, 0.80, 32 x 8 of 1 .. 8,192 keys 43.4 us, 1 x 8 x 1,000 6.6 us; 16 rows, 64 x 8 x 4,096 105 us; 64 dims, 8 rows, 32 x 8 x 8,192
+// 131,072 112 us, 0.80, 32 x 8 of 1 .. 8,192 keys 43.4 us, 1 x 8 x 1,000 6.6 us; 16 rows, 64 x 8 x 4,096 91.5 us; 64 dims, 8 rows, 32 x 8 x 8,192
 // 42.7 us. In the long one the schedulers issue in 62 % of the clocks, 295 instructions for 16 keys; the integer and conversion unit is
 // at 52 %, the tensor unit at 27 %, HBM at 79 %: what is left is waits between dependent instructions that 12 warps do not fill.
 #include "hsa_four.cuh"
@@ -44,7 +43,7 @@ __device__ __forceinline__ void sts128v(uint32_t addr, uint4 v) {
 // t and t + 4 lie apart; K's and V's scales in the same orders. Behind the slots, the scales in f16 of the pieces of a turn.
 template <int D, int NT>
 struct Slot {
-  static constexpr int kPieces = NT <= 2 ? 2 : 1;        // of a turn
+  static constexpr int kPieces = 2;                      // of a turn. One of 17 to 24 rows: 24 rows, 32 x 8 x 8,192 keys of 64 dims 80 us against 70
   static constexpr int kRow = D / 2, kChunks = kRow / 16, kHalf = kGroup * kRow;
   static constexpr int kScaleRow = D / 16, kScales = kGroup * kScaleRow;
   static constexpr int kBytes = 2 * kHalf + 2 * kScales;
