@@ -11,8 +11,8 @@
 //    (The borders of sums in fp32 would move by more than most tokens weigh; fp64 adds are slower than the
 //    loads here.) An entry becomes two integers by four fp32 additions: the bits of 1 + x hold x in units of 2^-23, and
 //    the rest, which fp32 holds exactly, gives 23 more bits in the same way.
-// Measured, fp32, 131,072 entries: 1 request x 5 rows 6.0 us, 64 requests 16.0 us, 0.54 of the measured copy rate (rows of 131,071, read entry by
-// entry: 18); 100 x 4 rows, bf16 22 us; 37 lookups x 8 rows of 50,001 entries 5.7 us. What is left in the short ones is the
+// Measured, fp32, 131,072 entries: 1 request x 5 rows 6.0 us, 64 requests 15.6 us, 0.55 of the measured copy rate (rows of 131,071, read entry by
+// entry: 18); 200 requests 38 us, 100 x 4 rows, bf16 17.3; 37 lookups x 8 rows of 50,001 entries 5.7 us. What is left in the short ones is the
 // launch, the cluster's start and loads that wait for one another.
 #include <string.h>
 
@@ -23,6 +23,10 @@ namespace hsa {
 namespace {
 
 constexpr int kStep = 128;               // pieces are multiples of this many entries
+// CTAs of 256 threads that an SM holds. 16-bit entries: batches of 8 and 3 CTAs, of 4 and 4, of 2 and 4: 100 x 4 rows of 131,072 17.6, 21.1, 21.9 us;
+// fp32: batches of 4 and 4 CTAs, of 8 and 3: 64 x 5 rows 16.0, 19.0
+template <typename T>
+constexpr int kCtas = sizeof(T) == 4 ? 4 : 3;
 constexpr int kFlush = 128;              // entries of a lane between 64-bit sums, at most: low parts are 2^22 for p and for q
 
 __device__ __forceinline__ float value_of(float x) { return x; }
@@ -113,22 +117,24 @@ template <typename T, bool WIDE, bool Q>
 __device__ __forceinline__ int64_t sum_piece(const Weights<T, Q>& w, int lo, int hi, int lane) {
   int64_t sum = 0;
   if constexpr (WIDE) {                  // 16 bytes at a time; lo is a multiple of kStep
-    constexpr int kPer = 16 / sizeof(T), kBatch = sizeof(T);             // 2 batches of 16-bit entries hold as many as 4 of fp32
+    constexpr int kPer = 16 / sizeof(T), kBatch = sizeof(T) == 4 ? 4 : 8;
     static_assert(kPer * kBatch <= kFlush, "low parts");
     const int n = (hi - lo) / kPer;
     const uint4* p = reinterpret_cast<const uint4*>(w.p + lo);
     const uint4* q = reinterpret_cast<const uint4*>(w.q + lo);
-    for (int first = lane; first < n; first += 32 * kBatch) {
+    // a batch of which some vectors lie behind the end spares those, which a whole one does not ask for
+    auto batch = [&](int first, bool whole) {
       uint4 a[kBatch], b[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int k = first + 32 * i;
-        a[i] = k < n ? p[k] : make_uint4(0u, 0u, 0u, 0u);
-        b[i] = Q && k < n ? q[k] : make_uint4(0u, 0u, 0u, 0u);
+        a[i] = whole || k < n ? p[k] : make_uint4(0u, 0u, 0u, 0u);
+        b[i] = Q && (whole || k < n) ? q[k] : make_uint4(0u, 0u, 0u, 0u);
       }
       int h = 0, l = 0;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
+        if (!whole && first - lane + 32 * i >= n) break;
         T x[kPer], y[kPer];
         memcpy(x, &a[i], 16);
         memcpy(y, &b[i], 16);
@@ -136,7 +142,10 @@ __device__ __forceinline__ int64_t sum_piece(const Weights<T, Q>& w, int lo, int
         for (int e = 0; e < kPer; e += 2) w.add2(x[e], x[e + 1], y[e], y[e + 1], lo + (first + 32 * i) * kPer + e, h, l);
       }
       sum += ((int64_t)h << 23) + l;
-    }
+    };
+    int first = lane;
+    for (; first - lane + 32 * kBatch <= n; first += 32 * kBatch) batch(first, true);
+    if (first - lane < n) batch(first, false);
     lo += n * kPer;
   }
   constexpr int kBatch = 16;
@@ -157,7 +166,7 @@ __device__ __forceinline__ int64_t sum_piece(const Weights<T, Q>& w, int lo, int
 }
 
 template <typename T, bool WIDE, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) draft_verify_kernel(const __grid_constant__ VerifyParams vp) {
+__global__ void __launch_bounds__(kThreads, kCtas<T> * 256 / kThreads) draft_verify_kernel(const __grid_constant__ VerifyParams vp) {
   constexpr int kWarps = kThreads / 32;
   const hsa_verify_args& p = vp.a;
   __shared__ int s_kept, s_without;
@@ -315,13 +324,15 @@ cudaError_t launch_draft_verify(const hsa_verify_args& a, uint32_t* status, cuda
   VerifyParams p;
   p.a = a;
   p.status = status;
-  // Clusters of 8 CTAs as long as every SM has a CTA at most, of 512 threads; else CTAs of 256, as many as run at a time, four to
-  // an SM, while each has 2,048 entries. 1 and 8 requests of 131,072 entries: 6.2 and 7.3 us, with 256 threads 7.3 and 9.4; 64: 22
-  // and 16.2
-  const bool few = (int64_t)a.batch * 8 <= kSms;
-  p.ctas = 1;
-  while (p.ctas < 8 && (int64_t)2 * p.ctas * a.batch <= 4 * kSms && a.vocabulary / p.ctas > 2048) p.ctas *= 2;
+  // A request's CTAs: about as many as run at a time, while a share has more than 16 KB; beyond that while it has 48 KB (fp32,
+  // 131,072 entries, 200 requests: 1, 2, 4, 8 CTAs 71, 63, 40, 38 us; bf16 62, 35, 29, 34; 32,000 entries 12.8, 11.8, 14.9, 23.1). Few
+  // requests: CTAs of 512 threads (1 and 8 requests of 131,072 fp32 entries 6.0 and 6.5 us, with 256 threads 7.3 and 9.4). With 16-bit
+  // entries an SM has room for one of them, and clusters of 8 soon do not all run at a time (16 requests: 10.3 us, 17 with 256 threads 7.1)
   const int size = a.dtype == HSA_F32 ? 4 : 2;
+  const bool few = (int64_t)a.batch * 8 <= (size == 4 ? kSms : 64);
+  const int64_t bytes = (int64_t)a.vocabulary * size;
+  p.ctas = 1;
+  while (p.ctas < 8 && ((int64_t)2 * p.ctas * a.batch <= 4 * kSms ? bytes / p.ctas > 16384 : bytes / (2 * p.ctas) >= 49152)) p.ctas *= 2;
   p.wide = ((reinterpret_cast<uintptr_t>(a.p) | reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)(a.p_stride * size) |
              (uintptr_t)(a.q ? a.q_stride * size : 0)) & 15) == 0;
   switch (a.dtype) {
