@@ -26,7 +26,7 @@
 // 4-bit pages (FOUR): eight more warps take the place of the loads by TMA. Each brings its 16 keys of a tile by asynchronous
 // copies as they lie in the pool, makes f16 of them (codes times scales, exact) and writes them into the rings' tiles. The reads
 // are 9/32 of those from 16-bit pages, so they decide no more. 64 keys of 128 dims take 1,215 clocks of an SM, in which the tensor path
-// is busy for 56 %, the converting warps for 70 to 80 % (they wait for a free tile in the rest, timed by the clock), and shared memory for
+// is busy for 59 %, the converting warps for 70 to 80 % (they wait for a free tile in the rest, timed by the clock), and shared memory for
 // 912 by count: 32 KB written and 32 read as converted tiles, 9 written and 9 read as they come, 32 KB of queries for the product with K.
 //  - Up to 64 query rows the second stream's queries lie 64 rows lower, so that its rows fall to the warps that the first
 //    stream's leave idle (64 x 5 queries x 16,384 keys 306 -> 291 us). The merge then goes through shared memory.
