@@ -378,18 +378,24 @@ class PagedCache:
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self.desc = hsa_paged_cache(self.batch, self.heads, self.head_dim, self.page_size, self.dtype, 0, n_pages, max_pages,
                                     _ptr(k), _ptr(v), _ptr(table), self.k_scale, self.v_scale, _ptr(k_s), _ptr(v_s))
-
-    @property
-    def ref(self):
-        return ctypes.byref(self.desc)
+        self.ref = ctypes.byref(self.desc)
 
 
-def _kv_rows(cache, k, v):
-    """(type, strides) of rows of keys and values that go into or come out of a cache."""
-    k_stride, v_stride = _rows("k", k, cache.heads, cache.head_dim), _rows("v", v, cache.heads, cache.head_dim)
-    if v.shape[0] != k.shape[0] or k.dtype is not v.dtype or k.get_device() != cache.device or v.get_device() != cache.device:
-        raise ValueError("k and v differ in shape or type, or are not on the cache's device")
-    return _dtype(k), k_stride, v_stride
+def _tokens(name, t, shape, dtype, device):
+    """Address and row stride of [rows][heads][head_dim] values, as _rows; all that is asked of them in one go."""
+    row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    n, heads, dim = shape
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or one != 1 or (heads > 1 and head != dim):
+        raise ValueError(f"{name}: expected {dtype} [{n}][{heads}][{dim}] on device {device}, each row contiguous, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device} with strides {list(t.stride())}")
+    return t.data_ptr(), row if n > 1 else heads * dim
+
+
+def _kv_tokens(cache, k, v):
+    """Type and number of the rows of keys and values that go into or come out of a cache, and where they are."""
+    n, device = k.shape[0] if k.dim() == 3 else 0, cache.device
+    shape, kind = (n, cache.heads, cache.head_dim), k.dtype
+    return _dtype(k), n, _tokens("k", k, shape, kind, device), _tokens("v", v, shape, kind, device)
 
 
 def hsa_paged_cache_write(cache: PagedCache, k, v, cu=None, start=None, stream=None):
@@ -397,9 +403,9 @@ def hsa_paged_cache_write(cache: PagedCache, k, v, cu=None, start=None, stream=N
     shares); start: int64 [batch] or None (0)."""
     device = cache.device
     stream = _stream_on("cache", device, stream)
-    dtype, k_stride, v_stride = _kv_rows(cache, k, v)
+    dtype, n, (at_k, k_stride), (at_v, v_stride) = _kv_tokens(cache, k, v)
     _check("hsa_paged_cache_write", load_library().hsa_paged_cache_write(
-        cache.ref, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride, k.shape[0],
+        cache.ref, at_k, at_v, dtype, k_stride, v_stride, n,
         _given("cu", cu, _DTYPES["i32"], (cache.batch + 1,), device),
         _given("start", start, _DTYPES["i64"], (cache.batch,), device), stream))
 
@@ -411,24 +417,24 @@ def hsa_paged_cache_append(cache: PagedCache, k, v, inv_freq, q=None, q_out=None
     each pair, or None (nothing turns); dims rotary_at .. rotary_at + rotary_dims - 1 of each head are rotated."""
     device = cache.device
     stream = _stream_on("cache", device, stream)
-    dtype, k_stride, v_stride = _kv_rows(cache, k, v)
-    n, heads_q, q_stride, out_stride, turning = k.shape[0], 0, 0, 0, 0
+    dtype, n, (at_k, k_stride), (at_v, v_stride) = _kv_tokens(cache, k, v)
+    heads_q = at_q = q_stride = at_out = out_stride = turning = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
     if q is not None:
         heads_q = q.shape[1] if q.dim() == 3 else 0
-        q_stride, out_stride = _rows("q", q, heads_q, cache.head_dim), _rows("q_out", q_out, heads_q, cache.head_dim)
-        if heads_q < 1 or q.shape[0] != n or q_out.shape[0] != n or not k.dtype is q.dtype is q_out.dtype or \
-                not device == q.get_device() == q_out.get_device():
-            raise ValueError("q and q_out differ from k in rows, type or device")
+        if heads_q < 1:
+            raise ValueError("q and q_out are [n_tokens][heads_q][head_dim]")
+        shape, kind = (n, heads_q, cache.head_dim), k.dtype
+        (at_q, q_stride), (at_out, out_stride) = _tokens("q", q, shape, kind, device), _tokens("q_out", q_out, shape, kind, device)
     if inv_freq is not None:
         if inv_freq.dim() != 1:
             raise ValueError("inv_freq is [rotary_dims / 2]")
         turning = 2 * inv_freq.shape[0]
-    a = _APPEND_ARGS.pack(dtype, heads_q, rotary_at, turning, pairs, n, _ptr(q) or 0, k.data_ptr(), v.data_ptr(), q_stride, k_stride,
-                          v_stride, out_stride, _given("cu", cu, _DTYPES["i32"], (cache.batch + 1,), device) or 0,
-                          _given("start", start, _DTYPES["i64"], (cache.batch,), device) or 0,
-                          _given("inv_freq", inv_freq, _DTYPES["f32"], (turning // 2,), device) or 0, _ptr(q_out) or 0)
+    i32, i64, f32 = _DTYPES["i32"], _DTYPES["i64"], _DTYPES["f32"]
+    a = _APPEND_ARGS.pack(dtype, heads_q, rotary_at, turning, pairs, n, at_q, at_k, at_v, q_stride, k_stride, v_stride, out_stride,
+                          _given("cu", cu, i32, (cache.batch + 1,), device) or 0, _given("start", start, i64, (cache.batch,), device) or 0,
+                          _given("inv_freq", inv_freq, f32, (turning // 2,), device) or 0, at_out)
     _check("hsa_paged_cache_append", load_library().hsa_paged_cache_append(cache.ref, a, stream))
 
 
@@ -437,9 +443,9 @@ def hsa_paged_cache_read(cache: PagedCache, k, v, cu=None, start=None, stream=No
     hsa_paged_cache_write."""
     device = cache.device
     stream = _stream_on("cache", device, stream)
-    dtype, k_stride, v_stride = _kv_rows(cache, k, v)
+    dtype, n, (at_k, k_stride), (at_v, v_stride) = _kv_tokens(cache, k, v)
     _check("hsa_paged_cache_read", load_library().hsa_paged_cache_read(
-        cache.ref, k.data_ptr(), v.data_ptr(), dtype, k_stride, v_stride, k.shape[0],
+        cache.ref, at_k, at_v, dtype, k_stride, v_stride, n,
         _given("cu", cu, _DTYPES["i32"], (cache.batch + 1,), device),
         _given("start", start, _DTYPES["i64"], (cache.batch,), device), stream))
 
