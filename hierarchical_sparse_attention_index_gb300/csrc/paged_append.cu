@@ -11,8 +11,8 @@
 // exact; what is left of a quarter turn goes through sincospif.
 // Codes of 4 bits are put in the pool's order in shared memory, so that whole 8-byte pieces are written; warps whose heads
 // are q's alone skip that.
-// Measured: 65,536 tokens of 32 + 8 + 8 heads of 128 dims, bf16, into E4M3 pages 240 us, 0.90 of the measured copy rate, into bf16 pages 245, 0.97; 16,384
-// into 4-bit pages 91 us, 0.71 (the schedulers issue in two thirds of the clocks; with codes for every head, and without
+// Measured: 65,536 tokens of 32 + 8 + 8 heads of 128 dims, bf16, into E4M3 pages 230 us, 0.94 of the measured copy rate, into bf16 pages 242, 0.98; 16,384
+// into 4-bit pages 89 us, 0.73 (the schedulers issue in two thirds of the clocks; with codes for every head, and without
 // packed arithmetic, 131); 64 single tokens 3.4 us (the launch, and loads that wait for one another).
 // Back into rows, 8 heads: 4 x 65,536 of 128 dims from 4-bit pages 168 us, 0.94, from E4M3 0.99, bf16 1.00; 3 x 2,500 of
 // 4 x 64 from E4M3 3.0 us.
@@ -384,8 +384,9 @@ template <int D, int KV, bool BF16>
 cudaError_t append(PagedAppendParams p, cudaStream_t s) {
   constexpr int kPer = D / 16;
   const int64_t heads = (int64_t)p.heads_q + 2 * p.w.heads, row = heads * kPer;        // units per token
-  // whole rows, about eight units to a thread; fewer rows, then slices of a row's heads, while there are SMs without a block
-  const int64_t most = imin64(kMaxRows, imax64(1, 8 * kThreads / row));
+  // whole rows, about twelve units to a thread (65,536 tokens of 48 heads into E4M3 pages, 6, 8, 12, 16, 24, 32 units: 238, 240, 230, 236,
+  // 233, 241 us, into bf16 243, 245, 242, 248, 246, 254); fewer rows, then slices of a row's heads, while there are SMs without a block
+  const int64_t most = imin64(kMaxRows, imax64(1, 12 * kThreads / row));
   p.w.rows_per_block = (int32_t)imax64(1, imin64(most, (p.w.n_tokens + 2 * kSms - 1) / (2 * kSms)));
   const int64_t blocks = (p.w.n_tokens + p.w.rows_per_block - 1) / p.w.rows_per_block;
   int64_t slices = imin64((2 * kSms + blocks - 1) / blocks, (row + kThreads - 1) / kThreads);
