@@ -51,7 +51,7 @@ struct Slot {
   static constexpr int kSlots = D == 128 ? (NT <= 2 ? 6 : 10) : (NT == 1 ? 10 : NT == 2 ? 12 : 15);
   static constexpr int kWide = kPieces * 4 * kScales;    // f16 scales: of K, then of V
   static constexpr int kWarpBytes = kSlots * kBytes + kWide;
-  static_assert(kCtas * (kWarps * kWarpBytes + 3072) <= 228 * 1024, "shared memory of an SM");
+  static_assert(kCtas * (kWarps * kWarpBytes + 3 * 1024) <= 228 * 1024, "shared memory of an SM");
   static_assert(8 * NT * kPagedOutLd<D> * 4 <= kSlots * kBytes, "a warp's outputs fit its ring");
   static __host__ __device__ __forceinline__ constexpr uint32_t k_at(int r, int c) { return (uint32_t)(four_place(r) * kRow + c * 16); }
   static __host__ __device__ __forceinline__ constexpr uint32_t v_at(int r, int c) { return (uint32_t)(r * kRow + (kChunks == 4 ? c ^ (r & 2) : c) * 16); }
