@@ -265,3 +265,24 @@ def test_calls_refuse_other_devices_and_types(H):  # noqa: F811
         with pytest.raises(ValueError):
             H.hsa_draft_verify(**{**ok, **bad})
     clean(H)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF, HF])
+@pytest.mark.parametrize("n,lookup", [(131072, False), (131071, False), (32000, False), (131072, True), (2047, False)])
+def test_verify_does_not_depend_on_the_batch(H, dtype, n, lookup):  # noqa: F811
+    """The same requests among 6 to 300 others, which take other numbers and sizes of CTAs: the same tokens."""
+    g = torch.Generator().manual_seed(n)
+    few, nq = 3, 2
+    p, q = (torch.softmax(3 * torch.randn(few, r, n, generator=g), -1).to(dtype).cuda() for r in (nq, nq - 1))
+    drafted = torch.randint(0, n, (few, nq - 1), generator=g, dtype=torch.int32).cuda()
+    u, v = torch.tensor([[0.0], [2.0], [0.5]]).cuda(), torch.rand(few, generator=g).cuda()
+    want = None
+    for times in (2, 7, 11, 34, 100):
+        batch = few * times
+        tokens, accepted = torch.full((batch, nq), 55, dtype=torch.int32, device="cuda"), torch.full((batch,), 55, dtype=torch.int32, device="cuda")
+        H.hsa_draft_verify(p.repeat(times, 1, 1), None if lookup else q.repeat(times, 1, 1), drafted.repeat(times, 1), u.repeat(times, 1),
+                           v.repeat(times), accepted, tokens)
+        clean(H)
+        want = want or (accepted[:few], tokens[:few])
+        for got, w in zip((accepted, tokens), want):
+            assert torch.equal(got.view(times, few, *got.shape[1:]), w.expand(times, *w.shape))
