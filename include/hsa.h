@@ -385,8 +385,9 @@ HSA_API hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const voi
                                  const int64_t* start, hsa_stream_t stream);
 
 /* hsa_paged_cache_write with the position rotation applied on the way: of row t, at position pos = start[b] + t -
- * cu[b] of its request, pair i of each head of q and k turns by the angle pos inv_freq[i] (taken modulo one turn
- * in 64-bit integers: off by at most 2^-52 of pos inv_freq / 2 pi turns) in fp32, with one rounding of the result:
+ * cu[b] of its request, pair i of each head of q and k turns by the angle pos inv_freq[i] (finite, of either sign; taken
+ * modulo one turn in 64-bit integers: off by at most 2^-52 of pos inv_freq / 2 pi turns and by |pos| 2^-64 turns) in fp32,
+ * with one rounding of the result:
  *   (x, y) -> (x cos - y sin, x sin + y cos),
  *   HSA_ROPE_HALVES: dims rotary_at + i and rotary_at + i + R / 2, HSA_ROPE_NEIGHBOURS: rotary_at + 2i and 2i + 1, i < R / 2.
  * The rotated queries go to q_out, which may be q itself (the same address and stride; otherwise the two must not overlap),
