@@ -244,10 +244,12 @@ __global__ void __launch_bounds__(kThreads, kCtas<T> * 256 / kThreads) draft_ver
       waiting = true;
     }
     if (!total) return false;
+    // border = floor(u total), exact: u = m 2^-shift with shift at least 24, so it is below total, whatever that is
     const uint32_t bits = __float_as_uint(fminf(fmaxf(u_sample, 0.f), 0x1.fffffep-1f));        // NaN: 0
-    const int left = (int)(bits >> 23) - 86;             // 2^(e - 150) in units of 2^-64
+    const int shift = 150 - (int)(bits >> 23);
     const uint64_t m = (bits & 0x7FFFFFu) | 0x800000u;
-    const uint64_t border = __umul64hi(total, left >= 0 ? m << left : left > -24 ? m >> -left : 0ull);
+    const uint64_t high = __umul64hi(total, m), low = total * m;
+    const uint64_t border = shift < 64 ? (high << (64 - shift)) | (low >> shift) : shift < 128 ? high >> (shift - 64) : 0ull;
     uint64_t rest = border - before;     // the first entry whose running sum in this CTA's share is above this
     int piece = -1;
     if (border >= before) {

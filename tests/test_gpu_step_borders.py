@@ -1,4 +1,5 @@
-"""Borders of what the calls of a speculative step promise: angles of turning back and of positions far past any page."""
+"""Borders of what the calls of a speculative step promise: angles of turning back and of positions far past any page, and randoms
+whose product with a sum is a few of its units."""
 import math
 
 import pytest
@@ -6,7 +7,7 @@ import torch
 
 from tests import four
 from tests import test_gpu_step as S
-from tests.test_gpu_step import HF, H  # noqa: F401  (H is a fixture)
+from tests.test_gpu_step import BF, HF, H  # noqa: F401  (H is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +34,32 @@ def test_append_angles_of_either_sign(H, first, halves):  # noqa: F811
     bound = 2.0 ** -11 * want.abs() + (2.0 ** -21 + angle[:, None]) * size * 1.001 + 2.0 ** -25
     off = (out.double() - want).abs()
     assert (off <= bound).all(), f"{(off / bound).max()} times the bound"
+
+
+@pytest.mark.parametrize("low", [1, 2, 3, 7, 50])
+@pytest.mark.parametrize("dtype", [torch.float32, BF, HF])
+def test_verify_small_randoms(H, dtype, low):  # noqa: F811
+    """A random so small that its product with the sum is a few units: the first token holds `low` of them. At the smallest random
+    whose product reaches `low` the token is the next one, at any below it the first."""
+    n, at = 2000, (700, 1500, 1999)
+    unit = 2.0 ** -46 if dtype is not HF else 2.0 ** -24                 # (f16 has no smaller value)
+    p = torch.zeros(1, 1, n)
+    p[0, 0, at[0]], p[0, 0, at[1]], p[0, 0, at[2]] = low * unit, 0.3, 0.4
+    p = p.to(dtype).cuda()
+    w = S.fixed(p[0, 0]).tolist()
+    total, first = sum(w), w[at[0]]
+    shift = 0                                                            # u = m 2^-shift, m of 24 bits
+    while -(-(first << shift) // total) < 1 << 23:
+        shift += 1
+    m = -(-(first << shift) // total)                                    # total m 2^-shift >= first, for the first time
+    assert m < 1 << 24
+    cases = [m - 1, m, m + 1, m - 2 if m - 2 >= 1 << 23 else m]
+    u = torch.tensor([c * 2.0 ** -shift for c in cases], dtype=torch.float64).float().cuda()
+    assert [int(x * 2 ** shift) for x in u.double().tolist()] == cases
+    k = len(cases)
+    accepted, tokens = torch.full((k,), 77, dtype=torch.int32).cuda(), torch.full((k, 1), 77, dtype=torch.int32).cuda()
+    H.hsa_draft_verify(p.expand(k, 1, n).contiguous(), None, torch.empty(k, 0, dtype=torch.int32, device="cuda"),
+                       torch.empty(k, 0, device="cuda"), u, accepted, tokens)
+    S.clean(H)
+    want = [at[0] if total * c < first << shift else at[1] for c in cases]
+    assert tokens[:, 0].tolist() == want and accepted.tolist() == [0] * k
