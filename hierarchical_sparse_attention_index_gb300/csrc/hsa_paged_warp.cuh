@@ -11,21 +11,21 @@ constexpr int kPagedGroup = 16;          // keys of a piece
 template <int D>
 constexpr int kPagedOutLd = D + 4;       // floats from row to row when the warps merge (bank spread)
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+__device__ __forceinline__ void page_copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // 16 bytes, of which all but the first `bytes` are zeros and not read
-__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, uint32_t bytes) {
+__device__ __forceinline__ void page_copy16z(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // a row's scales of 4-bit pages, N = 4 or 8 bytes, of which all but the first `bytes` are zeros and not read
 template <int N>
-__device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src, uint32_t bytes) {
+__device__ __forceinline__ void page_copy_scales(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void page_copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
-__device__ __forceinline__ void cp_async_wait() {
+__device__ __forceinline__ void page_copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {

@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
       if (seen == 0xFFFFu) {
 #pragma unroll
         for (int u = 0; u < kCopies; ++u) {
-          cp_async16(ring + T::k_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, k + u * 512);
-          cp_async16(ring + T::kHalf + T::v_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, v + u * 512);
+          page_copy16(ring + T::k_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, k + u * 512);
+          page_copy16(ring + T::kHalf + T::v_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, v + u * 512);
         }
       } else {
         // rows no query sees are not read: they become zeros, whatever the pool holds there
@@ -132,12 +132,12 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
         for (int u = 0; u < kCopies; ++u) {
           const int r = (u * 32 + lane) / T::kChunks;
           const uint32_t n = (seen >> r) & 1u ? 16u : 0u;
-          cp_async16z(ring + T::k_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, k + (n ? u * 512 : 0), n);
-          cp_async16z(ring + T::kHalf + T::v_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, v + (n ? u * 512 : 0), n);
+          page_copy16z(ring + T::k_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, k + (n ? u * 512 : 0), n);
+          page_copy16z(ring + T::kHalf + T::v_at((u * 32 + lane) / T::kChunks, lane % T::kChunks) + st, v + (n ? u * 512 : 0), n);
         }
       }
     }
-    cp_async_commit();
+    page_copies_commit();
   };
 #pragma unroll
   for (int s = 0; s < T::kStages - 1; ++s) issue(s, s);
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
 
   int stage = 0;
   for (int i = 0; i < n_groups; ++i) {
-    cp_async_wait<T::kStages - 2>();
+    page_copies_wait<T::kStages - 2>();
     __syncwarp();
     const bool skip = (bad >> stage) & 1u;
     const uint32_t sk = ring + (uint32_t)stage * T::kStage, sv = sk + T::kHalf;
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, (Tile<D, KV, NT>::kCtas)) paged_attn
   }
 
   // ---------------------------------------------------------------- merge the warps
-  cp_async_wait<0>();
+  page_copies_wait<0>();
   __syncwarp();
   float* so = reinterpret_cast<float*>(sm + (size_t)warp * T::kRing);   // [row][kOutLd]
 #pragma unroll

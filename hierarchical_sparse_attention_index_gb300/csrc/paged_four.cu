@@ -149,26 +149,26 @@ __global__ void __launch_bounds__(kThreads, (Slot<D, NT>::kCtas)) paged_four_ker
       const uint8_t* sc = s_src + piece * T::kScales;
       if (seen == 0xFFFFu) {
         if (bad) bad &= ~(1u << (i & 31));
-        cp_async_scales<T::kScaleRow>(at + s_dst, sc, T::kScaleRow);
+        page_copy_scales<T::kScaleRow>(at + s_dst, sc, T::kScaleRow);
 #pragma unroll
         for (int u = 0; u < kCopies; ++u) {
-          cp_async16(at + k_dst + u * 512, k + u * 512);
-          cp_async16(at + v_dst + u * 512, v + u * 512);
+          page_copy16(at + k_dst + u * 512, k + u * 512);
+          page_copy16(at + v_dst + u * 512, v + u * 512);
         }
       } else {
         // rows no query sees are not read: they become zeros, whatever the pool holds there
         bad = (bad & ~(1u << (i & 31))) | ((seen ? 0u : 1u) << (i & 31));
         const bool n = (seen >> rs) & 1u;
-        cp_async_scales<T::kScaleRow>(at + s_dst, n ? sc : p.k_s, n ? (uint32_t)T::kScaleRow : 0u);
+        page_copy_scales<T::kScaleRow>(at + s_dst, n ? sc : p.k_s, n ? (uint32_t)T::kScaleRow : 0u);
 #pragma unroll
         for (int u = 0; u < kCopies; ++u) {
           const uint32_t m = (seen >> (r0 + 8 * u)) & 1u ? 16u : 0u;
-          cp_async16z(at + k_dst + u * 512, m ? k + u * 512 : p.k_pool, m);
-          cp_async16z(at + v_dst + u * 512, m ? v + u * 512 : p.v_pool, m);
+          page_copy16z(at + k_dst + u * 512, m ? k + u * 512 : p.k_pool, m);
+          page_copy16z(at + v_dst + u * 512, m ? v + u * 512 : p.v_pool, m);
         }
       }
     }
-    cp_async_commit();
+    page_copies_commit();
   };
 #pragma unroll
   for (int s = 0; s < T::kSlots - kP; ++s) issue(s, ring + s * T::kBytes);
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, (Slot<D, NT>::kCtas)) paged_four_ker
     freed[h2] = ring + (T::kSlots - kP + h2) * T::kBytes;
   }
   for (int i = 0; i < turns; ++i) {
-    cp_async_wait<T::kSlots - 2 * kP>();
+    page_copies_wait<T::kSlots - 2 * kP>();
     __syncwarp();
     uint32_t none = 0;                   // bit h2: that piece of the turn is zeros
     if (bad) none = (bad >> (kP * i & 31)) & ((1u << kP) - 1u);
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, (Slot<D, NT>::kCtas)) paged_four_ker
   }
 
   // ---------------------------------------------------------------- merge the warps
-  cp_async_wait<0>();
+  page_copies_wait<0>();
   __syncwarp();
   float* so = reinterpret_cast<float*>(sm + (size_t)warp * T::kWarpBytes);   // [row][kPagedOutLd]
 #pragma unroll

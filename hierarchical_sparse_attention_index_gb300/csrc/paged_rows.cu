@@ -382,26 +382,26 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
         const uint8_t* sc = s_src + piece * kScales;
         gone = seen ? gone & ~(1u << load_slot) : gone | 1u << load_slot;
         if (seen == 0xFFFFu) {
-          cp_async_scales<kScaleRow>(at + scale_at, sc, kScaleRow);
+          page_copy_scales<kScaleRow>(at + scale_at, sc, kScaleRow);
 #pragma unroll
           for (int u = 0; u < kCopies; ++u) {
-            cp_async16(at + copy_at + u * 512, k + u * 512);
-            cp_async16(at + kHalf + copy_at + u * 512, v + u * 512);
+            page_copy16(at + copy_at + u * 512, k + u * 512);
+            page_copy16(at + kHalf + copy_at + u * 512, v + u * 512);
           }
         } else {
           const bool some = (seen >> r) & 1u;
-          cp_async_scales<kScaleRow>(at + scale_at, some ? sc : p.k_s, some ? (uint32_t)kScaleRow : 0u);
+          page_copy_scales<kScaleRow>(at + scale_at, some ? sc : p.k_s, some ? (uint32_t)kScaleRow : 0u);
 #pragma unroll
           for (int u = 0; u < kCopies; ++u) {
             const uint32_t m = (seen >> (r0 + 8 * u)) & 1u ? 16u : 0u;
-            cp_async16z(at + copy_at + u * 512, m ? k + u * 512 : p.k_pool, m);
-            cp_async16z(at + kHalf + copy_at + u * 512, m ? v + u * 512 : p.v_pool, m);
+            page_copy16z(at + copy_at + u * 512, m ? k + u * 512 : p.k_pool, m);
+            page_copy16z(at + kHalf + copy_at + u * 512, m ? v + u * 512 : p.v_pool, m);
           }
         }
         load_slot = load_slot + 1 == kSlots ? 0 : load_slot + 1;
       }
       ++loads;
-      cp_async_commit();
+      page_copies_commit();
     };
     // job `it` from here on: its pieces, its queries (16 or 8 lanes to a row, rows in turn over the eight warps)
     auto open = [&](int it) {
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
       for (int i = 0; i <= n; ++i) {     // K(i), then V(i - 1)
         const uint32_t last = slot == 0 ? kSlots - 1 : slot - 1;
         if (i < n) {
-          cp_async_wait<kSlots - 2>();
+          page_copies_wait<kSlots - 2>();
           __syncwarp();
           if (lane == 0) s_bad[t][tiles & 7][part] = (gone >> slot) & 1u;
           ++tiles;
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(Roles<FOUR>::kThreads, 1) paged_rows_kernel(co
       }
       if (!ok) break;
     }
-    cp_async_wait<0>();
+    page_copies_wait<0>();
   };
 
   if (warp >= kSoftWarps && warp < kOutWarp) {
