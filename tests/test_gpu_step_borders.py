@@ -1,5 +1,5 @@
-"""Borders of what the calls of a speculative step promise: angles of turning back and of positions far past any page, and randoms
-whose product with a sum is a few of its units."""
+"""Borders of what the calls of a speculative step promise: angles of turning back and of positions far past any page, randoms
+whose product with a sum is a few of its units, and every place written for rows that are no distributions."""
 import math
 
 import pytest
@@ -63,3 +63,28 @@ def test_verify_small_randoms(H, dtype, low):  # noqa: F811
     S.clean(H)
     want = [at[0] if total * c < first << shift else at[1] for c in cases]
     assert tokens[:, 0].tolist() == want and accepted.tolist() == [0] * k
+
+
+def test_verify_of_garbage_writes_every_place(H):  # noqa: F811
+    """Rows that are no distributions (too large a sum, random bits): each request gets its kept tokens, one of the vocabulary behind
+    them, and -1 in the rest; nothing is left as it was, and nothing else is written."""
+    batch, nq, n, was = 40, 4, 5003, -77
+    g = torch.Generator().manual_seed(1)
+    for p in (torch.ones(batch, nq, n), torch.randint(-2 ** 31, 2 ** 31 - 1, (batch, nq, n), generator=g, dtype=torch.int32).view(torch.float32)):
+        p = p.cuda()
+        q = p[:, 1:].contiguous().flip(1)
+        drafted = torch.randint(0, n, (batch, nq - 1), generator=g, dtype=torch.int32).cuda()
+        room = torch.full((batch * nq + 32,), was, dtype=torch.int32, device="cuda")
+        tokens, accepted = room[16:16 + batch * nq].view(batch, nq), torch.full((batch,), was, dtype=torch.int32, device="cuda")
+        for ua in (torch.rand(batch, nq - 1, generator=g), torch.zeros(batch, nq - 1), torch.full((batch, nq - 1), 2.0)):
+            tokens.fill_(was)
+            accepted.fill_(was)
+            H.hsa_draft_verify(p, q, drafted, ua.cuda(), torch.rand(batch, generator=g).cuda(), accepted, tokens)
+            S.clean(H)
+            assert ((accepted >= 0) & (accepted < nq)).all()
+            assert (room[:16] == was).all() and (room[16 + batch * nq:] == was).all()
+            place, a = torch.arange(nq).cuda()[None], accepted[:, None]
+            y = tokens.gather(1, a.long())
+            assert ((y >= 0) & (y < n)).all()
+            want = torch.where(place < a, torch.cat((drafted, drafted[:, :1]), 1), torch.where(place == a, y, -1))
+            assert torch.equal(tokens, want)
