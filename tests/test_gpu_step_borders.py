@@ -1,5 +1,5 @@
 """Borders of what the calls of a speculative step promise: angles of turning back and of positions far past any page, randoms
-whose product with a sum is a few of its units, and every place written for rows that are no distributions."""
+whose product with a sum is a few of its units, every place written for rows that are no distributions, and the largest vocabularies."""
 import math
 
 import pytest
@@ -88,3 +88,13 @@ def test_verify_of_garbage_writes_every_place(H):  # noqa: F811
             assert ((y >= 0) & (y < n)).all()
             want = torch.where(place < a, torch.cat((drafted, drafted[:, :1]), 1), torch.where(place == a, y, -1))
             assert torch.equal(tokens, want)
+
+
+@pytest.mark.parametrize("dtype,n", [(torch.float32, 1 << 24), (torch.float32, (1 << 24) - 1), (BF, 1 << 24), (HF, (1 << 24) - 129)])
+def test_verify_largest_vocabularies(H, dtype, n):  # noqa: F811
+    """As many entries as a row may have, and odd numbers near it: draws at both ends of the row and between."""
+    p, q, drafted, ua, _ = S.draft(3, 2, n, dtype, seed=3)
+    for at in (0.0, 0.5, 1.0 - 2.0 ** -24):
+        us = torch.full((3,), at, device="cuda")
+        S.verify(H, p, q, drafted, torch.tensor([[0.0], [2.0], [0.9]], device="cuda"), us)
+        S.verify(H, p, None, drafted, ua, us)
