@@ -11,9 +11,10 @@
 //    (The borders of sums in fp32 would move by more than most tokens weigh; fp64 adds are slower than the
 //    loads here.) An entry becomes two integers by four fp32 additions: the bits of 1 + x hold x in units of 2^-23, and
 //    the rest, which fp32 holds exactly, gives 23 more bits in the same way.
-// Measured, fp32, 131,072 entries: 1 request x 5 rows 6.0 us, 64 requests 15.6 us, 0.55 of the measured copy rate (rows of 131,071, read entry by
-// entry: 18); 200 requests 38 us, 100 x 4 rows, bf16 17.3; 37 lookups x 8 rows of 50,001 entries 5.7 us. What is left in the short ones is the
-// launch, the cluster's start and loads that wait for one another.
+// Measured, 131,072 entries, fp32: 1 request x 5 rows 6.0 us, 64 requests 15.6 us, 0.55 of the measured copy rate (rows of 131,071, read entry by
+// entry: 18), 200 requests 38 us, 0.71; bf16: 100 x 4 rows 17.3 us, 0.39; 37 lookups x 8 rows of 50,001 bf16 entries 5.7 us. What is left in the
+// short ones is the launch, the cluster's start and loads that wait for one another; with 16-bit entries also the sums, which take 10
+// instructions for each of 2 bytes as they take 11 for each of 4 (issue 50 % of the active clocks against 33, HBM 26 % against 38).
 #include <string.h>
 
 #include "hsa_common.cuh"

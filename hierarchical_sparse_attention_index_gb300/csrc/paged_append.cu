@@ -11,11 +11,15 @@
 // exact (the fraction is not, by up to 2^-64); what is left of a quarter turn goes through sincospif.
 // Codes of 4 bits are put in the pool's order in shared memory, so that whole 8-byte pieces are written; warps whose heads
 // are q's alone skip that.
-// Measured: 65,536 tokens of 32 + 8 + 8 heads of 128 dims, bf16, into E4M3 pages 230 us, 0.94 of the measured copy rate, into bf16 pages 242, 0.98; 16,384
-// into 4-bit pages 89 us, 0.73 (the schedulers issue in two thirds of the clocks; with codes for every head, and without
-// packed arithmetic, 131); 64 single tokens 3.4 us (the launch, and loads that wait for one another).
-// Back into rows, 8 heads: 4 x 65,536 of 128 dims from 4-bit pages 168 us, 0.94, from E4M3 0.99, bf16 1.00; 3 x 2,500 of
-// 4 x 64 from E4M3 3.0 us.
+// Measured: 65,536 tokens of 32 + 8 + 8 heads of 128 dims, bf16, into E4M3 pages 230 us, 0.94 of the measured copy rate, into bf16 pages 242, 0.98, into
+// 4-bit pages 253, 0.83; 16,384 into those 70 us, 0.75 (with the read of their rows 89; with codes for every head, and without
+// packed arithmetic, 131). There the schedulers issue in 68 % of the clocks, no unit is above 47 % and HBM at 56: what is left is
+// loads, fixed latencies and a block's first barriers, which the 28 warps of an SM do not cover. 64 single tokens 3.4 us (the launch, and loads that
+// wait for one another).
+// hsa_paged_cache_write of 65,536 tokens of 8 + 8 heads into 4-bit pages 94 us, 0.54 (into bf16 pages 83, 0.95), of 16,384 32 us, 0.40: every warp
+// makes codes, 20 instructions to an element (17.5 in the append, on average); issue 74 %, the integer and conversion unit 61 %, HBM 43.
+// Back into rows, 8 heads of 128 dims: 262,144 rows from 4-bit pages 215 us, 0.94, from E4M3 238, 1.00, from bf16 308, 1.03; 5,065 rows of
+// 4 heads of 64 dims from E4M3 3.0 us.
 #include "hsa_dense.h"
 #include "hsa_four.cuh"
 #include "hsa_rows.cuh"

@@ -492,7 +492,9 @@ struct Rounds {
   int64_t most(int64_t ctas, int64_t span) const { return splits_in(first(ctas) + count - 1, ctas, span); }
 };
 // The tcgen05 kernel, one CTA to an SM. 64 requests x 4 heads x 16,384 keys, ragged: n = 1, 4, 9: 246, 204, 229 us;
-// x 4,097: 73, 77, 105; 8 x 4 x 16,384: n = 3, 4, 5, 9: 54.6, 53.9, 74.5, 59.0
+// x 4,097: 73, 77, 105; 8 x 4 x 16,384: n = 3, 4, 5, 9: 54.6, 53.9, 74.5, 59.0. Over 4-bit pages the same constants are used, with lengths
+// alike within 10 % of the best; a job counts as long as the longest, though, so ragged lengths may get too few splits: 16 requests x 8 heads x 5
+// queries x 8 heads of up to 8,192 keys, 128 CTAs for 152 places: the rule's n = 1 70.5 us, n = 2, 3, 4, 5: 80, 64, 56.5, 65
 constexpr Rounds kTcRounds = {kSms, 8, true, 400};
 // The warp MMA kernel with 17 to 32 rows, two to an SM. Against as many CTAs as four to an SM would be, in no rounds: 16
 // requests x 8 heads x 20 rows, f16, 4,097 keys 30 us (46), 16,384 97 (115); 16 x 4 x 35 rows, E4M3, 4,097 36 (40), 16,384 93 (98);
@@ -500,7 +502,8 @@ constexpr Rounds kTcRounds = {kSms, 8, true, 400};
 constexpr Rounds kWideRounds = {2 * kSms, 6, false, 400};
 // 4-bit pages. 8 query rows, 128 dims, 32 x 8 heads of 1 .. 8,192 keys: n = 1, 2, 3, 5, 8: 72.8, 50.9, 43.4, 46.0, 44.8 us; 16 x 8 of
 // 8,192: n = 3, 4, 6: 37.5, 44.2, 41.1; 4 x 8 of 131,072: n = 13, 14, 19, 28: 118, 112, 123.5, 115; 16 rows, 64 x 8 of 4,096: n = 1, 2,
-// 4: 91.5, 104, 111, of 1 .. 4,096: 68, 70, 75; 8 x 8 of 16,384: n = 3, 4, 5: 62.6, 48.5, 75.7; 32 x 8 of 1 .. 8,192: n = 1, 4: 77, 64
+// 4: 91.5, 104, 111, of 1 .. 4,096: 68, 70, 75; 8 x 8 of 16,384: n = 3, 4, 5: 62.6, 48.5, 75.7. Here, too, a job counts as long as the
+// longest: for 16 rows, 32 x 8 of 1 .. 8,192 keys (256 CTAs for 304 places) the rule takes n = 1, 80 us, where n = 2, 3, 4, 6 take 63, 63, 61, 64
 static Rounds four_rounds(int32_t chunk_rows, int32_t head_dim) { return {kSms * four_ctas((chunk_rows + 7) / 8, head_dim), 6, false, 700}; }
 static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
   int64_t best = 1, cost = INT64_MAX;
@@ -520,7 +523,8 @@ static int64_t best_splits(const Rounds& r, int64_t ctas, int64_t span) {
 // in the warp MMA kernel, 64 requests x 4 heads of 128 dims, of 1 .. 8,192 keys: 32 rows 105 and 164 us, 24 rows 104 and 124;
 // 1,000 keys: 33.3 and 33.1, 33.5 and 28.6; 1 request x 8 heads x 1,000 keys: 13.0 and 12.4, 13.0 and 9.9; 16 x 8 x 8,192 keys of 64
 // dims: 28 rows 59.7 and 55.1, 18 rows 59.8 and 47.7. From 4-bit pages, 16 x 8 heads of 128 dims x 8,192 keys: 24 rows 73 and 65
-// us, 28 rows 73 and 120; 64 x 4, of 1 .. 4,097 keys: 60.5 and 60, 60 and 106; 16 x 8 x 8,192 of 64 dims: 63 and 40, 63 and 55.
+// us, 28 rows 73 and 120; 64 x 4, of 1 .. 4,097 keys: 60.5 and 60, 60 and 106; 16 x 8 x 8,192 of 64 dims: 63 and 40, 63 and 55 (so for 64
+// dims the border, one for both sizes, lies lower than it could over 4-bit pages).
 // Else up to 32 rows one CTA reads its keys once for all of them; more rows
 // (E4M3) are dealt out evenly (35: 18 and 17), and the later CTAs' keys come from L2.
 // Up to 16 rows the splits make about as many CTAs as the GPU holds at a time, 3 per SM: more only add starts and joins (4

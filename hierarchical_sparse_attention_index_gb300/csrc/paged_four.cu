@@ -15,10 +15,15 @@
 //    in pairs of keys as the products take them, and come from shared memory;
 //  - the keys of a piece are taken in the order t, t + 4 (four_key), so that every shared load is free of bank conflicts;
 //  - two pieces of 16 keys go through a turn of the loop together: two independent chains, one vote and one wait for both.
+// Fewer bits than 32 are in the weights, f16 for the product with V as in paged_attn.cu (a relative 2^-11 each, independent from key to
+// key; the sums take them unrounded: an f16 result of 64 x 5 queries is off by 2.8e-4 of its size, 2.1e-4 with fp32 weights; bf16
+// results by 1.7e-3 with either), and in bf16 queries, which become f16 by a power of two per row.
 // Measured (8 rows, bf16 queries, 128 dims): 16 requests x 8 heads x 8,192 keys 37.1 us, 0.60 of the measured copy rate, 4 x 8 x
 // 131,072 112 us, 0.80, 32 x 8 of 1 .. 8,192 keys 43.4 us, 1 x 8 x 1,000 6.6 us; 16 rows, 64 x 8 x 4,096 91.5 us; 64 dims, 8 rows, 32 x 8 x 8,192
 // 42.7 us. In the long one the schedulers issue in 62 % of the clocks, 295 instructions for 16 keys; the integer and conversion unit is
-// at 52 %, the tensor unit at 27 %, HBM at 79 %: what is left is waits between dependent instructions that 12 warps do not fill.
+// at 52 %, the tensor unit at 27 %, HBM at 79 %: what is left is waits between dependent instructions that 12 warps do not fill. With 16 rows
+// there are 8 warps to an SM, which issue in 48 % (the tensor unit is at 35, HBM at 41). Of 1 .. 8,192 keys the CTAs start in the order of the
+// grid, so that a long request's last splits start last: 768 CTAs for 456 places, issue 37 % over the whole launch.
 #include "hsa_four.cuh"
 #include "hsa_paged_warp.cuh"
 

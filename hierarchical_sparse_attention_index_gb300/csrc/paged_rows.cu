@@ -34,7 +34,9 @@
 //    tiles from the rings); twice the pieces for half the converting warps: 416 against 306. Q in tensor memory would spare its reads, but S of two
 //    streams twice and their O take all 512 columns.
 // Measured: 64 requests x 4 heads x 5 queries x 7 heads, f16, 16,384 keys each 276 us (16-bit pages: 328), of 1 .. 4,097 keys
-// 56.6; 16 x 8 heads x 8 queries x 16 heads, bf16, 8,192 keys 82.
+// 56.6; 16 x 8 heads x 8 queries x 16 heads, bf16, 8,192 keys 82. 64 dims, 16 x 8 heads, 8,192 keys: 28 and 40 rows 63 us, 128 rows 71, where 128
+// dims take 73 with 28 rows. Half the bytes and half the conversion save a seventh: the tensor path is busy for 35 %, issue is at 48, HBM at
+// 13, so that what a tile of 64 keys costs whatever its dims (barriers, and S on its way out and back) is likely to decide.
 #include <string.h>
 
 #include <numeric>

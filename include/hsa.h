@@ -390,9 +390,9 @@ HSA_API hsa_status hsa_paged_cache_write(const hsa_paged_cache* cache, const voi
  * with one rounding of the result:
  *   (x, y) -> (x cos - y sin, x sin + y cos),
  *   HSA_ROPE_HALVES: dims rotary_at + i and rotary_at + i + R / 2, HSA_ROPE_NEIGHBOURS: rotary_at + 2i and 2i + 1, i < R / 2.
- * The rotated queries go to q_out, which may be q itself (the same address and stride; otherwise the two must not overlap),
- * the rotated keys and the values to the pages as in hsa_paged_cache_write, from their fp32 values. Rows outside
- * [cu[0], cu[batch]) are padding: neither their q_out rows nor any page is written. A row whose position is
+ * The rotated queries go to q_out, which may be q itself (the same address and stride; otherwise the two must not overlap)
+ * and must not overlap k or v; the rotated keys and the values go to the pages as in hsa_paged_cache_write, from their
+ * fp32 values. Rows outside [cu[0], cu[batch]) are padding: neither their q_out rows nor any page is written. A row whose position is
  * skipped (HSA_FLAG_WRITE_RANGE) has its q_out written all the same. n_tokens = 0 launches nothing. */
 HSA_API hsa_status hsa_paged_cache_append(const hsa_paged_cache* cache, const hsa_append_args* args, hsa_stream_t stream);
 
