@@ -520,7 +520,7 @@ def _probabilities(name, t, shape):
 
 def hsa_draft_verify(p, q, drafted, u_accept, u_sample, accepted, tokens, n_draft=None, stream=None):
     """p: [batch][nq][vocabulary] target probabilities (float32, bfloat16 or float16), q: [batch][nq - 1][vocabulary] the
-    drafter's, in the same type, or None; both with their rows at one distance (p[:, :nq] of a longer buffer is copied first); drafted:
+    drafter's, in the same type, or None; both with their rows at one distance (pass a copy of p[:, :nq] of a longer buffer); drafted:
     int32 [batch][nq - 1]; u_accept: float32 [batch][nq - 1], u_sample: float32 [batch]; accepted: int32 [batch], tokens: int32
     [batch][nq] (written); n_draft: int32 [batch] or None (nq - 1)."""
     device, shape = p.get_device(), p.shape
